@@ -5,10 +5,11 @@
 the same results from the definitions in 64 bits.  With ``own`` false a pass is made of
 elementary torch operations in 32 bits; with ``own`` true it calls this package.
 
-Operators (x a row of logits, z = x / temperature, lse = log sum exp z, p = exp(z - lse)):
+Operators (x a row of logits, m = max x, d = (x - m) / temperature, s = ln sum exp d,
+ln p = d - s; the row's stats are m and s):
 
-  score          log p of given tokens, entropy, lse, top alternatives
-  score_grad     d logits from the gradients of log p and entropy
+  score          ln p of given tokens, entropy, stats, top alternatives
+  score_grad     d logits from the gradients of ln p and entropy
   distill        KL from a teacher's top entries to p, per row
   distill_grad   d logits of that loss
   distill_step   loss and d logits in one call
@@ -87,10 +88,10 @@ def work(case):
     n, v, k, es = case["rows"], case["vocab"], case["k"], DTYPES[case["dtype"]][1]
     logits = (n - _unread(case)) * v * es
     if case["op"] == "score":
-        return {"bytes": logits + n * (4 + 12 + 8 * k), "flops": 6 * n * v}
+        return {"bytes": logits + n * (4 + 16 + 8 * k), "flops": 6 * n * v}
     if case["op"] == "score_grad":
-        return {"bytes": logits + n * v * es + n * 20, "flops": 6 * n * v}
-    small = n * (8 * k + 12)
+        return {"bytes": logits + n * v * es + n * 24, "flops": 6 * n * v}
+    small = n * (8 * k + 16)
     if case["op"] == "distill":
         return {"bytes": logits + small, "flops": 4 * n * v}
     flops = 4 * n * v if case["op"] == "distill_grad" else 8 * n * v
@@ -118,7 +119,7 @@ def prepare(case, seed):
             x[torch.rand((n, v), generator=g, device=DEVICE) < 0.3] = -math.inf
             x[row % 16 == 7] = -math.inf
         if op == "score_grad":
-            _, s["entropy"], s["lse"] = _scores(x, s["tokens"], tau)
+            _, s["entropy"], s["stats"] = _scores(x, s["tokens"], tau)
             s["grad_logprob"] = torch.randn(n, generator=g, device=DEVICE)
             s["grad_entropy"] = 0.1 * torch.randn(n, generator=g, device=DEVICE)
         return s
@@ -131,7 +132,7 @@ def prepare(case, seed):
     if op != "distill":
         s["grad_loss"] = torch.randn(n, generator=g, device=DEVICE)
     if op == "distill_grad":
-        s["lse"] = torch.where(s["weight"] == 0, 0.0, _scores(x, None, tau)[2])
+        s["stats"] = torch.where(s["weight"][:, None] == 0, 0.0, _scores(x, None, tau)[2])
     return s
 
 
@@ -139,21 +140,20 @@ def prepare(case, seed):
 # the plain form
 # ---------------------------------------------------------------------------
 def _scores(x, tokens, tau):
-    """log p of the tokens (or None), entropy and lse; a row of -inf has lse -inf and entropy 0."""
-    z = x.float() / tau
-    top = z.amax(1, keepdim=True)
-    d = z - torch.where(top == -math.inf, 0.0, top)
+    """ln p of the tokens (or None), entropy and stats; a row of -inf has stats -inf and entropy 0."""
+    x = x.float()
+    top = x.amax(1, keepdim=True)
+    d = (x - torch.where(top == -math.inf, 0.0, top)) / tau
     e = torch.exp(d)
-    total = e.sum(1, keepdim=True)
+    total = e.sum(1)
     log_total = torch.log(total)
-    lse = log_total[:, 0] + top[:, 0]
-    mean = torch.where(e > 0, e * d, 0.0).sum(1) / total[:, 0]
-    entropy = torch.where(total[:, 0] > 0, log_total[:, 0] - mean, 0.0)
+    mean = torch.where(e > 0, e * d, 0.0).sum(1) / total
+    entropy = torch.where(total > 0, log_total - mean, 0.0)
     logprob = None
     if tokens is not None:
-        at = z.gather(1, tokens.long()[:, None])[:, 0]
-        logprob = torch.where(at == -math.inf, at, at - lse)
-    return logprob, entropy, lse
+        at = d.gather(1, tokens.long()[:, None])[:, 0]
+        logprob = torch.where(at == -math.inf, at, at - log_total)
+    return logprob, entropy, torch.stack((top[:, 0], log_total), 1)
 
 
 def _ordered(x):
@@ -164,7 +164,7 @@ def _ordered(x):
 
 def _plain_score(s):
     x = s["logits"].float()
-    logprob, entropy, lse = _scores(x, s["tokens"], s["tau"])
+    logprob, entropy, stats = _scores(x, s["tokens"], s["tau"])
     # the largest logits, the lowest id first among equal ones
     ids = torch.arange(x.shape[1], device=x.device)
     key = (_ordered(x) << 32) - ids
@@ -172,14 +172,13 @@ def _plain_score(s):
     top = -((best + (1 << 31)) % (1 << 32) - (1 << 31))
     at = x.gather(1, top)
     masked = at == -math.inf
-    top_logprobs = torch.where(masked, at, at / s["tau"] - lse[:, None])
-    return {"logprob": logprob, "entropy": entropy, "lse": lse,
+    top_logprobs = torch.where(masked, at, (at - stats[:, :1]) / s["tau"] - stats[:, 1:])
+    return {"logprob": logprob, "entropy": entropy, "stats": stats,
             "top_ids": torch.where(masked, -1, top).to(torch.int32), "top_logprobs": top_logprobs}
 
 
 def _plain_score_grad(s):
-    z = s["logits"].float() / s["tau"]
-    logp = z - s["lse"][:, None]
+    logp = (s["logits"].float() - s["stats"][:, :1]) / s["tau"] - s["stats"][:, 1:]
     p = torch.exp(logp)
     g, h = s["grad_logprob"][:, None], s["grad_entropy"][:, None]
     grad = -p * (g + h * (logp + s["entropy"][:, None]))
@@ -194,15 +193,15 @@ def _teacher(s):
     return e / e.sum(1, keepdim=True)
 
 
-def _plain_loss(s, z, lse, q):
-    at = z.gather(1, s["ids"].long().clamp(min=0)) - lse[:, None]
+def _plain_loss(s, logp, q):
+    at = logp.gather(1, s["ids"].long().clamp(min=0))
     log_q = torch.log(torch.where(q > 0, q, 1.0))
     kl = torch.where(q > 0, q * (log_q - at), 0.0).sum(1)
     return kl * s["tau"] ** 2 * s["weight"]
 
 
-def _plain_distill_grad(s, z, lse, q):
-    grad = torch.exp(z - lse[:, None])
+def _plain_distill_grad(s, logp, q):
+    grad = torch.exp(logp)
     grad.scatter_add_(1, s["ids"].long().clamp(min=0), -q)
     scale = s["grad_loss"] * s["weight"] * s["tau"]
     return (grad * scale[:, None]).to(s["logits"].dtype)
@@ -213,14 +212,14 @@ def _plain(s):
         return _plain_score(s)
     if s["op"] == "score_grad":
         return _plain_score_grad(s)
-    z, q = s["logits"].float() / s["tau"], _teacher(s)
+    x, q = s["logits"].float(), _teacher(s)
     if s["op"] == "distill_grad":
-        return {"grad": _plain_distill_grad(s, z, s["lse"], q)}
-    top = z.amax(1, keepdim=True)
-    lse = torch.log(torch.exp(z - top).sum(1)) + top[:, 0]
-    out = {"loss": _plain_loss(s, z, lse, q)}
+        return {"grad": _plain_distill_grad(s, (x - s["stats"][:, :1]) / s["tau"] - s["stats"][:, 1:], q)}
+    d = (x - x.amax(1, keepdim=True)) / s["tau"]
+    logp = d - torch.log(torch.exp(d).sum(1, keepdim=True))
+    out = {"loss": _plain_loss(s, logp, q)}
     if s["op"] == "distill_step":
-        out["grad"] = _plain_distill_grad(s, z, lse, q)
+        out["grad"] = _plain_distill_grad(s, logp, q)
     return out
 
 
@@ -233,14 +232,14 @@ def _plan(s):
     if s["op"] == "score":
         return kb.LogprobsPlan(s["logits"], s["tokens"], top_k=s["k"], temperature=s["tau"])
     if s["op"] == "score_grad":
-        return kb.LogprobsBackwardPlan(s["logits"], s["tokens"], s["lse"], s["entropy"],
+        return kb.LogprobsBackwardPlan(s["logits"], s["tokens"], s["stats"], s["entropy"],
                                        grad_logprob=s["grad_logprob"], grad_entropy=s["grad_entropy"],
                                        temperature=s["tau"])
     common = {"weight": s["weight"], "temperature": s["tau"]}
     if s["op"] == "distill":
         return kb.DistillPlan(s["logits"], s["ids"], s["values"], **common)
     if s["op"] == "distill_grad":
-        return kb.DistillBackwardPlan(s["logits"], s["ids"], s["values"], s["lse"], grad_loss=s["grad_loss"],
+        return kb.DistillBackwardPlan(s["logits"], s["ids"], s["values"], s["stats"], grad_loss=s["grad_loss"],
                                       **common)
     return kb.DistillStepPlan(s["logits"], s["ids"], s["values"], grad_loss=s["grad_loss"], **common)
 
@@ -252,7 +251,7 @@ def run(state):
         state["plan"] = _plan(state)
     out = state["plan"]()
     if state["op"] == "score":
-        return dict(zip(("logprob", "entropy", "lse", "top_ids", "top_logprobs"), out))
+        return dict(zip(("logprob", "entropy", "stats", "top_ids", "top_logprobs"), out))
     if state["op"] == "distill":
         return {"loss": out[0]}
     if state["op"] == "distill_step":
@@ -271,7 +270,9 @@ def _exact_rows(s, r):
         logp = torch.where(empty[:, None], -math.inf, logp)
         entropy = -torch.special.xlogy(logp.exp(), logp.exp()).sum(1)
         logprob = logp.gather(1, s["tokens"][r].long()[:, None])[:, 0]
-        return {"logprob": logprob, "entropy": entropy + 0.0, "lse": torch.logsumexp(x, 1),
+        top = x.amax(1)
+        stats = torch.stack((top * s["tau"], torch.where(empty, top, torch.logsumexp(x - top[:, None], 1))), 1)
+        return {"logprob": logprob, "entropy": entropy + 0.0, "stats": stats,
                 "top_logprobs": torch.topk(logp, s["k"], dim=1).values}
     if s["op"] == "score_grad":
         p = logp.exp()
