@@ -81,6 +81,8 @@ extern "C" {
                                wants this report uses kda_verify_scan_var        */
 /* 0x8 is reserved (no call raises it: the sampled filter is exact for any
    number of ties) */
+#define KDA_ST_BADTOKEN 0x10 /* a token or teacher id of V or more (spec_logprobs,
+                               spec_distill*); it is passed over                */
 
 /* element types of raw rows and logits */
 #define KDA_F32 0
@@ -562,6 +564,106 @@ int spec_accept(const void *logits, int logit_dtype, int B, int T, int V, const 
 #define KDA_NOALLOC_SCRATCH_BYTES ((size_t)1 << 20)
 int spec_accept_noalloc(const void *logits, int logit_dtype, int B, int T, int V, const int *drafts,
                         int *j_out, int *bonus_out, int *keep_out, int *dev_status, cudaStream_t stream);
+
+/*
+ * Scores of tokens and distillation: what a verify round's logits are worth besides
+ * the accept.  The pages stop at j and the bonus token (glm_spec.rs, glm5_spec_round
+ * step 4) and load trained drafters; these entry points are this library's own, for
+ * callers that hand out log-probabilities with the tokens, and that keep a drafter
+ * close to its target by distilling from the target's rows.
+ *
+ * Rows are given as N rows of V logits, ld elements from one row's first logit to the
+ * next one's (ld >= V; [B][T][V] is N = B T, ld = V).  Logits and their gradients need
+ * only the alignment of their element; the 4-byte arrays are 4-byte aligned.
+ * temperature lies in KDA_TEMPERATURE_MIN..MAX.  With z = x / temperature:
+ *   m = max x,  s = ln sum exp((x - m) / temperature),  ln p = (x - m) / temperature - s,
+ *   H = -sum p ln p
+ * (sums and statistics in f32).  A row's stats are the pair (m, s), f32 [N][2]: kept apart
+ * they lose nothing where m is large (log sum exp z = m / temperature + s).  A logit of
+ * -inf is a masked token: p = 0.  A row without any other logit is empty: stats -inf,
+ * H = 0, every log-probability -inf, gradients 0.  A row holding a NaN or +inf has NaN
+ * for its stats and results, and KDA_ST_NAN is set.  Results do not depend on the order
+ * in which blocks run.
+ */
+#define KDA_TOPK_MAX 128
+#define KDA_TEMPERATURE_MIN 1e-4f
+#define KDA_TEMPERATURE_MAX 1e4f
+
+/*
+ * spec_logprobs -- log-probabilities of given tokens, entropy and top alternatives.
+ *   tokens int32 [N] (NULL when logprob is): logprob[n] = ln p_t.  A negative token
+ *     is none (padding), one of V or more sets KDA_ST_BADTOKEN; both give 0.
+ *   K in 0..KDA_TOPK_MAX alternatives a row: top_ids int32 [N][K] and top_logprobs f32
+ *     [N][K], the largest logits in falling order, the lowest id first among equal
+ *     ones; masked tokens are no alternatives, and what is left over has id -1 and
+ *     log-probability -inf (all of a row with a NaN: -1 and NaN).
+ *   logprob, entropy f32 [N] and stats f32 [N][2], each may be NULL.
+ */
+int spec_logprobs(const void *logits, int logit_dtype, int N, int V, long long ld, const int *tokens, int K,
+                  float temperature, float *logprob, float *entropy, float *stats, int *top_ids,
+                  float *top_logprobs, int *dev_status, cudaStream_t stream);
+
+/*
+ * spec_logprobs_backward -- the gradient of those log-probabilities and entropies:
+ *   dlogits_i = (1/temperature) [ g (1{i = t} - p_i) - h p_i (ln p_i + H) ],
+ *   g = grad_logprob[n] (NULL: 0; 0 for a row whose token is none), h = grad_entropy[n]
+ *   (NULL: 0), stats and entropy as spec_logprobs gave them (entropy may be NULL without
+ *   grad_entropy).  dlogits has the logits' type, ldg elements from row to row; it may be
+ *   the logits themselves (with ldg = ld), else the two must not overlap.  A row with
+ *   g = h = 0 gets zeros, whatever its logits.
+ */
+int spec_logprobs_backward(const void *logits, int logit_dtype, int N, int V, long long ld, const int *tokens,
+                           const float *stats, const float *entropy, const float *grad_logprob,
+                           const float *grad_entropy, float temperature, void *dlogits, long long ldg,
+                           cudaStream_t stream);
+
+/* what the teacher's values are */
+#define KDA_TEACHER_LOGITS 0   /* logits: q = softmax(value / temperature) over a row's entries */
+#define KDA_TEACHER_LOGPROBS 1 /* log-probabilities at this temperature: q = exp(value), which
+                                  need not sum to one over the entries                  */
+
+/* The teacher's K (1..KDA_TOPK_MAX) entries of every row, all device memory: ids int32
+ * [N][K] (negative: no entry; V or more: none, and KDA_ST_BADTOKEN), values [N][K]
+ * (value_dtype KDA_F32 or KDA_BF16; -inf gives q = 0), weight f32 [N] or NULL for 1.
+ * An id that a row lists twice counts with both entries. */
+typedef struct kda_teacher {
+    const int *ids;
+    const void *values;
+    const float *weight;
+    int value_dtype;
+    int kind; /* KDA_TEACHER_LOGITS or KDA_TEACHER_LOGPROBS */
+    int K;
+} kda_teacher;
+
+/*
+ * spec_distill -- loss f32 [N] of the student's rows against the teacher's entries:
+ *   loss = weight temperature^2 sum_k q_k (ln q_k - ln p_{id_k}),
+ *   and stats f32 [N][2] (may be NULL), which the backward call takes.  A row of weight 0
+ *   is not read: loss and stats 0.  A row without entries has loss 0.  An entry that the
+ *   student masks has loss +inf, and so has an empty row; a sum of finite terms that
+ *   rounds past the range of f32 is held at its end.
+ */
+int spec_distill(const void *logits, int logit_dtype, int N, int V, long long ld, const kda_teacher *teacher,
+                 float temperature, float *loss, float *stats, int *dev_status, cudaStream_t stream);
+
+/*
+ * spec_distill_backward -- dlogits_i = g weight temperature (Q p_i - sum_{id_k = i} q_k),
+ *   Q = sum_k q_k, g = grad_loss[n] (NULL: 1).  dlogits and ldg as for
+ *   spec_logprobs_backward.  A row of weight or g 0, one without entries and an empty row
+ *   get zeros.
+ */
+int spec_distill_backward(const void *logits, int logit_dtype, int N, int V, long long ld,
+                          const kda_teacher *teacher, float temperature, const float *stats, const float *grad_loss,
+                          void *dlogits, long long ldg, int *dev_status, cudaStream_t stream);
+
+/*
+ * spec_distill_step -- both in one launch that reads the logits once: loss, stats (may
+ *   be NULL) and dlogits for grad_loss known beforehand (NULL: 1; a mean over rows is
+ *   1/rows).
+ */
+int spec_distill_step(const void *logits, int logit_dtype, int N, int V, long long ld, const kda_teacher *teacher,
+                      float temperature, const float *grad_loss, float *loss, float *stats, void *dlogits,
+                      long long ldg, int *dev_status, cudaStream_t stream);
 
 /* Static description of a return code, and the calling thread's last error text. */
 const char *kda_error_string(int code);

@@ -9,6 +9,7 @@ Names follow the C ABI: ``kda_verify_scan``, ``kda_rollback``, ``spec_accept``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -21,7 +22,9 @@ D = 128
 TMAX = 15
 HOST_KEEP_MAX = 2048
 OK, EINVAL, ENAN, ECUDA, ETIMEOUT = 0, 1, 2, 3, 4
-ST_NAN, ST_BADKEEP, ST_TIMEOUT = 0x1, 0x2, 0x4
+ST_NAN, ST_BADKEEP, ST_TIMEOUT, ST_BADTOKEN = 0x1, 0x2, 0x4, 0x10
+TOPK_MAX = 128
+TEACHER_LOGITS, TEACHER_LOGPROBS = 0, 1
 TAG_ACCEPT, TAG_DRAW = 0xFFFFFFFE, 0xFFFFFFFF  # counter word 3 of a session's accept tests / draws
 F32, BF16 = 0, 1
 MEM_HOST, MEM_DEVICE = 0, 1
@@ -33,9 +36,10 @@ EXPORTS = ("kda_verify_scan", "kda_rollback", "kda_verify_scan_var", "kda_rollba
            "kda_verify_scan_cols",
            "kda_rollback_cols", "spec_accept_var",
            "spec_window", "spec_accept_sampled", "spec_accept_sampled_session", "kda_philox4x32_10",
-           "spec_accept_sampled_scratch_bytes", "spec_accept_scratch_bytes", "spec_accept", "spec_accept_noalloc", "kda_error_string",
-           "kda_last_error", "kda_abi_version")
-ABI_VERSION = 9
+           "spec_accept_sampled_scratch_bytes", "spec_accept_scratch_bytes", "spec_accept", "spec_accept_noalloc",
+           "spec_logprobs", "spec_logprobs_backward", "spec_distill", "spec_distill_backward", "spec_distill_step",
+           "kda_error_string", "kda_last_error", "kda_abi_version")
+ABI_VERSION = 10
 WIN_CONF_KEEP, WIN_CONFIDENCE, WIN_SLOT_CONFIDENCE = 0, 1, 2
 
 
@@ -61,6 +65,11 @@ class KdaStashC(ctypes.Structure):
 class KdaSampling(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int), ("top_p", ctypes.c_float),
                 ("min_p", ctypes.c_float)]
+
+
+class KdaTeacher(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("values", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("value_dtype", ctypes.c_int), ("kind", ctypes.c_int), ("K", ctypes.c_int)]
 
 
 class KdaError(RuntimeError):
@@ -143,6 +152,15 @@ def lib(path: str | None = None):
     L.spec_accept_scratch_bytes.restype = sz
     L.spec_accept.argtypes = [vp, ci, ci, ci, ci, vp, vp, vp, vp, vp, vp, sz, vp]
     L.spec_accept.restype = ci
+    cf, ll, teacher = ctypes.c_float, ctypes.c_longlong, ctypes.POINTER(KdaTeacher)
+    L.spec_logprobs.argtypes = [vp, ci, ci, ci, ll, vp, ci, cf, vp, vp, vp, vp, vp, vp, vp]
+    L.spec_logprobs_backward.argtypes = [vp, ci, ci, ci, ll, vp, vp, vp, vp, vp, cf, vp, ll, vp]
+    L.spec_distill.argtypes = [vp, ci, ci, ci, ll, teacher, cf, vp, vp, vp, vp]
+    L.spec_distill_backward.argtypes = [vp, ci, ci, ci, ll, teacher, cf, vp, vp, vp, ll, vp, vp]
+    L.spec_distill_step.argtypes = [vp, ci, ci, ci, ll, teacher, cf, vp, vp, vp, vp, ll, vp, vp]
+    for fn in (L.spec_logprobs, L.spec_logprobs_backward, L.spec_distill, L.spec_distill_backward,
+               L.spec_distill_step):
+        fn.restype = ci
     L.kda_error_string.argtypes = [ci]
     L.kda_error_string.restype = ctypes.c_char_p
     L.kda_last_error.argtypes = []
@@ -749,6 +767,236 @@ def spec_accept(logits: torch.Tensor, drafts: torch.Tensor, j_out=None, bonus_ou
                            ctypes.c_void_p(_stream(stream)))
     _check("spec_accept", rc)
     return j_out, bonus_out, keep_out
+
+
+def _logit_rows(t: torch.Tensor, name: str):
+    """A logits tensor [..., V] as rows: (leading shape, N, V, ld).  The last dimension is
+    dense and the leading ones step evenly from row to row."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    _row_dtype(t)
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have the shape [..., V]")
+    lead, V = tuple(t.shape[:-1]), int(t.shape[-1])
+    if V < 1:
+        raise ValueError(f"{name} must have at least one logit a row")
+    N = 1
+    for s in lead:
+        N *= int(s)
+    if V > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be dense along its last dimension")
+    ld, step = V, None
+    if N > 0:
+        for size, stride in zip(reversed(lead), reversed(t.stride()[:-1])):
+            if size == 1:
+                continue
+            if step is None:
+                ld = stride
+            elif stride != step:
+                raise ValueError(f"{name} must step evenly from row to row")
+            step = stride * size
+    if ld < V:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return lead, N, V, int(ld)
+
+
+def _stream_pool(stream):
+    """The context whose allocations belong to ``stream``: a call's own outputs live in the
+    memory pool of the stream that writes them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+class _LogitPlan:
+    """Arguments of one call over logits, checked and marshalled once; a call of the plan is
+    one foreign call.  The tensors are referenced, and the outputs are the same tensors at
+    every call.  The stream is the one given (or current) when the plan is made."""
+
+    def __init__(self, name: str, logits: torch.Tensor, temperature: float, stream):
+        self.name, self.logits = name, logits
+        self.lead, self.N, self.V, self.ld = _logit_rows(logits, "logits")
+        self.temperature, self.stream = float(temperature), stream
+        self._fn = getattr(lib(), name)
+        self._keep = [logits]
+        self._head = [_ptr(logits), _row_dtype(logits), self.N, self.V, self.ld]
+
+    def _in(self, t, name, dtype, shape=None):
+        """Pointer of an input (or None)."""
+        if t is None:
+            return None
+        _dev(t, name, dtype, self.lead if shape is None else shape)
+        if t.device != self.logits.device:
+            raise ValueError(f"{name} must be on {self.logits.device}")
+        self._keep.append(t)
+        return _ptr(t)
+
+    def _out(self, t, name, dtype=torch.float32, shape=None):
+        """An output: the caller's tensor, checked, or a new one."""
+        shape = self.lead if shape is None else shape
+        if t is None:
+            with _stream_pool(self.stream):
+                t = torch.empty(shape, dtype=dtype, device=self.logits.device)
+        self._in(t, name, dtype, shape)
+        return t
+
+    def _stats_in(self, t):
+        return self._in(t, "stats", torch.float32, (*self.lead, 2))
+
+    def _stats_out(self, t):
+        return self._out(t, "stats_out", torch.float32, (*self.lead, 2))
+
+    def _grad(self, t):
+        """The gradient of the logits: the caller's tensor (rows as the logits', or the logits
+        themselves) or a new dense one."""
+        if t is None:
+            with _stream_pool(self.stream):
+                t = torch.empty(tuple(self.logits.shape), dtype=self.logits.dtype, device=self.logits.device)
+        lead, _, V, ldg = _logit_rows(t, "dlogits")
+        if lead != self.lead or V != self.V or t.dtype != self.logits.dtype or t.device != self.logits.device:
+            raise ValueError("dlogits must have the shape, type and device of the logits")
+        self._keep.append(t)
+        return t, ldg
+
+    def _status(self, t):
+        return None if t is None else self._in(t, "dev_status", torch.int32, tuple(t.shape))
+
+    def _bind(self, *rest):
+        self._args = (*self._head, *rest, ctypes.c_void_p(_stream(self.stream)))
+
+    def __call__(self):
+        rc = self._fn(*self._args)
+        if rc:
+            _check(self.name, rc)
+        return self.out
+
+
+class LogprobsPlan(_LogitPlan):
+    """spec_logprobs for fixed tensors: logits [..., V] (float32 or bfloat16), tokens int32
+    [...] or None, top_k alternatives in 0..128.  A call returns (logprob, entropy, stats,
+    top_ids, top_logprobs): logprob is None without tokens, stats [..., 2] holds the row's
+    maximum m and s = ln sum exp((x - m) / temperature), the last two have shape
+    [..., top_k]."""
+
+    def __init__(self, logits, tokens=None, top_k: int = 0, temperature: float = 1.0, logprob_out=None,
+                 entropy_out=None, stats_out=None, top_ids_out=None, top_logprobs_out=None, dev_status=None,
+                 stream=None):
+        super().__init__("spec_logprobs", logits, temperature, stream)
+        tok = self._in(tokens, "tokens", torch.int32)
+        k = int(top_k)
+        if not 0 <= k <= TOPK_MAX:
+            raise ValueError(f"top_k must lie in 0..{TOPK_MAX}")
+        if tokens is None and logprob_out is not None:
+            raise ValueError("logprob_out needs tokens")
+        logprob = None if tokens is None else self._out(logprob_out, "logprob_out")
+        entropy, stats = self._out(entropy_out, "entropy_out"), self._stats_out(stats_out)
+        top_ids = self._out(top_ids_out, "top_ids_out", torch.int32, (*self.lead, k))
+        top = self._out(top_logprobs_out, "top_logprobs_out", torch.float32, (*self.lead, k))
+        self.out = (logprob, entropy, stats, top_ids, top)
+        self._bind(tok, k, self.temperature, _ptr(logprob), _ptr(entropy), _ptr(stats), _ptr(top_ids), _ptr(top),
+                   self._status(dev_status))
+
+
+class LogprobsBackwardPlan(_LogitPlan):
+    """spec_logprobs_backward for fixed tensors: stats and entropy as spec_logprobs gave them,
+    grad_logprob and grad_entropy f32 [...] (either may be None).  dlogits: None for a new
+    tensor, or one to write, which may be the logits.  A call returns dlogits."""
+
+    def __init__(self, logits, tokens, stats, entropy=None, grad_logprob=None, grad_entropy=None,
+                 temperature: float = 1.0, dlogits=None, stream=None):
+        super().__init__("spec_logprobs_backward", logits, temperature, stream)
+        f = torch.float32
+        args = (self._in(tokens, "tokens", torch.int32), self._stats_in(stats), self._in(entropy, "entropy", f),
+                self._in(grad_logprob, "grad_logprob", f), self._in(grad_entropy, "grad_entropy", f))
+        self.out, ldg = self._grad(dlogits)
+        self._bind(*args, self.temperature, _ptr(self.out), ldg)
+
+
+class _DistillPlan(_LogitPlan):
+    def _teacher(self, ids, values, weight, kind):
+        if not isinstance(ids, torch.Tensor) or ids.dim() != len(self.lead) + 1:
+            raise ValueError("ids must have the shape [..., K]")
+        K = int(ids.shape[-1])
+        shape = (*self.lead, K)
+        if not isinstance(values, torch.Tensor):
+            raise TypeError("values must be a CUDA tensor")
+        t = KdaTeacher(self._in(ids, "ids", torch.int32, shape), self._in(values, "values", values.dtype, shape),
+                       self._in(weight, "weight", torch.float32), _row_dtype(values), int(kind), K)
+        self._keep.append(t)
+        return ctypes.byref(t)
+
+
+class DistillPlan(_DistillPlan):
+    """spec_distill for fixed tensors: student logits [..., V], the teacher's ids int32 and
+    values (float32 or bfloat16) [..., K], weight f32 [...] or None, kind TEACHER_LOGITS or
+    TEACHER_LOGPROBS.  A call returns loss [...] and stats [..., 2]
+    (as LogprobsPlan), f32."""
+
+    def __init__(self, logits, ids, values, weight=None, kind: int = TEACHER_LOGITS, temperature: float = 1.0,
+                 loss_out=None, stats_out=None, dev_status=None, stream=None):
+        super().__init__("spec_distill", logits, temperature, stream)
+        teacher = self._teacher(ids, values, weight, kind)
+        self.out = (self._out(loss_out, "loss_out"), self._stats_out(stats_out))
+        self._bind(teacher, self.temperature, _ptr(self.out[0]), _ptr(self.out[1]), self._status(dev_status))
+
+
+class DistillBackwardPlan(_DistillPlan):
+    """spec_distill_backward for fixed tensors: stats as spec_distill gave them, grad_loss f32
+    [...] or None for 1, dlogits as LogprobsBackwardPlan.  A call returns dlogits."""
+
+    def __init__(self, logits, ids, values, stats, grad_loss=None, weight=None, kind: int = TEACHER_LOGITS,
+                 temperature: float = 1.0, dlogits=None, dev_status=None, stream=None):
+        super().__init__("spec_distill_backward", logits, temperature, stream)
+        teacher = self._teacher(ids, values, weight, kind)
+        args = (self._stats_in(stats), self._in(grad_loss, "grad_loss", torch.float32))
+        self.out, ldg = self._grad(dlogits)
+        self._bind(teacher, self.temperature, *args, _ptr(self.out), ldg, self._status(dev_status))
+
+
+class DistillStepPlan(_DistillPlan):
+    """spec_distill_step for fixed tensors: DistillPlan and DistillBackwardPlan in one
+    launch, for a grad_loss known beforehand.  A call returns (loss, stats, dlogits)."""
+
+    def __init__(self, logits, ids, values, grad_loss=None, weight=None, kind: int = TEACHER_LOGITS,
+                 temperature: float = 1.0, loss_out=None, stats_out=None, dlogits=None, dev_status=None, stream=None):
+        super().__init__("spec_distill_step", logits, temperature, stream)
+        teacher = self._teacher(ids, values, weight, kind)
+        g = self._in(grad_loss, "grad_loss", torch.float32)
+        loss, stats = self._out(loss_out, "loss_out"), self._stats_out(stats_out)
+        grad, ldg = self._grad(dlogits)
+        self.out = (loss, stats, grad)
+        self._bind(teacher, self.temperature, g, _ptr(loss), _ptr(stats), _ptr(grad), ldg, self._status(dev_status))
+
+
+def spec_logprobs(logits, tokens=None, top_k: int = 0, temperature: float = 1.0, **kw):
+    """Log-probabilities of given tokens, entropy, stats and top alternatives: one call of a
+    LogprobsPlan, which describes the arguments and results."""
+    return LogprobsPlan(logits, tokens, top_k, temperature, **kw)()
+
+
+def spec_logprobs_backward(logits, tokens, stats, entropy=None, grad_logprob=None, grad_entropy=None,
+                           temperature: float = 1.0, **kw):
+    """d logits of log-probabilities and entropies: one call of a LogprobsBackwardPlan."""
+    return LogprobsBackwardPlan(logits, tokens, stats, entropy, grad_logprob, grad_entropy, temperature, **kw)()
+
+
+def spec_distill(logits, ids, values, weight=None, kind: int = TEACHER_LOGITS, temperature: float = 1.0, **kw):
+    """Distillation loss and stats of every row: one call of a DistillPlan."""
+    return DistillPlan(logits, ids, values, weight, kind, temperature, **kw)()
+
+
+def spec_distill_backward(logits, ids, values, stats, grad_loss=None, weight=None, kind: int = TEACHER_LOGITS,
+                          temperature: float = 1.0, **kw):
+    """d logits of the distillation loss: one call of a DistillBackwardPlan."""
+    return DistillBackwardPlan(logits, ids, values, stats, grad_loss, weight, kind, temperature, **kw)()
+
+
+def spec_distill_step(logits, ids, values, grad_loss=None, weight=None, kind: int = TEACHER_LOGITS,
+                      temperature: float = 1.0, **kw):
+    """Distillation loss, stats and d logits in one launch: one call of a DistillStepPlan."""
+    return DistillStepPlan(logits, ids, values, grad_loss, weight, kind, temperature, **kw)()
 
 
 class RoundPlan:
