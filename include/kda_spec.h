@@ -586,6 +586,7 @@ int spec_accept_noalloc(const void *logits, int logit_dtype, int B, int T, int V
  * in which blocks run.
  */
 #define KDA_TOPK_MAX 128
+#define KDA_ROW_MAX (1 << 30) /* logits of a row */
 #define KDA_TEMPERATURE_MIN 1e-4f
 #define KDA_TEMPERATURE_MAX 1e4f
 

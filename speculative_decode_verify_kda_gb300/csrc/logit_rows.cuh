@@ -1,19 +1,37 @@
 // logit_rows.cuh -- what the row reductions over logits share (spec_logprobs.cu,
-// spec_distill.cu): element access, the order of (value, id) and sums over a CTA.
+// spec_distill.cu).
+//
+// A row is read in 16-byte vectors and belongs to one CTA or to a cluster of CTAs, each
+// of which takes a run of the row's vectors.  A thread holds VPT vectors in registers (a
+// tile); up to 1024 threads x 8 vectors x 8 CTAs hold a row of 524288 bf16 or 262144 f32
+// logits, so the row is read from memory once and what comes after its sum (the gradient,
+// the alternatives) works on the registers.  Longer rows take more rounds of tiles and are
+// read again for the second part.
+//
+// The sums are taken relative to the warp's own maximum, and a warp's triple (maximum, sum
+// of weights, weighted sum of exponents) joins the others' once, through the shared memory
+// of the CTA or of every CTA of the cluster: one barrier between reading a row and knowing
+// its statistics.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "kda_internal.h"
 
 namespace kda {
 namespace rows {
 
-constexpr int THREADS = 256;
+namespace cg = cooperative_groups;
+
+constexpr int MAX_CL = 8;          // CTAs of a cluster (the portable size)
+constexpr int MAX_THREADS = 1024;
+constexpr int MAX_VPT = 8;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 template <bool BF16>
@@ -34,6 +52,55 @@ __device__ __forceinline__ void put(void *p, long long i, float x)
     } else {
         static_cast<float *>(p)[i] = x;
     }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));  // at most 2 ulp off; -inf gives 0
+    return r;
+}
+
+// Two f32 operations in one instruction.
+struct F2 {
+    unsigned long long b;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split(F2 a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.b));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+    return r;
 }
 
 // max that keeps a NaN
@@ -68,23 +135,451 @@ __device__ __forceinline__ int key_id(unsigned long long key)
     return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
 }
 
-// Reductions over the CTA's THREADS threads; `buf` holds one value a warp and may be
-// used again after the call.
-template <class T, class Op>
-__device__ __forceinline__ T block_reduce(T v, Op op, T *buf)
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ float warp_max_nan(float x)
+{
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float warp_sum(float x)
 {
 #pragma unroll
     for (int o = 16; o; o >>= 1)
-        v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = buf[0];
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The value of rank r (0 the largest) among the warp's 32.
+template <class T>
+__device__ __forceinline__ T warp_rank(T x, int r)
+{
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int w = 1; w < THREADS / 32; ++w)
-        v = op(v, buf[w]);
-    return v;
+    for (int k = 2; k <= 32; k <<= 1) {
+#pragma unroll
+        for (int j = k >> 1; j; j >>= 1) {  // a bitonic network, descending over the lanes
+            const T y = __shfl_xor_sync(0xffffffffu, x, j);
+            const bool up = ((lane & k) == 0) == ((lane & j) == 0);
+            x = up == (x > y) ? x : y;
+        }
+    }
+    return __shfl_sync(0xffffffffu, x, r);
+}
+
+// ---------------------------------------------------------------------------
+// A row in 16-byte vectors
+// ---------------------------------------------------------------------------
+// The vector at p whose first element has the place `first` in a row of V: the elements
+// outside of the row are -inf and not read.
+template <bool BF16>
+__device__ __noinline__ uint4 edge_vector(const char *p, int first, int V)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (BF16) {
+            const volatile uint16_t *x = reinterpret_cast<const volatile uint16_t *>(p) + 2 * k;
+            const int e = first + 2 * k;
+            const uint32_t lo = e >= 0 && e < V ? x[0] : 0xff80u, hi = e + 1 >= 0 && e + 1 < V ? x[1] : 0xff80u;
+            w[k] = lo | (hi << 16);
+        } else {
+            const int e = first + k;
+            w[k] = e >= 0 && e < V ? reinterpret_cast<const volatile uint32_t *>(p)[k] : 0xff800000u;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The vector's elements, the first of which has the place `first` in a row of V, one by one to
+// p; those outside of the row are left out.
+template <bool BF16>
+__device__ __noinline__ void store_elements(char *p, int first, int V, uint4 v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 8 : 4); ++k) {
+        if (first + k < 0 || first + k >= V)
+            continue;
+        if (BF16)
+            reinterpret_cast<uint16_t *>(p)[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
+        else
+            reinterpret_cast<uint32_t *>(p)[k] = w[k];
+    }
+}
+
+template <bool BF16>
+struct RowPtr {
+    static constexpr int PER = BF16 ? 8 : 4;  // elements of a vector
+    static constexpr int ES = BF16 ? 2 : 4;
+    static constexpr uint32_t MASKED = BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
+
+    char *base;   // the row's address rounded down to a vector
+    int skip;     // elements of the first vector that precede the row
+    int V, nvec;  // elements and vectors of the row
+    int full0, full1;  // the vectors [full0, full1) lie wholly inside the row
+
+    __device__ __forceinline__ RowPtr(const void *p, long long first, int V_) : V(V_)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(first) * ES;
+        skip = static_cast<int>(at & 15u) / ES;
+        base = reinterpret_cast<char *>(at & ~static_cast<uintptr_t>(15));
+        nvec = (skip + V + PER - 1) / PER;
+        full0 = skip > 0;
+        full1 = (skip + V) / PER;
+    }
+    __device__ __forceinline__ bool full(int i) const { return i >= full0 && i < full1; }
+    __device__ __forceinline__ int first_id(int i) const { return i * PER - skip; }
+
+    // A vector that lies wholly inside the row.  No ordinary load may take this one's place:
+    // the logits may be overwritten later in the same kernel.
+    __device__ __forceinline__ uint4 load(int i) const
+    {
+        uint4 v;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(base + 16ll * i));
+        return v;
+    }
+    __device__ __forceinline__ uint4 load_edge(int i) const { return edge_vector<BF16>(base + 16ll * i, first_id(i), V); }
+    __device__ __forceinline__ float at(int id) const
+    {
+        const char *p = base + (static_cast<long long>(skip) + id) * ES;
+        if (BF16)
+            return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const volatile uint16_t *>(p)) << 16);
+        return *reinterpret_cast<const volatile float *>(p);
+    }
+    __device__ __forceinline__ void set(int id, float x) const
+    {
+        put<BF16>(base, static_cast<long long>(skip) + id, x);
+    }
+    __device__ __forceinline__ void store(int i, uint4 v) const
+    {
+        *reinterpret_cast<uint4 *>(base + 16ll * i) = v;
+    }
+    // Vector i of `src` (which starts at another place in its vector, or crosses an end of the
+    // row) into this row.
+    __device__ __forceinline__ void store_edge(const RowPtr &src, int i, uint4 v) const
+    {
+        const int e = src.first_id(i);
+        store_elements<BF16>(base + (static_cast<long long>(skip) + e) * ES, e, V, v);
+    }
+};
+
+// The vectors first, first + step, ... below `end` of a row in registers, masked past the end.
+template <bool BF16, int VPT>
+struct Tile {
+    uint4 v[VPT];
+
+    __device__ __forceinline__ void load(const RowPtr<BF16> &row, int first, int step, int end)
+    {
+        constexpr uint32_t M = RowPtr<BF16>::MASKED;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * step;
+            v[j] = make_uint4(M, M, M, M);
+            if (i < end && row.full(i))
+                v[j] = row.load(i);
+        }
+        if (row.full0 > 0)
+            load_edge(row, 0, first, step, end);
+        if (row.full1 < row.nvec && (row.full0 == 0 || row.nvec > 1))
+            load_edge(row, row.nvec - 1, first, step, end);
+    }
+    // Vector i, which crosses an end of the row, if it is one of the thread's.
+    __device__ __forceinline__ void load_edge(const RowPtr<BF16> &row, int i, int first, int step, int end)
+    {
+        const int j0 = (i - first) / step;
+        if (i < first || i >= end || j0 >= VPT || first + j0 * step != i)
+            return;
+        const uint4 u = row.load_edge(i);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (j == j0)
+                v[j] = u;
+    }
+
+    // f(pair of neighbouring elements) for every pair.
+    template <class F>
+    __device__ __forceinline__ void each(F f) const
+    {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            each_of(v[j], f);
+    }
+    template <class F>
+    static __device__ __forceinline__ void each_of(const uint4 &u, F f)
+    {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        if (BF16) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                f(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+        } else {
+            f(__uint_as_float(w[0]), __uint_as_float(w[1]));
+            f(__uint_as_float(w[2]), __uint_as_float(w[3]));
+        }
+    }
+
+    __device__ __forceinline__ float max_of() const
+    {
+        if (BF16) {
+            uint32_t m = max_nan_bf16x2(max_nan_bf16x2(v[0].x, v[0].y), max_nan_bf16x2(v[0].z, v[0].w));
+#pragma unroll
+            for (int j = 1; j < VPT; ++j)
+                m = max_nan_bf16x2(m, max_nan_bf16x2(max_nan_bf16x2(v[j].x, v[j].y), max_nan_bf16x2(v[j].z, v[j].w)));
+            return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+        }
+        float m = -INFINITY;
+        each([&](float p, float q) { m = max_nan(m, max_nan(p, q)); });
+        return m;
+    }
+};
+
+// f(pair) of every pair of a tile of `src` into the same elements of `out`, or zeros.
+template <bool BF16, int VPT, class F>
+__device__ __forceinline__ void store_tile(const Tile<BF16, VPT> &t, const RowPtr<BF16> &src,
+                                           const RowPtr<BF16> &out, int first, int step, int end, bool zero, F f)
+{
+    const bool even = src.skip == out.skip;  // vector for vector
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = first + j * step;
+        if (i >= end)
+            break;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (!zero) {
+            int k = 0;
+            t.each_of(t.v[j], [&](float p, float q) {
+                const float2 d = split(f(p, q));
+                if (BF16) {
+                    w[k++] = pack_bf16(d.x, d.y);
+                } else {
+                    w[k++] = __float_as_uint(d.x);
+                    w[k++] = __float_as_uint(d.y);
+                }
+            });
+        }
+        const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+        if (even && src.full(i))
+            out.store(i, v);
+        else
+            out.store_edge(src, i, v);
+    }
+}
+
+// Running maximum and sums of a warp's share of a row, in units of exp2: c = log2(e) / tau,
+// d = (x - m) c, S = sum 2^d, E = sum d 2^d.  m is the warp's, S and E are the lane's.
+template <bool ENTROPY>
+struct Running {
+    float m = -INFINITY, S = 0.0f, E = 0.0f;
+
+    template <bool BF16, int VPT>
+    __device__ __forceinline__ void add(const Tile<BF16, VPT> &t, float tile_max, float c)
+    {
+        const float top = max_nan(m, warp_max_nan(tile_max));
+        if (top == -INFINITY)  // nothing but masked tokens so far
+            return;
+        if (S != 0.0f || E != 0.0f) {  // an earlier round's sums move to the new maximum
+            const float d = fmaxf((m - top) * c, -1e4f), w = ex2(d);
+            E = (E + S * d) * w;
+            S *= w;
+        }
+        m = top;
+        const F2 neg = f2(-top, -top), cc = f2(c, c);
+        F2 s = f2(0.0f, 0.0f), e = s;
+        t.each([&](float p, float q) {
+            float2 d = split((f2(p, q) + neg) * cc);
+            if (ENTROPY) {  // a masked token's term is 0, not 0 times -inf
+                d.x = fmaxf(d.x, -1e4f);
+                d.y = fmaxf(d.y, -1e4f);
+            }
+            const F2 w = f2(ex2(d.x), ex2(d.y));
+            s = s + w;
+            if (ENTROPY)
+                e = fma2(w, f2(d.x, d.y), e);
+        });
+        const float2 s2 = split(s), e2 = split(e);
+        S += s2.x + s2.y;
+        E += e2.x + e2.y;
+    }
+};
+
+// What a warp hands to the others: its maximum and sums, and a value of its largest ones.
+struct __align__(16) Part {
+    float m, S, E;
+    uint32_t key;
+};
+constexpr int MAX_PARTS = MAX_CL * (MAX_THREADS / 32);
+
+struct Stats {
+    float m, lnS, entropy;  // NaN for a row with a NaN or +inf, (-inf, -inf, 0) for an empty one
+    __device__ __forceinline__ bool bad() const { return m != m; }
+    __device__ __forceinline__ bool empty() const { return m == -INFINITY; }
+};
+
+// The row's statistics from its parts (every lane of the calling warp gets them).  The order
+// of the sums is fixed by the parts' places.
+__device__ __forceinline__ Stats join(const Part *parts, int n, float c)
+{
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY;
+    for (int p = lane; p < n; p += 32)
+        m = max_nan(m, parts[p].m);
+    m = warp_max_nan(m);
+    if (m == -INFINITY)
+        return Stats{m, m, 0.0f};
+    if (!(m < INFINITY))
+        return Stats{NAN, NAN, NAN};
+    float S = 0.0f, E = 0.0f;
+    for (int p = lane; p < n; p += 32) {
+        const Part q = parts[p];
+        const float d = fmaxf((q.m - m) * c, -1e4f), w = ex2(d);
+        S += q.S * w;
+        E += (q.E + q.S * d) * w;
+    }
+    S = warp_sum(S);
+    E = warp_sum(E);
+    const float lnS = logf(S);
+    return Stats{m, lnS, fmaxf(lnS - LN2 * E / S, 0.0f)};
+}
+
+// The CTA's place: its row, its run of the row's vectors, and its cluster.
+struct Place {
+    long long row;
+    int rank, cl, warps;
+    __device__ __forceinline__ Place(int cl_)
+        : row(blockIdx.x / cl_), rank(blockIdx.x % cl_), cl(cl_), warps(blockDim.x >> 5)
+    {
+    }
+    __device__ __forceinline__ int begin(int nvec) const { return rank * per(nvec); }
+    __device__ __forceinline__ int end(int nvec) const { return min(nvec, (rank + 1) * per(nvec)); }
+    __device__ __forceinline__ int per(int nvec) const { return (nvec + cl - 1) / cl; }
+    // Every CTA of the cluster runs from here on.  Between the two calls: anything that stays
+    // inside the CTA.
+    __device__ __forceinline__ void arrive() const
+    {
+        if (cl > 1)
+            asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    }
+    __device__ __forceinline__ void wait() const
+    {
+        if (cl > 1)
+            asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    }
+    // Barrier over the CTAs that share the row.
+    __device__ __forceinline__ void sync() const
+    {
+        if (cl > 1) {
+            arrive();
+            wait();
+        } else {
+            __syncthreads();
+        }
+    }
+    template <class T>
+    __device__ __forceinline__ T *in_cta(T *shared, int r) const
+    {
+        return cl > 1 ? cg::this_cluster().map_shared_rank(shared, r) : shared;
+    }
+    // The warp's part into every CTA of the row (call by all lanes with the same part).
+    __device__ __forceinline__ void hand_out(Part *parts, const Part &p) const
+    {
+        const int lane = threadIdx.x & 31;
+        if (lane < cl)
+            in_cta(parts, lane)[rank * warps + (threadIdx.x >> 5)] = p;
+    }
+    __device__ __forceinline__ int parts() const { return cl * warps; }
+};
+
+// Threads of a CTA, vectors of a thread and CTAs of a row for N rows of nvec vectors.
+struct Shape {
+    int threads, vpt, cl;
+};
+
+// Vectors that the longest of N rows may touch.
+inline long long vectors_of(const void *p, int V, long long ld, int bf16)
+{
+    const long long per = bf16 ? 8 : 4;
+    const bool even = (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per == 0;
+    return (V + per - 1) / per + (even ? 0 : 1);
+}
+
+inline Shape shape_of(long long N, long long nvec)
+{
+    constexpr int SMS = 152;
+    // one CTA a row; more while the GPU has SMs to spare and a CTA still has 256 vectors
+    int cl = 1;
+    while (cl < MAX_CL && N * cl * 2 <= SMS && nvec >= 256ll * 2 * cl)
+        cl *= 2;
+    const long long per = (nvec + cl - 1) / cl;
+    int threads = 32;
+    while (threads < 256 && per > threads * 2ll)
+        threads *= 2;
+    int vpt = 1;
+    while (vpt < MAX_VPT && per > static_cast<long long>(threads) * vpt)
+        vpt *= 2;
+    return Shape{threads, vpt, cl};
+}
+
+// The same for a pass that needs nothing of the rest of the row: CTAs of a row.
+struct Chunks {
+    int threads, vpt, chunks;
+};
+
+inline Chunks chunks_of(long long nvec)
+{
+    int threads = 32, vpt = 1;
+    while (threads < 256 && nvec > threads)
+        threads *= 2;
+    while (vpt < 4 && nvec > static_cast<long long>(threads) * vpt)
+        vpt *= 2;
+    return Chunks{threads, vpt, static_cast<int>((nvec + threads * vpt - 1) / (threads * vpt))};
+}
+
+// f with the vectors of a thread as a constant.
+template <class F>
+inline int with_vpt(int vpt, F f)
+{
+    switch (vpt) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    default: return f(std::integral_constant<int, 8>());
+    }
+}
+
+// Launches kernel(args) with `cl` CTAs a cluster, as a programmatic dependent of the launch
+// before it.
+template <class A>
+inline int launch_rows(void (*kernel)(A), const A &args, long long blocks, int threads, int cl, cudaStream_t stream,
+                       const char *what)
+{
+    if (blocks > 0x7fffffffll)
+        return fail(KDA_EINVAL, "too many rows for one launch");
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cl);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cl > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+    if (e != cudaSuccess)
+        return fail(KDA_ECUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+    return check_launch(what);
 }
 
 // Argument checks that every entry point over logits makes (KDA_OK or KDA_EINVAL).
@@ -92,8 +587,8 @@ inline int check_logits(const void *logits, int dtype, int N, int V, long long l
 {
     if (N < 0)
         return fail(KDA_EINVAL, "N must be >= 0");
-    if (V < 1)
-        return fail(KDA_EINVAL, "V must be >= 1");
+    if (V < 1 || V > KDA_ROW_MAX)
+        return fail(KDA_EINVAL, "V must lie in 1..2^30");
     if (dtype != KDA_F32 && dtype != KDA_BF16)
         return fail(KDA_EINVAL, "logit_dtype must be KDA_F32 or KDA_BF16");
     if (ld < V)

@@ -9,8 +9,12 @@
 //   d x_i = g w tau (Q p_i - sum_{k: id_k = i} q_k),  Q = sum_k q_k.
 // tau^2 keeps the gradient's size when tau changes (d ln p / d x has a factor 1 / tau).
 //
-// One CTA a row; the row is read once for the maximum, once for the sum and once for
-// the gradient.
+// distill_kernel: a row stays in the registers of its CTA or cluster (logit_rows.cuh)
+// between the sum and the gradient, so loss and gradient together read the logits once.
+// The gradient is written as g w tau Q p for every element; after that, the CTA that
+// holds a teacher's entry writes that element again with its q taken off.
+// distill_backward_kernel: the gradient alone, from the saved statistics, in one pass
+// without any exchange.
 #include <cfloat>
 
 #include "logit_rows.cuh"
@@ -25,147 +29,226 @@ struct Distill {
     void *dx;
     long long ld, ldg;
     int V, K;
+    int cl;  // CTAs of a row (the backward pass alone: runs of a row)
     const int *ids;
     const void *values;
     int value_bf16, value_logprobs;
     const float *weight, *g, *stats_in;
-    float tau, c;
+    float tau, c;  // c = log2(e) / tau
     float *loss, *stats_out;
     int *status;
 };
 
+constexpr int EACH = KDA_TOPK_MAX / 32;  // entries of a lane
+
 // The teacher's entries of the CTA's row.
 struct Entries {
-    int id[KDA_TOPK_MAX];     // -1: no entry
-    float q[KDA_TOPK_MAX];    // probability
+    int id[KDA_TOPK_MAX];   // -1: no entry
+    float q[KDA_TOPK_MAX];  // probability
     float lnq[KDA_TOPK_MAX];
+    float x[KDA_TOPK_MAX];  // the student's logit, where id lies in the CTA's run or all are wanted
+    float Q;                // sum of q: 1 for renormalised entries, 0 without any, NaN for a NaN
 };
 
-// Fills `t` and returns Q (1 for renormalised entries, 0 when there is none, NaN for a NaN
-// among the values).  All threads call it; it ends with a barrier.
-__device__ __forceinline__ float read_entries(const Distill &a, long long n, Entries &t, float *fbuf)
+// Fills `t`; called by one warp.  x is read for ids in [lo, hi).
+template <bool BF16>
+__device__ __forceinline__ void read_entries(const Distill &a, long long n, const RowPtr<BF16> &row, int lo, int hi,
+                                             Entries &t)
 {
-    const int k = threadIdx.x;
-    int id = -1;
-    float v = -INFINITY;
-    if (k < a.K) {
-        id = a.ids[n * a.K + k];
-        if (id >= a.V) {
-            if (a.status)
+    const int lane = threadIdx.x & 31;
+    int id[EACH];
+    float v[EACH], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int k = lane + 32 * i;
+        id[i] = -1;
+        v[i] = -INFINITY;
+        if (k < a.K) {
+            const long long o = n * a.K + k;
+            id[i] = a.ids[o];
+            v[i] = a.value_bf16 ? element<true>(a.values, o) : element<false>(a.values, o);
+            if (id[i] >= a.V && a.status)
                 atomicOr(a.status, KDA_ST_BADTOKEN);
-            id = -1;
-        }
-        if (id >= 0) {
-            v = a.value_bf16 ? element<true>(a.values, n * a.K + k) : element<false>(a.values, n * a.K + k);
-            if (!a.value_logprobs)
-                v /= a.tau;
         }
     }
-    const float top = block_reduce(v, [](float p, float q) { return max_nan(p, q); }, fbuf);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        if (id[i] < 0 || id[i] >= a.V) {
+            id[i] = -1;
+            v[i] = -INFINITY;
+        }
+        t.id[lane + 32 * i] = id[i];
+        t.x[lane + 32 * i] = id[i] >= lo && id[i] < hi ? row.at(id[i]) : 0.0f;
+        if (!a.value_logprobs)
+            v[i] /= a.tau;
+        top = max_nan(top, v[i]);
+    }
+    top = warp_max_nan(top);
     const bool none = top == -INFINITY;
     const float ref = none || a.value_logprobs ? 0.0f : top;
-    const float e = none ? 0.0f : expf(v - ref);
-    float Q = block_reduce(e, [](float p, float q) { return p + q; }, fbuf);
+    float e[EACH], Q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        e[i] = expf(v[i] - ref);
+        Q += e[i];
+    }
+    Q = warp_sum(Q);
     if (!(top < INFINITY))
         Q = NAN;
-    const float lnsum = a.value_logprobs || none ? 0.0f : logf(Q);
-    if (k < KDA_TOPK_MAX) {
-        t.id[k] = id;
-        t.q[k] = a.value_logprobs ? e : none ? 0.0f : e / Q;
-        t.lnq[k] = v - ref - lnsum;
+    const bool whole = !a.value_logprobs && !none;  // to be renormalised
+    const float lnsum = whole ? logf(Q) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        t.q[lane + 32 * i] = whole ? e[i] / Q : e[i];
+        t.lnq[lane + 32 * i] = v[i] - ref - lnsum;
     }
-    __syncthreads();
-    return none ? 0.0f : a.value_logprobs || Q != Q ? Q : 1.0f;
+    if (lane == 0)
+        t.Q = whole && Q == Q ? 1.0f : Q;
 }
 
-template <bool BF16, bool LOSS, bool GRAD>
-__global__ void __launch_bounds__(THREADS) distill_kernel(const Distill a)
+// d x of the entries whose ids lie in [lo, hi), over what store_tile wrote there.  An id
+// listed twice is written once, by its first entry.
+template <bool BF16>
+__device__ __forceinline__ void take_off(const Distill &a, const Entries &t, const RowPtr<BF16> &out, int lo, int hi,
+                                         float m, float off, float scale)
 {
-    __shared__ float fbuf[THREADS / 32];
+    for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+        const int id = t.id[k];
+        if (id < lo || id >= hi)
+            continue;
+        bool first = true;
+        float q = 0.0f;
+        for (int j = 0; j < a.K; ++j) {
+            const bool same = t.id[j] == id;
+            first &= !(same && j < k);
+            q += same ? t.q[j] : 0.0f;
+        }
+        if (first)
+            out.set(id, scale * (t.Q * ex2(fmaf(t.x[k] - m, a.c, off)) - q));
+    }
+}
+
+template <bool BF16, int VPT, bool GRAD>
+__global__ void __launch_bounds__(MAX_THREADS) distill_kernel(const Distill a)
+{
+    __shared__ Part parts[MAX_PARTS];
     __shared__ Entries t;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long n = blockIdx.x, base = n * a.ld;
-    const int V = a.V, tid = threadIdx.x;
+    const Place at(a.cl);
+    const int tid = threadIdx.x, step = blockDim.x, round = step * VPT;
+    const long long n = at.row;
+    const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(GRAD ? a.dx : nullptr, GRAD ? n * a.ldg : 0, a.V);
+    const int begin = at.begin(row.nvec), end = at.end(row.nvec);
     const float w = a.weight ? a.weight[n] : 1.0f;
     const float scale = GRAD ? w * a.tau * (a.g ? a.g[n] : 1.0f) : 0.0f;
-    if (w == 0.0f || (!LOSS && scale == 0.0f)) {  // a row that takes no part is not read
-        if (LOSS && tid == 0) {
+    Tile<BF16, VPT> tile;
+    if (w == 0.0f) {  // a row that takes no part is not read
+        if (at.rank == 0 && tid == 0) {
             a.loss[n] = 0.0f;
             if (a.stats_out)
                 a.stats_out[2 * n] = a.stats_out[2 * n + 1] = 0.0f;
         }
         if (GRAD)
-            for (int i = tid; i < V; i += THREADS)
-                put<BF16>(a.dx, n * a.ldg + i, 0.0f);
+            for (int b = begin; b < end; b += round)
+                store_tile(tile, row, out, b + tid, step, end, true, [](float, float) { return F2{0}; });
         return;
     }
-    const float Q = read_entries(a, n, t, fbuf);
-    float m, lnS;
-    if (LOSS) {
-        m = -INFINITY;
-        for (int i = tid; i < V; i += THREADS)
-            m = max_nan(m, element<BF16>(a.x, base + i));
-        m = block_reduce(m, [](float p, float q) { return max_nan(p, q); }, fbuf);
-        if (!(m < INFINITY))
-            m = NAN;
-        float S = 0.0f;
-        if (m != -INFINITY)
-            for (int i = tid; i < V; i += THREADS)
-                S += exp2f((element<BF16>(a.x, base + i) - m) * a.c);
-        lnS = logf(block_reduce(S, [](float p, float q) { return p + q; }, fbuf));
-        float part = 0.0f;
-        if (tid < a.K && t.id[tid] >= 0 && t.q[tid] != 0.0f) {
-            const float x = element<BF16>(a.x, base + t.id[tid]);
-            const float lp = m == -INFINITY ? -INFINITY : (x - m) / a.tau - lnS;
-            part = t.q[tid] * (t.lnq[tid] - lp);
+    at.arrive();
+    // the ids of the CTA's run; the first CTA reads every entry's logit for the loss
+    const int lo = max(0, row.first_id(begin)), hi = min(a.V, row.first_id(end));
+    Running<false> run;
+    int b = begin;
+    do {
+        tile.load(row, b + tid, step, end);
+        if (b == begin && tid < 32)
+            read_entries(a, n, row, at.rank ? lo : 0, at.rank ? hi : a.V, t);
+        run.add(tile, tile.max_of(), a.c);
+        b += round;
+    } while (b < end);
+    const Part part{run.m, warp_sum(run.S), 0.0f, 0u};
+    at.wait();
+    at.hand_out(parts, part);
+    at.sync();
+    const Stats st = join(parts, at.parts(), a.c);
+    if (at.rank == 0 && tid < 32) {
+        float kl = 0.0f, most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int k = tid + 32 * i;
+            if (t.q[k] != 0.0f) {
+                const float lp = st.empty() ? -INFINITY : (t.x[k] - st.m) / a.tau - st.lnS;
+                const float term = t.q[k] * (t.lnq[k] - lp);
+                kl += term;
+                most = max_nan(most, term);
+            }
         }
-        float kl = block_reduce(part, [](float p, float q) { return p + q; }, fbuf);
-        const float most = block_reduce(part, [](float p, float q) { return max_nan(p, q); }, fbuf);
+        kl = warp_sum(kl);
+        most = warp_max_nan(most);
         if (kl == INFINITY && most < INFINITY)  // finite terms, rounded past the range
             kl = FLT_MAX;
         if (tid == 0) {
-            a.loss[n] = Q == 0.0f ? 0.0f : kl * (a.tau * a.tau) * w;
+            a.loss[n] = t.Q == 0.0f ? 0.0f : kl * (a.tau * a.tau) * w;
             if (a.stats_out) {
-                a.stats_out[2 * n] = m;
-                a.stats_out[2 * n + 1] = lnS;
+                a.stats_out[2 * n] = st.m;
+                a.stats_out[2 * n + 1] = st.lnS;
             }
-            if ((m != m || Q != Q) && a.status)
+            if ((st.bad() || t.Q != t.Q) && a.status)
                 atomicOr(a.status, KDA_ST_NAN);
         }
-    } else {
-        m = a.stats_in[2 * n];
-        lnS = a.stats_in[2 * n + 1];
     }
-    if (!GRAD)
-        return;
-    // p = exp2(d log2(e) + off)
-    const float off = -lnS * LOG2E;
-    const bool zero = m == -INFINITY || Q == 0.0f || scale == 0.0f;
-    float fix = 0.0f;
-    bool first = false;
-    if (tid < a.K && t.id[tid] >= 0 && !zero) {
-        first = true;
-        for (int j = 0; j < tid; ++j)
-            first &= t.id[j] != t.id[tid];
-        float q = 0.0f;
-        for (int j = tid; j < a.K; ++j)
-            q += t.id[j] == t.id[tid] ? t.q[j] : 0.0f;
-        const float x = element<BF16>(a.x, base + t.id[tid]);
-        fix = scale * (Q * exp2f(fmaf(x - m, a.c, off)) - q);
-    }
-    __syncthreads();  // the entries' logits are read before the gradient may replace them
-    for (int i = tid; i < V; i += THREADS) {
-        float d = 0.0f;
+    if (GRAD) {
+        const bool zero = st.empty() || t.Q == 0.0f || scale == 0.0f;
+        const float off = -st.lnS * LOG2E, m = st.m, sq = scale * t.Q;
+        b = begin;
+        do {
+            if (round < end - begin && !zero)  // of several rounds the registers hold the last one alone
+                tile.load(row, b + tid, step, end);
+            store_tile(tile, row, out, b + tid, step, end, zero, [&](float p, float q) {
+                const float2 u = split(fma2(f2(p, q) + f2(-m, -m), f2(a.c, a.c), f2(off, off)));
+                return f2(ex2(u.x), ex2(u.y)) * f2(sq, sq);
+            });
+            b += round;
+        } while (b < end);
         if (!zero) {
-            const float x = element<BF16>(a.x, base + i);
-            d = scale * Q * exp2f(fmaf(x - m, a.c, off));
+            __syncthreads();
+            take_off(a, t, out, lo, hi, m, off, scale);
         }
-        put<BF16>(a.dx, n * a.ldg + i, d);
     }
-    __syncthreads();
-    if (first)
-        put<BF16>(a.dx, n * a.ldg + t.id[tid], fix);
+}
+
+template <bool BF16, int VPT>
+__global__ void __launch_bounds__(256) distill_backward_kernel(const Distill a)
+{
+    __shared__ Entries t;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long n = blockIdx.x / a.cl;
+    const int chunk = blockIdx.x % a.cl, tid = threadIdx.x, step = blockDim.x;
+    const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(a.dx, n * a.ldg, a.V);
+    const int first = chunk * step * VPT, last = min(row.nvec, first + step * VPT);
+    const int lo = max(0, row.first_id(first)), hi = min(a.V, row.first_id(last));
+    const float w = a.weight ? a.weight[n] : 1.0f;
+    const float scale = w == 0.0f ? 0.0f : w * a.tau * (a.g ? a.g[n] : 1.0f);
+    const float m = a.stats_in[2 * n], off = -a.stats_in[2 * n + 1] * LOG2E;
+    bool zero = m == -INFINITY || scale == 0.0f;
+    Tile<BF16, VPT> tile;
+    if (!zero) {  // the same for the whole CTA
+        tile.load(row, first + tid, step, last);
+        if (tid < 32)
+            read_entries(a, n, row, lo, hi, t);
+        __syncthreads();
+        zero = t.Q == 0.0f;
+    }
+    const float sq = zero ? 0.0f : scale * t.Q;
+    store_tile(tile, row, out, first + tid, step, last, zero, [&](float p, float q) {
+        const float2 u = split(fma2(f2(p, q) + f2(-m, -m), f2(a.c, a.c), f2(off, off)));
+        return f2(ex2(u.x), ex2(u.y)) * f2(sq, sq);
+    });
+    if (!zero) {
+        __syncthreads();
+        take_off(a, t, out, lo, hi, m, off, scale);
+    }
 }
 
 int check_teacher(const kda_teacher *t, int N)
@@ -186,30 +269,54 @@ int check_teacher(const kda_teacher *t, int N)
     return KDA_OK;
 }
 
-template <bool LOSS, bool GRAD>
-int launch(const Distill &a, int dtype, int N, cudaStream_t stream)
+template <bool GRAD>
+int launch(Distill a, int dtype, int N, cudaStream_t stream)
 {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(N));
-    cfg.blockDim = dim3(THREADS);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = dtype == KDA_BF16 ? cudaLaunchKernelEx(&cfg, distill_kernel<true, LOSS, GRAD>, a)
-                                            : cudaLaunchKernelEx(&cfg, distill_kernel<false, LOSS, GRAD>, a);
-    if (e != cudaSuccess)
-        return fail(KDA_ECUDA, std::string("distill_kernel launch: ") + cudaGetErrorString(e));
-    return check_launch("distill_kernel");
+    const bool bf16 = dtype == KDA_BF16;
+    const Shape sh = shape_of(N, vectors_of(a.x, a.V, a.ld, bf16));
+    a.cl = sh.cl;
+    return with_vpt(sh.vpt, [&](auto vpt) {
+        constexpr int VPT = decltype(vpt)::value;
+        return launch_rows(bf16 ? distill_kernel<true, VPT, GRAD> : distill_kernel<false, VPT, GRAD>, a,
+                           static_cast<long long>(N) * sh.cl, sh.threads, sh.cl, stream, "distill_kernel");
+    });
+}
+
+int launch_backward(Distill a, int dtype, int N, cudaStream_t stream)
+{
+    const bool bf16 = dtype == KDA_BF16;
+    const Chunks ch = chunks_of(vectors_of(a.x, a.V, a.ld, bf16));
+    a.cl = ch.chunks;
+    return with_vpt(ch.vpt, [&](auto vpt) {
+        constexpr int VPT = decltype(vpt)::value;
+        return launch_rows(bf16 ? distill_backward_kernel<true, VPT> : distill_backward_kernel<false, VPT>, a,
+                           static_cast<long long>(N) * ch.chunks, ch.threads, 1, stream, "distill_backward_kernel");
+    });
 }
 
 Distill params(const void *x, void *dx, long long ld, long long ldg, int V, const kda_teacher &t, float tau,
                const float *g, const float *stats_in, float *loss, float *stats_out, int *status)
 {
-    return Distill{x,     dx,    ld, ldg,    V,   t.K,           t.ids, t.values, t.value_dtype == KDA_BF16,
-                   t.kind == KDA_TEACHER_LOGPROBS, t.weight, g,  stats_in, tau, LOG2E / tau, loss,  stats_out,  status};
+    Distill a{};
+    a.x = x;
+    a.dx = dx;
+    a.ld = ld;
+    a.ldg = ldg;
+    a.V = V;
+    a.K = t.K;
+    a.ids = t.ids;
+    a.values = t.values;
+    a.value_bf16 = t.value_dtype == KDA_BF16;
+    a.value_logprobs = t.kind == KDA_TEACHER_LOGPROBS;
+    a.weight = t.weight;
+    a.g = g;
+    a.stats_in = stats_in;
+    a.tau = tau;
+    a.c = LOG2E / tau;
+    a.loss = loss;
+    a.stats_out = stats_out;
+    a.status = status;
+    return a;
 }
 
 }  // namespace
@@ -231,7 +338,7 @@ extern "C" int spec_distill(const void *logits, int logit_dtype, int N, int V, l
         return fail(KDA_EINVAL, "loss must not be NULL");
     if (!aligned4(loss) || !aligned4(stats) || !aligned4(dev_status))
         return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
-    return launch<true, false>(params(logits, nullptr, ld, 0, V, *teacher, temperature, nullptr, nullptr, loss, stats,
+    return launch<false>(params(logits, nullptr, ld, 0, V, *teacher, temperature, nullptr, nullptr, loss, stats,
                                       dev_status), logit_dtype, N, stream);
 }
 
@@ -252,7 +359,7 @@ extern "C" int spec_distill_backward(const void *logits, int logit_dtype, int N,
         return fail(KDA_EINVAL, "stats must not be NULL");
     if (!aligned4(stats) || !aligned4(grad_loss) || !aligned4(dev_status))
         return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
-    return launch<false, true>(params(logits, dlogits, ld, ldg, V, *teacher, temperature, grad_loss, stats, nullptr,
+    return launch_backward(params(logits, dlogits, ld, ldg, V, *teacher, temperature, grad_loss, stats, nullptr,
                                       nullptr, dev_status), logit_dtype, N, stream);
 }
 
@@ -272,6 +379,6 @@ extern "C" int spec_distill_step(const void *logits, int logit_dtype, int N, int
         return fail(KDA_EINVAL, "loss must not be NULL");
     if (!aligned4(grad_loss) || !aligned4(loss) || !aligned4(stats) || !aligned4(dev_status))
         return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
-    return launch<true, true>(params(logits, dlogits, ld, ldg, V, *teacher, temperature, grad_loss, nullptr, loss, stats,
+    return launch<true>(params(logits, dlogits, ld, ldg, V, *teacher, temperature, grad_loss, nullptr, loss, stats,
                                      dev_status), logit_dtype, N, stream);
 }

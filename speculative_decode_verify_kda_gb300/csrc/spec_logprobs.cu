@@ -6,8 +6,20 @@
 //   d x_i = (1/temperature) [ g (1{i = t} - p_i) - h p_i (ln p_i + H) ]
 // for g = dL/d log p_t and h = dL/dH.
 //
-// One CTA a row.  The row is read once for the maximum, once for the two sums and
-// once for each alternative (the largest key below the last one taken).
+// logprobs_kernel: a row stays in the registers of its CTA or cluster (logit_rows.cuh), so
+// it is read once.  The top alternatives come out of the same registers: from the
+// threads' maxima, which the sums need anyway, a threshold is taken that at least K
+// logits reach, the few that reach it go to a list in the first CTA's shared memory, and
+// counting how many of the list precede an entry gives its place.
+//
+// The threshold: each warp orders its lanes' maxima and names the r-th largest; the w-th
+// largest of those, with r w >= K, is reached by r lanes' maxima of w warps, that is by K
+// logits at least.  For logits in no particular order about K of them reach it.  Where
+// more than the list holds do (many equal logits), the threshold is taken again with a
+// logit's place in the row as a part of its value; where that too leaves more, the first
+// CTA finds the alternatives one after the other.  All three give the same answer.
+#include <algorithm>
+
 #include "logit_rows.cuh"
 
 namespace kda {
@@ -16,114 +28,295 @@ namespace {
 using namespace rows;
 using Key = unsigned long long;
 
+constexpr int LIST = 2048;  // candidates a row's list holds
+
 struct Score {
     const void *x;
     long long ld;
-    int V, K;
+    int V, K, cl;
+    int r, w;  // the threshold is the w-th largest of the warps' r-th largest maxima
     const int *tokens;
     float tau, c;  // c = log2(e) / tau
     float *logprob, *entropy, *stats, *top_logprobs;
     int *top_ids, *status;
 };
 
-template <bool BF16>
-__global__ void __launch_bounds__(THREADS) logprobs_kernel(const Score a)
+struct ScoreShared {
+    Part parts[MAX_PARTS];
+    Key bound;
+    int count;
+    __align__(16) Key list[LIST];
+};
+
+// The w-th largest (from 1) of n values, by all threads of the CTA.
+template <class T, class Get>
+__device__ __forceinline__ T rank_of(Get get, int n, int w, Key *out)
 {
-    __shared__ float fbuf[THREADS / 32];
-    __shared__ Key kbuf[THREADS / 32];
+    if (n <= 32) {
+        const int lane = threadIdx.x & 31;
+        return warp_rank<T>(lane < n ? get(lane) : T(0), w - 1);
+    }
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const T mine = get(i);
+        int before = 0;
+        for (int j = 0; j < n; ++j) {
+            const T other = get(j);
+            before += other > mine || (other == mine && j < i);
+        }
+        if (before == w - 1)
+            *out = mine;
+    }
+    __syncthreads();
+    return static_cast<T>(*out);
+}
+
+__device__ __forceinline__ void append(int *count, Key *list, Key key)
+{
+    const int at = atomicAdd(count, 1);
+    if (at < LIST)
+        list[at] = key;
+}
+
+// Calls f with the key of every logit above -inf of the CTA's share, read again.
+template <bool BF16, class F>
+__device__ __forceinline__ void each_key(const RowPtr<BF16> &row, int first, int step, int end, F f)
+{
+    for (int i = first; i < end; i += step) {
+        int id = row.first_id(i);
+        Tile<BF16, 1>::each_of(row.full(i) ? row.load(i) : row.load_edge(i), [&](float p, float q) {
+            if (p > -INFINITY)
+                f(key_of(p, id));
+            if (q > -INFINITY)
+                f(key_of(q, id + 1));
+            id += 2;
+        });
+    }
+}
+
+// Second try at the list, for a row with many equal logits: the lanes' largest keys (value,
+// then place) of the row read again, and the threshold from those, which min(K, 32) lanes of
+// ceil(K / 32) warps reach.
+template <bool BF16>
+__device__ __noinline__ void list_by_key(int K, RowPtr<BF16> row, Place at, ScoreShared &sh)
+{
+    const int first = at.begin(row.nvec) + threadIdx.x, end = at.end(row.nvec), lane = threadIdx.x & 31;
+    Key best = 0;
+    each_key(row, first, blockDim.x, end, [&](Key k) { best = k > best ? k : best; });
+    __syncwarp();
+    best = warp_rank<Key>(best, min(K, 32) - 1);
+    Key *keys = reinterpret_cast<Key *>(sh.parts);
+    at.sync();  // the parts and the count have been read by every CTA
+    if (lane < at.cl)
+        at.in_cta(keys, lane)[at.rank * at.warps + (threadIdx.x >> 5)] = best;
+    if (threadIdx.x == 0)
+        sh.count = 0;
+    at.sync();
+    const int n = at.parts(), w = (K + 31) / 32;
+    const Key bound = w <= n ? rank_of<Key>([&](int i) { return keys[i]; }, n, w, &sh.bound) : 0;
+    int *count = at.in_cta(&sh.count, 0);
+    Key *list = at.in_cta(sh.list, 0);
+    each_key(row, first, blockDim.x, end, [&](Key k) {
+        if (k >= bound)
+            append(count, list, k);
+    });
+    at.sync();
+}
+
+// Last resort, by the first CTA alone: the alternatives one after the other, each the largest
+// key below the last one.
+template <bool BF16>
+__device__ __noinline__ void list_by_rounds(int K, RowPtr<BF16> row, ScoreShared &sh)
+{
+    Key *best_of = reinterpret_cast<Key *>(sh.parts), last = ~0ull;
+    int n = 0;
+    for (; n < K && last; ++n) {
+        Key best = 0;
+        each_key(row, threadIdx.x, blockDim.x, row.nvec, [&](Key k) { best = k < last && k > best ? k : best; });
+        __syncwarp();
+        best = warp_rank<Key>(best, 0);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+            best_of[threadIdx.x >> 5] = best;
+        __syncthreads();
+        for (int i = 0; i < (blockDim.x >> 5); ++i)
+            best = best_of[i] > best ? best_of[i] : best;
+        last = best;
+        if (threadIdx.x == 0)
+            sh.list[n] = best;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        sh.count = n;
+    __syncthreads();
+}
+
+template <bool BF16, int VPT>
+__global__ void __launch_bounds__(MAX_THREADS) logprobs_kernel(const Score a)
+{
+    __shared__ ScoreShared sh;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long n = blockIdx.x, base = n * a.ld;
-    const int V = a.V, tid = threadIdx.x;
-    float m = -INFINITY;
-    for (int i = tid; i < V; i += THREADS)
-        m = max_nan(m, element<BF16>(a.x, base + i));
-    m = block_reduce(m, [](float p, float q) { return max_nan(p, q); }, fbuf);
-    const bool bad = !(m < INFINITY), empty = m == -INFINITY;
-    float S = 0.0f, E = 0.0f;
-    if (!bad && !empty) {
-        for (int i = tid; i < V; i += THREADS) {
-            // below -1e4 (a masked token) the weight is 0 and so is its term of the entropy
-            const float d = fmaxf((element<BF16>(a.x, base + i) - m) * a.c, -1e4f);
-            const float e = exp2f(d);
-            S += e;
-            E += e * d;
-        }
-    }
-    S = block_reduce(S, [](float p, float q) { return p + q; }, fbuf);
-    E = block_reduce(E, [](float p, float q) { return p + q; }, fbuf);
-    const float lnS = logf(S);
+    const Place at(a.cl);
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        sh.count = 0;
+    at.arrive();
+    const RowPtr<BF16> row(a.x, at.row * a.ld, a.V);
+    const int begin = at.begin(row.nvec), end = at.end(row.nvec), step = blockDim.x, round = step * VPT;
+    Tile<BF16, VPT> t;
+    Running<true> run;
+    float most = -INFINITY;
+    int b = begin;
+    do {
+        t.load(row, b + tid, step, end);
+        const float m = t.max_of();
+        most = max_nan(most, m);
+        run.add(t, m, a.c);
+        b += round;
+    } while (b < end);
+    const uint32_t mine = most > -INFINITY ? ordered(most) : 0u;
+    const uint32_t named = a.K > 0 ? warp_rank<uint32_t>(mine, a.r - 1) : 0u;
+    const Part part{run.m, warp_sum(run.S), warp_sum(run.E), named};
+    at.wait();
+    at.hand_out(sh.parts, part);
+    at.sync();
+    const int n = at.parts();
+    const Stats st = join(sh.parts, n, a.c);
+    const bool bad = st.bad(), empty = st.empty();
     const float none = bad ? NAN : -INFINITY;
-    if (tid == 0) {
+    if (at.rank == 0 && tid == 0) {
+        const long long o = at.row;
         float lp = 0.0f;
         if (a.tokens) {
-            const int t = a.tokens[n];
-            if (t >= V && a.status)
+            const int token = a.tokens[o];
+            if (token >= a.V && a.status)
                 atomicOr(a.status, KDA_ST_BADTOKEN);
-            if (t >= 0 && t < V)
-                lp = bad || empty ? none : (element<BF16>(a.x, base + t) - m) / a.tau - lnS;
+            if (token >= 0 && token < a.V)
+                lp = bad || empty ? none : (row.at(token) - st.m) / a.tau - st.lnS;
         }
         if (a.logprob)
-            a.logprob[n] = lp;
+            a.logprob[o] = lp;
         if (a.entropy)
-            a.entropy[n] = bad ? NAN : empty ? 0.0f : lnS - LN2 * E / S;
+            a.entropy[o] = st.entropy;
         if (a.stats) {
-            a.stats[2 * n] = bad ? NAN : m;
-            a.stats[2 * n + 1] = bad || empty ? none : lnS;
+            a.stats[2 * o] = st.m;
+            a.stats[2 * o + 1] = st.lnS;
         }
         if (bad && a.status)
             atomicOr(a.status, KDA_ST_NAN);
     }
-    Key last = ~0ull;
-    for (int k = 0; k < a.K; ++k) {
-        Key best = 0;
-        if (!bad && !empty && last) {
-            for (int i = tid; i < V; i += THREADS) {
-                const float x = element<BF16>(a.x, base + i);
-                const Key key = x > -INFINITY ? key_of(x, i) : 0;
-                if (key < last && key > best)
-                    best = key;
-            }
-        }
-        best = block_reduce(best, [](Key p, Key q) { return p > q ? p : q; }, kbuf);
-        last = best;
-        if (tid == 0) {
-            const long long o = n * a.K + k;
-            a.top_ids[o] = best ? key_id(best) : -1;
-            a.top_logprobs[o] = best ? (from_ordered(static_cast<uint32_t>(best >> 32)) - m) / a.tau - lnS : none;
+    if (a.K == 0)
+        return;
+    if (!bad && !empty) {
+        const uint32_t bound =
+            a.w <= n ? rank_of<uint32_t>([&](int i) { return sh.parts[i].key; }, n, a.w, &sh.bound) : 0u;
+        if (mine && mine >= bound) {
+            const float least = bound ? from_ordered(bound) : -INFINITY;
+            int *count = at.in_cta(&sh.count, 0);
+            Key *list = at.in_cta(sh.list, 0);
+            b = begin;
+            do {
+                if (round < end - begin)  // of several rounds the registers hold the last one alone
+                    t.load(row, b + tid, step, end);
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    int id = row.first_id(b + tid + j * step);
+                    t.each_of(t.v[j], [&](float p, float q) {
+                        if (p >= least && p > -INFINITY)
+                            append(count, list, key_of(p, id));
+                        if (q >= least && q > -INFINITY)
+                            append(count, list, key_of(q, id + 1));
+                        id += 2;
+                    });
+                }
+                b += round;
+            } while (b < end);
         }
     }
+    at.sync();
+    int found = *at.in_cta(&sh.count, 0);
+    if (found > LIST) {  // the same for every CTA of the row
+        list_by_key(a.K, row, at, sh);
+        found = *at.in_cta(&sh.count, 0);
+    }
+    at.arrive();  // the first CTA's shared memory has been read by the others
+    if (at.rank == 0) {
+        if (found > LIST) {
+            list_by_rounds(a.K, row, sh);
+            found = sh.count;
+        }
+        const long long o = at.row * a.K;
+        for (int i = tid; i < found; i += step) {
+            const Key key = sh.list[i];
+            int place = 0;
+            for (int j = 0; j < found; ++j)
+                place += sh.list[j] > key;
+            if (place < a.K) {
+                a.top_ids[o + place] = key_id(key);
+                a.top_logprobs[o + place] =
+                    (from_ordered(static_cast<uint32_t>(key >> 32)) - st.m) / a.tau - st.lnS;
+            }
+        }
+        for (int k = found + tid; k < a.K; k += step) {
+            a.top_ids[o + k] = -1;
+            a.top_logprobs[o + k] = none;
+        }
+    }
+    at.wait();
 }
 
 struct ScoreGrad {
     const void *x;
     void *dx;
     long long ld, ldg;
-    int V;
+    int V, chunks;
     const int *tokens;
     const float *stats, *entropy, *g, *h;
-    float tau;
+    float tau, c;
 };
 
-template <bool BF16>
-__global__ void __launch_bounds__(THREADS) logprobs_backward_kernel(const ScoreGrad a)
+// One CTA a run of a row's vectors, one tile a thread: read, weighted, written.  With
+// u = (x - m) c - s log2(e), p = 2^u and
+//   d x_i = p (A + B u) + [i = t] g / tau,  A = -(g + h H) / tau, B = -h ln 2 / tau.
+template <bool BF16, int VPT>
+__global__ void __launch_bounds__(256) logprobs_backward_kernel(const ScoreGrad a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long n = blockIdx.x;
+    const long long n = blockIdx.x / a.chunks;
+    const int chunk = blockIdx.x % a.chunks, tid = threadIdx.x, step = blockDim.x;
+    const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(a.dx, n * a.ldg, a.V);
+    const int first = chunk * step * VPT, last = min(row.nvec, first + step * VPT);
     const int t = a.tokens ? a.tokens[n] : -1;
     const bool has = t >= 0 && t < a.V;
     const float g = a.g && has ? a.g[n] : 0.0f, h = a.h ? a.h[n] : 0.0f;
-    const float m = a.stats[2 * n], lnS = a.stats[2 * n + 1], H = a.h ? a.entropy[n] : 0.0f;
-    const float inv = 1.0f / a.tau;
-    for (int i = threadIdx.x; i < a.V; i += THREADS) {
-        float d = 0.0f;
-        if (m != -INFINITY && (g != 0.0f || h != 0.0f)) {
-            const float lp = fmaf(element<BF16>(a.x, n * a.ld + i) - m, inv, -lnS);
-            const float p = exp2f(lp * LOG2E);
-            d = (i == t ? g : 0.0f) - p * (g + h * (fmaxf(lp, -1e4f) + H));
+    const float m = a.stats[2 * n], lnS = a.stats[2 * n + 1];
+    const bool zero = m == -INFINITY || (g == 0.0f && h == 0.0f);
+    const float A = -(g + (h != 0.0f ? h * a.entropy[n] : 0.0f)) / a.tau, B = -h * LN2 / a.tau;
+    const float off = -lnS * LOG2E;
+    Tile<BF16, VPT> x;
+    if (!zero)
+        x.load(row, first + tid, step, last);
+    float at_token = 0.0f;
+    const bool mine = has && !zero && (row.skip + t) / row.PER >= first && (row.skip + t) / row.PER < last;
+    if (mine) {  // the same for the whole CTA
+        if (tid == 0) {
+            const float u = fmaf(row.at(t) - m, a.c, off);
+            at_token = ex2(u) * fmaf(B, fmaxf(u, -1e4f), A) + g / a.tau;
         }
-        put<BF16>(a.dx, n * a.ldg + i, d * inv);
+        __syncthreads();  // the token's logit is read before its gradient may replace it
+    }
+    auto weigh = [&](float p, float q) {
+        const F2 u = fma2(f2(p, q) + f2(-m, -m), f2(a.c, a.c), f2(off, off));
+        const float2 v = split(u);
+        const F2 low = f2(fmaxf(v.x, -1e4f), fmaxf(v.y, -1e4f));
+        return f2(ex2(v.x), ex2(v.y)) * fma2(f2(B, B), low, f2(A, A));
+    };
+    store_tile(x, row, out, first + tid, step, last, zero, weigh);
+    if (mine) {
+        __syncthreads();  // after the element's ordinary value
+        if (tid == 0)
+            out.set(t, at_token);
     }
 }
 
@@ -152,22 +345,19 @@ extern "C" int spec_logprobs(const void *logits, int logit_dtype, int N, int V, 
                           static_cast<const void *>(dev_status)})
         if (!rows::aligned4(p))
             return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
-    Score a{logits, ld, V, K, tokens, temperature, rows::LOG2E / temperature, logprob, entropy, stats, top_logprobs,
-            top_ids, dev_status};
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(N));
-    cfg.blockDim = dim3(rows::THREADS);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = logit_dtype == KDA_BF16 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, a)
-                                                  : cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, a);
-    if (e != cudaSuccess)
-        return fail(KDA_ECUDA, std::string("logprobs_kernel launch: ") + cudaGetErrorString(e));
-    return check_launch("logprobs_kernel");
+    const bool bf16 = logit_dtype == KDA_BF16;
+    const Shape sh = rows::shape_of(N, rows::vectors_of(logits, V, ld, bf16));
+    // r lanes of w warps make the threshold: about two thirds of the warps, so that one warp of
+    // small logits does not lower it
+    const int warps = sh.cl * sh.threads / 32;
+    const int r = std::max(1, std::min(32, (5 * K + 3 * warps - 1) / (3 * warps)));
+    Score a{logits, ld, V, K, sh.cl, r, (K + r - 1) / r, tokens, temperature, rows::LOG2E / temperature, logprob,
+            entropy, stats, top_logprobs, top_ids, dev_status};
+    return rows::with_vpt(sh.vpt, [&](auto vpt) {
+        constexpr int VPT = decltype(vpt)::value;
+        return rows::launch_rows(bf16 ? logprobs_kernel<true, VPT> : logprobs_kernel<false, VPT>, a,
+                                 static_cast<long long>(N) * sh.cl, sh.threads, sh.cl, stream, "logprobs_kernel");
+    });
 }
 
 extern "C" int spec_logprobs_backward(const void *logits, int logit_dtype, int N, int V, long long ld,
@@ -194,19 +384,14 @@ extern "C" int spec_logprobs_backward(const void *logits, int logit_dtype, int N
                           static_cast<const void *>(grad_entropy)})
         if (!rows::aligned4(p))
             return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
-    ScoreGrad a{logits, dlogits, ld, ldg, V, tokens, stats, entropy, grad_logprob, grad_entropy, temperature};
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(N));
-    cfg.blockDim = dim3(rows::THREADS);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = logit_dtype == KDA_BF16 ? cudaLaunchKernelEx(&cfg, logprobs_backward_kernel<true>, a)
-                                                  : cudaLaunchKernelEx(&cfg, logprobs_backward_kernel<false>, a);
-    if (e != cudaSuccess)
-        return fail(KDA_ECUDA, std::string("logprobs_backward_kernel launch: ") + cudaGetErrorString(e));
-    return check_launch("logprobs_backward_kernel");
+    const bool bf16 = logit_dtype == KDA_BF16;
+    const rows::Chunks ch = rows::chunks_of(rows::vectors_of(logits, V, ld, bf16));
+    ScoreGrad a{logits, dlogits, ld, ldg, V, ch.chunks, tokens, stats, entropy, grad_logprob, grad_entropy,
+                temperature, rows::LOG2E / temperature};
+    return rows::with_vpt(ch.vpt, [&](auto vpt) {
+        constexpr int VPT = decltype(vpt)::value;
+        return rows::launch_rows(bf16 ? logprobs_backward_kernel<true, VPT> : logprobs_backward_kernel<false, VPT>, a,
+                                 static_cast<long long>(N) * ch.chunks, ch.threads, 1, stream,
+                                 "logprobs_backward_kernel");
+    });
 }
