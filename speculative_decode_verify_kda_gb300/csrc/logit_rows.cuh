@@ -2,11 +2,12 @@
 // spec_distill.cu).
 //
 // A row is read in 16-byte vectors and belongs to one CTA or to a cluster of CTAs, each
-// of which takes a run of the row's vectors.  A thread holds VPT vectors in registers (a
-// tile); up to 1024 threads x 8 vectors x 8 CTAs hold a row of 524288 bf16 or 262144 f32
-// logits, so the row is read from memory once and what comes after its sum (the gradient,
-// the alternatives) works on the registers.  Longer rows take more rounds of tiles and are
-// read again for the second part.
+// of which takes a run of the row's vectors.
+//
+// Few rows, or short ones: a thread holds VPT vectors in registers (a tile), and what comes
+// after the row's sum (the gradient, the alternatives) works on those.  Longer runs take
+// more rounds of tiles and are read again.
+// Many long rows: the vectors pass through shared memory ahead of their use (Run).
 //
 // The sums are taken relative to the warp's own maximum, and a warp's triple (maximum, sum
 // of weights, weighted sum of exponents) joins the others' once, through the shared memory
@@ -30,7 +31,7 @@ namespace rows {
 namespace cg = cooperative_groups;
 
 constexpr int MAX_CL = 8;          // CTAs of a cluster (the portable size)
-constexpr int MAX_THREADS = 1024;
+constexpr int MAX_THREADS = 256;   // of a CTA that holds its run in registers
 constexpr int MAX_VPT = 8;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -157,13 +158,13 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// The value of rank r (0 the largest) among the warp's 32.
-template <class T>
+// The value of rank r (0 the largest) among the warp's first N lanes (a power of two).
+template <class T, int N = 32>
 __device__ __forceinline__ T warp_rank(T x, int r)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 2; k <= 32; k <<= 1) {
+    for (int k = 2; k <= N; k <<= 1) {
 #pragma unroll
         for (int j = k >> 1; j; j >>= 1) {  // a bitonic network, descending over the lanes
             const T y = __shfl_xor_sync(0xffffffffu, x, j);
@@ -306,39 +307,50 @@ struct Tile {
                 v[j] = u;
     }
 
-    // f(pair of neighbouring elements) for every pair.
-    template <class F>
+    // f(pair of neighbouring elements) for every pair; RAISE: elements below -1e30 as -1e30.
+    template <bool RAISE = false, class F>
     __device__ __forceinline__ void each(F f) const
     {
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
-            each_of(v[j], f);
+            each_of<RAISE>(v[j], f);
     }
-    template <class F>
+    template <bool RAISE = false, class F>
     static __device__ __forceinline__ void each_of(const uint4 &u, F f)
     {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         if (BF16) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                f(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+            for (int k = 0; k < 4; ++k) {
+                uint32_t x = w[k];
+                if (RAISE)  // 0xf149 is the bf16 next to -1e30
+                    asm("max.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[k]), "r"(0xf149f149u));
+                f(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+            }
+        } else if (RAISE) {
+            f(fmaxf(__uint_as_float(w[0]), -1e30f), fmaxf(__uint_as_float(w[1]), -1e30f));
+            f(fmaxf(__uint_as_float(w[2]), -1e30f), fmaxf(__uint_as_float(w[3]), -1e30f));
         } else {
             f(__uint_as_float(w[0]), __uint_as_float(w[1]));
             f(__uint_as_float(w[2]), __uint_as_float(w[3]));
         }
     }
 
+    // The largest element of the vectors [J0, J1), or a NaN.
+    template <int J0 = 0, int J1 = VPT>
     __device__ __forceinline__ float max_of() const
     {
         if (BF16) {
-            uint32_t m = max_nan_bf16x2(max_nan_bf16x2(v[0].x, v[0].y), max_nan_bf16x2(v[0].z, v[0].w));
+            uint32_t m = max_nan_bf16x2(max_nan_bf16x2(v[J0].x, v[J0].y), max_nan_bf16x2(v[J0].z, v[J0].w));
 #pragma unroll
-            for (int j = 1; j < VPT; ++j)
+            for (int j = J0 + 1; j < J1; ++j)
                 m = max_nan_bf16x2(m, max_nan_bf16x2(max_nan_bf16x2(v[j].x, v[j].y), max_nan_bf16x2(v[j].z, v[j].w)));
             return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
         }
         float m = -INFINITY;
-        each([&](float p, float q) { m = max_nan(m, max_nan(p, q)); });
+#pragma unroll
+        for (int j = J0; j < J1; ++j)
+            each_of(v[j], [&](float p, float q) { m = max_nan(m, max_nan(p, q)); });
         return m;
     }
 };
@@ -375,49 +387,122 @@ __device__ __forceinline__ void store_tile(const Tile<BF16, VPT> &t, const RowPt
     }
 }
 
-// Running maximum and sums of a warp's share of a row, in units of exp2: c = log2(e) / tau,
-// d = (x - m) c, S = sum 2^d, E = sum d 2^d.  m is the warp's, S and E are the lane's.
-template <bool ENTROPY>
-struct Running {
-    float m = -INFINITY, S = 0.0f, E = 0.0f;
-
-    template <bool BF16, int VPT>
-    __device__ __forceinline__ void add(const Tile<BF16, VPT> &t, float tile_max, float c)
-    {
-        const float top = max_nan(m, warp_max_nan(tile_max));
-        if (top == -INFINITY)  // nothing but masked tokens so far
-            return;
-        if (S != 0.0f || E != 0.0f) {  // an earlier round's sums move to the new maximum
-            const float d = fmaxf((m - top) * c, -1e4f), w = ex2(d);
-            E = (E + S * d) * w;
-            S *= w;
-        }
-        m = top;
-        const F2 neg = f2(-top, -top), cc = f2(c, c);
-        F2 s = f2(0.0f, 0.0f), e = s;
-        t.each([&](float p, float q) {
-            float2 d = split((f2(p, q) + neg) * cc);
-            if (ENTROPY) {  // a masked token's term is 0, not 0 times -inf
-                d.x = fmaxf(d.x, -1e4f);
-                d.y = fmaxf(d.y, -1e4f);
-            }
-            const F2 w = f2(ex2(d.x), ex2(d.y));
-            s = s + w;
-            if (ENTROPY)
-                e = fma2(w, f2(d.x, d.y), e);
-        });
-        const float2 s2 = split(s), e2 = split(e);
-        S += s2.x + s2.y;
-        E += e2.x + e2.y;
-    }
-};
-
 // What a warp hands to the others: its maximum and sums, and a value of its largest ones.
 struct __align__(16) Part {
     float m, S, E;
     uint32_t key;
 };
-constexpr int MAX_PARTS = MAX_CL * (MAX_THREADS / 32);
+
+
+// The same for a tile whose vectors, STEP apart, all lie in the row and go to whole vectors at p.
+template <int STEP, bool BF16, int VPT, class F>
+__device__ __forceinline__ void store_whole(const Tile<BF16, VPT> &t, uint4 *p, F f)
+{
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        uint32_t w[4];
+        int k = 0;
+        t.each_of(t.v[j], [&](float x, float y) {
+            const float2 d = split(f(x, y));
+            if (BF16) {
+                w[k++] = pack_bf16(d.x, d.y);
+            } else {
+                w[k++] = __float_as_uint(d.x);
+                w[k++] = __float_as_uint(d.y);
+            }
+        });
+        p[j * STEP] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Logits to exponents of two.
+struct Scale {
+    float c;       // log2(e) / temperature
+    float margin;  // 16 / c
+};
+
+// Sums of a warp's share of a row relative to a logit `at`, in units of exp2: c =
+// log2(e) / tau, d = (x - at) c, S = sum 2^d, E = sum d 2^d; the sums are the lane's.
+//
+// `at` is the warp's largest logit so far or one at most 2^16 times less likely, so it
+// rarely moves after the first tile.  A term costs one multiply-add, x c - ref with ref =
+// at c rounded: what the rounding left out is the same for every term and is put back by
+// settle().  Where |ref| is so large that nothing of the differences would be left of it,
+// they are taken before they are scaled.
+template <bool ENTROPY>
+struct Running {
+    float at = -INFINITY, limit = -INFINITY;  // a maximum above `limit` moves `at`
+    float ref = NAN;                          // at c, rounded; NaN where differences come first
+    F2 s = F2{0}, e = F2{0};
+
+    // The sums relative to `top`.
+    __device__ __forceinline__ void settle(float top, float c, float &S, float &E) const
+    {
+        const float2 s2 = split(s), e2 = split(e);
+        // a term's exponent was (x - at) c + left
+        const float left = ref == ref ? fmaf(at, c, -ref) : 0.0f;
+        const float d = fmaxf((at - top) * c - left, -1e4f), w = ex2(d);
+        S = (s2.x + s2.y) * w;
+        E = (e2.x + e2.y) * w + S * d;
+    }
+    template <bool BF16, int N>
+    __device__ __forceinline__ void add(const Tile<BF16, N> &t, float tile_max, Scale z)
+    {
+        const float c = z.c;
+        if (__any_sync(0xffffffffu, !(tile_max <= limit))) {
+            const float top = max_nan(at, warp_max_nan(tile_max));
+            float S, E;
+            settle(top, c, S, E);
+            const bool any = at != -INFINITY;
+            s = f2(any ? S : 0.0f, 0.0f);
+            e = f2(any ? E : 0.0f, 0.0f);
+            at = top;
+            limit = top + z.margin;
+            ref = top * c;
+            if (!(fabsf(ref) < 1e6f))
+                ref = NAN;
+        }
+        // a tile's sums are formed apart: a long row's are then sums of sums
+        const F2 cc = f2(c, c);
+        F2 ts = f2(0.0f, 0.0f), te = ts;
+        if (ref == ref) {
+            // A masked token's term of the entropy is 0, not 0 times -inf: its logit is raised
+            // to -1e30, where its weight is 0 as well.
+            const F2 neg = f2(-ref, -ref);
+            t.template each<ENTROPY>([&](float p, float q) {
+                const F2 d = fma2(f2(p, q), cc, neg);
+                const float2 u = split(d);
+                const F2 w = f2(ex2(u.x), ex2(u.y));
+                ts = ts + w;
+                if (ENTROPY)
+                    te = fma2(w, d, te);
+            });
+        } else if (at != -INFINITY) {  // (-inf: nothing but masked tokens so far)
+            const F2 neg = f2(-at, -at);
+            t.template each<false>([&](float p, float q) {
+                const float2 u = split((f2(p, q) + neg) * cc);
+                const F2 d = f2(fmaxf(u.x, -1e4f), fmaxf(u.y, -1e4f));
+                const float2 v = split(d);
+                const F2 w = f2(ex2(v.x), ex2(v.y));
+                ts = ts + w;
+                te = fma2(w, d, te);
+            });
+        }
+        s = s + ts;
+        if (ENTROPY)
+            e = e + te;
+    }
+
+    // The warp's part, from the lanes' largest logits.
+    __device__ __forceinline__ Part part(float most, float c, uint32_t key) const
+    {
+        const float top = warp_max_nan(most);
+        float S = 0.0f, E = 0.0f;
+        if (top != -INFINITY)
+            settle(top, c, S, E);
+        return Part{top, warp_sum(S), ENTROPY ? warp_sum(E) : 0.0f, key};
+    }
+};
 
 struct Stats {
     float m, lnS, entropy;  // NaN for a row with a NaN or +inf, (-inf, -inf, 0) for an empty one
@@ -454,14 +539,16 @@ __device__ __forceinline__ Stats join(const Part *parts, int n, float c)
 // The CTA's place: its row, its run of the row's vectors, and its cluster.
 struct Place {
     long long row;
-    int rank, cl, warps;
-    __device__ __forceinline__ Place(int cl_)
-        : row(blockIdx.x / cl_), rank(blockIdx.x % cl_), cl(cl_), warps(blockDim.x >> 5)
+    int rank, cl, shift, warps;  // cl = 2^shift
+    __device__ __forceinline__ Place(int cl_, int threads)
+        : cl(cl_), shift((cl_ > 1) + (cl_ > 2) + (cl_ > 4)), warps(threads >> 5)
     {
+        row = blockIdx.x >> shift;
+        rank = blockIdx.x & (cl - 1);
     }
     __device__ __forceinline__ int begin(int nvec) const { return rank * per(nvec); }
     __device__ __forceinline__ int end(int nvec) const { return min(nvec, (rank + 1) * per(nvec)); }
-    __device__ __forceinline__ int per(int nvec) const { return (nvec + cl - 1) / cl; }
+    __device__ __forceinline__ int per(int nvec) const { return (nvec + cl - 1) >> shift; }
     // Every CTA of the cluster runs from here on.  Between the two calls: anything that stays
     // inside the CTA.
     __device__ __forceinline__ void arrive() const
@@ -499,6 +586,135 @@ struct Place {
     __device__ __forceinline__ int parts() const { return cl * warps; }
 };
 
+// ---------------------------------------------------------------------------
+// A run of vectors through shared memory
+// ---------------------------------------------------------------------------
+// Each of T threads copies the vectors that it will use into slots of its own in shared
+// memory, groups of VT vectors ahead of their use (cp.async): nothing has to be waited for
+// but the thread's own copies.
+
+// Waits until at most `pending` of the thread's newest groups of copies are under way.
+__device__ __forceinline__ void copies_done(int pending)
+{
+    switch (pending) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+template <bool BF16, int T, int VT>
+struct Run {
+    static constexpr int GROUP = T * VT;
+    using TileT = Tile<BF16, VT>;
+
+    const RowPtr<BF16> row;
+    int begin, end, groups;
+    int whole0, whole1;  // the groups [whole0, whole1) lie wholly in the row and the run
+    uint4 *slots;        // this thread's: slot s, vector v at [s GROUP + v T]
+
+    __device__ __forceinline__ Run(const RowPtr<BF16> &row_, const Place &at, uint4 *shared)
+        : row(row_), slots(shared + threadIdx.x)
+    {
+        begin = at.begin(row.nvec);
+        end = at.end(row.nvec);
+        groups = max(1, (at.per(row.nvec) + GROUP - 1) / GROUP);
+        whole0 = begin < row.full0;
+        whole1 = max(0, min(row.full1, end) - begin) / GROUP;
+    }
+    __device__ __forceinline__ bool whole(int g) const { return g >= whole0 && g < whole1; }
+    // The thread's first vector of group g.
+    __device__ __forceinline__ int vector(int g) const { return begin + g * GROUP + static_cast<int>(threadIdx.x); }
+
+    static __device__ __forceinline__ void copy(uint32_t to, const char *from)
+    {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    }
+    // Starts the copies of group g into slot s (past the last group: an empty group of copies).
+    __device__ __forceinline__ void start(int g, int s) const
+    {
+        if (g < groups) {
+            uint4 *to = slots + s * GROUP;
+            const int i0 = vector(g);
+            const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+            const char *src = row.base + 16ll * i0;
+            if (whole(g)) {
+#pragma unroll
+                for (int v = 0; v < VT; ++v)
+                    copy(dst + v * T * 16, src + v * T * 16);
+            } else {
+#pragma unroll 1
+                for (int v = 0; v < VT; ++v) {
+                    const int i = i0 + v * T;
+                    if (i >= end)
+                        break;
+                    if (row.full(i))
+                        copy(dst + v * T * 16, src + v * T * 16);
+                    else  // the one or two vectors of a row that cross its ends
+                        to[v * T] = row.load_edge(i);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // The vectors of group g from slot s.
+    __device__ __forceinline__ void get(TileT &t, int g, int s) const
+    {
+        constexpr uint32_t M = RowPtr<BF16>::MASKED;
+        const uint4 *from = slots + s * GROUP;
+        if (whole(g)) {
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+                t.v[v] = from[v * T];
+        } else {
+            const int i0 = vector(g);
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+                t.v[v] = i0 + v * T < end ? from[v * T] : make_uint4(M, M, M, M);
+        }
+    }
+    // f(tile, g) for every group, through SLOTS slots that are used again and again.
+    template <int SLOTS, class F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        static_assert(SLOTS <= 4, "copies_done waits for up to three groups");
+#pragma unroll 1
+        for (int g = 0; g < SLOTS; ++g)
+            start(g, g);
+        int s = 0;
+        for (int g = 0; g < groups; ++g) {
+            TileT t;
+            copies_done(SLOTS - 1);
+            get(t, g, s);
+            start(g + SLOTS, s);
+            s = s + 1 == SLOTS ? 0 : s + 1;
+            f(t, g);
+        }
+    }
+    // value(pair) of every pair of group g's tile into the same elements of `out`, or zeros.
+    template <class F>
+    __device__ __forceinline__ void put(const TileT &t, int g, const RowPtr<BF16> &out, bool zero, F value) const
+    {
+        const int i0 = vector(g);
+        if (whole(g) && row.skip == out.skip && !zero)
+            store_whole<T>(t, reinterpret_cast<uint4 *>(out.base) + i0, value);
+        else
+            store_tile(t, row, out, i0, T, end, zero, value);
+    }
+};
+
+// Allows a kernel the shared memory that it is launched with.
+template <class A>
+inline int allow_shared(void (*kernel)(A), size_t bytes)
+{
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e != cudaSuccess)
+        return fail(KDA_ECUDA, std::string("shared memory: ") + cudaGetErrorString(e));
+    return KDA_OK;
+}
+
 // Threads of a CTA, vectors of a thread and CTAs of a row for N rows of nvec vectors.
 struct Shape {
     int threads, vpt, cl;
@@ -521,7 +737,7 @@ inline Shape shape_of(long long N, long long nvec)
         cl *= 2;
     const long long per = (nvec + cl - 1) / cl;
     int threads = 32;
-    while (threads < 256 && per > threads * 2ll)
+    while (threads < MAX_THREADS && per > threads * 2ll)
         threads *= 2;
     int vpt = 1;
     while (vpt < MAX_VPT && per > static_cast<long long>(threads) * vpt)
@@ -559,14 +775,15 @@ inline int with_vpt(int vpt, F f)
 // Launches kernel(args) with `cl` CTAs a cluster, as a programmatic dependent of the launch
 // before it.
 template <class A>
-inline int launch_rows(void (*kernel)(A), const A &args, long long blocks, int threads, int cl, cudaStream_t stream,
-                       const char *what)
+inline int launch_rows(void (*kernel)(A), const A &args, long long blocks, int threads, int cl, size_t smem,
+                       cudaStream_t stream, const char *what)
 {
     if (blocks > 0x7fffffffll)
         return fail(KDA_EINVAL, "too many rows for one launch");
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

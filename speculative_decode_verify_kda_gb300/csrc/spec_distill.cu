@@ -15,6 +15,7 @@
 // holds a teacher's entry writes that element again with its q taken off.
 // distill_backward_kernel: the gradient alone, from the saved statistics, in one pass
 // without any exchange.
+#include <algorithm>
 #include <cfloat>
 
 #include "logit_rows.cuh"
@@ -27,115 +28,201 @@ using namespace rows;
 struct Distill {
     const void *x;
     void *dx;
-    long long ld, ldg;
+    long long ld, ldg, N;
     int V, K;
     int cl;  // CTAs of a row (the backward pass alone: runs of a row)
     const int *ids;
     const void *values;
     int value_bf16, value_logprobs;
     const float *weight, *g, *stats_in;
-    float tau, c;  // c = log2(e) / tau
+    float tau;
+    Scale z;
     float *loss, *stats_out;
     int *status;
 };
 
 constexpr int EACH = KDA_TOPK_MAX / 32;  // entries of a lane
 
-// The teacher's entries of the CTA's row.
-struct Entries {
-    int id[KDA_TOPK_MAX];   // -1: no entry
-    float q[KDA_TOPK_MAX];  // probability
+// The teacher's entries of a row.
+struct __align__(16) Entries {
+    int id[KDA_TOPK_MAX];    // -1: no entry, or one whose id an earlier entry has
+    float off[KDA_TOPK_MAX]; // sum of the q of the entries with this id
+    float q[KDA_TOPK_MAX];   // probability
     float lnq[KDA_TOPK_MAX];
-    float x[KDA_TOPK_MAX];  // the student's logit, where id lies in the CTA's run or all are wanted
-    float Q;                // sum of q: 1 for renormalised entries, 0 without any, NaN for a NaN
+    float x[KDA_TOPK_MAX];   // the student's logit, where it was asked for
+    float Q;                 // sum of q: 1 for renormalised entries, 0 without any, NaN for a NaN
 };
 
-// Fills `t`; called by one warp.  x is read for ids in [lo, hi).
+// One warp reads a row's entries in three steps, so that the latencies of the loads can be
+// spent on something else: ids and values, the student's logits at the ids, the
+// probabilities.
 template <bool BF16>
-__device__ __forceinline__ void read_entries(const Distill &a, long long n, const RowPtr<BF16> &row, int lo, int hi,
-                                             Entries &t)
+struct Reader {
+    int id[EACH];
+    float v[EACH], x[EACH];
+
+    __device__ __forceinline__ void load(const Distill &a, long long n)
+    {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int k = (threadIdx.x & 31) + 32 * i;
+            id[i] = -1;
+            v[i] = -INFINITY;
+            if (k < a.K) {
+                const long long o = n * a.K + k;
+                id[i] = a.ids[o];
+                v[i] = a.value_bf16 ? element<true>(a.values, o) : element<false>(a.values, o);
+            }
+        }
+    }
+    // The logits of ids in [lo, hi).
+    __device__ __forceinline__ void gather(const Distill &a, const RowPtr<BF16> &row, int lo, int hi)
+    {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            if (id[i] >= a.V && a.status)
+                atomicOr(a.status, KDA_ST_BADTOKEN);
+            if (id[i] < 0 || id[i] >= a.V) {
+                id[i] = -1;
+                v[i] = -INFINITY;
+            }
+            x[i] = id[i] >= lo && id[i] < hi ? row.at(id[i]) : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void finish(const Distill &a, Entries &t)
+    {
+        const int lane = threadIdx.x & 31;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            if (!a.value_logprobs)
+                v[i] /= a.tau;
+            top = max_nan(top, v[i]);
+        }
+        top = warp_max_nan(top);
+        const bool none = top == -INFINITY;
+        const float ref = none || a.value_logprobs ? 0.0f : top;
+        float e[EACH], Q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            e[i] = expf(v[i] - ref);
+            Q += e[i];
+        }
+        Q = warp_sum(Q);
+        if (!(top < INFINITY))
+            Q = NAN;
+        const bool whole = !a.value_logprobs && !none;  // to be renormalised
+        const float lnsum = whole ? logf(Q) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const float q = whole ? e[i] / Q : e[i];
+            t.id[lane + 32 * i] = id[i];
+            t.off[lane + 32 * i] = q;
+            t.q[lane + 32 * i] = q;
+            t.lnq[lane + 32 * i] = v[i] - ref - lnsum;
+            t.x[lane + 32 * i] = x[i];
+        }
+        if (lane == 0)
+            t.Q = whole && Q == Q ? 1.0f : Q;
+        __syncwarp();
+        // an id listed twice: its first entry takes every q off
+        int same[EACH] = {};
+        const int4 *ids = reinterpret_cast<const int4 *>(t.id);
+        for (int j = 0; j < (a.K + 3) / 4; ++j) {
+            const int4 o = ids[j];
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                if (32 * i < a.K)
+                    same[i] += (o.x == id[i]) + (o.y == id[i]) + (o.z == id[i]) + (o.w == id[i]);
+        }
+        bool twice = false;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            twice |= id[i] >= 0 && same[i] > 1;
+        if (__any_sync(0xffffffffu, twice)) {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                const int k = lane + 32 * i;
+                if (id[i] >= 0 && same[i] > 1) {
+                    float q = 0.0f;
+                    for (int j = 0; j < a.K; ++j) {
+                        if (t.id[j] == id[i]) {
+                            if (j < k) {
+                                id[i] = -1;
+                                break;
+                            }
+                            q += t.q[j];
+                        }
+                    }
+                    t.off[k] = q;
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                t.id[lane + 32 * i] = id[i];
+        }
+    }
+};
+
+// Loss and statistics of a row, by one warp.
+__device__ __forceinline__ void write_loss(const Distill &a, long long n, float w, const Stats &st, const Entries &t)
 {
     const int lane = threadIdx.x & 31;
-    int id[EACH];
-    float v[EACH], top = -INFINITY;
+    float kl = 0.0f, most = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int k = lane + 32 * i;
-        id[i] = -1;
-        v[i] = -INFINITY;
-        if (k < a.K) {
-            const long long o = n * a.K + k;
-            id[i] = a.ids[o];
-            v[i] = a.value_bf16 ? element<true>(a.values, o) : element<false>(a.values, o);
-            if (id[i] >= a.V && a.status)
-                atomicOr(a.status, KDA_ST_BADTOKEN);
+        if (t.q[k] != 0.0f) {
+            const float lp = st.empty() ? -INFINITY : (t.x[k] - st.m) / a.tau - st.lnS;
+            const float term = t.q[k] * (t.lnq[k] - lp);
+            kl += term;
+            most = max_nan(most, term);
         }
     }
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        if (id[i] < 0 || id[i] >= a.V) {
-            id[i] = -1;
-            v[i] = -INFINITY;
+    kl = warp_sum(kl);
+    most = warp_max_nan(most);
+    if (kl == INFINITY && most < INFINITY)  // finite terms, rounded past the range
+        kl = FLT_MAX;
+    if (lane == 0) {
+        a.loss[n] = t.Q == 0.0f ? 0.0f : kl * (a.tau * a.tau) * w;
+        if (a.stats_out) {
+            a.stats_out[2 * n] = st.m;
+            a.stats_out[2 * n + 1] = st.lnS;
         }
-        t.id[lane + 32 * i] = id[i];
-        t.x[lane + 32 * i] = id[i] >= lo && id[i] < hi ? row.at(id[i]) : 0.0f;
-        if (!a.value_logprobs)
-            v[i] /= a.tau;
-        top = max_nan(top, v[i]);
+        if ((st.bad() || t.Q != t.Q) && a.status)
+            atomicOr(a.status, KDA_ST_NAN);
     }
-    top = warp_max_nan(top);
-    const bool none = top == -INFINITY;
-    const float ref = none || a.value_logprobs ? 0.0f : top;
-    float e[EACH], Q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        e[i] = expf(v[i] - ref);
-        Q += e[i];
-    }
-    Q = warp_sum(Q);
-    if (!(top < INFINITY))
-        Q = NAN;
-    const bool whole = !a.value_logprobs && !none;  // to be renormalised
-    const float lnsum = whole ? logf(Q) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        t.q[lane + 32 * i] = whole ? e[i] / Q : e[i];
-        t.lnq[lane + 32 * i] = v[i] - ref - lnsum;
-    }
-    if (lane == 0)
-        t.Q = whole && Q == Q ? 1.0f : Q;
 }
 
-// d x of the entries whose ids lie in [lo, hi), over what store_tile wrote there.  An id
-// listed twice is written once, by its first entry.
+// d x of the entries whose ids lie in [lo, hi), over what store_tile wrote there, by threads
+// `who` of `many`.
 template <bool BF16>
 __device__ __forceinline__ void take_off(const Distill &a, const Entries &t, const RowPtr<BF16> &out, int lo, int hi,
-                                         float m, float off, float scale)
+                                         float m, float off, float scale, int who, int many)
 {
-    for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+    for (int k = who; k < a.K; k += many) {
         const int id = t.id[k];
-        if (id < lo || id >= hi)
-            continue;
-        bool first = true;
-        float q = 0.0f;
-        for (int j = 0; j < a.K; ++j) {
-            const bool same = t.id[j] == id;
-            first &= !(same && j < k);
-            q += same ? t.q[j] : 0.0f;
-        }
-        if (first)
-            out.set(id, scale * (t.Q * ex2(fmaf(t.x[k] - m, a.c, off)) - q));
+        if (id >= lo && id < hi)
+            out.set(id, scale * (t.Q * ex2(fmaf(t.x[k] - m, a.z.c, off)) - t.off[k]));
     }
+}
+
+// scale Q p of a pair.
+__device__ __forceinline__ F2 weighted(float p, float q, float m, float c, float off, float sq)
+{
+    const float2 u = split(fma2(f2(p, q) + f2(-m, -m), f2(c, c), f2(off, off)));
+    return f2(ex2(u.x), ex2(u.y)) * f2(sq, sq);
 }
 
 template <bool BF16, int VPT, bool GRAD>
-__global__ void __launch_bounds__(MAX_THREADS) distill_kernel(const Distill a)
+__global__ void __launch_bounds__(MAX_THREADS, 3) distill_kernel(const Distill a)
 {
-    __shared__ Part parts[MAX_PARTS];
+    __shared__ Part parts[MAX_CL * (MAX_THREADS / 32)];
     __shared__ Entries t;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Place at(a.cl);
+    const Place at(a.cl, blockDim.x);
     const int tid = threadIdx.x, step = blockDim.x, round = step * VPT;
     const long long n = at.row;
     const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(GRAD ? a.dx : nullptr, GRAD ? n * a.ldg : 0, a.V);
@@ -158,45 +245,28 @@ __global__ void __launch_bounds__(MAX_THREADS) distill_kernel(const Distill a)
     // the ids of the CTA's run; the first CTA reads every entry's logit for the loss
     const int lo = max(0, row.first_id(begin)), hi = min(a.V, row.first_id(end));
     Running<false> run;
+    float most = -INFINITY;
     int b = begin;
     do {
         tile.load(row, b + tid, step, end);
-        if (b == begin && tid < 32)
-            read_entries(a, n, row, at.rank ? lo : 0, at.rank ? hi : a.V, t);
-        run.add(tile, tile.max_of(), a.c);
+        if (b == begin && tid < 32) {
+            Reader<BF16> r;
+            r.load(a, n);
+            r.gather(a, row, at.rank ? lo : 0, at.rank ? hi : a.V);
+            r.finish(a, t);
+        }
+        const float m = tile.max_of();
+        most = max_nan(most, m);
+        run.add(tile, m, a.z);
         b += round;
     } while (b < end);
-    const Part part{run.m, warp_sum(run.S), 0.0f, 0u};
+    const Part part = run.part(most, a.z.c, 0u);
     at.wait();
     at.hand_out(parts, part);
     at.sync();
-    const Stats st = join(parts, at.parts(), a.c);
-    if (at.rank == 0 && tid < 32) {
-        float kl = 0.0f, most = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            const int k = tid + 32 * i;
-            if (t.q[k] != 0.0f) {
-                const float lp = st.empty() ? -INFINITY : (t.x[k] - st.m) / a.tau - st.lnS;
-                const float term = t.q[k] * (t.lnq[k] - lp);
-                kl += term;
-                most = max_nan(most, term);
-            }
-        }
-        kl = warp_sum(kl);
-        most = warp_max_nan(most);
-        if (kl == INFINITY && most < INFINITY)  // finite terms, rounded past the range
-            kl = FLT_MAX;
-        if (tid == 0) {
-            a.loss[n] = t.Q == 0.0f ? 0.0f : kl * (a.tau * a.tau) * w;
-            if (a.stats_out) {
-                a.stats_out[2 * n] = st.m;
-                a.stats_out[2 * n + 1] = st.lnS;
-            }
-            if ((st.bad() || t.Q != t.Q) && a.status)
-                atomicOr(a.status, KDA_ST_NAN);
-        }
-    }
+    const Stats st = join(parts, at.parts(), a.z.c);
+    if (at.rank == 0 && tid < 32)
+        write_loss(a, n, w, st, t);
     if (GRAD) {
         const bool zero = st.empty() || t.Q == 0.0f || scale == 0.0f;
         const float off = -st.lnS * LOG2E, m = st.m, sq = scale * t.Q;
@@ -204,15 +274,13 @@ __global__ void __launch_bounds__(MAX_THREADS) distill_kernel(const Distill a)
         do {
             if (round < end - begin && !zero)  // of several rounds the registers hold the last one alone
                 tile.load(row, b + tid, step, end);
-            store_tile(tile, row, out, b + tid, step, end, zero, [&](float p, float q) {
-                const float2 u = split(fma2(f2(p, q) + f2(-m, -m), f2(a.c, a.c), f2(off, off)));
-                return f2(ex2(u.x), ex2(u.y)) * f2(sq, sq);
-            });
+            store_tile(tile, row, out, b + tid, step, end, zero,
+                       [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); });
             b += round;
         } while (b < end);
         if (!zero) {
             __syncthreads();
-            take_off(a, t, out, lo, hi, m, off, scale);
+            take_off(a, t, out, lo, hi, m, off, scale, tid, step);
         }
     }
 }
@@ -235,19 +303,118 @@ __global__ void __launch_bounds__(256) distill_backward_kernel(const Distill a)
     Tile<BF16, VPT> tile;
     if (!zero) {  // the same for the whole CTA
         tile.load(row, first + tid, step, last);
-        if (tid < 32)
-            read_entries(a, n, row, lo, hi, t);
+        if (tid < 32) {
+            Reader<BF16> r;
+            r.load(a, n);
+            r.gather(a, row, lo, hi);
+            r.finish(a, t);
+        }
         __syncthreads();
         zero = t.Q == 0.0f;
     }
     const float sq = zero ? 0.0f : scale * t.Q;
-    store_tile(tile, row, out, first + tid, step, last, zero, [&](float p, float q) {
-        const float2 u = split(fma2(f2(p, q) + f2(-m, -m), f2(a.c, a.c), f2(off, off)));
-        return f2(ex2(u.x), ex2(u.y)) * f2(sq, sq);
-    });
+    store_tile(tile, row, out, first + tid, step, last, zero,
+               [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); });
     if (!zero) {
         __syncthreads();
-        take_off(a, t, out, lo, hi, m, off, scale);
+        take_off(a, t, out, lo, hi, m, off, scale, tid, step);
+    }
+}
+
+// For many long rows.  T threads pass their CTA's run of the row through shared memory; one
+// more warp reads the teacher's entries meanwhile and writes the loss.  With a gradient the
+// run stays in shared memory between the sum and the gradient where it fits (HELD); where
+// it does not, and without a gradient, it passes through a few slots, for the gradient once
+// more, out of L2.
+constexpr int LONG_T = 256, LONG_VT = 4, LONG_SLOTS = 3, LONG_GROUP = LONG_T * LONG_VT;
+
+template <bool BF16, bool GRAD, bool HELD>
+__global__ void __launch_bounds__(LONG_T + 32, 4) distill_long_kernel(const Distill a)
+{
+    extern __shared__ uint4 slots[];
+    __shared__ Part parts[MAX_CL * (LONG_T / 32)];
+    __shared__ Entries t;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Place at(a.cl, LONG_T);
+    const int tid = threadIdx.x;
+    const bool reader = tid >= LONG_T;
+    const long long n = at.row;
+    const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(GRAD ? a.dx : nullptr, GRAD ? n * a.ldg : 0, a.V);
+    using R = Run<BF16, LONG_T, LONG_VT>;
+    const R run(row, at, slots);
+    const float w = a.weight ? a.weight[n] : 1.0f, g = GRAD && a.g ? a.g[n] : 1.0f;
+    if (w == 0.0f) {  // a row that takes no part is not read
+        if (at.rank == 0 && tid == LONG_T) {
+            a.loss[n] = 0.0f;
+            if (a.stats_out)
+                a.stats_out[2 * n] = a.stats_out[2 * n + 1] = 0.0f;
+        }
+        if (GRAD && !reader)
+            for (int k = 0; k < run.groups; ++k)
+                run.put(typename R::TileT(), k, out, true, [](float, float) { return F2{0}; });
+        return;
+    }
+    at.arrive();
+    const float scale = GRAD ? w * a.tau * g : 0.0f;
+    const int lo = max(0, row.first_id(run.begin)), hi = min(a.V, row.first_id(run.end));
+    if (reader) {
+        Reader<BF16> r;
+        r.load(a, n);
+        // the first CTA reads every entry's logit for the loss
+        r.gather(a, row, at.rank ? lo : 0, at.rank ? hi : a.V);
+        r.finish(a, t);
+        at.wait();
+    } else {
+        Running<false> sums;
+        float most = -INFINITY;
+        auto add = [&](const typename R::TileT &x) {
+            const float m = x.max_of();
+            most = max_nan(most, m);
+            sums.add(x, m, a.z);
+        };
+        if (HELD) {
+            for (int k = 0; k < run.groups; ++k)
+                run.start(k, k);
+            for (int k = 0; k < run.groups; ++k) {
+                typename R::TileT x;
+                copies_done(min(3, run.groups - 1 - k));
+                run.get(x, k, k);
+                add(x);
+            }
+        } else {
+            run.template each<LONG_SLOTS>([&](const typename R::TileT &x, int) { add(x); });
+        }
+        const Part part = sums.part(most, a.z.c, 0u);
+        at.wait();
+        at.hand_out(parts, part);
+    }
+    at.sync();
+    if (!GRAD && !reader)
+        return;
+    const Stats st = join(parts, at.parts(), a.z.c);
+    const bool zero = st.empty() || t.Q == 0.0f || scale == 0.0f;
+    const float off = -st.lnS * LOG2E, m = st.m, sq = scale * t.Q;
+    if (reader) {
+        if (at.rank == 0)
+            write_loss(a, n, w, st, t);
+    } else {
+        auto value = [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); };
+        if (HELD) {
+            for (int k = 0; k < run.groups; ++k) {
+                typename R::TileT x;
+                run.get(x, k, k);
+                run.put(x, k, out, zero, value);
+            }
+        } else {
+            run.template each<LONG_SLOTS>(
+                [&](const typename R::TileT &x, int k) { run.put(x, k, out, zero, value); });
+        }
+    }
+    if (GRAD) {
+        __syncthreads();
+        if (!zero)
+            take_off(a, t, out, lo, hi, m, off, scale, tid, LONG_T + 32);
     }
 }
 
@@ -269,32 +436,65 @@ int check_teacher(const kda_teacher *t, int N)
     return KDA_OK;
 }
 
+// Many rows, each of more than a tile a thread.
+bool is_long(long long N, long long nvec) { return N > 152 && nvec > MAX_THREADS * MAX_VPT / 2; }
+
+template <bool BF16, bool GRAD, bool HELD>
+int launch_long(const Distill &a, size_t smem, cudaStream_t stream)
+{
+    auto *kernel = distill_long_kernel<BF16, GRAD, HELD>;
+    if (int rc = allow_shared(kernel, smem))
+        return rc;
+    return launch_rows(kernel, a, a.N * a.cl, LONG_T + 32, a.cl, smem, stream, "distill_long_kernel");
+}
+
+template <bool BF16, bool GRAD>
+int launch_long(Distill a, long long nvec, cudaStream_t stream)
+{
+    constexpr size_t group = static_cast<size_t>(LONG_GROUP) * 16;
+    a.cl = 1;
+    if (GRAD) {
+        constexpr long long HELD_GROUPS = 65536 / group;  // three CTAs an SM
+        while (a.cl < MAX_CL && nvec > a.cl * HELD_GROUPS * LONG_GROUP)
+            a.cl *= 2;
+        const long long groups = ((nvec + a.cl - 1) / a.cl + LONG_GROUP - 1) / LONG_GROUP;
+        if (groups * group <= 200 * 1024)
+            return launch_long<BF16, true, true>(a, groups * group, stream);
+        a.cl = 1;
+    }
+    return launch_long<BF16, GRAD, false>(a, LONG_SLOTS * group, stream);
+}
+
 template <bool GRAD>
-int launch(Distill a, int dtype, int N, cudaStream_t stream)
+int launch(Distill a, int dtype, cudaStream_t stream)
 {
     const bool bf16 = dtype == KDA_BF16;
-    const Shape sh = shape_of(N, vectors_of(a.x, a.V, a.ld, bf16));
+    const long long nvec = vectors_of(a.x, a.V, a.ld, bf16);
+    if (is_long(a.N, nvec))
+        return bf16 ? launch_long<true, GRAD>(a, nvec, stream) : launch_long<false, GRAD>(a, nvec, stream);
+    const Shape sh = shape_of(a.N, nvec);
     a.cl = sh.cl;
     return with_vpt(sh.vpt, [&](auto vpt) {
         constexpr int VPT = decltype(vpt)::value;
         return launch_rows(bf16 ? distill_kernel<true, VPT, GRAD> : distill_kernel<false, VPT, GRAD>, a,
-                           static_cast<long long>(N) * sh.cl, sh.threads, sh.cl, stream, "distill_kernel");
+                           a.N * sh.cl, sh.threads, sh.cl, 0, stream, "distill_kernel");
     });
 }
 
-int launch_backward(Distill a, int dtype, int N, cudaStream_t stream)
+int launch_backward(Distill a, int dtype, cudaStream_t stream)
 {
     const bool bf16 = dtype == KDA_BF16;
-    const Chunks ch = chunks_of(vectors_of(a.x, a.V, a.ld, bf16));
+    const long long nvec = vectors_of(a.x, a.V, a.ld, bf16);
+    const Chunks ch = chunks_of(nvec);
     a.cl = ch.chunks;
     return with_vpt(ch.vpt, [&](auto vpt) {
         constexpr int VPT = decltype(vpt)::value;
         return launch_rows(bf16 ? distill_backward_kernel<true, VPT> : distill_backward_kernel<false, VPT>, a,
-                           static_cast<long long>(N) * ch.chunks, ch.threads, 1, stream, "distill_backward_kernel");
+                           a.N * ch.chunks, ch.threads, 1, 0, stream, "distill_backward_kernel");
     });
 }
 
-Distill params(const void *x, void *dx, long long ld, long long ldg, int V, const kda_teacher &t, float tau,
+Distill params(const void *x, void *dx, long long ld, long long ldg, int N, int V, const kda_teacher &t, float tau,
                const float *g, const float *stats_in, float *loss, float *stats_out, int *status)
 {
     Distill a{};
@@ -302,6 +502,7 @@ Distill params(const void *x, void *dx, long long ld, long long ldg, int V, cons
     a.dx = dx;
     a.ld = ld;
     a.ldg = ldg;
+    a.N = N;
     a.V = V;
     a.K = t.K;
     a.ids = t.ids;
@@ -312,7 +513,7 @@ Distill params(const void *x, void *dx, long long ld, long long ldg, int V, cons
     a.g = g;
     a.stats_in = stats_in;
     a.tau = tau;
-    a.c = LOG2E / tau;
+    a.z = Scale{LOG2E / tau, 16.0f * LN2 * tau};
     a.loss = loss;
     a.stats_out = stats_out;
     a.status = status;
@@ -338,8 +539,8 @@ extern "C" int spec_distill(const void *logits, int logit_dtype, int N, int V, l
         return fail(KDA_EINVAL, "loss must not be NULL");
     if (!aligned4(loss) || !aligned4(stats) || !aligned4(dev_status))
         return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
-    return launch<false>(params(logits, nullptr, ld, 0, V, *teacher, temperature, nullptr, nullptr, loss, stats,
-                                      dev_status), logit_dtype, N, stream);
+    return launch<false>(params(logits, nullptr, ld, 0, N, V, *teacher, temperature, nullptr, nullptr, loss, stats,
+                                      dev_status), logit_dtype, stream);
 }
 
 extern "C" int spec_distill_backward(const void *logits, int logit_dtype, int N, int V, long long ld,
@@ -359,8 +560,8 @@ extern "C" int spec_distill_backward(const void *logits, int logit_dtype, int N,
         return fail(KDA_EINVAL, "stats must not be NULL");
     if (!aligned4(stats) || !aligned4(grad_loss) || !aligned4(dev_status))
         return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
-    return launch_backward(params(logits, dlogits, ld, ldg, V, *teacher, temperature, grad_loss, stats, nullptr,
-                                      nullptr, dev_status), logit_dtype, N, stream);
+    return launch_backward(params(logits, dlogits, ld, ldg, N, V, *teacher, temperature, grad_loss, stats, nullptr,
+                                      nullptr, dev_status), logit_dtype, stream);
 }
 
 extern "C" int spec_distill_step(const void *logits, int logit_dtype, int N, int V, long long ld,
@@ -379,6 +580,6 @@ extern "C" int spec_distill_step(const void *logits, int logit_dtype, int N, int
         return fail(KDA_EINVAL, "loss must not be NULL");
     if (!aligned4(grad_loss) || !aligned4(loss) || !aligned4(stats) || !aligned4(dev_status))
         return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
-    return launch<true>(params(logits, dlogits, ld, ldg, V, *teacher, temperature, grad_loss, nullptr, loss, stats,
-                                     dev_status), logit_dtype, N, stream);
+    return launch<true>(params(logits, dlogits, ld, ldg, N, V, *teacher, temperature, grad_loss, nullptr, loss, stats,
+                                     dev_status), logit_dtype, stream);
 }

@@ -28,24 +28,30 @@ namespace {
 using namespace rows;
 using Key = unsigned long long;
 
-constexpr int LIST = 2048;  // candidates a row's list holds
+constexpr int LIST = 2048;         // candidates that a row's list holds
+constexpr int LONG_LIST = 512;     // (of the kernel for long rows)
 
 struct Score {
     const void *x;
-    long long ld;
+    long long ld, N;
     int V, K, cl;
     int r, w;  // the threshold is the w-th largest of the warps' r-th largest maxima
     const int *tokens;
-    float tau, c;  // c = log2(e) / tau
+    float tau;
+    Scale z;
     float *logprob, *entropy, *stats, *top_logprobs;
     int *top_ids, *status;
 };
 
-struct ScoreShared {
+constexpr int MAX_PARTS = MAX_CL * (MAX_THREADS / 32);
+
+// The list of a row's candidates and what finds its threshold.
+template <int CAP>
+struct Candidates {
     Part parts[MAX_PARTS];
     Key bound;
     int count;
-    __align__(16) Key list[LIST];
+    __align__(16) Key list[CAP];
 };
 
 // The w-th largest (from 1) of n values, by all threads of the CTA.
@@ -70,10 +76,11 @@ __device__ __forceinline__ T rank_of(Get get, int n, int w, Key *out)
     return static_cast<T>(*out);
 }
 
+template <int CAP>
 __device__ __forceinline__ void append(int *count, Key *list, Key key)
 {
     const int at = atomicAdd(count, 1);
-    if (at < LIST)
+    if (at < CAP)
         list[at] = key;
 }
 
@@ -96,8 +103,8 @@ __device__ __forceinline__ void each_key(const RowPtr<BF16> &row, int first, int
 // Second try at the list, for a row with many equal logits: the lanes' largest keys (value,
 // then place) of the row read again, and the threshold from those, which min(K, 32) lanes of
 // ceil(K / 32) warps reach.
-template <bool BF16>
-__device__ __noinline__ void list_by_key(int K, RowPtr<BF16> row, Place at, ScoreShared &sh)
+template <bool BF16, int CAP>
+__device__ __noinline__ void list_by_key(int K, RowPtr<BF16> row, Place at, Candidates<CAP> &sh)
 {
     const int first = at.begin(row.nvec) + threadIdx.x, end = at.end(row.nvec), lane = threadIdx.x & 31;
     Key best = 0;
@@ -117,15 +124,15 @@ __device__ __noinline__ void list_by_key(int K, RowPtr<BF16> row, Place at, Scor
     Key *list = at.in_cta(sh.list, 0);
     each_key(row, first, blockDim.x, end, [&](Key k) {
         if (k >= bound)
-            append(count, list, k);
+            append<CAP>(count, list, k);
     });
     at.sync();
 }
 
 // Last resort, by the first CTA alone: the alternatives one after the other, each the largest
 // key below the last one.
-template <bool BF16>
-__device__ __noinline__ void list_by_rounds(int K, RowPtr<BF16> row, ScoreShared &sh)
+template <bool BF16, int CAP>
+__device__ __noinline__ void list_by_rounds(int K, RowPtr<BF16> row, Candidates<CAP> &sh)
 {
     Key *best_of = reinterpret_cast<Key *>(sh.parts), last = ~0ull;
     int n = 0;
@@ -150,13 +157,58 @@ __device__ __noinline__ void list_by_rounds(int K, RowPtr<BF16> row, ScoreShared
     __syncthreads();
 }
 
-template <bool BF16, int VPT>
-__global__ void __launch_bounds__(MAX_THREADS) logprobs_kernel(const Score a)
+// The row's results that are not alternatives, by one thread.
+template <bool BF16>
+__device__ __forceinline__ void write_scores(const Score &a, long long n, const RowPtr<BF16> &row, const Stats &st)
 {
-    __shared__ ScoreShared sh;
+    float lp = 0.0f;
+    if (a.tokens) {
+        const int token = a.tokens[n];
+        if (token >= a.V && a.status)
+            atomicOr(a.status, KDA_ST_BADTOKEN);
+        if (token >= 0 && token < a.V)
+            lp = st.bad() ? NAN : st.empty() ? -INFINITY : (row.at(token) - st.m) / a.tau - st.lnS;
+    }
+    if (a.logprob)
+        a.logprob[n] = lp;
+    if (a.entropy)
+        a.entropy[n] = st.entropy;
+    if (a.stats) {
+        a.stats[2 * n] = st.m;
+        a.stats[2 * n + 1] = st.lnS;
+    }
+    if (st.bad() && a.status)
+        atomicOr(a.status, KDA_ST_NAN);
+}
+
+// The alternatives from the row's list, by all threads of a CTA.
+__device__ __forceinline__ void write_top(const Score &a, long long n, float m, float lnS, const Key *list, int found)
+{
+    const long long o = n * a.K;
+    for (int i = threadIdx.x; i < found; i += blockDim.x) {
+        const Key key = list[i];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < found; ++j)
+            place += list[j] > key;
+        if (place < a.K) {
+            a.top_ids[o + place] = key_id(key);
+            a.top_logprobs[o + place] = (from_ordered(static_cast<uint32_t>(key >> 32)) - m) / a.tau - lnS;
+        }
+    }
+    for (int k = found + threadIdx.x; k < a.K; k += blockDim.x) {
+        a.top_ids[o + k] = -1;
+        a.top_logprobs[o + k] = m != m ? NAN : -INFINITY;
+    }
+}
+
+template <bool BF16, int VPT>
+__global__ void __launch_bounds__(MAX_THREADS, 3) logprobs_kernel(const Score a)
+{
+    __shared__ Candidates<LIST> sh;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Place at(a.cl);
+    const Place at(a.cl, blockDim.x);
     const int tid = threadIdx.x;
     if (tid == 0)
         sh.count = 0;
@@ -171,43 +223,22 @@ __global__ void __launch_bounds__(MAX_THREADS) logprobs_kernel(const Score a)
         t.load(row, b + tid, step, end);
         const float m = t.max_of();
         most = max_nan(most, m);
-        run.add(t, m, a.c);
+        run.add(t, m, a.z);
         b += round;
     } while (b < end);
     const uint32_t mine = most > -INFINITY ? ordered(most) : 0u;
     const uint32_t named = a.K > 0 ? warp_rank<uint32_t>(mine, a.r - 1) : 0u;
-    const Part part{run.m, warp_sum(run.S), warp_sum(run.E), named};
+    const Part part = run.part(most, a.z.c, named);
     at.wait();
     at.hand_out(sh.parts, part);
     at.sync();
     const int n = at.parts();
-    const Stats st = join(sh.parts, n, a.c);
-    const bool bad = st.bad(), empty = st.empty();
-    const float none = bad ? NAN : -INFINITY;
-    if (at.rank == 0 && tid == 0) {
-        const long long o = at.row;
-        float lp = 0.0f;
-        if (a.tokens) {
-            const int token = a.tokens[o];
-            if (token >= a.V && a.status)
-                atomicOr(a.status, KDA_ST_BADTOKEN);
-            if (token >= 0 && token < a.V)
-                lp = bad || empty ? none : (row.at(token) - st.m) / a.tau - st.lnS;
-        }
-        if (a.logprob)
-            a.logprob[o] = lp;
-        if (a.entropy)
-            a.entropy[o] = st.entropy;
-        if (a.stats) {
-            a.stats[2 * o] = st.m;
-            a.stats[2 * o + 1] = st.lnS;
-        }
-        if (bad && a.status)
-            atomicOr(a.status, KDA_ST_NAN);
-    }
+    const Stats st = join(sh.parts, n, a.z.c);
+    if (at.rank == 0 && tid == 0)
+        write_scores(a, at.row, row, st);
     if (a.K == 0)
         return;
-    if (!bad && !empty) {
+    if (!st.bad() && !st.empty()) {
         const uint32_t bound =
             a.w <= n ? rank_of<uint32_t>([&](int i) { return sh.parts[i].key; }, n, a.w, &sh.bound) : 0u;
         if (mine && mine >= bound) {
@@ -223,9 +254,9 @@ __global__ void __launch_bounds__(MAX_THREADS) logprobs_kernel(const Score a)
                     int id = row.first_id(b + tid + j * step);
                     t.each_of(t.v[j], [&](float p, float q) {
                         if (p >= least && p > -INFINITY)
-                            append(count, list, key_of(p, id));
+                            append<LIST>(count, list, key_of(p, id));
                         if (q >= least && q > -INFINITY)
-                            append(count, list, key_of(q, id + 1));
+                            append<LIST>(count, list, key_of(q, id + 1));
                         id += 2;
                     });
                 }
@@ -245,24 +276,134 @@ __global__ void __launch_bounds__(MAX_THREADS) logprobs_kernel(const Score a)
             list_by_rounds(a.K, row, sh);
             found = sh.count;
         }
-        const long long o = at.row * a.K;
-        for (int i = tid; i < found; i += step) {
-            const Key key = sh.list[i];
-            int place = 0;
-            for (int j = 0; j < found; ++j)
-                place += sh.list[j] > key;
-            if (place < a.K) {
-                a.top_ids[o + place] = key_id(key);
-                a.top_logprobs[o + place] =
-                    (from_ordered(static_cast<uint32_t>(key >> 32)) - st.m) / a.tau - st.lnS;
-            }
-        }
-        for (int k = found + tid; k < a.K; k += step) {
-            a.top_ids[o + k] = -1;
-            a.top_logprobs[o + k] = none;
-        }
+        write_top(a, at.row, st.m, st.lnS, sh.list, found);
     }
     at.wait();
+}
+
+// For many long rows: one CTA a row, which passes through shared memory ahead of its use.  A
+// thread keeps the maxima of up to SPANS equal spans of its share of the row, half a group or
+// a multiple; the spans that reach the threshold are read again, through L2, to fill the list.
+constexpr int LONG_T = 256, LONG_VT = 4, LONG_SLOTS = 3, HALF = LONG_VT / 2;
+constexpr int LONG_WARPS = LONG_T / 32, SPANS = 16, WORK = 1024;
+
+struct LongShared {
+    Candidates<LONG_LIST> top;
+    float lnS;
+    int works;
+    uint16_t work[WORK];
+    float span[SPANS][LONG_T];
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(LONG_T, 4) logprobs_long_kernel(const Score a)
+{
+    extern __shared__ uint4 slots[];
+    __shared__ LongShared sh;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0)
+        sh.top.count = sh.works = 0;
+    const Place at(1, LONG_T);
+    const long long n = at.row;
+    const RowPtr<BF16> row(a.x, n * a.ld, a.V);
+    using R = Run<BF16, LONG_T, LONG_VT>;
+    const R run(row, at, slots);
+    const int each = (2 * run.groups + SPANS - 1) / SPANS;  // halves of a group in a span
+    Running<true> sums;
+    float most = -INFINITY, top = -INFINITY;
+    int span = 0, left = each;
+    auto half = [&](float m) {
+        top = max_nan(top, m);
+        if (--left == 0) {
+            sh.span[span++][tid] = top;  // read by this thread alone
+            most = max_nan(most, top);
+            top = -INFINITY;
+            left = each;
+        }
+    };
+    run.template each<LONG_SLOTS>([&](const typename R::TileT &t, int) {
+        const float m0 = t.template max_of<0, HALF>(), m1 = t.template max_of<HALF, LONG_VT>();
+        sums.add(t, max_nan(m0, m1), a.z);
+        half(m0);
+        half(m1);
+    });
+    if (left != each) {
+        sh.span[span++][tid] = top;
+        most = max_nan(most, top);
+    }
+    const uint32_t mine = most > -INFINITY ? ordered(most) : 0u;
+    const uint32_t named = a.K > 0 ? warp_rank<uint32_t>(mine, a.r - 1) : 0u;
+    const Part part = sums.part(most, a.z.c, named);
+    if (lane == 0)
+        sh.top.parts[warp] = part;
+    __syncthreads();
+    if (warp == LONG_WARPS - 1) {
+        const Stats st = join(sh.top.parts, LONG_WARPS, a.z.c);
+        if (lane == 0) {
+            write_scores(a, n, row, st);
+            sh.lnS = st.lnS;  // read by the others after the next barrier
+        }
+    }
+    if (a.K == 0)
+        return;
+    const Part mate = sh.top.parts[lane % LONG_WARPS];
+    const float m = warp_max_nan(mate.m);
+    const bool plain = m > -INFINITY && m < INFINITY;
+    float least = -INFINITY;
+    if (plain) {
+        const uint32_t bound = warp_rank<uint32_t, LONG_WARPS>(mate.key, a.w - 1);
+        if (bound)
+            least = from_ordered(bound);
+        if (mine && mine >= bound) {
+            for (int s = 0; s < span; ++s) {
+                const float v = sh.span[s][tid];
+                if (v >= least && v > -INFINITY) {
+                    const int i = atomicAdd(&sh.works, 1);
+                    if (i < WORK)
+                        sh.work[i] = static_cast<uint16_t>(s * LONG_T + tid);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    int found = 0;
+    if (plain) {
+        const int works = sh.works;
+        if (works <= WORK) {
+            // HALF threads a span, each with one vector of every half group
+            for (int i = tid / HALF; i < works; i += LONG_T / HALF) {
+                const int item = sh.work[i], first = item / LONG_T * each, owner = item % LONG_T;
+                for (int h = first; h < first + each; ++h) {
+                    const int vec = (h * HALF + tid % HALF) * LONG_T + owner;
+                    if (vec >= row.nvec)
+                        break;
+                    int id = row.first_id(vec);
+                    Tile<BF16, 1>::each_of(row.full(vec) ? row.load(vec) : row.load_edge(vec), [&](float p, float q) {
+                        if (max(p, q) >= least) {
+                            if (p >= least && p > -INFINITY)
+                                append<LONG_LIST>(&sh.top.count, sh.top.list, key_of(p, id));
+                            if (q >= least && q > -INFINITY)
+                                append<LONG_LIST>(&sh.top.count, sh.top.list, key_of(q, id + 1));
+                        }
+                        id += 2;
+                    });
+                }
+            }
+        }
+        __syncthreads();
+        found = works <= WORK ? sh.top.count : LONG_LIST + 1;
+        if (found > LONG_LIST) {
+            list_by_key(a.K, row, at, sh.top);
+            found = sh.top.count;
+            if (found > LONG_LIST) {
+                list_by_rounds(a.K, row, sh.top);
+                found = sh.top.count;
+            }
+        }
+    }
+    write_top(a, n, m < INFINITY ? m : NAN, sh.lnS, sh.top.list, found);
 }
 
 struct ScoreGrad {
@@ -320,6 +461,18 @@ __global__ void __launch_bounds__(256) logprobs_backward_kernel(const ScoreGrad 
     }
 }
 
+// Many rows, each of more than a tile a thread.
+bool is_long(long long N, long long nvec) { return N > 152 && nvec > MAX_THREADS * MAX_VPT / 2; }
+
+template <bool BF16>
+int launch_long(const Score &a, cudaStream_t stream)
+{
+    constexpr size_t smem = static_cast<size_t>(LONG_SLOTS) * LONG_VT * LONG_T * 16;
+    if (int rc = allow_shared(logprobs_long_kernel<BF16>, smem))
+        return rc;
+    return launch_rows(logprobs_long_kernel<BF16>, a, a.N, LONG_T, 1, smem, stream, "logprobs_long_kernel");
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -346,17 +499,27 @@ extern "C" int spec_logprobs(const void *logits, int logit_dtype, int N, int V, 
         if (!rows::aligned4(p))
             return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
     const bool bf16 = logit_dtype == KDA_BF16;
-    const Shape sh = rows::shape_of(N, rows::vectors_of(logits, V, ld, bf16));
+    const long long nvec = rows::vectors_of(logits, V, ld, bf16);
+    Score a{logits, ld, N, V, K, 1, 1, 1, tokens, temperature,
+            Scale{rows::LOG2E / temperature, 16.0f * rows::LN2 * temperature}, logprob, entropy, stats,
+            top_logprobs, top_ids, dev_status};
     // r lanes of w warps make the threshold: about two thirds of the warps, so that one warp of
     // small logits does not lower it
-    const int warps = sh.cl * sh.threads / 32;
-    const int r = std::max(1, std::min(32, (5 * K + 3 * warps - 1) / (3 * warps)));
-    Score a{logits, ld, V, K, sh.cl, r, (K + r - 1) / r, tokens, temperature, rows::LOG2E / temperature, logprob,
-            entropy, stats, top_logprobs, top_ids, dev_status};
+    auto threshold = [&](int warps) {
+        a.r = std::max(1, std::min(32, (5 * K + 3 * warps - 1) / (3 * warps)));
+        a.w = (K + a.r - 1) / a.r;
+    };
+    if (is_long(N, nvec)) {
+        threshold(LONG_WARPS);
+        return bf16 ? launch_long<true>(a, stream) : launch_long<false>(a, stream);
+    }
+    const Shape sh = rows::shape_of(N, nvec);
+    a.cl = sh.cl;
+    threshold(sh.cl * sh.threads / 32);
     return rows::with_vpt(sh.vpt, [&](auto vpt) {
         constexpr int VPT = decltype(vpt)::value;
         return rows::launch_rows(bf16 ? logprobs_kernel<true, VPT> : logprobs_kernel<false, VPT>, a,
-                                 static_cast<long long>(N) * sh.cl, sh.threads, sh.cl, stream, "logprobs_kernel");
+                                 static_cast<long long>(N) * sh.cl, sh.threads, sh.cl, 0, stream, "logprobs_kernel");
     });
 }
 
@@ -391,7 +554,7 @@ extern "C" int spec_logprobs_backward(const void *logits, int logit_dtype, int N
     return rows::with_vpt(ch.vpt, [&](auto vpt) {
         constexpr int VPT = decltype(vpt)::value;
         return rows::launch_rows(bf16 ? logprobs_backward_kernel<true, VPT> : logprobs_backward_kernel<false, VPT>, a,
-                                 static_cast<long long>(N) * ch.chunks, ch.threads, 1, stream,
+                                 static_cast<long long>(N) * ch.chunks, ch.threads, 1, 0, stream,
                                  "logprobs_backward_kernel");
     });
 }

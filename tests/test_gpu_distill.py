@@ -262,3 +262,116 @@ def test_scores_are_a_teacher():
     at = grad.gather(1, ids.long())
     p = top.exp()
     assert torch.allclose(at, 2.0 * p * (p.sum(1, keepdim=True) - 1), atol=1e-5)
+
+
+# ---------------------------------------------------------------------------
+# many long rows: the kernels whose CTAs stay and take row after row.  The 64-bit values are
+# formed for some of the rows.
+# ---------------------------------------------------------------------------
+def copy_of(t):
+    """The same values at the same place within a vector (whose sums are formed alike)."""
+    whole = torch.empty(0, dtype=t.dtype, device=t.device).set_(t.untyped_storage()).clone()
+    return whole.as_strided(t.shape, t.stride(), t.storage_offset())
+
+
+def check_some(x, ids, values, tau, dtype, weight, g, t=None, which=None):
+    N = x.shape[0]
+    rows = sorted({0, 1, N // 3, N // 2, N - 2, N - 1}) if which is None else which
+    w, gg = weight[rows], g[rows]
+    loss, stats, grad, P, D = ref.distill(x[rows], ids[rows], values[rows], tau, w, gg)
+    t = dev(x, dtype) if t is None else t
+    kw = {"weight": to_dev(weight), "temperature": tau}
+    i, v, gd = to_dev(ids), dev(values), to_dev(g)
+    size = np.abs(w) * tau * tau * 4e-5 + 1e-5 * np.abs(loss)
+    gtol = (np.abs(gg) * np.abs(w) * tau)[:, None] * (5e-5 * (P + D) + 1e-30)
+    if dtype == "bf16":
+        gtol = gtol + 2.0**-8 * np.abs(grad)
+    l1, z1 = kb.spec_distill(t, i, v, **kw)
+    same_or_near(l1[rows], loss, size, "loss")
+    same_or_near(z1[rows][:, 1], stats[:, 1], 1e-5 + 1e-6 * np.abs(stats[:, 1]), "ln S")
+    d1 = kb.spec_distill_backward(t, i, v, z1, grad_loss=gd, **kw)
+    same_or_near(d1[rows], grad, gtol, "gradient")
+    l2, z2, d2 = kb.spec_distill_step(t, i, v, grad_loss=gd, **kw)
+    same_or_near(l2[rows], loss, size, "loss of the step")
+    same_or_near(d2[rows], grad, gtol, "gradient of the step")
+    # every row: the step and the two calls agree, a row's gradient sums to g w tau (Q - Q) = 0
+    same = (l1 == l2) | (torch.isnan(l1) & torch.isnan(l2)) | ((l1 - l2).abs() <= 1e-6 + 1e-5 * l1.abs())
+    assert same.all()
+    a, b = d1.float(), d2.float()
+    assert ((a == b) | (torch.isnan(a) & torch.isnan(b)) | ((a - b).abs() <= 1e-7 + 0.01 * a.abs())).all()
+    u = copy_of(t)
+    kb.spec_distill_step(u, i, v, grad_loss=gd, dlogits=u, **kw)
+    assert torch.equal(u.view(torch.uint8), d2.view(torch.uint8)), "step in place"
+    u = copy_of(t)
+    kb.spec_distill_backward(u, i, v, z1, grad_loss=gd, dlogits=u, **kw)
+    assert torch.equal(u.view(torch.uint8), d1.view(torch.uint8)), "in place"
+    return l2, z2, d2
+
+
+def weights(N, seed):
+    rng = np.random.default_rng(seed)
+    w = (0.5 + rng.random(N)).astype(np.float32)
+    w[15::16] = 0
+    return w, rng.standard_normal(N).astype(np.float32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,K", [(153, 16384, 20), (160, 16391, 128), (500, 33000, 3), (1000, 16400, 64),
+                                   (200, 131072, 64), (170, 300007, 33), (155, 600011, 5)])
+def test_many_long_rows(N, V, K, dtype):
+    """Shares that stay in one CTA, in clusters of two, four and eight, with and without whole
+    vectors; every sixteenth row has no weight."""
+    x = ref.rows("peaked", N, V, dtype, N + K)
+    rng = np.random.default_rng(K)
+    ids = ((rng.integers(0, V, (N, 1)) + np.arange(K) * rng.integers(1, V // K, (N, 1))) % V).astype(np.int32)
+    values = (3 * rng.standard_normal((N, K))).astype(np.float32)
+    w, g = weights(N, K)
+    _, _, d = check_some(x, ids, values, 2.0, dtype, w, g)
+    assert (d[15::16] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_are_read_twice(dtype):
+    """Shares beyond what eight CTAs hold between the sum and the gradient."""
+    N, V, K = 153, 1600011 // (2 if dtype == "f32" else 1), 16
+    x = np.tile(ref.rows("peaked", 3, V, dtype, 1), (N // 3, 1))
+    rng = np.random.default_rng(K)
+    ids = rng.integers(0, V, (N, K)).astype(np.int32)
+    values = (3 * rng.standard_normal((N, K))).astype(np.float32)
+    w, g = weights(N, K)
+    check_some(x, ids, values, 1.0, dtype, w, g, which=[0, 77, 152])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", [k for k in ref.KINDS if k not in ("huge", "normal")])
+def test_many_long_rows_of_kinds(kind, dtype):
+    N, V, K = 180, 16391, 12
+    x = ref.rows(kind, N, V, dtype, 7)
+    for n in (1, 90, 179):  # beside rows of another kind
+        x[n] = ref.rows("normal", 1, V, dtype, n)[0]
+    ids, values = entries(N, V, K, 9)
+    ids[60], values[90] = -1, -np.inf  # rows without entries
+    check_some(x, ids, values, 1.0, dtype, *weights(N, 3))
+
+
+def test_many_long_rows_with_bad_rows_and_strides():
+    N, V, ld, off = 200, 16385, 16411, 3
+    x = ref.rows("normal", N, V, "bf16", 7)
+    x[1, V - 1] = np.nan
+    x[15] = np.nan  # of weight 0
+    x[N // 3, 0] = np.inf
+    buf = torch.full((off + N * ld,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    t = buf[off:].view(N, ld)[:, :V]
+    t.copy_(dev(x, "bf16"))
+    ids, values = entries(N, V, 9, 5, "repeated")
+    w, g = weights(N, 3)
+    loss, _, d = check_some(x, ids, values, 1.0, "bf16", w, g, t=t)
+    bad = torch.isnan(loss).nonzero()[:, 0].tolist()
+    assert bad == [1, N // 3] and (d[15] == 0).all()
+    dst = torch.full((7 + N * ld + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = dst[7:7 + N * ld].view(N, ld)[:, :V]
+    kb.spec_distill_step(t, to_dev(ids), to_dev(values), weight=to_dev(w), grad_loss=to_dev(g), dlogits=out)
+    assert torch.equal(torch.nan_to_num(out.float(), 5.0), torch.nan_to_num(d.float(), 5.0))
+    rest = torch.ones_like(dst, dtype=torch.bool)
+    rest[7:7 + N * ld].view(N, ld)[:, :V] = False
+    assert (dst[rest] == 7).all(), "written outside its rows"

@@ -304,3 +304,72 @@ def test_backward_against_differences():
     got = kb.spec_logprobs_backward(one, t[:1], stats, H0, torch.tensor([a], device="cuda"),
                                     torch.tensor([b], device="cuda"))
     assert np.abs(got.double().cpu().numpy()[0] - diff).max() < 2.5e-3
+
+
+# ---------------------------------------------------------------------------
+# many long rows: the kernels whose CTAs stay and take row after row.  The 64-bit values are
+# formed for some of the rows.
+# ---------------------------------------------------------------------------
+def some(N):
+    return sorted({0, 1, N // 3, N // 2, N - 2, N - 1})
+
+
+def check_some(x, tokens, K, tau, dtype, t=None):
+    t = dev(x, dtype) if t is None else t
+    rows = some(x.shape[0])
+    out = kb.spec_logprobs(t, to_dev(np.asarray(tokens, np.int32)), K, tau)
+    lp, H, stats, ids, top = (o[rows] for o in out)
+    want = ref.score(x[rows], np.asarray(tokens)[rows], K, tau)
+    assert np.array_equal(ids.cpu().numpy(), want[3])
+    near(lp, want[0], 1e-5, 4 * 2.0**-24, "logprob")
+    near(H, want[1], 2e-5, 1e-6, "entropy")
+    near(stats[:, 1], want[2][:, 1], 1e-5, 4 * 2.0**-24, "ln S")
+    near(top, want[4], 1e-5, 4 * 2.0**-24, "top_logprobs")
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,K", [(153, 16384, 20), (160, 16391, 128), (1300, 8192, 1), (3000, 8193, 7),
+                                   (700, 40001, 0), (200, 131072, 64), (170, 300007, 33)])
+def test_many_long_rows(N, V, K, dtype):
+    x = ref.rows("peaked", N, V, dtype, N + K)
+    check_some(x, tokens_for(N, V, 3), K, 0.7, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", [k for k in ref.KINDS if k != "normal"])
+def test_many_long_rows_of_kinds(kind, dtype):
+    x = ref.rows(kind, 180, 16391, dtype, 7)
+    for n in (1, 90, 179):  # beside rows of another kind
+        x[n] = ref.rows("normal", 1, 16391, dtype, n)[0]
+    check_some(x, tokens_for(180, 16391, 4), 50, 1.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_long_rows_with_bad_rows_and_strides(dtype):
+    N, V, ld, off = 200, 16385, 16411, 3
+    buf = torch.full((off + N * ld,), float("nan"), dtype=DT[dtype], device="cuda")
+    t = buf[off:].view(N, ld)[:, :V]
+    x = ref.rows("some_masked", N, V, dtype, 7)
+    x[N // 3, V - 1] = np.nan
+    x[1, 0] = np.inf
+    t.copy_(dev(x, dtype))
+    out = check_some(x, tokens_for(N, V, 4), 5, 1.0, dtype, t=t)
+    bad = torch.isnan(out[0]).nonzero()[:, 0].tolist()
+    assert bad == [1, N // 3]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_long_rows_give_what_few_give(dtype):
+    """The kernel that is chosen for the number of rows changes no alternative and no more than
+    the last places of the sums."""
+    x = ref.rows("normal", 400, 20011, dtype, 7)
+    t, tok = dev(x, dtype), to_dev(tokens_for(400, 20011, 4).astype(np.int32))
+    many = kb.spec_logprobs(t, tok, 30)
+    few = kb.spec_logprobs(t[100:110], tok[100:110], 30)
+    assert torch.equal(many[3][100:110], few[3])
+    for a, b in zip(many, few):
+        assert torch.allclose(a[100:110].float(), b.float(), atol=2e-6, rtol=1e-6)
+    again = kb.spec_logprobs(t, tok, 30)
+    for a, b in zip(many, again):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
