@@ -615,11 +615,13 @@ struct Run {
     uint4 *slots;        // this thread's: slot s, vector v at [s GROUP + v T]
 
     __device__ __forceinline__ Run(const RowPtr<BF16> &row_, const Place &at, uint4 *shared)
-        : row(row_), slots(shared + threadIdx.x)
+        : Run(row_, at.begin(row_.nvec), at.end(row_.nvec), shared)
     {
-        begin = at.begin(row.nvec);
-        end = at.end(row.nvec);
-        groups = max(1, (at.per(row.nvec) + GROUP - 1) / GROUP);
+    }
+    __device__ __forceinline__ Run(const RowPtr<BF16> &row_, int begin_, int end_, uint4 *shared)
+        : row(row_), begin(begin_), end(end_), slots(shared + threadIdx.x)
+    {
+        groups = max(1, (end - begin + GROUP - 1) / GROUP);
         whole0 = begin < row.full0;
         whole1 = max(0, min(row.full1, end) - begin) / GROUP;
     }
@@ -745,19 +747,34 @@ inline Shape shape_of(long long N, long long nvec)
     return Shape{threads, vpt, cl};
 }
 
-// The same for a pass that needs nothing of the rest of the row: CTAs of a row.
-struct Chunks {
-    int threads, vpt, chunks;
+// A pass that needs nothing of the rest of a row: CTAs of T threads, each with a run of up to
+// RUN_GROUPS groups of PIECE_VT vectors a thread, which pass through PIECE_SLOTS slots.
+constexpr int PIECE_VT = 4, PIECE_SLOTS = 3;
+
+struct Pieces {
+    int threads, per, runs;  // per: vectors of a run
+    size_t shared;
 };
 
-inline Chunks chunks_of(long long nvec)
+inline Pieces pieces_of(long long nvec)
 {
-    int threads = 32, vpt = 1;
-    while (threads < 256 && nvec > threads)
-        threads *= 2;
-    while (vpt < 4 && nvec > static_cast<long long>(threads) * vpt)
-        vpt *= 2;
-    return Chunks{threads, vpt, static_cast<int>((nvec + threads * vpt - 1) / (threads * vpt))};
+    constexpr int RUN_GROUPS = 4;
+    const int threads = nvec <= 32 * PIECE_VT ? 32 : nvec <= 128 * PIECE_VT ? 128 : 256;
+    const int group = threads * PIECE_VT, per = group * RUN_GROUPS;
+    const long long groups = (nvec + group - 1) / group;
+    return Pieces{threads, per, static_cast<int>((nvec + per - 1) / per),
+                  static_cast<size_t>(groups < PIECE_SLOTS ? groups : PIECE_SLOTS) * group * 16};
+}
+
+// f with the threads of a CTA as a constant.
+template <class F>
+inline int with_threads(int threads, F f)
+{
+    switch (threads) {
+    case 32: return f(std::integral_constant<int, 32>());
+    case 128: return f(std::integral_constant<int, 128>());
+    default: return f(std::integral_constant<int, 256>());
+    }
 }
 
 // f with the vectors of a thread as a constant.

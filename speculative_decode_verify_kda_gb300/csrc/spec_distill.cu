@@ -13,8 +13,6 @@
 // between the sum and the gradient, so loss and gradient together read the logits once.
 // The gradient is written as g w tau Q p for every element; after that, the CTA that
 // holds a teacher's entry writes that element again with its q taken off.
-// distill_backward_kernel: the gradient alone, from the saved statistics, in one pass
-// without any exchange.
 #include <algorithm>
 #include <cfloat>
 
@@ -30,7 +28,8 @@ struct Distill {
     void *dx;
     long long ld, ldg, N;
     int V, K;
-    int cl;  // CTAs of a row (the backward pass alone: runs of a row)
+    int cl;         // CTAs of a row
+    int per, runs;  // the gradient alone: vectors of a run, runs of a row
     const int *ids;
     const void *values;
     int value_bf16, value_logprobs;
@@ -285,42 +284,6 @@ __global__ void __launch_bounds__(MAX_THREADS, 3) distill_kernel(const Distill a
     }
 }
 
-template <bool BF16, int VPT>
-__global__ void __launch_bounds__(256) distill_backward_kernel(const Distill a)
-{
-    __shared__ Entries t;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long n = blockIdx.x / a.cl;
-    const int chunk = blockIdx.x % a.cl, tid = threadIdx.x, step = blockDim.x;
-    const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(a.dx, n * a.ldg, a.V);
-    const int first = chunk * step * VPT, last = min(row.nvec, first + step * VPT);
-    const int lo = max(0, row.first_id(first)), hi = min(a.V, row.first_id(last));
-    const float w = a.weight ? a.weight[n] : 1.0f;
-    const float scale = w == 0.0f ? 0.0f : w * a.tau * (a.g ? a.g[n] : 1.0f);
-    const float m = a.stats_in[2 * n], off = -a.stats_in[2 * n + 1] * LOG2E;
-    bool zero = m == -INFINITY || scale == 0.0f;
-    Tile<BF16, VPT> tile;
-    if (!zero) {  // the same for the whole CTA
-        tile.load(row, first + tid, step, last);
-        if (tid < 32) {
-            Reader<BF16> r;
-            r.load(a, n);
-            r.gather(a, row, lo, hi);
-            r.finish(a, t);
-        }
-        __syncthreads();
-        zero = t.Q == 0.0f;
-    }
-    const float sq = zero ? 0.0f : scale * t.Q;
-    store_tile(tile, row, out, first + tid, step, last, zero,
-               [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); });
-    if (!zero) {
-        __syncthreads();
-        take_off(a, t, out, lo, hi, m, off, scale, tid, step);
-    }
-}
-
 // For many long rows.  T threads pass their CTA's run of the row through shared memory; one
 // more warp reads the teacher's entries meanwhile and writes the loss.  With a gradient the
 // run stays in shared memory between the sum and the gradient where it fits (HELD); where
@@ -418,6 +381,55 @@ __global__ void __launch_bounds__(LONG_T + 32, 4) distill_long_kernel(const Dist
     }
 }
 
+// The gradient alone.  A row is cut into runs that need nothing of one another; a run passes
+// through shared memory while one more warp reads the entries.
+template <bool BF16, int T>
+__global__ void __launch_bounds__(T + 32) distill_backward_kernel(const Distill a)
+{
+    extern __shared__ uint4 slots[];
+    __shared__ Entries t;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long n = blockIdx.x / a.runs;
+    const int begin = static_cast<int>(blockIdx.x % a.runs) * a.per, tid = threadIdx.x;
+    const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(a.dx, n * a.ldg, a.V);
+    using R = Run<BF16, T, PIECE_VT>;
+    const R run(row, begin, min(row.nvec, begin + a.per), slots);
+    const int lo = max(0, row.first_id(run.begin)), hi = min(a.V, row.first_id(run.end));
+    const float w = a.weight ? a.weight[n] : 1.0f, g = a.g ? a.g[n] : 1.0f;
+    const float m = a.stats_in[2 * n], off = -a.stats_in[2 * n + 1] * LOG2E;
+    const float scale = w == 0.0f ? 0.0f : w * a.tau * g;
+    const bool out_of_it = m == -INFINITY || scale == 0.0f;  // the row is not read
+    auto meet = [] { asm volatile("barrier.sync 1, %0;" ::"n"(T + 32) : "memory"); };
+    if (tid >= T) {
+        if (out_of_it)
+            return;
+        Reader<BF16> r;
+        r.load(a, n);
+        r.gather(a, row, lo, hi);
+        r.finish(a, t);
+        meet();  // the entries are there, and the logits at them have been read
+    } else if (out_of_it) {
+        for (int k = 0; k < run.groups; ++k)
+            run.put(typename R::TileT(), k, out, true, [](float, float) { return F2{0}; });
+        return;
+    } else {
+        float sq = 0.0f;
+        bool zero = false;
+        run.template each<PIECE_SLOTS>([&](const typename R::TileT &x, int k) {
+            if (k == 0) {
+                meet();
+                zero = t.Q == 0.0f;
+                sq = scale * t.Q;
+            }
+            run.put(x, k, out, zero, [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); });
+        });
+    }
+    meet();  // the gradient is written, the corrections come over it
+    if (t.Q != 0.0f)
+        take_off(a, t, out, lo, hi, m, off, scale, tid, T + 32);
+}
+
 int check_teacher(const kda_teacher *t, int N)
 {
     if (!t)
@@ -485,12 +497,15 @@ int launch_backward(Distill a, int dtype, cudaStream_t stream)
 {
     const bool bf16 = dtype == KDA_BF16;
     const long long nvec = vectors_of(a.x, a.V, a.ld, bf16);
-    const Chunks ch = chunks_of(nvec);
-    a.cl = ch.chunks;
-    return with_vpt(ch.vpt, [&](auto vpt) {
-        constexpr int VPT = decltype(vpt)::value;
-        return launch_rows(bf16 ? distill_backward_kernel<true, VPT> : distill_backward_kernel<false, VPT>, a,
-                           a.N * ch.chunks, ch.threads, 1, 0, stream, "distill_backward_kernel");
+    const Pieces cut = pieces_of(nvec);
+    a.per = cut.per;
+    a.runs = cut.runs;
+    return with_threads(cut.threads, [&](auto threads) {
+        constexpr int T = decltype(threads)::value;
+        auto *kernel = bf16 ? distill_backward_kernel<true, T> : distill_backward_kernel<false, T>;
+        if (int rc = allow_shared(kernel, cut.shared))
+            return rc;
+        return launch_rows(kernel, a, a.N * cut.runs, T + 32, 1, cut.shared, stream, "distill_backward_kernel");
     });
 }
 

@@ -410,50 +410,54 @@ struct ScoreGrad {
     const void *x;
     void *dx;
     long long ld, ldg;
-    int V, chunks;
+    int V, per, runs;  // vectors of a run, runs of a row
     const int *tokens;
     const float *stats, *entropy, *g, *h;
     float tau, c;
 };
 
-// One CTA a run of a row's vectors, one tile a thread: read, weighted, written.  With
+// A row is cut into runs that need nothing of one another: read, weighted, written.  With
 // u = (x - m) c - s log2(e), p = 2^u and
 //   d x_i = p (A + B u) + [i = t] g / tau,  A = -(g + h H) / tau, B = -h ln 2 / tau.
-template <bool BF16, int VPT>
-__global__ void __launch_bounds__(256) logprobs_backward_kernel(const ScoreGrad a)
+template <bool BF16, int T>
+__global__ void __launch_bounds__(T) logprobs_backward_kernel(const ScoreGrad a)
 {
+    extern __shared__ uint4 slots[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long n = blockIdx.x / a.chunks;
-    const int chunk = blockIdx.x % a.chunks, tid = threadIdx.x, step = blockDim.x;
+    const long long n = blockIdx.x / a.runs;
+    const int begin = static_cast<int>(blockIdx.x % a.runs) * a.per, tid = threadIdx.x;
     const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(a.dx, n * a.ldg, a.V);
-    const int first = chunk * step * VPT, last = min(row.nvec, first + step * VPT);
+    using R = Run<BF16, T, PIECE_VT>;
+    const R run(row, begin, min(row.nvec, begin + a.per), slots);
     const int t = a.tokens ? a.tokens[n] : -1;
     const bool has = t >= 0 && t < a.V;
     const float g = a.g && has ? a.g[n] : 0.0f, h = a.h ? a.h[n] : 0.0f;
-    const float m = a.stats[2 * n], lnS = a.stats[2 * n + 1];
-    const bool zero = m == -INFINITY || (g == 0.0f && h == 0.0f);
+    const float m = a.stats[2 * n], off = -a.stats[2 * n + 1] * LOG2E;
+    if (m == -INFINITY || (g == 0.0f && h == 0.0f)) {
+        for (int k = 0; k < run.groups; ++k)
+            run.put(typename R::TileT(), k, out, true, [](float, float) { return F2{0}; });
+        return;
+    }
     const float A = -(g + (h != 0.0f ? h * a.entropy[n] : 0.0f)) / a.tau, B = -h * LN2 / a.tau;
-    const float off = -lnS * LOG2E;
-    Tile<BF16, VPT> x;
-    if (!zero)
-        x.load(row, first + tid, step, last);
+    const int at = (row.skip + t) / row.PER;
+    const bool mine = has && at >= run.begin && at < run.end;  // the same for the whole CTA
     float at_token = 0.0f;
-    const bool mine = has && !zero && (row.skip + t) / row.PER >= first && (row.skip + t) / row.PER < last;
-    if (mine) {  // the same for the whole CTA
+    if (mine) {
         if (tid == 0) {
             const float u = fmaf(row.at(t) - m, a.c, off);
             at_token = ex2(u) * fmaf(B, fmaxf(u, -1e4f), A) + g / a.tau;
         }
         __syncthreads();  // the token's logit is read before its gradient may replace it
     }
-    auto weigh = [&](float p, float q) {
-        const F2 u = fma2(f2(p, q) + f2(-m, -m), f2(a.c, a.c), f2(off, off));
-        const float2 v = split(u);
-        const F2 low = f2(fmaxf(v.x, -1e4f), fmaxf(v.y, -1e4f));
-        return f2(ex2(v.x), ex2(v.y)) * fma2(f2(B, B), low, f2(A, A));
-    };
-    store_tile(x, row, out, first + tid, step, last, zero, weigh);
+    const F2 neg = f2(-m, -m), cc = f2(a.c, a.c), oo = f2(off, off), AA = f2(A, A), BB = f2(B, B);
+    run.template each<PIECE_SLOTS>([&](const typename R::TileT &x, int k) {
+        run.put(x, k, out, false, [&](float p, float q) {
+            const float2 v = split(fma2(f2(p, q) + neg, cc, oo));
+            const F2 w = f2(ex2(v.x), ex2(v.y));
+            return w * fma2(BB, f2(fmaxf(v.x, -1e4f), fmaxf(v.y, -1e4f)), AA);
+        });
+    });
     if (mine) {
         __syncthreads();  // after the element's ordinary value
         if (tid == 0)
@@ -548,13 +552,15 @@ extern "C" int spec_logprobs_backward(const void *logits, int logit_dtype, int N
         if (!rows::aligned4(p))
             return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
     const bool bf16 = logit_dtype == KDA_BF16;
-    const rows::Chunks ch = rows::chunks_of(rows::vectors_of(logits, V, ld, bf16));
-    ScoreGrad a{logits, dlogits, ld, ldg, V, ch.chunks, tokens, stats, entropy, grad_logprob, grad_entropy,
-                temperature, rows::LOG2E / temperature};
-    return rows::with_vpt(ch.vpt, [&](auto vpt) {
-        constexpr int VPT = decltype(vpt)::value;
-        return rows::launch_rows(bf16 ? logprobs_backward_kernel<true, VPT> : logprobs_backward_kernel<false, VPT>, a,
-                                 static_cast<long long>(N) * ch.chunks, ch.threads, 1, 0, stream,
+    const rows::Pieces cut = rows::pieces_of(rows::vectors_of(logits, V, ld, bf16));
+    const ScoreGrad a{logits, dlogits, ld, ldg, V, cut.per, cut.runs, tokens, stats, entropy, grad_logprob,
+                      grad_entropy, temperature, rows::LOG2E / temperature};
+    return rows::with_threads(cut.threads, [&](auto threads) {
+        constexpr int T = decltype(threads)::value;
+        auto *kernel = bf16 ? logprobs_backward_kernel<true, T> : logprobs_backward_kernel<false, T>;
+        if (int rc = rows::allow_shared(kernel, cut.shared))
+            return rc;
+        return rows::launch_rows(kernel, a, static_cast<long long>(N) * cut.runs, T, 1, cut.shared, stream,
                                  "logprobs_backward_kernel");
     });
 }
