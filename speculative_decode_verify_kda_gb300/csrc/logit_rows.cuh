@@ -2,12 +2,8 @@
 // spec_distill.cu).
 //
 // A row is read in 16-byte vectors and belongs to one CTA or to a cluster of CTAs, each
-// of which takes a run of the row's vectors.
-//
-// Few rows, or short ones: a thread holds VPT vectors in registers (a tile), and what comes
-// after the row's sum (the gradient, the alternatives) works on those.  Longer runs take
-// more rounds of tiles and are read again.
-// Many long rows: the vectors pass through shared memory ahead of their use (Run).
+// of which takes a run of the row's vectors.  They pass through shared memory ahead of their
+// use (Run); a thread works on a few of them at a time, in registers (Tile).
 //
 // The sums are taken relative to the warp's own maximum, and a warp's triple (maximum, sum
 // of weights, weighted sum of exponents) joins the others' once, through the shared memory
@@ -30,9 +26,8 @@ namespace rows {
 
 namespace cg = cooperative_groups;
 
+constexpr int SMS = 152;           // of a GB300
 constexpr int MAX_CL = 8;          // CTAs of a cluster (the portable size)
-constexpr int MAX_THREADS = 256;   // of a CTA that holds its run in registers
-constexpr int MAX_VPT = 8;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 template <bool BF16>
@@ -307,29 +302,38 @@ struct Tile {
                 v[j] = u;
     }
 
-    // f(pair of neighbouring elements) for every pair; RAISE: elements below -1e30 as -1e30.
-    template <bool RAISE = false, class F>
+    // f(pair of neighbouring elements) for every pair; with a floor: elements below it raised.
+    template <class F>
     __device__ __forceinline__ void each(F f) const
     {
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
-            each_of<RAISE>(v[j], f);
+            each_of(v[j], f);
     }
-    template <bool RAISE = false, class F>
+    template <class F>
+    __device__ __forceinline__ void each_above(uint32_t floor, F f) const
+    {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (BF16)
+                    asm("max.bf16x2 %0, %0, %1;" : "+r"(w[k]) : "r"(floor));
+                else
+                    w[k] = __float_as_uint(fmaxf(__uint_as_float(w[k]), __uint_as_float(floor)));
+            }
+            each_of(make_uint4(w[0], w[1], w[2], w[3]), f);
+        }
+    }
+    template <class F>
     static __device__ __forceinline__ void each_of(const uint4 &u, F f)
     {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         if (BF16) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t x = w[k];
-                if (RAISE)  // 0xf149 is the bf16 next to -1e30
-                    asm("max.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[k]), "r"(0xf149f149u));
-                f(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-            }
-        } else if (RAISE) {
-            f(fmaxf(__uint_as_float(w[0]), -1e30f), fmaxf(__uint_as_float(w[1]), -1e30f));
-            f(fmaxf(__uint_as_float(w[2]), -1e30f), fmaxf(__uint_as_float(w[3]), -1e30f));
+            for (int k = 0; k < 4; ++k)
+                f(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
         } else {
             f(__uint_as_float(w[0]), __uint_as_float(w[1]));
             f(__uint_as_float(w[2]), __uint_as_float(w[3]));
@@ -419,6 +423,7 @@ __device__ __forceinline__ void store_whole(const Tile<BF16, VPT> &t, uint4 *p, 
 struct Scale {
     float c;       // log2(e) / temperature
     float margin;  // 16 / c
+    float inv;     // 1 / temperature
 };
 
 // Sums of a warp's share of a row relative to a logit `at`, in units of exp2: c =
@@ -427,79 +432,76 @@ struct Scale {
 // `at` is the warp's largest logit so far or one at most 2^16 times less likely, so it
 // rarely moves after the first tile.  A term costs one multiply-add, x c - ref with ref =
 // at c rounded: what the rounding left out is the same for every term and is put back by
-// settle().  Where |ref| is so large that nothing of the differences would be left of it,
-// they are taken before they are scaled.
+// settle().  From |at| c = 2^30 on it could be more than an exponent holds; two different
+// f32 logits are then 2^6 apart in units of exp2, so that nothing but the largest ones
+// counts, and a smaller c with |at| c = 2^30 gives just that.
 template <bool ENTROPY>
 struct Running {
+    static constexpr float FAR = 1073741824.0f;
     float at = -INFINITY, limit = -INFINITY;  // a maximum above `limit` moves `at`
-    float ref = NAN;                          // at c, rounded; NaN where differences come first
+    float c = 0.0f, ref = 0.0f;
     F2 s = F2{0}, e = F2{0};
 
-    // The sums relative to `top`.
-    __device__ __forceinline__ void settle(float top, float c, float &S, float &E) const
+    // The sums relative to `top`; z.c is the row's.
+    __device__ __forceinline__ void settle(float top, Scale z, float &S, float &E) const
     {
         const float2 s2 = split(s), e2 = split(e);
         // a term's exponent was (x - at) c + left
-        const float left = ref == ref ? fmaf(at, c, -ref) : 0.0f;
-        const float d = fmaxf((at - top) * c - left, -1e4f), w = ex2(d);
+        const float left = fmaf(at, c, -ref), d = fmaxf((at - top) * z.c - left, -1e4f), w = ex2(d);
         S = (s2.x + s2.y) * w;
-        E = (e2.x + e2.y) * w + S * d;
+        E = c == z.c ? (e2.x + e2.y) * w + S * d : 0.0f;  // (among equal logits d = 0)
     }
+
     template <bool BF16, int N>
     __device__ __forceinline__ void add(const Tile<BF16, N> &t, float tile_max, Scale z)
     {
-        const float c = z.c;
         if (__any_sync(0xffffffffu, !(tile_max <= limit))) {
             const float top = max_nan(at, warp_max_nan(tile_max));
-            float S, E;
-            settle(top, c, S, E);
-            const bool any = at != -INFINITY;
-            s = f2(any ? S : 0.0f, 0.0f);
-            e = f2(any ? E : 0.0f, 0.0f);
+            float S = 0.0f, E = 0.0f;
+            if (at != -INFINITY)
+                settle(top, z, S, E);
+            s = f2(S, 0.0f);
+            e = f2(E, 0.0f);
             at = top;
             limit = top + z.margin;
+            c = fabsf(top * z.c) < FAR ? z.c : FAR / fabsf(top);
             ref = top * c;
-            if (!(fabsf(ref) < 1e6f))
-                ref = NAN;
         }
+        if (at == -INFINITY)  // nothing but masked tokens so far
+            return;
         // a tile's sums are formed apart: a long row's are then sums of sums
-        const F2 cc = f2(c, c);
+        const F2 cc = f2(c, c), neg = f2(-ref, -ref);
         F2 ts = f2(0.0f, 0.0f), te = ts;
-        if (ref == ref) {
-            // A masked token's term of the entropy is 0, not 0 times -inf: its logit is raised
-            // to -1e30, where its weight is 0 as well.
-            const F2 neg = f2(-ref, -ref);
-            t.template each<ENTROPY>([&](float p, float q) {
+        if (ENTROPY) {
+            // a masked token's term of the entropy is 0, not 0 times -inf: its logit is raised
+            // to -1e30 (0xf149 as bf16), where its weight is 0 as well, unless that is among
+            // the largest ones
+            const bool raise = c == z.c;
+            const uint32_t floor = BF16 ? (raise ? 0xf149f149u : 0xff80ff80u) : (raise ? 0xf149f2cau : 0xff800000u);
+            t.each_above(floor, [&](float p, float q) {
                 const F2 d = fma2(f2(p, q), cc, neg);
                 const float2 u = split(d);
                 const F2 w = f2(ex2(u.x), ex2(u.y));
                 ts = ts + w;
-                if (ENTROPY)
-                    te = fma2(w, d, te);
-            });
-        } else if (at != -INFINITY) {  // (-inf: nothing but masked tokens so far)
-            const F2 neg = f2(-at, -at);
-            t.template each<false>([&](float p, float q) {
-                const float2 u = split((f2(p, q) + neg) * cc);
-                const F2 d = f2(fmaxf(u.x, -1e4f), fmaxf(u.y, -1e4f));
-                const float2 v = split(d);
-                const F2 w = f2(ex2(v.x), ex2(v.y));
-                ts = ts + w;
                 te = fma2(w, d, te);
+            });
+            e = e + te;
+        } else {
+            t.each([&](float p, float q) {
+                const float2 u = split(fma2(f2(p, q), cc, neg));
+                ts = ts + f2(ex2(u.x), ex2(u.y));
             });
         }
         s = s + ts;
-        if (ENTROPY)
-            e = e + te;
     }
 
     // The warp's part, from the lanes' largest logits.
-    __device__ __forceinline__ Part part(float most, float c, uint32_t key) const
+    __device__ __forceinline__ Part part(float most, Scale z, uint32_t key) const
     {
         const float top = warp_max_nan(most);
         float S = 0.0f, E = 0.0f;
         if (top != -INFINITY)
-            settle(top, c, S, E);
+            settle(top, z, S, E);
         return Part{top, warp_sum(S), ENTROPY ? warp_sum(E) : 0.0f, key};
     }
 };
@@ -516,6 +518,7 @@ __device__ __forceinline__ Stats join(const Part *parts, int n, float c)
 {
     const int lane = threadIdx.x & 31;
     float m = -INFINITY;
+#pragma unroll 1
     for (int p = lane; p < n; p += 32)
         m = max_nan(m, parts[p].m);
     m = warp_max_nan(m);
@@ -524,6 +527,7 @@ __device__ __forceinline__ Stats join(const Part *parts, int n, float c)
     if (!(m < INFINITY))
         return Stats{NAN, NAN, NAN};
     float S = 0.0f, E = 0.0f;
+#pragma unroll 1
     for (int p = lane; p < n; p += 32) {
         const Part q = parts[p];
         const float d = fmaxf((q.m - m) * c, -1e4f), w = ex2(d);
@@ -533,7 +537,7 @@ __device__ __forceinline__ Stats join(const Part *parts, int n, float c)
     S = warp_sum(S);
     E = warp_sum(E);
     const float lnS = logf(S);
-    return Stats{m, lnS, fmaxf(lnS - LN2 * E / S, 0.0f)};
+    return Stats{m, lnS, fmaxf(lnS - LN2 * __fdividef(E, S), 0.0f)};
 }
 
 // The CTA's place: its row, its run of the row's vectors, and its cluster.
@@ -676,33 +680,58 @@ struct Run {
                 t.v[v] = i0 + v * T < end ? from[v * T] : make_uint4(M, M, M, M);
         }
     }
-    // f(tile, g) for every group, through SLOTS slots that are used again and again.
+    // f(tile, g, s) for every group, through SLOTS slots s that are used again and again; keep: not
+    // before f is done with the slot.
     template <int SLOTS, class F>
-    __device__ __forceinline__ void each(F f) const
+    __device__ __forceinline__ void each(bool keep, F f) const
     {
         static_assert(SLOTS <= 4, "copies_done waits for up to three groups");
 #pragma unroll 1
         for (int g = 0; g < SLOTS; ++g)
             start(g, g);
         int s = 0;
+#pragma unroll 1
         for (int g = 0; g < groups; ++g) {
             TileT t;
             copies_done(SLOTS - 1);
             get(t, g, s);
-            start(g + SLOTS, s);
+            const bool early = whole(g) && !keep;
+            if (early)
+                start(g + SLOTS, s);
+            f(t, g, s);
+            if (!early)
+                start(g + SLOTS, s);
             s = s + 1 == SLOTS ? 0 : s + 1;
-            f(t, g);
         }
     }
-    // value(pair) of every pair of group g's tile into the same elements of `out`, or zeros.
+    // value(pair) of every pair of group g, whose tile is t and which is in slot s, into the
+    // same elements of `out`.  Only whole groups whose rows start alike within a vector are
+    // stored from the tile: then the slot is not looked at.
     template <class F>
-    __device__ __forceinline__ void put(const TileT &t, int g, const RowPtr<BF16> &out, bool zero, F value) const
+    __device__ __forceinline__ void put(const TileT &t, int g, int s, const RowPtr<BF16> &out, F value) const
     {
         const int i0 = vector(g);
-        if (whole(g) && row.skip == out.skip && !zero)
+        if (row.skip == out.skip && whole(g)) {
             store_whole<T>(t, reinterpret_cast<uint4 *>(out.base) + i0, value);
-        else
-            store_tile(t, row, out, i0, T, end, zero, value);
+            return;
+        }
+#pragma unroll 1
+        for (int v = 0; v < VT; ++v) {
+            const int i = i0 + v * T;
+            if (i >= end)
+                break;
+            Tile<BF16, 1> one;
+            one.v[0] = slots[s * GROUP + v * T];
+            store_tile(one, row, out, i, T, end, false, value);
+        }
+    }
+    // Zeros into the run's elements of `out`.
+    __device__ __forceinline__ void clear(const RowPtr<BF16> &out) const
+    {
+        Tile<BF16, 1> none;
+#pragma unroll 1
+        for (int i = begin + static_cast<int>(threadIdx.x); i < end; i += T)
+            store_tile(none, row, out, i, T, end, true, [](float, float) { return F2{0}; });
     }
 };
 
@@ -717,34 +746,12 @@ inline int allow_shared(void (*kernel)(A), size_t bytes)
     return KDA_OK;
 }
 
-// Threads of a CTA, vectors of a thread and CTAs of a row for N rows of nvec vectors.
-struct Shape {
-    int threads, vpt, cl;
-};
-
 // Vectors that the longest of N rows may touch.
 inline long long vectors_of(const void *p, int V, long long ld, int bf16)
 {
     const long long per = bf16 ? 8 : 4;
     const bool even = (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % per == 0;
     return (V + per - 1) / per + (even ? 0 : 1);
-}
-
-inline Shape shape_of(long long N, long long nvec)
-{
-    constexpr int SMS = 152;
-    // one CTA a row; more while the GPU has SMs to spare and a CTA still has 256 vectors
-    int cl = 1;
-    while (cl < MAX_CL && N * cl * 2 <= SMS && nvec >= 256ll * 2 * cl)
-        cl *= 2;
-    const long long per = (nvec + cl - 1) / cl;
-    int threads = 32;
-    while (threads < MAX_THREADS && per > threads * 2ll)
-        threads *= 2;
-    int vpt = 1;
-    while (vpt < MAX_VPT && per > static_cast<long long>(threads) * vpt)
-        vpt *= 2;
-    return Shape{threads, vpt, cl};
 }
 
 // A pass that needs nothing of the rest of a row: CTAs of T threads, each with a run of up to
@@ -774,18 +781,6 @@ inline int with_threads(int threads, F f)
     case 32: return f(std::integral_constant<int, 32>());
     case 128: return f(std::integral_constant<int, 128>());
     default: return f(std::integral_constant<int, 256>());
-    }
-}
-
-// f with the vectors of a thread as a constant.
-template <class F>
-inline int with_vpt(int vpt, F f)
-{
-    switch (vpt) {
-    case 1: return f(std::integral_constant<int, 1>());
-    case 2: return f(std::integral_constant<int, 2>());
-    case 4: return f(std::integral_constant<int, 4>());
-    default: return f(std::integral_constant<int, 8>());
     }
 }
 

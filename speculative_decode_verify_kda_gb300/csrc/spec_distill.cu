@@ -9,10 +9,8 @@
 //   d x_i = g w tau (Q p_i - sum_{k: id_k = i} q_k),  Q = sum_k q_k.
 // tau^2 keeps the gradient's size when tau changes (d ln p / d x has a factor 1 / tau).
 //
-// distill_kernel: a row stays in the registers of its CTA or cluster (logit_rows.cuh)
-// between the sum and the gradient, so loss and gradient together read the logits once.
-// The gradient is written as g w tau Q p for every element; after that, the CTA that
-// holds a teacher's entry writes that element again with its q taken off.
+// The gradient is written as g w tau Q p for every element; after that, the CTA that holds a
+// teacher's entry writes that element again with its q taken off.
 #include <algorithm>
 #include <cfloat>
 
@@ -95,7 +93,7 @@ struct Reader {
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             if (!a.value_logprobs)
-                v[i] /= a.tau;
+                v[i] *= a.z.inv;
             top = max_nan(top, v[i]);
         }
         top = warp_max_nan(top);
@@ -104,17 +102,17 @@ struct Reader {
         float e[EACH], Q = 0.0f;
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
-            e[i] = expf(v[i] - ref);
+            e[i] = 32 * i < a.K ? expf(v[i] - ref) : 0.0f;
             Q += e[i];
         }
         Q = warp_sum(Q);
         if (!(top < INFINITY))
             Q = NAN;
         const bool whole = !a.value_logprobs && !none;  // to be renormalised
-        const float lnsum = whole ? logf(Q) : 0.0f;
+        const float lnsum = whole ? logf(Q) : 0.0f, part = 1.0f / Q;
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
-            const float q = whole ? e[i] / Q : e[i];
+            const float q = whole ? e[i] * part : e[i];
             t.id[lane + 32 * i] = id[i];
             t.off[lane + 32 * i] = q;
             t.q[lane + 32 * i] = q;
@@ -127,6 +125,7 @@ struct Reader {
         // an id listed twice: its first entry takes every q off
         int same[EACH] = {};
         const int4 *ids = reinterpret_cast<const int4 *>(t.id);
+#pragma unroll 1
         for (int j = 0; j < (a.K + 3) / 4; ++j) {
             const int4 o = ids[j];
 #pragma unroll
@@ -144,6 +143,7 @@ struct Reader {
                 const int k = lane + 32 * i;
                 if (id[i] >= 0 && same[i] > 1) {
                     float q = 0.0f;
+#pragma unroll 1
                     for (int j = 0; j < a.K; ++j) {
                         if (t.id[j] == id[i]) {
                             if (j < k) {
@@ -173,7 +173,7 @@ __device__ __forceinline__ void write_loss(const Distill &a, long long n, float 
     for (int i = 0; i < EACH; ++i) {
         const int k = lane + 32 * i;
         if (t.q[k] != 0.0f) {
-            const float lp = st.empty() ? -INFINITY : (t.x[k] - st.m) / a.tau - st.lnS;
+            const float lp = st.empty() ? -INFINITY : (t.x[k] - st.m) * a.z.inv - st.lnS;
             const float term = t.q[k] * (t.lnq[k] - lp);
             kl += term;
             most = max_nan(most, term);
@@ -200,6 +200,7 @@ template <bool BF16>
 __device__ __forceinline__ void take_off(const Distill &a, const Entries &t, const RowPtr<BF16> &out, int lo, int hi,
                                          float m, float off, float scale, int who, int many)
 {
+#pragma unroll 1
     for (int k = who; k < a.K; k += many) {
         const int id = t.id[k];
         if (id >= lo && id < hi)
@@ -214,108 +215,37 @@ __device__ __forceinline__ F2 weighted(float p, float q, float m, float c, float
     return f2(ex2(u.x), ex2(u.y)) * f2(sq, sq);
 }
 
-template <bool BF16, int VPT, bool GRAD>
-__global__ void __launch_bounds__(MAX_THREADS, 3) distill_kernel(const Distill a)
-{
-    __shared__ Part parts[MAX_CL * (MAX_THREADS / 32)];
-    __shared__ Entries t;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Place at(a.cl, blockDim.x);
-    const int tid = threadIdx.x, step = blockDim.x, round = step * VPT;
-    const long long n = at.row;
-    const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(GRAD ? a.dx : nullptr, GRAD ? n * a.ldg : 0, a.V);
-    const int begin = at.begin(row.nvec), end = at.end(row.nvec);
-    const float w = a.weight ? a.weight[n] : 1.0f;
-    const float scale = GRAD ? w * a.tau * (a.g ? a.g[n] : 1.0f) : 0.0f;
-    Tile<BF16, VPT> tile;
-    if (w == 0.0f) {  // a row that takes no part is not read
-        if (at.rank == 0 && tid == 0) {
-            a.loss[n] = 0.0f;
-            if (a.stats_out)
-                a.stats_out[2 * n] = a.stats_out[2 * n + 1] = 0.0f;
-        }
-        if (GRAD)
-            for (int b = begin; b < end; b += round)
-                store_tile(tile, row, out, b + tid, step, end, true, [](float, float) { return F2{0}; });
-        return;
-    }
-    at.arrive();
-    // the ids of the CTA's run; the first CTA reads every entry's logit for the loss
-    const int lo = max(0, row.first_id(begin)), hi = min(a.V, row.first_id(end));
-    Running<false> run;
-    float most = -INFINITY;
-    int b = begin;
-    do {
-        tile.load(row, b + tid, step, end);
-        if (b == begin && tid < 32) {
-            Reader<BF16> r;
-            r.load(a, n);
-            r.gather(a, row, at.rank ? lo : 0, at.rank ? hi : a.V);
-            r.finish(a, t);
-        }
-        const float m = tile.max_of();
-        most = max_nan(most, m);
-        run.add(tile, m, a.z);
-        b += round;
-    } while (b < end);
-    const Part part = run.part(most, a.z.c, 0u);
-    at.wait();
-    at.hand_out(parts, part);
-    at.sync();
-    const Stats st = join(parts, at.parts(), a.z.c);
-    if (at.rank == 0 && tid < 32)
-        write_loss(a, n, w, st, t);
-    if (GRAD) {
-        const bool zero = st.empty() || t.Q == 0.0f || scale == 0.0f;
-        const float off = -st.lnS * LOG2E, m = st.m, sq = scale * t.Q;
-        b = begin;
-        do {
-            if (round < end - begin && !zero)  // of several rounds the registers hold the last one alone
-                tile.load(row, b + tid, step, end);
-            store_tile(tile, row, out, b + tid, step, end, zero,
-                       [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); });
-            b += round;
-        } while (b < end);
-        if (!zero) {
-            __syncthreads();
-            take_off(a, t, out, lo, hi, m, off, scale, tid, step);
-        }
-    }
-}
-
-// For many long rows.  T threads pass their CTA's run of the row through shared memory; one
-// more warp reads the teacher's entries meanwhile and writes the loss.  With a gradient the
+// Loss, or loss and gradient.  T threads pass their CTA's run of the row through shared memory;
+// one more warp reads the teacher's entries meanwhile and writes the loss.  With a gradient the
 // run stays in shared memory between the sum and the gradient where it fits (HELD); where
 // it does not, and without a gradient, it passes through a few slots, for the gradient once
 // more, out of L2.
-constexpr int LONG_T = 256, LONG_VT = 4, LONG_SLOTS = 3, LONG_GROUP = LONG_T * LONG_VT;
+constexpr int ROW_VT = 4, ROW_SLOTS = 3;
 
-template <bool BF16, bool GRAD, bool HELD>
-__global__ void __launch_bounds__(LONG_T + 32, 4) distill_long_kernel(const Distill a)
+template <bool BF16, int T, bool GRAD, bool HELD>
+__global__ void __launch_bounds__(T + 32, T == 256 ? 4 : T == 128 ? 6 : 8) distill_kernel(const Distill a)
 {
     extern __shared__ uint4 slots[];
-    __shared__ Part parts[MAX_CL * (LONG_T / 32)];
+    __shared__ Part parts[MAX_CL * (T / 32)];
     __shared__ Entries t;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Place at(a.cl, LONG_T);
+    const Place at(a.cl, T);
     const int tid = threadIdx.x;
-    const bool reader = tid >= LONG_T;
+    const bool reader = tid >= T;
     const long long n = at.row;
     const RowPtr<BF16> row(a.x, n * a.ld, a.V), out(GRAD ? a.dx : nullptr, GRAD ? n * a.ldg : 0, a.V);
-    using R = Run<BF16, LONG_T, LONG_VT>;
+    using R = Run<BF16, T, ROW_VT>;
     const R run(row, at, slots);
     const float w = a.weight ? a.weight[n] : 1.0f, g = GRAD && a.g ? a.g[n] : 1.0f;
     if (w == 0.0f) {  // a row that takes no part is not read
-        if (at.rank == 0 && tid == LONG_T) {
+        if (at.rank == 0 && tid == T) {
             a.loss[n] = 0.0f;
             if (a.stats_out)
                 a.stats_out[2 * n] = a.stats_out[2 * n + 1] = 0.0f;
         }
         if (GRAD && !reader)
-            for (int k = 0; k < run.groups; ++k)
-                run.put(typename R::TileT(), k, out, true, [](float, float) { return F2{0}; });
+            run.clear(out);
         return;
     }
     at.arrive();
@@ -337,8 +267,10 @@ __global__ void __launch_bounds__(LONG_T + 32, 4) distill_long_kernel(const Dist
             sums.add(x, m, a.z);
         };
         if (HELD) {
+#pragma unroll 1
             for (int k = 0; k < run.groups; ++k)
                 run.start(k, k);
+#pragma unroll 1
             for (int k = 0; k < run.groups; ++k) {
                 typename R::TileT x;
                 copies_done(min(3, run.groups - 1 - k));
@@ -346,9 +278,9 @@ __global__ void __launch_bounds__(LONG_T + 32, 4) distill_long_kernel(const Dist
                 add(x);
             }
         } else {
-            run.template each<LONG_SLOTS>([&](const typename R::TileT &x, int) { add(x); });
+            run.template each<ROW_SLOTS>(false, [&](const typename R::TileT &x, int, int) { add(x); });
         }
-        const Part part = sums.part(most, a.z.c, 0u);
+        const Part part = sums.part(most, a.z, 0u);
         at.wait();
         at.hand_out(parts, part);
     }
@@ -363,21 +295,25 @@ __global__ void __launch_bounds__(LONG_T + 32, 4) distill_long_kernel(const Dist
             write_loss(a, n, w, st, t);
     } else {
         auto value = [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); };
-        if (HELD) {
+        if (zero) {
+            run.clear(out);
+        } else if (HELD) {
+#pragma unroll 1
             for (int k = 0; k < run.groups; ++k) {
                 typename R::TileT x;
                 run.get(x, k, k);
-                run.put(x, k, out, zero, value);
+                run.put(x, k, k, out, value);
             }
         } else {
-            run.template each<LONG_SLOTS>(
-                [&](const typename R::TileT &x, int k) { run.put(x, k, out, zero, value); });
+            run.template each<ROW_SLOTS>(row.skip != out.skip, [&](const typename R::TileT &x, int k, int s) {
+                run.put(x, k, s, out, value);
+            });
         }
     }
     if (GRAD) {
         __syncthreads();
         if (!zero)
-            take_off(a, t, out, lo, hi, m, off, scale, tid, LONG_T + 32);
+            take_off(a, t, out, lo, hi, m, off, scale, tid, T + 32);
     }
 }
 
@@ -410,20 +346,20 @@ __global__ void __launch_bounds__(T + 32) distill_backward_kernel(const Distill 
         r.finish(a, t);
         meet();  // the entries are there, and the logits at them have been read
     } else if (out_of_it) {
-        for (int k = 0; k < run.groups; ++k)
-            run.put(typename R::TileT(), k, out, true, [](float, float) { return F2{0}; });
+        run.clear(out);
         return;
     } else {
         float sq = 0.0f;
-        bool zero = false;
-        run.template each<PIECE_SLOTS>([&](const typename R::TileT &x, int k) {
+        run.template each<PIECE_SLOTS>(row.skip != out.skip, [&](const typename R::TileT &x, int k, int s) {
             if (k == 0) {
                 meet();
-                zero = t.Q == 0.0f;
                 sq = scale * t.Q;
             }
-            run.put(x, k, out, zero, [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); });
+            if (t.Q != 0.0f)
+                run.put(x, k, s, out, [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); });
         });
+        if (t.Q == 0.0f)
+            run.clear(out);
     }
     meet();  // the gradient is written, the corrections come over it
     if (t.Q != 0.0f)
@@ -448,33 +384,33 @@ int check_teacher(const kda_teacher *t, int N)
     return KDA_OK;
 }
 
-// Many rows, each of more than a tile a thread.
-bool is_long(long long N, long long nvec) { return N > 152 && nvec > MAX_THREADS * MAX_VPT / 2; }
-
-template <bool BF16, bool GRAD, bool HELD>
-int launch_long(const Distill &a, size_t smem, cudaStream_t stream)
+template <int T, bool GRAD, bool HELD>
+int launch_with(const Distill &a, bool bf16, size_t smem, cudaStream_t stream)
 {
-    auto *kernel = distill_long_kernel<BF16, GRAD, HELD>;
+    auto *kernel = bf16 ? distill_kernel<true, T, GRAD, HELD> : distill_kernel<false, T, GRAD, HELD>;
     if (int rc = allow_shared(kernel, smem))
         return rc;
-    return launch_rows(kernel, a, a.N * a.cl, LONG_T + 32, a.cl, smem, stream, "distill_long_kernel");
+    return launch_rows(kernel, a, a.N * a.cl, T + 32, a.cl, smem, stream, "distill_kernel");
 }
 
-template <bool BF16, bool GRAD>
-int launch_long(Distill a, long long nvec, cudaStream_t stream)
+// Threads by the vectors of a run: what is fixed for a warp weighs on short runs, so those of
+// many rows get few warps (us for 8000 bf16 rows of 1000 / 5000 / 9000 / 17000 logits, 32
+// threads: 15.6 / 36 / 61 / -, 64: 20.3 / 34.5 / 48 / -, 128: 31 / 43 / 56 / 82, 256: 44 / 59 /
+// 70 / 94); where the GPU is not full a row's latency counts, and they get more (15 rows of
+// 1001 f32: 64 threads 3.03, 128 2.83, 256 2.88).
+template <bool GRAD, bool HELD>
+int launch_held(const Distill &a, bool bf16, long long per, cudaStream_t stream)
 {
-    constexpr size_t group = static_cast<size_t>(LONG_GROUP) * 16;
-    a.cl = 1;
-    if (GRAD) {
-        constexpr long long HELD_GROUPS = 65536 / group;  // three CTAs an SM
-        while (a.cl < MAX_CL && nvec > a.cl * HELD_GROUPS * LONG_GROUP)
-            a.cl *= 2;
-        const long long groups = ((nvec + a.cl - 1) / a.cl + LONG_GROUP - 1) / LONG_GROUP;
-        if (groups * group <= 200 * 1024)
-            return launch_long<BF16, true, true>(a, groups * group, stream);
-        a.cl = 1;
-    }
-    return launch_long<BF16, GRAD, false>(a, LONG_SLOTS * group, stream);
+    const bool full = a.N * a.cl > 2 * SMS;
+    const size_t most = static_cast<size_t>(per) * 16;
+    auto smem = [&](int t) { return HELD ? most : std::min<size_t>(most, ROW_SLOTS * ROW_VT * t * 16); };
+    if (per <= (full ? 400 : 32))
+        return launch_with<32, GRAD, HELD>(a, bf16, smem(32), stream);
+    if (per <= (full ? 1536 : 96))
+        return launch_with<64, GRAD, HELD>(a, bf16, smem(64), stream);
+    if (per <= (full ? 2880 : 1024))
+        return launch_with<128, GRAD, HELD>(a, bf16, smem(128), stream);
+    return launch_with<256, GRAD, HELD>(a, bf16, smem(256), stream);
 }
 
 template <bool GRAD>
@@ -482,15 +418,25 @@ int launch(Distill a, int dtype, cudaStream_t stream)
 {
     const bool bf16 = dtype == KDA_BF16;
     const long long nvec = vectors_of(a.x, a.V, a.ld, bf16);
-    if (is_long(a.N, nvec))
-        return bf16 ? launch_long<true, GRAD>(a, nvec, stream) : launch_long<false, GRAD>(a, nvec, stream);
-    const Shape sh = shape_of(a.N, nvec);
-    a.cl = sh.cl;
-    return with_vpt(sh.vpt, [&](auto vpt) {
-        constexpr int VPT = decltype(vpt)::value;
-        return launch_rows(bf16 ? distill_kernel<true, VPT, GRAD> : distill_kernel<false, VPT, GRAD>, a,
-                           a.N * sh.cl, sh.threads, sh.cl, 0, stream, "distill_kernel");
-    });
+    // With a gradient a run is held if an SM then has three CTAs (or two, where eight CTAs a row
+    // cannot do better); beyond that a row is read twice by one CTA.
+    constexpr long long THREE = 4480, TWO = 6912;
+    a.cl = 1;
+    bool held = GRAD;
+    if (GRAD) {
+        while (a.cl < MAX_CL && nvec > a.cl * THREE)
+            a.cl *= 2;
+        held = (nvec + a.cl - 1) / a.cl <= TWO;
+        if (!held)
+            a.cl = 1;
+    }
+    // Few rows: more CTAs a row while there are SMs to spare and a run keeps 512 vectors (us for 1
+    // / 8 / 32 / 64 bf16 rows of 32768 logits: one CTA 4.96 / 4.97 / 4.99 / 4.99, two 4.28 / 4.38 /
+    // 4.37 / 4.44, four 3.76 / 3.88 / 4.04 / 4.50, eight 3.62 / 3.82 / 4.21 / 5.47).
+    while (a.cl < MAX_CL && a.N * a.cl * 2 <= SMS && nvec >= 1024ll * a.cl)
+        a.cl *= 2;
+    const long long per = (nvec + a.cl - 1) / a.cl;
+    return held ? launch_held<GRAD, GRAD>(a, bf16, per, stream) : launch_held<GRAD, false>(a, bf16, per, stream);
 }
 
 int launch_backward(Distill a, int dtype, cudaStream_t stream)
@@ -528,7 +474,7 @@ Distill params(const void *x, void *dx, long long ld, long long ldg, int N, int 
     a.g = g;
     a.stats_in = stats_in;
     a.tau = tau;
-    a.z = Scale{LOG2E / tau, 16.0f * LN2 * tau};
+    a.z = Scale{LOG2E / tau, 16.0f * LN2 * tau, 1.0f / tau};
     a.loss = loss;
     a.stats_out = stats_out;
     a.status = status;

@@ -6,19 +6,15 @@
 //   d x_i = (1/temperature) [ g (1{i = t} - p_i) - h p_i (ln p_i + H) ]
 // for g = dL/d log p_t and h = dL/dH.
 //
-// logprobs_kernel: a row stays in the registers of its CTA or cluster (logit_rows.cuh), so
-// it is read once.  The top alternatives come out of the same registers: from the
-// threads' maxima, which the sums need anyway, a threshold is taken that at least K
-// logits reach, the few that reach it go to a list in the first CTA's shared memory, and
-// counting how many of the list precede an entry gives its place.
-//
-// The threshold: each warp orders its lanes' maxima and names the r-th largest; the w-th
-// largest of those, with r w >= K, is reached by r lanes' maxima of w warps, that is by K
-// logits at least.  For logits in no particular order about K of them reach it.  Where
-// more than the list holds do (many equal logits), the threshold is taken again with a
-// logit's place in the row as a part of its value; where that too leaves more, the first
-// CTA finds the alternatives one after the other.  All three give the same answer.
+// A row is read once for its maximum and sums.  The top alternatives come from the threads'
+// maxima, which the sums need anyway: what K of those reach is a threshold that K logits at
+// least reach, and for logits in no particular order not many more.  The few that do go to
+// a list in shared memory, and counting how many of the list precede an entry gives its
+// place.  Where more reach the threshold than the list holds (many equal logits), it is
+// taken again with a logit's place in the row as a part of its value; where that too leaves
+// more, the alternatives are found one after the other.  All three give the same answer.
 #include <algorithm>
+#include <cfloat>
 
 #include "logit_rows.cuh"
 
@@ -28,22 +24,21 @@ namespace {
 using namespace rows;
 using Key = unsigned long long;
 
-constexpr int LIST = 2048;         // candidates that a row's list holds
-constexpr int LONG_LIST = 512;     // (of the kernel for long rows)
+constexpr int CLUSTER = 8, CLUSTER_T = 256;  // CTAs of a row and their threads where rows are few
+constexpr int CLUSTER_LIST = 2048;           // candidates that a row's list holds there
 
 struct Score {
     const void *x;
     long long ld, N;
-    int V, K, cl;
-    int r, w;  // the threshold is the w-th largest of the warps' r-th largest maxima
+    int V, K;
+    int r, w;  // the threshold is what w of the warps' r-th largest maxima reach
     const int *tokens;
-    float tau;
     Scale z;
     float *logprob, *entropy, *stats, *top_logprobs;
     int *top_ids, *status;
 };
 
-constexpr int MAX_PARTS = MAX_CL * (MAX_THREADS / 32);
+constexpr int MAX_PARTS = CLUSTER * CLUSTER_T / 32;
 
 // The list of a row's candidates and what finds its threshold.
 template <int CAP>
@@ -54,26 +49,46 @@ struct Candidates {
     __align__(16) Key list[CAP];
 };
 
-// The w-th largest (from 1) of n values, by all threads of the CTA.
-template <class T, class Get>
-__device__ __forceinline__ T rank_of(Get get, int n, int w, Key *out)
+// The w-th largest (from 1) of n keys, by all threads of the CTA.
+__device__ __forceinline__ Key rank_of(const Key *keys, int n, int w, Key *out)
 {
     if (n <= 32) {
         const int lane = threadIdx.x & 31;
-        return warp_rank<T>(lane < n ? get(lane) : T(0), w - 1);
+        return warp_rank<Key>(lane < n ? keys[lane] : 0, w - 1);
     }
+#pragma unroll 1
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const T mine = get(i);
+        const Key mine = keys[i];
         int before = 0;
-        for (int j = 0; j < n; ++j) {
-            const T other = get(j);
-            before += other > mine || (other == mine && j < i);
-        }
+#pragma unroll 4
+        for (int j = 0; j < n; ++j)
+            before += keys[j] > mine || (keys[j] == mine && j < i);
         if (before == w - 1)
             *out = mine;
     }
     __syncthreads();
-    return static_cast<T>(*out);
+    return *out;
+}
+
+// The largest number with 16 low zero bits that at least K of the warp's 32 N values reach (0
+// if fewer than K are above 0): two bits a step.  Called by whole warps.
+template <int N>
+__device__ __forceinline__ uint32_t reached(const uint32_t (&v)[N], int K)
+{
+    static_assert(32 * N < 1024, "three counts share a word");
+    uint32_t t = 0;
+#pragma unroll 1
+    for (int at = 30; at >= 16; at -= 2) {
+        const uint32_t t1 = t | 1u << at, t2 = t | 2u << at, t3 = t | 3u << at;
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            n += (v[i] >= t1 ? 1u : 0u) + (v[i] >= t2 ? 1u << 10 : 0u) + (v[i] >= t3 ? 1u << 20 : 0u);
+        n = __reduce_add_sync(0xffffffffu, n);
+        const uint32_t k = K;
+        t = (n >> 20) >= k ? t3 : (n >> 10 & 1023u) >= k ? t2 : (n & 1023u) >= k ? t1 : t;
+    }
+    return t;
 }
 
 template <int CAP>
@@ -84,10 +99,24 @@ __device__ __forceinline__ void append(int *count, Key *list, Key key)
         list[at] = key;
 }
 
+// The logits of a vector that reach `least`; id is the first one's.
+template <bool BF16, int CAP>
+__device__ __noinline__ void append_reaching(int *count, Key *list, uint4 u, int id, float least)
+{
+    Tile<BF16, 1>::each_of(u, [&](float p, float q) {
+        if (p >= least && p > -INFINITY)
+            append<CAP>(count, list, key_of(p, id));
+        if (q >= least && q > -INFINITY)
+            append<CAP>(count, list, key_of(q, id + 1));
+        id += 2;
+    });
+}
+
 // Calls f with the key of every logit above -inf of the CTA's share, read again.
 template <bool BF16, class F>
 __device__ __forceinline__ void each_key(const RowPtr<BF16> &row, int first, int step, int end, F f)
 {
+#pragma unroll 1
     for (int i = first; i < end; i += step) {
         int id = row.first_id(i);
         Tile<BF16, 1>::each_of(row.full(i) ? row.load(i) : row.load_edge(i), [&](float p, float q) {
@@ -119,7 +148,7 @@ __device__ __noinline__ void list_by_key(int K, RowPtr<BF16> row, Place at, Cand
         sh.count = 0;
     at.sync();
     const int n = at.parts(), w = (K + 31) / 32;
-    const Key bound = w <= n ? rank_of<Key>([&](int i) { return keys[i]; }, n, w, &sh.bound) : 0;
+    const Key bound = w <= n ? rank_of(keys, n, w, &sh.bound) : 0;
     int *count = at.in_cta(&sh.count, 0);
     Key *list = at.in_cta(sh.list, 0);
     each_key(row, first, blockDim.x, end, [&](Key k) {
@@ -136,6 +165,7 @@ __device__ __noinline__ void list_by_rounds(int K, RowPtr<BF16> row, Candidates<
 {
     Key *best_of = reinterpret_cast<Key *>(sh.parts), last = ~0ull;
     int n = 0;
+#pragma unroll 1
     for (; n < K && last; ++n) {
         Key best = 0;
         each_key(row, threadIdx.x, blockDim.x, row.nvec, [&](Key k) { best = k < last && k > best ? k : best; });
@@ -145,6 +175,7 @@ __device__ __noinline__ void list_by_rounds(int K, RowPtr<BF16> row, Candidates<
         if ((threadIdx.x & 31) == 0)
             best_of[threadIdx.x >> 5] = best;
         __syncthreads();
+#pragma unroll 1
         for (int i = 0; i < (blockDim.x >> 5); ++i)
             best = best_of[i] > best ? best_of[i] : best;
         last = best;
@@ -167,7 +198,7 @@ __device__ __forceinline__ void write_scores(const Score &a, long long n, const 
         if (token >= a.V && a.status)
             atomicOr(a.status, KDA_ST_BADTOKEN);
         if (token >= 0 && token < a.V)
-            lp = st.bad() ? NAN : st.empty() ? -INFINITY : (row.at(token) - st.m) / a.tau - st.lnS;
+            lp = st.bad() ? NAN : st.empty() ? -INFINITY : (row.at(token) - st.m) * a.z.inv - st.lnS;
     }
     if (a.logprob)
         a.logprob[n] = lp;
@@ -185,6 +216,7 @@ __device__ __forceinline__ void write_scores(const Score &a, long long n, const 
 __device__ __forceinline__ void write_top(const Score &a, long long n, float m, float lnS, const Key *list, int found)
 {
     const long long o = n * a.K;
+#pragma unroll 1
     for (int i = threadIdx.x; i < found; i += blockDim.x) {
         const Key key = list[i];
         int place = 0;
@@ -193,32 +225,38 @@ __device__ __forceinline__ void write_top(const Score &a, long long n, float m, 
             place += list[j] > key;
         if (place < a.K) {
             a.top_ids[o + place] = key_id(key);
-            a.top_logprobs[o + place] = (from_ordered(static_cast<uint32_t>(key >> 32)) - m) / a.tau - lnS;
+            a.top_logprobs[o + place] = (from_ordered(static_cast<uint32_t>(key >> 32)) - m) * a.z.inv - lnS;
         }
     }
+#pragma unroll 1
     for (int k = found + threadIdx.x; k < a.K; k += blockDim.x) {
         a.top_ids[o + k] = -1;
         a.top_logprobs[o + k] = m != m ? NAN : -INFINITY;
     }
 }
 
+// For few long rows: a cluster of CTAs a row, which holds it in registers.  Each warp orders its
+// lanes' maxima and names the r-th largest; what w of those reach, with r w >= K, is reached
+// by r lanes' maxima of w warps.  One barrier of the cluster lies between reading the row and
+// knowing its statistics and the threshold, one more before the first CTA orders the list.
 template <bool BF16, int VPT>
-__global__ void __launch_bounds__(MAX_THREADS, 3) logprobs_kernel(const Score a)
+__global__ void __launch_bounds__(CLUSTER_T) logprobs_cluster_kernel(const Score a)
 {
-    __shared__ Candidates<LIST> sh;
+    __shared__ Candidates<CLUSTER_LIST> sh;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Place at(a.cl, blockDim.x);
+    const Place at(CLUSTER, CLUSTER_T);
     const int tid = threadIdx.x;
     if (tid == 0)
         sh.count = 0;
     at.arrive();
     const RowPtr<BF16> row(a.x, at.row * a.ld, a.V);
-    const int begin = at.begin(row.nvec), end = at.end(row.nvec), step = blockDim.x, round = step * VPT;
+    const int begin = at.begin(row.nvec), end = at.end(row.nvec), step = CLUSTER_T, round = step * VPT;
     Tile<BF16, VPT> t;
     Running<true> run;
     float most = -INFINITY;
     int b = begin;
+#pragma unroll 1
     do {
         t.load(row, b + tid, step, end);
         const float m = t.max_of();
@@ -228,7 +266,7 @@ __global__ void __launch_bounds__(MAX_THREADS, 3) logprobs_kernel(const Score a)
     } while (b < end);
     const uint32_t mine = most > -INFINITY ? ordered(most) : 0u;
     const uint32_t named = a.K > 0 ? warp_rank<uint32_t>(mine, a.r - 1) : 0u;
-    const Part part = run.part(most, a.z.c, named);
+    const Part part = run.part(most, a.z, named);
     at.wait();
     at.hand_out(sh.parts, part);
     at.sync();
@@ -239,26 +277,26 @@ __global__ void __launch_bounds__(MAX_THREADS, 3) logprobs_kernel(const Score a)
     if (a.K == 0)
         return;
     if (!st.bad() && !st.empty()) {
-        const uint32_t bound =
-            a.w <= n ? rank_of<uint32_t>([&](int i) { return sh.parts[i].key; }, n, a.w, &sh.bound) : 0u;
+        uint32_t v[MAX_PARTS / 32];
+#pragma unroll
+        for (int i = 0; i < MAX_PARTS / 32; ++i)
+            v[i] = 32 * i + (tid & 31) < n ? sh.parts[32 * i + (tid & 31)].key : 0u;
+        const uint32_t bound = reached(v, a.w);
         if (mine && mine >= bound) {
             const float least = bound ? from_ordered(bound) : -INFINITY;
             int *count = at.in_cta(&sh.count, 0);
             Key *list = at.in_cta(sh.list, 0);
             b = begin;
+#pragma unroll 1
             do {
                 if (round < end - begin)  // of several rounds the registers hold the last one alone
                     t.load(row, b + tid, step, end);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
-                    int id = row.first_id(b + tid + j * step);
-                    t.each_of(t.v[j], [&](float p, float q) {
-                        if (p >= least && p > -INFINITY)
-                            append<LIST>(count, list, key_of(p, id));
-                        if (q >= least && q > -INFINITY)
-                            append<LIST>(count, list, key_of(q, id + 1));
-                        id += 2;
-                    });
+                    Tile<BF16, 1> one;
+                    one.v[0] = t.v[j];
+                    if (one.max_of() >= least)
+                        append_reaching<BF16, CLUSTER_LIST>(count, list, t.v[j], row.first_id(b + tid + j * step), least);
                 }
                 b += round;
             } while (b < end);
@@ -266,13 +304,13 @@ __global__ void __launch_bounds__(MAX_THREADS, 3) logprobs_kernel(const Score a)
     }
     at.sync();
     int found = *at.in_cta(&sh.count, 0);
-    if (found > LIST) {  // the same for every CTA of the row
+    if (found > CLUSTER_LIST) {  // the same for every CTA of the row
         list_by_key(a.K, row, at, sh);
         found = *at.in_cta(&sh.count, 0);
     }
     at.arrive();  // the first CTA's shared memory has been read by the others
     if (at.rank == 0) {
-        if (found > LIST) {
+        if (found > CLUSTER_LIST) {
             list_by_rounds(a.K, row, sh);
             found = sh.count;
         }
@@ -281,34 +319,82 @@ __global__ void __launch_bounds__(MAX_THREADS, 3) logprobs_kernel(const Score a)
     at.wait();
 }
 
-// For many long rows: one CTA a row, which passes through shared memory ahead of its use.  A
+// One CTA a row, which passes through shared memory ahead of its use.  A
 // thread keeps the maxima of up to SPANS equal spans of its share of the row, half a group or
-// a multiple; the spans that reach the threshold are read again, through L2, to fill the list.
-constexpr int LONG_T = 256, LONG_VT = 4, LONG_SLOTS = 3, HALF = LONG_VT / 2;
-constexpr int LONG_WARPS = LONG_T / 32, SPANS = 16, WORK = 1024;
+// a multiple.  The threshold is the K-th largest of the threads' maxima, to 16 bits; the
+// spans that reach it are read again, through L2, to fill the list.
+constexpr int ROW_VT = 4, ROW_SLOTS = 2, SPANS = 16, WORK = 1024;
 
-struct LongShared {
-    Candidates<LONG_LIST> top;
+template <int T>
+struct RowShared {
+    static constexpr int LIST = T == 256 ? 1024 : 512;
+    Candidates<LIST> top;
+    uint32_t bound, most[T];
     float lnS;
     int works;
     uint16_t work[WORK];
-    float span[SPANS][LONG_T];
+    uint16_t span[SPANS][T];  // the upper halves of the maxima's ordered() values
 };
 
-template <bool BF16>
-__global__ void __launch_bounds__(LONG_T, 4) logprobs_long_kernel(const Score a)
+// Leaves those of the list that reach what K of it reach, by a whole CTA of T threads.
+template <int T, int LIST>
+__device__ __noinline__ int thin_list(int K, Key *list, int *count, uint32_t *bound)
 {
+    const int found = *count;
+    if (threadIdx.x < 32) {
+        uint32_t v[LIST / 32];
+#pragma unroll
+        for (int i = 0; i < LIST / 32; ++i) {
+            const int k = 32 * i + threadIdx.x;
+            v[i] = k < found ? static_cast<uint32_t>(list[k] >> 32) : 0u;
+        }
+        uint32_t t = 0;
+#pragma unroll 1
+        for (int at = 31; at >= 0; --at) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < LIST / 32; ++i)
+                n += v[i] >= (t | 1u << at);
+            if (__reduce_add_sync(0xffffffffu, n) >= K)
+                t |= 1u << at;
+        }
+        if (threadIdx.x == 0)
+            *bound = t;
+    }
+    Key mine[LIST / T];
+#pragma unroll
+    for (int i = 0; i < LIST / T; ++i) {
+        const int k = T * i + threadIdx.x;
+        mine[i] = k < found ? list[k] : 0;
+    }
+    __syncthreads();
+    const Key least = static_cast<Key>(*bound) << 32;
+    if (threadIdx.x == 0)
+        *count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < LIST / T; ++i)
+        if (mine[i] && mine[i] >= least)
+            append<LIST>(count, list, mine[i]);
+    __syncthreads();
+    return *count;
+}
+
+template <bool BF16, int T>
+__global__ void __launch_bounds__(T, T >= 128 ? 1024 / T : 12) logprobs_row_kernel(const Score a)
+{
+    constexpr int WARPS = T / 32, VT = ROW_VT, HALF = VT / 2, LANES = 4, LIST = RowShared<T>::LIST;
     extern __shared__ uint4 slots[];
-    __shared__ LongShared sh;
+    __shared__ RowShared<T> sh;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0)
         sh.top.count = sh.works = 0;
-    const Place at(1, LONG_T);
+    const Place at(1, T);
     const long long n = at.row;
     const RowPtr<BF16> row(a.x, n * a.ld, a.V);
-    using R = Run<BF16, LONG_T, LONG_VT>;
+    using R = Run<BF16, T, VT>;
     const R run(row, at, slots);
     const int each = (2 * run.groups + SPANS - 1) / SPANS;  // halves of a group in a span
     Running<true> sums;
@@ -317,91 +403,93 @@ __global__ void __launch_bounds__(LONG_T, 4) logprobs_long_kernel(const Score a)
     auto half = [&](float m) {
         top = max_nan(top, m);
         if (--left == 0) {
-            sh.span[span++][tid] = top;  // read by this thread alone
+            sh.span[span++][tid] = ordered(top) >> 16;  // read by this thread alone
             most = max_nan(most, top);
             top = -INFINITY;
             left = each;
         }
     };
-    run.template each<LONG_SLOTS>([&](const typename R::TileT &t, int) {
-        const float m0 = t.template max_of<0, HALF>(), m1 = t.template max_of<HALF, LONG_VT>();
+    run.template each<ROW_SLOTS>(false, [&](const typename R::TileT &t, int, int) {
+        const float m0 = t.template max_of<0, HALF>(), m1 = t.template max_of<HALF, VT>();
         sums.add(t, max_nan(m0, m1), a.z);
         half(m0);
         half(m1);
     });
     if (left != each) {
-        sh.span[span++][tid] = top;
+        sh.span[span++][tid] = ordered(top) >> 16;
         most = max_nan(most, top);
     }
     const uint32_t mine = most > -INFINITY ? ordered(most) : 0u;
-    const uint32_t named = a.K > 0 ? warp_rank<uint32_t>(mine, a.r - 1) : 0u;
-    const Part part = sums.part(most, a.z.c, named);
+    const Part part = sums.part(most, a.z, 0u);
     if (lane == 0)
         sh.top.parts[warp] = part;
+    sh.most[tid] = mine;
     __syncthreads();
-    if (warp == LONG_WARPS - 1) {
-        const Stats st = join(sh.top.parts, LONG_WARPS, a.z.c);
+    if (warp == WARPS - 1) {
+        const Stats st = join(sh.top.parts, WARPS, a.z.c);
         if (lane == 0) {
             write_scores(a, n, row, st);
-            sh.lnS = st.lnS;  // read by the others after the next barrier
+            sh.lnS = st.lnS;
         }
     }
     if (a.K == 0)
         return;
-    const Part mate = sh.top.parts[lane % LONG_WARPS];
-    const float m = warp_max_nan(mate.m);
+    if (warp == 0) {
+        uint32_t v[T / 32];
+#pragma unroll
+        for (int i = 0; i < T / 32; ++i)
+            v[i] = sh.most[32 * i + lane];
+        const uint32_t bound = reached(v, a.K);
+        if (lane == 0)
+            sh.bound = bound;
+    }
+    const float m = warp_max_nan(sh.top.parts[lane % WARPS].m);
+    __syncthreads();
     const bool plain = m > -INFINITY && m < INFINITY;
-    float least = -INFINITY;
-    if (plain) {
-        const uint32_t bound = warp_rank<uint32_t, LONG_WARPS>(mate.key, a.w - 1);
-        if (bound)
-            least = from_ordered(bound);
-        if (mine && mine >= bound) {
-            for (int s = 0; s < span; ++s) {
-                const float v = sh.span[s][tid];
-                if (v >= least && v > -INFINITY) {
-                    const int i = atomicAdd(&sh.works, 1);
-                    if (i < WORK)
-                        sh.work[i] = static_cast<uint16_t>(s * LONG_T + tid);
-                }
+    const uint32_t bound = sh.bound;
+    const float least = bound ? from_ordered(bound) : -INFINITY;
+    if (plain && mine && mine >= bound) {
+        const uint32_t need = max(bound, ordered(-FLT_MAX)) >> 16;  // (the bound's lower half is 0)
+#pragma unroll 4
+        for (int s = 0; s < span; ++s) {
+            if (sh.span[s][tid] >= need) {
+                const int i = atomicAdd(&sh.works, 1);
+                if (i < WORK)
+                    sh.work[i] = static_cast<uint16_t>(s * T + tid);
             }
         }
     }
     __syncthreads();
     int found = 0;
     if (plain) {
-        const int works = sh.works;
+        const int works = sh.works, vectors = each * HALF;
         if (works <= WORK) {
-            // HALF threads a span, each with one vector of every half group
-            for (int i = tid / HALF; i < works; i += LONG_T / HALF) {
-                const int item = sh.work[i], first = item / LONG_T * each, owner = item % LONG_T;
-                for (int h = first; h < first + each; ++h) {
-                    const int vec = (h * HALF + tid % HALF) * LONG_T + owner;
+#pragma unroll 1
+            for (int i = tid / LANES; i < works; i += T / LANES) {
+                const int item = sh.work[i], first = item / T * vectors, owner = item % T;
+#pragma unroll 1
+                for (int v = tid % LANES; v < vectors; v += LANES) {
+                    const int vec = (first + v) * T + owner;
                     if (vec >= row.nvec)
                         break;
-                    int id = row.first_id(vec);
-                    Tile<BF16, 1>::each_of(row.full(vec) ? row.load(vec) : row.load_edge(vec), [&](float p, float q) {
-                        if (max(p, q) >= least) {
-                            if (p >= least && p > -INFINITY)
-                                append<LONG_LIST>(&sh.top.count, sh.top.list, key_of(p, id));
-                            if (q >= least && q > -INFINITY)
-                                append<LONG_LIST>(&sh.top.count, sh.top.list, key_of(q, id + 1));
-                        }
-                        id += 2;
-                    });
+                    append_reaching<BF16, LIST>(&sh.top.count, sh.top.list,
+                                                     row.full(vec) ? row.load(vec) : row.load_edge(vec),
+                                                     row.first_id(vec), least);
                 }
             }
         }
         __syncthreads();
-        found = works <= WORK ? sh.top.count : LONG_LIST + 1;
-        if (found > LONG_LIST) {
+        found = works <= WORK ? sh.top.count : LIST + 1;
+        if (found > LIST) {
             list_by_key(a.K, row, at, sh.top);
             found = sh.top.count;
-            if (found > LONG_LIST) {
+            if (found > LIST) {
                 list_by_rounds(a.K, row, sh.top);
                 found = sh.top.count;
             }
         }
+        if (found > 2 * a.K + 64)  // (a short row, whose vectors are hardly more than K)
+            found = thin_list<T, LIST>(a.K, sh.top.list, &sh.top.count, &sh.bound);
     }
     write_top(a, n, m < INFINITY ? m : NAN, sh.lnS, sh.top.list, found);
 }
@@ -413,7 +501,7 @@ struct ScoreGrad {
     int V, per, runs;  // vectors of a run, runs of a row
     const int *tokens;
     const float *stats, *entropy, *g, *h;
-    float tau, c;
+    Scale z;
 };
 
 // A row is cut into runs that need nothing of one another: read, weighted, written.  With
@@ -435,24 +523,23 @@ __global__ void __launch_bounds__(T) logprobs_backward_kernel(const ScoreGrad a)
     const float g = a.g && has ? a.g[n] : 0.0f, h = a.h ? a.h[n] : 0.0f;
     const float m = a.stats[2 * n], off = -a.stats[2 * n + 1] * LOG2E;
     if (m == -INFINITY || (g == 0.0f && h == 0.0f)) {
-        for (int k = 0; k < run.groups; ++k)
-            run.put(typename R::TileT(), k, out, true, [](float, float) { return F2{0}; });
+        run.clear(out);
         return;
     }
-    const float A = -(g + (h != 0.0f ? h * a.entropy[n] : 0.0f)) / a.tau, B = -h * LN2 / a.tau;
+    const float A = -(g + (h != 0.0f ? h * a.entropy[n] : 0.0f)) * a.z.inv, B = -h * LN2 * a.z.inv;
     const int at = (row.skip + t) / row.PER;
     const bool mine = has && at >= run.begin && at < run.end;  // the same for the whole CTA
     float at_token = 0.0f;
     if (mine) {
         if (tid == 0) {
-            const float u = fmaf(row.at(t) - m, a.c, off);
-            at_token = ex2(u) * fmaf(B, fmaxf(u, -1e4f), A) + g / a.tau;
+            const float u = fmaf(row.at(t) - m, a.z.c, off);
+            at_token = ex2(u) * fmaf(B, fmaxf(u, -1e4f), A) + g * a.z.inv;
         }
         __syncthreads();  // the token's logit is read before its gradient may replace it
     }
-    const F2 neg = f2(-m, -m), cc = f2(a.c, a.c), oo = f2(off, off), AA = f2(A, A), BB = f2(B, B);
-    run.template each<PIECE_SLOTS>([&](const typename R::TileT &x, int k) {
-        run.put(x, k, out, false, [&](float p, float q) {
+    const F2 neg = f2(-m, -m), cc = f2(a.z.c, a.z.c), oo = f2(off, off), AA = f2(A, A), BB = f2(B, B);
+    run.template each<PIECE_SLOTS>(row.skip != out.skip, [&](const typename R::TileT &x, int k, int s) {
+        run.put(x, k, s, out, [&](float p, float q) {
             const float2 v = split(fma2(f2(p, q) + neg, cc, oo));
             const F2 w = f2(ex2(v.x), ex2(v.y));
             return w * fma2(BB, f2(fmaxf(v.x, -1e4f), fmaxf(v.y, -1e4f)), AA);
@@ -465,16 +552,54 @@ __global__ void __launch_bounds__(T) logprobs_backward_kernel(const ScoreGrad a)
     }
 }
 
-// Many rows, each of more than a tile a thread.
-bool is_long(long long N, long long nvec) { return N > 152 && nvec > MAX_THREADS * MAX_VPT / 2; }
-
-template <bool BF16>
-int launch_long(const Score &a, cudaStream_t stream)
+template <int T>
+int launch_row(const Score &a, bool bf16, long long nvec, cudaStream_t stream)
 {
-    constexpr size_t smem = static_cast<size_t>(LONG_SLOTS) * LONG_VT * LONG_T * 16;
-    if (int rc = allow_shared(logprobs_long_kernel<BF16>, smem))
+    const size_t most = static_cast<size_t>(ROW_SLOTS) * ROW_VT * T * 16;
+    const size_t smem = std::min(most, static_cast<size_t>((nvec + T - 1) / T) * T * 16);
+    auto *kernel = bf16 ? logprobs_row_kernel<true, T> : logprobs_row_kernel<false, T>;
+    if (int rc = allow_shared(kernel, smem))
         return rc;
-    return launch_rows(logprobs_long_kernel<BF16>, a, a.N, LONG_T, 1, smem, stream, "logprobs_long_kernel");
+    return launch_rows(kernel, a, a.N, T, 1, smem, stream, "logprobs_row_kernel");
+}
+
+template <int VPT>
+int launch_cluster(Score a, bool bf16, cudaStream_t stream)
+{
+    // r lanes of w warps make the threshold: about two thirds of the warps, so that one warp of
+    // small logits does not lower it
+    constexpr int WARPS = CLUSTER * CLUSTER_T / 32;
+    a.r = std::max(1, std::min(32, (5 * a.K + 3 * WARPS - 1) / (3 * WARPS)));
+    a.w = (a.K + a.r - 1) / a.r;
+    return launch_rows(bf16 ? logprobs_cluster_kernel<true, VPT> : logprobs_cluster_kernel<false, VPT>, a,
+                       a.N * CLUSTER, CLUSTER_T, CLUSTER, 0, stream, "logprobs_cluster_kernel");
+}
+
+// Which kernel, and how many threads a row.  us on GB300, K = 20 unless said otherwise:
+//   bf16 rows of logits          eight CTAs a row   one CTA of 256 threads
+//     1 / 8 / 16 / 32 of  32768   4.7 / 5.4 / 5.6 / 7.0    5.7 / 6.1 / 6.2 / 6.2
+//     1 / 8 / 16 / 32 of 131072   5.7 / 6.3 / 6.9 / 8.5   11.5 / 11.6 / 11.5 / 11.6
+//     1 of 8192 / 16384           4.9 / 4.8                4.4 / 4.9
+//   8000 bf16 rows of 1000 / 5000 / 9000 logits: 32 threads 28 / 44 / 52, 64: 28 / 39 / 49, 128: 37 / 48 /
+//     59, 256: 64 / 75 / 89; 1000 of 17000: 64 threads 16.3, 128 12.8, 256 16.8; 2000 f32 of 32768: 128
+//     threads 47, 256 51; 4096 of 131072 (K = 64): 128 threads 205, 256 182.
+// The threshold comes from the threads' maxima, so there are at least 2 K threads.
+int launch_scores(const Score &a, bool bf16, long long nvec, cudaStream_t stream)
+{
+    if ((a.N * CLUSTER <= SMS && nvec >= 3072) || (a.N * CLUSTER <= 2 * SMS && nvec >= 8192)) {
+        const long long per = (nvec + CLUSTER - 1) / CLUSTER;
+        return per <= 2 * CLUSTER_T   ? launch_cluster<2>(a, bf16, stream)
+               : per <= 4 * CLUSTER_T ? launch_cluster<4>(a, bf16, stream)
+                                      : launch_cluster<8>(a, bf16, stream);
+    }
+    const bool full = a.N > 2 * SMS;
+    if (nvec <= (full ? 160 : 32) && a.K <= 16)
+        return launch_row<32>(a, bf16, nvec, stream);
+    if (nvec <= (full ? 1536 : 96) && a.K <= 32)
+        return launch_row<64>(a, bf16, nvec, stream);
+    if (nvec <= (full ? 8192 : 512) && a.K <= 64)
+        return launch_row<128>(a, bf16, nvec, stream);
+    return launch_row<256>(a, bf16, nvec, stream);
 }
 
 }  // namespace
@@ -502,29 +627,22 @@ extern "C" int spec_logprobs(const void *logits, int logit_dtype, int N, int V, 
                           static_cast<const void *>(dev_status)})
         if (!rows::aligned4(p))
             return fail(KDA_EINVAL, "4-byte arrays must be 4-byte aligned");
+    Score a{};
+    a.x = logits;
+    a.ld = ld;
+    a.N = N;
+    a.V = V;
+    a.K = K;
+    a.tokens = tokens;
+    a.z = Scale{LOG2E / temperature, 16.0f * LN2 * temperature, 1.0f / temperature};
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.stats = stats;
+    a.top_logprobs = top_logprobs;
+    a.top_ids = top_ids;
+    a.status = dev_status;
     const bool bf16 = logit_dtype == KDA_BF16;
-    const long long nvec = rows::vectors_of(logits, V, ld, bf16);
-    Score a{logits, ld, N, V, K, 1, 1, 1, tokens, temperature,
-            Scale{rows::LOG2E / temperature, 16.0f * rows::LN2 * temperature}, logprob, entropy, stats,
-            top_logprobs, top_ids, dev_status};
-    // r lanes of w warps make the threshold: about two thirds of the warps, so that one warp of
-    // small logits does not lower it
-    auto threshold = [&](int warps) {
-        a.r = std::max(1, std::min(32, (5 * K + 3 * warps - 1) / (3 * warps)));
-        a.w = (K + a.r - 1) / a.r;
-    };
-    if (is_long(N, nvec)) {
-        threshold(LONG_WARPS);
-        return bf16 ? launch_long<true>(a, stream) : launch_long<false>(a, stream);
-    }
-    const Shape sh = rows::shape_of(N, nvec);
-    a.cl = sh.cl;
-    threshold(sh.cl * sh.threads / 32);
-    return rows::with_vpt(sh.vpt, [&](auto vpt) {
-        constexpr int VPT = decltype(vpt)::value;
-        return rows::launch_rows(bf16 ? logprobs_kernel<true, VPT> : logprobs_kernel<false, VPT>, a,
-                                 static_cast<long long>(N) * sh.cl, sh.threads, sh.cl, 0, stream, "logprobs_kernel");
-    });
+    return launch_scores(a, bf16, vectors_of(logits, V, ld, bf16), stream);
 }
 
 extern "C" int spec_logprobs_backward(const void *logits, int logit_dtype, int N, int V, long long ld,
@@ -554,7 +672,8 @@ extern "C" int spec_logprobs_backward(const void *logits, int logit_dtype, int N
     const bool bf16 = logit_dtype == KDA_BF16;
     const rows::Pieces cut = rows::pieces_of(rows::vectors_of(logits, V, ld, bf16));
     const ScoreGrad a{logits, dlogits, ld, ldg, V, cut.per, cut.runs, tokens, stats, entropy, grad_logprob,
-                      grad_entropy, temperature, rows::LOG2E / temperature};
+                      grad_entropy,
+                      Scale{rows::LOG2E / temperature, 0.0f, 1.0f / temperature}};
     return rows::with_threads(cut.threads, [&](auto threads) {
         constexpr int T = decltype(threads)::value;
         auto *kernel = bf16 ? logprobs_backward_kernel<true, T> : logprobs_backward_kernel<false, T>;
