@@ -50,9 +50,10 @@ struct __align__(16) Entries {
     float Q;                 // sum of q: 1 for renormalised entries, 0 without any, NaN for a NaN
 };
 
-// One warp reads a row's entries in three steps, so that the latencies of the loads can be
-// spent on something else: ids and values, the student's logits at the ids, the
-// probabilities.
+// One warp reads a row's entries in steps, so that the latencies of the loads can be spent on
+// something else: load() ids and values, gather() the student's logits at the ids, finish()
+// the probabilities, keep() those logits, once() ids listed twice.  gather() comes before and
+// keep() after the barrier behind which the gradient may replace the logits.
 template <bool BF16>
 struct Reader {
     int id[EACH];
@@ -117,15 +118,25 @@ struct Reader {
             t.off[lane + 32 * i] = q;
             t.q[lane + 32 * i] = q;
             t.lnq[lane + 32 * i] = v[i] - ref - lnsum;
-            t.x[lane + 32 * i] = x[i];
         }
         if (lane == 0)
             t.Q = whole && Q == Q ? 1.0f : Q;
+    }
+    __device__ __forceinline__ void keep(Entries &t) const
+    {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            t.x[(threadIdx.x & 31) + 32 * i] = x[i];
         __syncwarp();
-        // an id listed twice: its first entry takes every q off
+    }
+    // An id listed twice: its first entry takes every q off.  Not needed before the gradient's
+    // corrections, so it is done while the others write the gradient.
+    __device__ __forceinline__ void once(const Distill &a, Entries &t)
+    {
+        const int lane = threadIdx.x & 31;
         int same[EACH] = {};
         const int4 *ids = reinterpret_cast<const int4 *>(t.id);
-#pragma unroll 1
+#pragma unroll 2
         for (int j = 0; j < (a.K + 3) / 4; ++j) {
             const int4 o = ids[j];
 #pragma unroll
@@ -137,30 +148,30 @@ struct Reader {
 #pragma unroll
         for (int i = 0; i < EACH; ++i)
             twice |= id[i] >= 0 && same[i] > 1;
-        if (__any_sync(0xffffffffu, twice)) {
+        if (!__any_sync(0xffffffffu, twice))
+            return;
 #pragma unroll
-            for (int i = 0; i < EACH; ++i) {
-                const int k = lane + 32 * i;
-                if (id[i] >= 0 && same[i] > 1) {
-                    float q = 0.0f;
+        for (int i = 0; i < EACH; ++i) {
+            const int k = lane + 32 * i;
+            if (id[i] >= 0 && same[i] > 1) {
+                float q = 0.0f;
 #pragma unroll 1
-                    for (int j = 0; j < a.K; ++j) {
-                        if (t.id[j] == id[i]) {
-                            if (j < k) {
-                                id[i] = -1;
-                                break;
-                            }
-                            q += t.q[j];
+                for (int j = 0; j < a.K; ++j) {
+                    if (t.id[j] == id[i]) {
+                        if (j < k) {
+                            id[i] = -1;
+                            break;
                         }
+                        q += t.q[j];
                     }
-                    t.off[k] = q;
                 }
+                t.off[k] = q;
             }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < EACH; ++i)
-                t.id[lane + 32 * i] = id[i];
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            t.id[lane + 32 * i] = id[i];
     }
 };
 
@@ -251,8 +262,8 @@ __global__ void __launch_bounds__(T + 32, T == 256 ? 4 : T == 128 ? 6 : 8) disti
     at.arrive();
     const float scale = GRAD ? w * a.tau * g : 0.0f;
     const int lo = max(0, row.first_id(run.begin)), hi = min(a.V, row.first_id(run.end));
+    Reader<BF16> r;
     if (reader) {
-        Reader<BF16> r;
         r.load(a, n);
         // the first CTA reads every entry's logit for the loss
         r.gather(a, row, at.rank ? lo : 0, at.rank ? hi : a.V);
@@ -291,8 +302,11 @@ __global__ void __launch_bounds__(T + 32, T == 256 ? 4 : T == 128 ? 6 : 8) disti
     const bool zero = st.empty() || t.Q == 0.0f || scale == 0.0f;
     const float off = -st.lnS * LOG2E, m = st.m, sq = scale * t.Q;
     if (reader) {
+        r.keep(t);
         if (at.rank == 0)
             write_loss(a, n, w, st, t);
+        if (GRAD)
+            r.once(a, t);
     } else {
         auto value = [&](float p, float q) { return weighted(p, q, m, a.z.c, off, sq); };
         if (zero) {
@@ -344,7 +358,9 @@ __global__ void __launch_bounds__(T + 32) distill_backward_kernel(const Distill 
         r.load(a, n);
         r.gather(a, row, lo, hi);
         r.finish(a, t);
-        meet();  // the entries are there, and the logits at them have been read
+        meet();  // Q is there, and the logits at the ids have been read
+        r.keep(t);
+        r.once(a, t);
     } else if (out_of_it) {
         run.clear(out);
         return;
