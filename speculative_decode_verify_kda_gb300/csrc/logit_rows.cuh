@@ -5,8 +5,8 @@
 // of which takes a run of the row's vectors.  They pass through shared memory ahead of their
 // use (Run); a thread works on a few of them at a time, in registers (Tile).
 //
-// The sums are taken relative to the warp's own maximum, and a warp's triple (maximum, sum
-// of weights, weighted sum of exponents) joins the others' once, through the shared memory
+// The sums are taken relative to a logit of the warp's own (Running), and a warp's triple
+// (maximum, sum of weights, weighted sum of exponents) joins the others' once, through the shared memory
 // of the CTA or of every CTA of the cluster: one barrier between reading a row and knowing
 // its statistics.
 #pragma once
@@ -595,7 +595,10 @@ struct Place {
 // ---------------------------------------------------------------------------
 // Each of T threads copies the vectors that it will use into slots of its own in shared
 // memory, groups of VT vectors ahead of their use (cp.async): nothing has to be waited for
-// but the thread's own copies.
+// but the thread's own copies, and a vector that crosses an end of the row is read element
+// by element by the thread that uses it.  (A row per CTA, several CTAs an SM: CTAs that stay
+// and take row after row through such slots measured slower, 364 against 170 us for the step
+// on 8192 bf16 rows of 32768: what is done once a row costs more than a CTA's start.)
 
 // Waits until at most `pending` of the thread's newest groups of copies are under way.
 __device__ __forceinline__ void copies_done(int pending)
@@ -735,12 +738,15 @@ struct Run {
     }
 };
 
-// Allows a kernel the shared memory that it is launched with.
+// Allows a kernel `most` bytes of dynamic shared memory, the same number at every call: calls of
+// other host threads may lie between this one and its launch.
 template <class A>
-inline int allow_shared(void (*kernel)(A), size_t bytes)
+inline int allow_shared(void (*kernel)(A), size_t most)
 {
+    if (most <= 24 * 1024)  // with what the kernels hold besides, below what needs no leave
+        return KDA_OK;
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess)
         return fail(KDA_ECUDA, std::string("shared memory: ") + cudaGetErrorString(e));
     return KDA_OK;
@@ -755,8 +761,10 @@ inline long long vectors_of(const void *p, int V, long long ld, int bf16)
 }
 
 // A pass that needs nothing of the rest of a row: CTAs of T threads, each with a run of up to
-// RUN_GROUPS groups of PIECE_VT vectors a thread, which pass through PIECE_SLOTS slots.
+// RUN_GROUPS groups of PIECE_VT vectors a thread, which pass through PIECE_SLOTS slots.  Runs of
+// 2 / 4 / 8 / 16 groups took 87 / 79 / 81 / 88 us for the gradient of 1024 f32 rows of 65537.
 constexpr int PIECE_VT = 4, PIECE_SLOTS = 3;
+constexpr size_t piece_shared(int threads) { return static_cast<size_t>(PIECE_SLOTS) * PIECE_VT * threads * 16; }
 
 struct Pieces {
     int threads, per, runs;  // per: vectors of a run

@@ -400,11 +400,16 @@ int check_teacher(const kda_teacher *t, int N)
     return KDA_OK;
 }
 
+// Vectors of a run with which an SM holds three CTAs, or two.
+constexpr long long THREE = 4480, TWO = 6912;
+
 template <int T, bool GRAD, bool HELD>
-int launch_with(const Distill &a, bool bf16, size_t smem, cudaStream_t stream)
+int launch_with(const Distill &a, bool bf16, long long per, cudaStream_t stream)
 {
+    constexpr size_t most = (HELD ? TWO : ROW_SLOTS * ROW_VT * T) * 16;
+    const size_t smem = std::min(most, static_cast<size_t>(per) * 16);
     auto *kernel = bf16 ? distill_kernel<true, T, GRAD, HELD> : distill_kernel<false, T, GRAD, HELD>;
-    if (int rc = allow_shared(kernel, smem))
+    if (int rc = allow_shared(kernel, most))
         return rc;
     return launch_rows(kernel, a, a.N * a.cl, T + 32, a.cl, smem, stream, "distill_kernel");
 }
@@ -418,15 +423,13 @@ template <bool GRAD, bool HELD>
 int launch_held(const Distill &a, bool bf16, long long per, cudaStream_t stream)
 {
     const bool full = a.N * a.cl > 2 * SMS;
-    const size_t most = static_cast<size_t>(per) * 16;
-    auto smem = [&](int t) { return HELD ? most : std::min<size_t>(most, ROW_SLOTS * ROW_VT * t * 16); };
     if (per <= (full ? 400 : 32))
-        return launch_with<32, GRAD, HELD>(a, bf16, smem(32), stream);
+        return launch_with<32, GRAD, HELD>(a, bf16, per, stream);
     if (per <= (full ? 1536 : 96))
-        return launch_with<64, GRAD, HELD>(a, bf16, smem(64), stream);
+        return launch_with<64, GRAD, HELD>(a, bf16, per, stream);
     if (per <= (full ? 2880 : 1024))
-        return launch_with<128, GRAD, HELD>(a, bf16, smem(128), stream);
-    return launch_with<256, GRAD, HELD>(a, bf16, smem(256), stream);
+        return launch_with<128, GRAD, HELD>(a, bf16, per, stream);
+    return launch_with<256, GRAD, HELD>(a, bf16, per, stream);
 }
 
 template <bool GRAD>
@@ -435,8 +438,8 @@ int launch(Distill a, int dtype, cudaStream_t stream)
     const bool bf16 = dtype == KDA_BF16;
     const long long nvec = vectors_of(a.x, a.V, a.ld, bf16);
     // With a gradient a run is held if an SM then has three CTAs (or two, where eight CTAs a row
-    // cannot do better); beyond that a row is read twice by one CTA.
-    constexpr long long THREE = 4480, TWO = 6912;
+    // cannot do better); beyond that a row is read twice by one CTA.  Held against read twice, us:
+    // 4096 bf16 rows of 131072 (four CTAs a row) 332 against 456, 480 of 32768 14.3 against 17.2.
     a.cl = 1;
     bool held = GRAD;
     if (GRAD) {
@@ -465,7 +468,7 @@ int launch_backward(Distill a, int dtype, cudaStream_t stream)
     return with_threads(cut.threads, [&](auto threads) {
         constexpr int T = decltype(threads)::value;
         auto *kernel = bf16 ? distill_backward_kernel<true, T> : distill_backward_kernel<false, T>;
-        if (int rc = allow_shared(kernel, cut.shared))
+        if (int rc = allow_shared(kernel, piece_shared(T)))
             return rc;
         return launch_rows(kernel, a, a.N * cut.runs, T + 32, 1, cut.shared, stream, "distill_backward_kernel");
     });

@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(CLUSTER_T) logprobs_cluster_kernel(const Score
                     Tile<BF16, 1> one;
                     one.v[0] = t.v[j];
                     if (one.max_of() >= least)
-                        append_reaching<BF16, CLUSTER_LIST>(count, list, t.v[j], row.first_id(b + tid + j * step), least);
+                        append_reaching<BF16, CLUSTER_LIST>(count, list, t.v[j], row.first_id(b + tid + j * step),
+                                                            least);
                 }
                 b += round;
             } while (b < end);
@@ -319,10 +320,12 @@ __global__ void __launch_bounds__(CLUSTER_T) logprobs_cluster_kernel(const Score
     at.wait();
 }
 
-// One CTA a row, which passes through shared memory ahead of its use.  A
-// thread keeps the maxima of up to SPANS equal spans of its share of the row, half a group or
-// a multiple.  The threshold is the K-th largest of the threads' maxima, to 16 bits; the
-// spans that reach it are read again, through L2, to fill the list.
+// One CTA a row, which passes through shared memory ahead of its use.  A thread keeps the
+// maxima of up to SPANS equal spans of its share of the row, half a group or a multiple.  The
+// threshold is the K-th largest of the threads' maxima, to 16 bits; the spans that reach it
+// are read again, through L2, to fill the list.  Without alternatives 4096 bf16 rows of 131072
+// take 163 us (6.6 TB/s), with 64 of them 184: what bounds it is the instructions (about 7 an
+// element, of which the sums are 4.9), no longer the reads.
 constexpr int ROW_VT = 4, ROW_SLOTS = 2, SPANS = 16, WORK = 1024;
 
 template <int T>
@@ -473,8 +476,8 @@ __global__ void __launch_bounds__(T, T >= 128 ? 1024 / T : 12) logprobs_row_kern
                     if (vec >= row.nvec)
                         break;
                     append_reaching<BF16, LIST>(&sh.top.count, sh.top.list,
-                                                     row.full(vec) ? row.load(vec) : row.load_edge(vec),
-                                                     row.first_id(vec), least);
+                                                row.full(vec) ? row.load(vec) : row.load_edge(vec),
+                                                row.first_id(vec), least);
                 }
             }
         }
@@ -527,8 +530,8 @@ __global__ void __launch_bounds__(T) logprobs_backward_kernel(const ScoreGrad a)
         return;
     }
     const float A = -(g + (h != 0.0f ? h * a.entropy[n] : 0.0f)) * a.z.inv, B = -h * LN2 * a.z.inv;
-    const int at = (row.skip + t) / row.PER;
-    const bool mine = has && at >= run.begin && at < run.end;  // the same for the whole CTA
+    const int at = has ? (row.skip + t) / row.PER : -1;
+    const bool mine = at >= run.begin && at < run.end;  // the same for the whole CTA
     float at_token = 0.0f;
     if (mine) {
         if (tid == 0) {
@@ -558,7 +561,7 @@ int launch_row(const Score &a, bool bf16, long long nvec, cudaStream_t stream)
     const size_t most = static_cast<size_t>(ROW_SLOTS) * ROW_VT * T * 16;
     const size_t smem = std::min(most, static_cast<size_t>((nvec + T - 1) / T) * T * 16);
     auto *kernel = bf16 ? logprobs_row_kernel<true, T> : logprobs_row_kernel<false, T>;
-    if (int rc = allow_shared(kernel, smem))
+    if (int rc = allow_shared(kernel, most))
         return rc;
     return launch_rows(kernel, a, a.N, T, 1, smem, stream, "logprobs_row_kernel");
 }
@@ -672,12 +675,11 @@ extern "C" int spec_logprobs_backward(const void *logits, int logit_dtype, int N
     const bool bf16 = logit_dtype == KDA_BF16;
     const rows::Pieces cut = rows::pieces_of(rows::vectors_of(logits, V, ld, bf16));
     const ScoreGrad a{logits, dlogits, ld, ldg, V, cut.per, cut.runs, tokens, stats, entropy, grad_logprob,
-                      grad_entropy,
-                      Scale{rows::LOG2E / temperature, 0.0f, 1.0f / temperature}};
+                      grad_entropy, Scale{rows::LOG2E / temperature, 0.0f, 1.0f / temperature}};
     return rows::with_threads(cut.threads, [&](auto threads) {
         constexpr int T = decltype(threads)::value;
         auto *kernel = bf16 ? logprobs_backward_kernel<true, T> : logprobs_backward_kernel<false, T>;
-        if (int rc = rows::allow_shared(kernel, cut.shared))
+        if (int rc = rows::allow_shared(kernel, rows::piece_shared(T)))
             return rc;
         return rows::launch_rows(kernel, a, static_cast<long long>(N) * cut.runs, T, 1, cut.shared, stream,
                                  "logprobs_backward_kernel");

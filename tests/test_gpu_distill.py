@@ -265,8 +265,7 @@ def test_scores_are_a_teacher():
 
 
 # ---------------------------------------------------------------------------
-# many long rows: the kernels whose CTAs stay and take row after row.  The 64-bit values are
-# formed for some of the rows.
+# many long rows.  The 64-bit values are formed for some of the rows.
 # ---------------------------------------------------------------------------
 def copy_of(t):
     """The same values at the same place within a vector (whose sums are formed alike)."""
@@ -375,3 +374,50 @@ def test_many_long_rows_with_bad_rows_and_strides():
     rest = torch.ones_like(dst, dtype=torch.bool)
     rest[7:7 + N * ld].view(N, ld)[:, :V] = False
     assert (dst[rest] == 7).all(), "written outside its rows"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 19, 38, 76, 77, 153, 305])
+@pytest.mark.parametrize("V,K", [(257, 5), (3201, 33), (12288, 20), (23041, 64), (35840, 7), (35848, 128)])
+def test_around_every_choice_of_kernel(N, V, K, dtype):
+    """Rows and lengths on both sides of where the launch changes."""
+    if N * V > 8e6:
+        N = N % 100 + 1
+    x = ref.rows("peaked", N, V, dtype, N + V)
+    ids, values = entries(N, V, K, V, "repeated" if K == 33 else "short" if K == 20 else "distinct")
+    w, g = weights(N, 3)
+    check_some(x, ids, values, 1.0, dtype, w, g, which=sorted({0, N // 2, N - 1}))
+
+
+def test_a_step_of_several_host_threads():
+    """Held runs of different sizes are launched from several threads at once."""
+    import threading
+    shapes = [(200, 33000), (200, 60000), (200, 9000), (4, 33000)]
+    data = []
+    for N, V in shapes:
+        x = ref.rows("normal", N, V, "bf16", N + V)
+        ids, values = entries(N, V, 9, 4)
+        data.append((x, ids, values, dev(x, "bf16"), to_dev(ids), to_dev(values)))
+    torch.cuda.synchronize()
+    got, wrong = {}, []
+
+    def work(j):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                got[j] = kb.spec_distill_step(*data[j][3:], stream=s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in range(len(shapes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    for j in range(len(shapes)):
+        x, ids, values = (a[:2] for a in data[j][:3])
+        loss, _, grad, P, D = ref.distill(x, ids, values, 1.0)
+        same_or_near(got[j][0][:2], loss, 4e-5 + 1e-5 * np.abs(loss), "loss")
+        same_or_near(got[j][2][:2].float(), grad, 5e-5 * (P + D) + 1e-30 + 2.0**-8 * np.abs(grad), "gradient")

@@ -307,8 +307,7 @@ def test_backward_against_differences():
 
 
 # ---------------------------------------------------------------------------
-# many long rows: the kernels whose CTAs stay and take row after row.  The 64-bit values are
-# formed for some of the rows.
+# many long rows.  The 64-bit values are formed for some of the rows.
 # ---------------------------------------------------------------------------
 def some(N):
     return sorted({0, 1, N // 3, N // 2, N - 2, N - 1})
@@ -373,3 +372,74 @@ def test_many_long_rows_give_what_few_give(dtype):
     again = kb.spec_logprobs(t, tok, 30)
     for a, b in zip(many, again):
         assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 19, 20, 38, 39, 304, 305])
+@pytest.mark.parametrize("V,K", [(24576, 20), (24584, 128), (12289, 33), (65535, 5), (770, 16), (1281, 17)])
+def test_around_every_choice_of_kernel(N, V, K, dtype):
+    """Rows, lengths and numbers of alternatives on both sides of where the launch changes."""
+    if N * V > 8e6:
+        N = N % 100 + 1
+    x = ref.rows("peaked", N, V, dtype, N + V)
+    check_some(x, tokens_for(N, V, 3), K, 1.0, dtype) if N > 2 else check(x, tokens_for(N, V, 3), K, 1.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [16, 17, 32, 33, 64, 65, 128])
+@pytest.mark.parametrize("V", [40, 130, 257, 511, 1000, 1100, 2100])
+def test_short_rows_with_many_alternatives(V, K, dtype):
+    for kind in ("normal", "two_values"):
+        for N in (3, 310):
+            x = ref.rows(kind, N, V, dtype, V + K)
+            check_some(x, tokens_for(N, V, 3), K, 1.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [2, 30, 400])
+@pytest.mark.parametrize("V", [20000, 150001])
+def test_large_logits_in_the_vectors_of_few_threads(V, N, dtype):
+    """More logits than a list holds, above all others, repeat at the distance at which threads
+    take vectors: no threshold from the threads' maxima tells them apart."""
+    if N * V > 2e7:
+        N = 40
+    i = np.arange(V)
+    row = np.where(i % 512 < 96, 8.0 + (i % 6007) * 2.0**-10, (i % 13) * 0.25).astype(np.float32)
+    x = ref.typed(np.tile(row, (N, 1)), dtype)
+    check_some(x, tokens_for(N, V, 3), 20, 1.0, dtype) if N > 2 else check(x, tokens_for(N, V, 3), 20, 1.0, dtype)
+
+
+def test_calls_from_several_host_threads():
+    """Calls of different shapes from several threads, each on a stream of its own."""
+    import threading
+    shapes = [(400, 33000, 20), (400, 9000, 20), (3, 33000, 5), (400, 100, 5)]
+    xs = [ref.rows("normal", N, V, "bf16", N + V) for N, V, _ in shapes]
+    ts = [dev(x, "bf16") for x in xs]
+    ones = torch.ones(400, device="cuda")
+    torch.cuda.synchronize()
+    got, wrong = {}, []
+
+    def work(j):
+        try:
+            N, V, K = shapes[j]
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                out = kb.spec_logprobs(ts[j], None, K, stream=s)
+                d = kb.spec_logprobs_backward(ts[j], None, out[2], out[1],
+                                              grad_entropy=ones[:N], stream=s)
+            s.synchronize()
+            got[j] = (out, d)
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in range(len(shapes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    for j, (N, V, K) in enumerate(shapes):
+        want = ref.score(xs[j][:2], None, K, 1.0)
+        assert np.array_equal(got[j][0][3][:2].cpu().numpy(), want[3])
+        near(got[j][0][2][:2], want[2], 1e-5, 1e-6, "stats")
+        assert torch.isfinite(got[j][1].float()).all()

@@ -25,7 +25,7 @@ def score(L, **k):
                            k.get("stats", FAKE), k.get("ids", FAKE), k.get("top", FAKE), k.get("st"), None)
 
 
-BAD = [{"N": -1}, {"V": 0}, {"V": -5}, {"ld": 99}, {"dt": 2}, {"dt": -1}, {"x": None}, {"x": FAKE + 1},
+BAD = [{"N": -1}, {"V": 0}, {"V": -5}, {"V": 2**30 + 1, "ld": 2**31}, {"ld": 99}, {"dt": 2}, {"dt": -1}, {"x": None}, {"x": FAKE + 1},
        {"x": FAKE + 2, "dt": kb.F32}, {"tau": 0.0}, {"tau": -1.0}, {"tau": float("nan")}, {"tau": float("inf")},
        {"tau": 1e-5}, {"tau": 1e5}]
 
