@@ -864,7 +864,9 @@ class _LogitPlan:
         return None if t is None else self._in(t, "dev_status", torch.int32, tuple(t.shape))
 
     def _bind(self, *rest):
-        self._args = (*self._head, *rest, ctypes.c_void_p(_stream(self.stream)))
+        args = (*self._head, *rest, ctypes.c_void_p(_stream(self.stream)))
+        # numbers as C numbers: converted here, not at every call
+        self._args = tuple(t(a) if isinstance(a, (int, float)) else a for t, a in zip(self._fn.argtypes, args))
 
     def __call__(self):
         rc = self._fn(*self._args)

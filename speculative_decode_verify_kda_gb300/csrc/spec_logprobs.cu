@@ -532,16 +532,11 @@ __global__ void __launch_bounds__(T) logprobs_backward_kernel(const ScoreGrad a)
     const float A = -(g + (h != 0.0f ? h * a.entropy[n] : 0.0f)) * a.z.inv, B = -h * LN2 * a.z.inv;
     const int at = has ? (row.skip + t) / row.PER : -1;
     const bool mine = at >= run.begin && at < run.end;  // the same for the whole CTA
-    float at_token = 0.0f;
-    if (mine) {
-        if (tid == 0) {
-            const float u = fmaf(row.at(t) - m, a.z.c, off);
-            at_token = ex2(u) * fmaf(B, fmaxf(u, -1e4f), A) + g * a.z.inv;
-        }
-        __syncthreads();  // the token's logit is read before its gradient may replace it
-    }
+    const float x_token = mine && tid == 0 ? row.at(t) : 0.0f;
     const F2 neg = f2(-m, -m), cc = f2(a.z.c, a.z.c), oo = f2(off, off), AA = f2(A, A), BB = f2(B, B);
     run.template each<PIECE_SLOTS>(row.skip != out.skip, [&](const typename R::TileT &x, int k, int s) {
+        if (k == 0 && mine)
+            __syncthreads();  // the token's logit is read before its gradient may replace it
         run.put(x, k, s, out, [&](float p, float q) {
             const float2 v = split(fma2(f2(p, q) + neg, cc, oo));
             const F2 w = f2(ex2(v.x), ex2(v.y));
@@ -550,8 +545,10 @@ __global__ void __launch_bounds__(T) logprobs_backward_kernel(const ScoreGrad a)
     });
     if (mine) {
         __syncthreads();  // after the element's ordinary value
-        if (tid == 0)
-            out.set(t, at_token);
+        if (tid == 0) {
+            const float u = fmaf(x_token - m, a.z.c, off);
+            out.set(t, ex2(u) * fmaf(B, fmaxf(u, -1e4f), A) + g * a.z.inv);
+        }
     }
 }
 
