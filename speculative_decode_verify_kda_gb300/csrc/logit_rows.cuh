@@ -553,8 +553,13 @@ struct Place {
     __device__ __forceinline__ int begin(int nvec) const { return rank * per(nvec); }
     __device__ __forceinline__ int end(int nvec) const { return min(nvec, (rank + 1) * per(nvec)); }
     __device__ __forceinline__ int per(int nvec) const { return (nvec + cl - 1) >> shift; }
-    // Every CTA of the cluster runs from here on.  Between the two calls: anything that stays
-    // inside the CTA.
+    // started() ... wait(): every CTA of the cluster runs from here on, so its shared memory may
+    // be written.  arrive() ... wait(): what a CTA wrote before is seen by all after.
+    __device__ __forceinline__ void started() const
+    {
+        if (cl > 1)
+            asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    }
     __device__ __forceinline__ void arrive() const
     {
         if (cl > 1)

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(T + 32, T == 256 ? 4 : T == 128 ? 6 : 8) disti
             run.clear(out);
         return;
     }
-    at.arrive();
+    at.started();
     const float scale = GRAD ? w * a.tau * g : 0.0f;
     const int lo = max(0, row.first_id(run.begin)), hi = min(a.V, row.first_id(run.end));
     Reader<BF16> r;

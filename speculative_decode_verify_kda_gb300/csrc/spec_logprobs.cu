@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(CLUSTER_T) logprobs_cluster_kernel(const Score
     const int tid = threadIdx.x;
     if (tid == 0)
         sh.count = 0;
-    at.arrive();
+    at.started();
     const RowPtr<BF16> row(a.x, at.row * a.ld, a.V);
     const int begin = at.begin(row.nvec), end = at.end(row.nvec), step = CLUSTER_T, round = step * VPT;
     Tile<BF16, VPT> t;
