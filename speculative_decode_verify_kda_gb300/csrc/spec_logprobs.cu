@@ -323,9 +323,11 @@ __global__ void __launch_bounds__(CLUSTER_T) logprobs_cluster_kernel(const Score
 // One CTA a row, which passes through shared memory ahead of its use.  A thread keeps the
 // maxima of up to SPANS equal spans of its share of the row, half a group or a multiple.  The
 // threshold is the K-th largest of the threads' maxima, to 16 bits; the spans that reach it
-// are read again, through L2, to fill the list.  Without alternatives 4096 bf16 rows of 131072
-// take 163 us (6.6 TB/s), with 64 of them 184: what bounds it is the instructions (about 7 an
-// element, of which the sums are 4.9), no longer the reads.
+// are read again, through L2, to fill the list.  4096 bf16 rows of 131072 take 153 us without
+// alternatives (7.0 TB/s: the reads bound it), 166 with 20 and 185 with 64: a CTA that looks
+// for alternatives reads nothing ahead, and what it reads again is 5 % more (to 32 bytes a
+// vector).  Two slots, not three or four: four CTAs an SM hide more than deeper slots do
+// (three slots and CTAs 195 us, 512 threads and two CTAs 219).
 constexpr int ROW_VT = 4, ROW_SLOTS = 2, SPANS = 16, WORK = 1024;
 
 template <int T>
