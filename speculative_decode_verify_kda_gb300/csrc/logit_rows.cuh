@@ -391,7 +391,8 @@ __device__ __forceinline__ void store_tile(const Tile<BF16, VPT> &t, const RowPt
     }
 }
 
-// What a warp hands to the others: its maximum and sums, and a value of its largest ones.
+// What a warp hands to the others: its maximum, its sums without the maximum's own term (whose
+// weight is 1), and a value of its largest ones.
 struct __align__(16) Part {
     float m, S, E;
     uint32_t key;
@@ -495,13 +496,23 @@ struct Running {
         s = s + ts;
     }
 
-    // The warp's part, from the lanes' largest logits.
+    // The warp's part, from the lanes' largest logits.  The largest one's own term is 1 and its
+    // exponent 0: what was added for it is taken back out of its lane's sums (it was formed by the
+    // same operations), so that in a row where one token has nearly everything the others'
+    // share is not lost in the rounding of that one exponential.
     __device__ __forceinline__ Part part(float most, Scale z, uint32_t key) const
     {
         const float top = warp_max_nan(most);
         float S = 0.0f, E = 0.0f;
-        if (top != -INFINITY)
-            settle(top, z, S, E);
+        if (top != -INFINITY) {
+            const float2 s2 = split(s), e2 = split(e);
+            const float own = fmaf(top, c, -ref), w_own = ex2(own);
+            const unsigned lanes = __ballot_sync(0xffffffffu, most == top);
+            const bool here = lanes && (threadIdx.x & 31) == __ffs(lanes) - 1;
+            const float left = fmaf(at, c, -ref), d = (at - top) * z.c - left, w = ex2(d);
+            S = (here ? fmaxf(s2.x + s2.y - w_own, 0.0f) : s2.x + s2.y) * w;
+            E = c == z.c ? (here ? fmaf(-w_own, own, e2.x + e2.y) : e2.x + e2.y) * w + S * d : 0.0f;
+        }
         return Part{top, warp_sum(S), ENTROPY ? warp_sum(E) : 0.0f, key};
     }
 };
@@ -526,18 +537,26 @@ __device__ __forceinline__ Stats join(const Part *parts, int n, float c)
         return Stats{m, m, 0.0f};
     if (!(m < INFINITY))
         return Stats{NAN, NAN, NAN};
-    float S = 0.0f, E = 0.0f;
+    // S = 1 + R: one part that holds the row's maximum gives the 1
+    int first = n;
+#pragma unroll 1
+    for (int p = lane; p < n; p += 32)
+        if (first == n && parts[p].m == m)
+            first = p;
+    first = __reduce_min_sync(0xffffffffu, first);
+    float R = 0.0f, E = 0.0f;
 #pragma unroll 1
     for (int p = lane; p < n; p += 32) {
         const Part q = parts[p];
         const float d = fmaxf((q.m - m) * c, -1e4f), w = ex2(d);
-        S += q.S * w;
-        E += (q.E + q.S * d) * w;
+        const float one = q.m != -INFINITY && p != first ? 1.0f : 0.0f;
+        R += (q.S + one) * w;
+        E += (q.E + (q.S + one) * d) * w;
     }
-    S = warp_sum(S);
+    R = warp_sum(R);
     E = warp_sum(E);
-    const float lnS = logf(S);
-    return Stats{m, lnS, fmaxf(lnS - LN2 * __fdividef(E, S), 0.0f)};
+    const float lnS = log1pf(R);
+    return Stats{m, lnS, fmaxf(lnS - LN2 * __fdividef(E, 1.0f + R), 0.0f)};
 }
 
 // The CTA's place: its row, its run of the row's vectors, and its cluster.
