@@ -388,7 +388,7 @@ __device__ __noinline__ int thin_list(int K, Key *list, int *count, uint32_t *bo
 template <bool BF16, int T>
 __global__ void __launch_bounds__(T, T >= 128 ? 1024 / T : 12) logprobs_row_kernel(const Score a)
 {
-    constexpr int WARPS = T / 32, VT = ROW_VT, HALF = VT / 2, LANES = 4, LIST = RowShared<T>::LIST;
+    constexpr int WARPS = T / 32, VT = ROW_VT, HALF = VT / 2, LIST = RowShared<T>::LIST;
     extern __shared__ uint4 slots[];
     __shared__ RowShared<T> sh;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -469,11 +469,12 @@ __global__ void __launch_bounds__(T, T >= 128 ? 1024 / T : 12) logprobs_row_kern
     if (plain) {
         const int works = sh.works, vectors = each * HALF;
         if (works <= WORK) {
+            const int lanes = vectors == 2 ? 1 : 2;  // 2^lanes threads a span
 #pragma unroll 1
-            for (int i = tid / LANES; i < works; i += T / LANES) {
+            for (int i = tid >> lanes; i < works; i += T >> lanes) {
                 const int item = sh.work[i], first = item / T * vectors, owner = item % T;
 #pragma unroll 1
-                for (int v = tid % LANES; v < vectors; v += LANES) {
+                for (int v = tid & ((1 << lanes) - 1); v < vectors; v += 1 << lanes) {
                     const int vec = (first + v) * T + owner;
                     if (vec >= row.nvec)
                         break;
