@@ -762,12 +762,12 @@ struct Run {
     }
 };
 
-// Allows a kernel `most` bytes of dynamic shared memory, the same number at every call: calls of
-// other host threads may lie between this one and its launch.
+// Allows a kernel its launch with `bytes` of dynamic shared memory: `most`, the same number at
+// every call, since calls of other host threads may lie between this one and its launch.
 template <class A>
-inline int allow_shared(void (*kernel)(A), size_t most)
+inline int allow_shared(void (*kernel)(A), size_t bytes, size_t most)
 {
-    if (most <= 24 * 1024)  // with what the kernels hold besides, below what needs no leave
+    if (bytes <= 24 * 1024)  // with what the kernels hold besides, less than what needs no leave
         return KDA_OK;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));

@@ -409,7 +409,7 @@ int launch_with(const Distill &a, bool bf16, long long per, cudaStream_t stream)
     constexpr size_t most = (HELD ? TWO : ROW_SLOTS * ROW_VT * T) * 16;
     const size_t smem = std::min(most, static_cast<size_t>(per) * 16);
     auto *kernel = bf16 ? distill_kernel<true, T, GRAD, HELD> : distill_kernel<false, T, GRAD, HELD>;
-    if (int rc = allow_shared(kernel, most))
+    if (int rc = allow_shared(kernel, smem, most))
         return rc;
     return launch_rows(kernel, a, a.N * a.cl, T + 32, a.cl, smem, stream, "distill_kernel");
 }
@@ -468,7 +468,7 @@ int launch_backward(Distill a, int dtype, cudaStream_t stream)
     return with_threads(cut.threads, [&](auto threads) {
         constexpr int T = decltype(threads)::value;
         auto *kernel = bf16 ? distill_backward_kernel<true, T> : distill_backward_kernel<false, T>;
-        if (int rc = allow_shared(kernel, piece_shared(T)))
+        if (int rc = allow_shared(kernel, cut.shared, piece_shared(T)))
             return rc;
         return launch_rows(kernel, a, a.N * cut.runs, T + 32, 1, cut.shared, stream, "distill_backward_kernel");
     });

@@ -561,7 +561,7 @@ int launch_row(const Score &a, bool bf16, long long nvec, cudaStream_t stream)
     const size_t most = static_cast<size_t>(ROW_SLOTS) * ROW_VT * T * 16;
     const size_t smem = std::min(most, static_cast<size_t>((nvec + T - 1) / T) * T * 16);
     auto *kernel = bf16 ? logprobs_row_kernel<true, T> : logprobs_row_kernel<false, T>;
-    if (int rc = allow_shared(kernel, most))
+    if (int rc = allow_shared(kernel, smem, most))
         return rc;
     return launch_rows(kernel, a, a.N, T, 1, smem, stream, "logprobs_row_kernel");
 }
@@ -679,7 +679,7 @@ extern "C" int spec_logprobs_backward(const void *logits, int logit_dtype, int N
     return rows::with_threads(cut.threads, [&](auto threads) {
         constexpr int T = decltype(threads)::value;
         auto *kernel = bf16 ? logprobs_backward_kernel<true, T> : logprobs_backward_kernel<false, T>;
-        if (int rc = rows::allow_shared(kernel, rows::piece_shared(T)))
+        if (int rc = rows::allow_shared(kernel, cut.shared, rows::piece_shared(T)))
             return rc;
         return rows::launch_rows(kernel, a, static_cast<long long>(N) * cut.runs, T, 1, cut.shared, stream,
                                  "logprobs_backward_kernel");
