@@ -6,9 +6,9 @@
 // use (Run); a thread works on a few of them at a time, in registers (Tile).
 //
 // The sums are taken relative to a logit of the warp's own (Running), and a warp's triple
-// (maximum, sum of weights, weighted sum of exponents) joins the others' once, through the shared memory
-// of the CTA or of every CTA of the cluster: one barrier between reading a row and knowing
-// its statistics.
+// (maximum, sum of weights, weighted sum of exponents) joins the others' once, through the
+// shared memory of the CTA or of every CTA of the cluster: one barrier between reading a row
+// and knowing its statistics.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -153,13 +153,13 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// The value of rank r (0 the largest) among the warp's first N lanes (a power of two).
-template <class T, int N = 32>
+// The value of rank r (0 the largest) among the warp's 32.
+template <class T>
 __device__ __forceinline__ T warp_rank(T x, int r)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 2; k <= N; k <<= 1) {
+    for (int k = 2; k <= 32; k <<= 1) {
 #pragma unroll
         for (int j = k >> 1; j; j >>= 1) {  // a bitonic network, descending over the lanes
             const T y = __shfl_xor_sync(0xffffffffu, x, j);

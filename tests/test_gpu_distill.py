@@ -421,3 +421,22 @@ def test_a_step_of_several_host_threads():
         loss, _, grad, P, D = ref.distill(x, ids, values, 1.0)
         same_or_near(got[j][0][:2], loss, 4e-5 + 1e-5 * np.abs(loss), "loss")
         same_or_near(got[j][2][:2].float(), grad, 5e-5 * (P + D) + 1e-30 + 2.0**-8 * np.abs(grad), "gradient")
+
+
+def test_the_longest_row():
+    """2^30 logits: 0 but for three, so that every result can be written down."""
+    V = 2**30
+    x = torch.zeros((1, V), dtype=torch.bfloat16, device="cuda")
+    at = [V - 1, 5, V // 2 + 3]
+    x[0, at] = torch.tensor([20.0, 22.0, 21.0], dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([[V - 1, 7]], dtype=torch.int32, device="cuda")
+    values = torch.tensor([[0.0, 0.0]], device="cuda")
+    z = np.array([20.0, 22.0, 21.0])
+    lnS = np.log((V - 3) * np.exp(-22.0) + np.exp(z - 22.0).sum())
+    loss, stats, grad = kb.spec_distill_step(x, ids, values)
+    same_or_near(stats, np.array([[22.0, lnS]]), 1e-3, "stats")
+    same_or_near(loss, np.array([np.log(0.5) - 0.5 * (-2.0 - lnS) - 0.5 * (-22.0 - lnS)]), 2e-3, "loss")
+    p = np.exp(z - 22.0 - lnS)
+    got = grad[0, at].float().cpu().numpy()
+    assert np.abs(got - np.array([p[0] - 0.5, p[1], p[2]])).max() < 4e-3
+    assert abs(float(grad[0, 7]) + 0.5) < 4e-3 and abs(float(grad[0, 8]) - np.exp(-22.0 - lnS)) < 4e-12

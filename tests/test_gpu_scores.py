@@ -443,3 +443,69 @@ def test_calls_from_several_host_threads():
         assert np.array_equal(got[j][0][3][:2].cpu().numpy(), want[3])
         near(got[j][0][2][:2], want[2], 1e-5, 1e-6, "stats")
         assert torch.isfinite(got[j][1].float()).all()
+
+
+def test_the_longest_row():
+    """2^30 logits: 0 but for three, so that every result can be written down."""
+    V = 2**30
+    x = torch.zeros((1, V), dtype=torch.bfloat16, device="cuda")
+    at = [V - 1, 5, V // 2 + 3]
+    x[0, at] = torch.tensor([20.0, 22.0, 21.0], dtype=torch.bfloat16, device="cuda")
+    tok = torch.tensor([V - 1], dtype=torch.int32, device="cuda")
+    lp, H, stats, ids, top = kb.spec_logprobs(x, tok, 4)
+    z = np.array([20.0, 22.0, 21.0])
+    S = (V - 3) * np.exp(-22.0) + np.exp(z - 22.0).sum()
+    lnS = np.log(S)
+    assert ids[0].tolist() == [5, V // 2 + 3, V - 1, 0]
+    # 2^30 equal terms: a lane adds 2^19 of them or so, in sums of 32
+    near(stats, np.array([[22.0, lnS]]), 1e-3, 0.0, "stats")
+    near(lp, np.array([-2.0 - lnS]), 1e-3, 0.0, "logprob")
+    want = -((V - 3) * np.exp(-22.0 - lnS) * (-22.0 - lnS) + (np.exp(z - 22.0 - lnS) * (z - 22.0 - lnS)).sum())
+    near(H, np.array([want]), 2e-2, 0.0, "entropy")
+    kb.spec_logprobs_backward(x, tok, stats, grad_logprob=torch.ones(1, device="cuda"), dlogits=x)
+    p = np.exp(z - 22.0 - lnS)
+    got = x[0, at].float().cpu().numpy()
+    assert np.abs(got - np.array([1 - p[0], -p[1], -p[2]])).max() < 4e-3
+    assert abs(float(x[0, 77]) + np.exp(-22.0 - lnS)) < 4e-12
+
+
+def test_binding_refuses_wrong_tensors():
+    x = torch.zeros(3, 40, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    f = torch.zeros(3, device="cuda")
+    stats = torch.zeros(3, 2, device="cuda")
+    with pytest.raises(ValueError):
+        kb.spec_logprobs(x, torch.zeros(4, **i32), 2)
+    with pytest.raises(TypeError):
+        kb.spec_logprobs(x, torch.zeros(3, dtype=torch.int64, device="cuda"), 2)
+    with pytest.raises(ValueError):
+        kb.spec_logprobs(x, torch.zeros(3, 2, **i32)[:, 0], 2)
+    with pytest.raises(ValueError):
+        kb.spec_logprobs(x, None, 129)
+    with pytest.raises(ValueError):
+        kb.spec_logprobs(x, None, 2, logprob_out=f)
+    with pytest.raises(ValueError):
+        kb.spec_logprobs(x, None, 2, top_ids_out=torch.zeros(3, 3, **i32))
+    with pytest.raises(TypeError):
+        kb.spec_logprobs(x.half(), None, 2)
+    with pytest.raises(ValueError):
+        kb.spec_logprobs(x[0], None, 2)
+    with pytest.raises(ValueError):
+        kb.spec_logprobs_backward(x, None, f, f, grad_entropy=f)
+    with pytest.raises(ValueError):
+        kb.spec_logprobs_backward(x, None, stats, f, grad_entropy=f, dlogits=x.bfloat16())
+    with pytest.raises(kb.KdaError):
+        kb.spec_logprobs_backward(x, None, stats, f)
+    for tau in (0.0, -1.0, float("nan"), 1e6):
+        with pytest.raises(kb.KdaError):
+            kb.spec_logprobs(x, None, 2, temperature=tau)
+    ids, v = torch.zeros(3, 2, **i32), torch.zeros(3, 2, device="cuda")
+    for bad in (dict(ids=ids[0]), dict(ids=ids[:2]), dict(values=v[:, :1]), dict(weight=v), dict(values=None)):
+        with pytest.raises((ValueError, TypeError)):
+            kb.spec_distill_step(x, **{**dict(ids=ids, values=v), **bad})
+    with pytest.raises(TypeError):
+        kb.spec_distill(x, ids, v.half())
+    with pytest.raises(kb.KdaError):
+        kb.spec_distill(x, torch.zeros(3, 129, **i32), torch.zeros(3, 129, device="cuda"))
+    with pytest.raises(kb.KdaError):
+        kb.spec_distill(x, ids, v, kind=2)
