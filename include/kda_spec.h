@@ -610,8 +610,9 @@ int spec_logprobs(const void *logits, int logit_dtype, int N, int V, long long l
  *   g = grad_logprob[n] (NULL: 0; 0 for a row whose token is none), h = grad_entropy[n]
  *   (NULL: 0), stats and entropy as spec_logprobs gave them (entropy may be NULL without
  *   grad_entropy).  dlogits has the logits' type, ldg elements from row to row; it may be
- *   the logits themselves (with ldg = ld), else the two must not overlap.  A row with
- *   g = h = 0 gets zeros, whatever its logits.
+ *   the logits themselves (with ldg = ld), else the memory from its first row's start to
+ *   its last row's end must lie apart from theirs.  A row with g = h = 0 gets zeros,
+ *   whatever its logits.
  */
 int spec_logprobs_backward(const void *logits, int logit_dtype, int N, int V, long long ld, const int *tokens,
                            const float *stats, const float *entropy, const float *grad_logprob,
@@ -658,9 +659,10 @@ int spec_distill_backward(const void *logits, int logit_dtype, int N, int V, lon
                           void *dlogits, long long ldg, int *dev_status, cudaStream_t stream);
 
 /*
- * spec_distill_step -- both in one launch that reads the logits once: loss, stats (may
- *   be NULL) and dlogits for grad_loss known beforehand (NULL: 1; a mean over rows is
- *   1/rows).
+ * spec_distill_step -- both in one launch: loss, stats (may be NULL) and dlogits for
+ *   grad_loss known beforehand (NULL: 1; a mean over rows is 1/rows).  The logits are read
+ *   once; rows of more than 442 thousand bf16 or 221 thousand f32 logits, which eight CTAs
+ *   cannot hold, twice.
  */
 int spec_distill_step(const void *logits, int logit_dtype, int N, int V, long long ld, const kda_teacher *teacher,
                       float temperature, const float *grad_loss, float *loss, float *stats, void *dlogits,
