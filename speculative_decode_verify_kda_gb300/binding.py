@@ -769,6 +769,14 @@ def spec_accept(logits: torch.Tensor, drafts: torch.Tensor, j_out=None, bonus_ou
     return j_out, bonus_out, keep_out
 
 
+def _c_int(n: int, name: str) -> int:
+    """n for an int argument of the library: ctypes would pass the lower 32 bits of a larger
+    one, and the library's own checks would see that number."""
+    if not -2**31 <= n < 2**31:
+        raise ValueError(f"{name} must fit in 32 bits, got {n}")
+    return n
+
+
 def _logit_rows(t: torch.Tensor, name: str):
     """A logits tensor [..., V] as rows: (leading shape, N, V, ld).  The last dimension is
     dense and the leading ones step evenly from row to row."""
@@ -783,6 +791,8 @@ def _logit_rows(t: torch.Tensor, name: str):
     N = 1
     for s in lead:
         N *= int(s)
+    _c_int(N, f"the number of rows of {name}")
+    _c_int(V, f"V of {name}")
     if V > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be dense along its last dimension")
     ld, step = V, None
@@ -920,12 +930,12 @@ class _DistillPlan(_LogitPlan):
     def _teacher(self, ids, values, weight, kind):
         if not isinstance(ids, torch.Tensor) or ids.dim() != len(self.lead) + 1:
             raise ValueError("ids must have the shape [..., K]")
-        K = int(ids.shape[-1])
+        K = _c_int(int(ids.shape[-1]), "K of ids")
         shape = (*self.lead, K)
         if not isinstance(values, torch.Tensor):
             raise TypeError("values must be a CUDA tensor")
         t = KdaTeacher(self._in(ids, "ids", torch.int32, shape), self._in(values, "values", values.dtype, shape),
-                       self._in(weight, "weight", torch.float32), _row_dtype(values), int(kind), K)
+                       self._in(weight, "weight", torch.float32), _row_dtype(values), _c_int(int(kind), "kind"), K)
         self._keep.append(t)
         return ctypes.byref(t)
 
