@@ -642,8 +642,8 @@ typedef struct kda_teacher {
  *   loss = weight temperature^2 sum_k q_k (ln q_k - ln p_{id_k}),
  *   and stats f32 [N][2] (may be NULL), which the backward call takes.  A row of weight 0
  *   is not read: loss and stats 0.  A row without entries has loss 0.  An entry that the
- *   student masks has loss +inf, and so has an empty row; a sum of finite terms that
- *   rounds past the range of f32 is held at its end.
+ *   student masks has loss +inf, and so has an empty row (-inf for a negative weight); a
+ *   loss of finite terms that passes the range of f32 is held at its end.
  */
 int spec_distill(const void *logits, int logit_dtype, int N, int V, long long ld, const kda_teacher *teacher,
                  float temperature, float *loss, float *stats, int *dev_status, cudaStream_t stream);

@@ -175,27 +175,49 @@ struct Reader {
     }
 };
 
+// The loss of finite terms, one of which or a product of which passes the range of f32 on the way:
+// in 64 bits, held at the ends of the range.  +inf for an entry that the student masks.  By
+// one warp; rows of logits of the type's lowest value come here, no others.
+__device__ __noinline__ float loss_in_64_bits(const Entries &t, int K, float m, float lnS, float tau, float w)
+{
+    double sum = 0.0;
+    bool masked = false;
+#pragma unroll 1
+    for (int k = threadIdx.x & 31; k < K; k += 32) {
+        if (t.q[k] == 0.0f)
+            continue;
+        masked |= t.x[k] == -INFINITY;
+        sum += static_cast<double>(t.q[k]) *
+               ((static_cast<double>(t.lnq[k]) + lnS) * tau - (static_cast<double>(t.x[k]) - m));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (__any_sync(0xffffffffu, masked))
+        return w * INFINITY;
+    return static_cast<float>(fmin(fmax(sum * tau * w, -static_cast<double>(FLT_MAX)), static_cast<double>(FLT_MAX)));
+}
+
 // Loss and statistics of a row, by one warp.
 __device__ __forceinline__ void write_loss(const Distill &a, long long n, float w, const Stats &st, const Entries &t)
 {
     const int lane = threadIdx.x & 31;
-    float kl = 0.0f, most = -INFINITY;
+    float kl = 0.0f;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int k = lane + 32 * i;
         if (t.q[k] != 0.0f) {
             const float lp = st.empty() ? -INFINITY : (t.x[k] - st.m) * a.z.inv - st.lnS;
-            const float term = t.q[k] * (t.lnq[k] - lp);
-            kl += term;
-            most = max_nan(most, term);
+            kl += t.q[k] * (t.lnq[k] - lp);
         }
     }
     kl = warp_sum(kl);
-    most = warp_max_nan(most);
-    if (kl == INFINITY && most < INFINITY)  // finite terms, rounded past the range
-        kl = FLT_MAX;
+    float loss = t.Q == 0.0f ? 0.0f : kl * (a.tau * a.tau) * w;
+    // (the sum, and with it this, is the same in every lane)
+    if (!(fabsf(loss) <= FLT_MAX) && fabsf(st.m) <= FLT_MAX && fabsf(t.Q) <= FLT_MAX && fabsf(w) <= FLT_MAX)
+        loss = loss_in_64_bits(t, a.K, st.m, st.lnS, a.tau, w);
     if (lane == 0) {
-        a.loss[n] = t.Q == 0.0f ? 0.0f : kl * (a.tau * a.tau) * w;
+        a.loss[n] = loss;
         if (a.stats_out) {
             a.stats_out[2 * n] = st.m;
             a.stats_out[2 * n + 1] = st.lnS;

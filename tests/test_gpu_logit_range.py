@@ -1,0 +1,103 @@
+"""Scores and distillation where f32 ends: logits of the type's lowest and largest finite
+values, temperatures from 1e-4 to 1e4, weights far from 1, teacher values that are no numbers.
+The 64-bit values, brought into the range of f32 as each test says, are the reference.
+
+Tolerances, derived before the first run (u = 2^-24).  A teacher's q: the argument
+(v - top) / tau carries three roundings (of the difference, of 1 / tau and of the
+product) of at most |d| = 20 each, 60 u; expf 4 u; a sum of at most 128 terms by lanes 7 u,
+quotient 2 u: within 80 u, 5e-6 of itself (1e-5 allowed), and ln q within 1e-5 and 4 u of its
+size.  ln p = (x - m) / tau - ln S: 1e-5 for ln S (derived in test_gpu_scores.py) and 4 u of the
+size of the quotient.  A loss w tau^2 sum q (ln q - ln p) is then within
+w tau^2 (2e-5 + 1e-5 sum q (|ln q| + |ln p|))."""
+import numpy as np
+import pytest
+import torch
+
+import score_ref as ref
+from gpu_util import to_dev
+from libs import ensure_built
+
+from speculative_decode_verify_kda_gb300 import binding as kb
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+FLT_MAX = float(np.finfo(np.float32).max)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def dev(x, dtype="f32"):
+    return to_dev(np.asarray(x, np.float32)).to(DT[dtype])
+
+
+def near(got, want, tol, what):
+    got = got.double().cpu().numpy()
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    with np.errstate(invalid="ignore"):
+        ok = (np.isnan(got) & np.isnan(want)) | (got == want) | (np.abs(got - want) <= tol)
+    assert ok.all(), f"{what}: {np.argwhere(~ok)[:4].tolist()} got {got[~ok][:4]} want {want[~ok][:4]}"
+
+
+def end_rows(kind, N, V, dtype, seed):
+    """score_ref's rows, and rows whose logits lie at both ends of the type's range."""
+    if kind != "both_ends":
+        return ref.rows(kind, N, V, dtype, seed)
+    top = np.random.default_rng(seed).random((N, V)) < 4.0 / V
+    top[:, V // 2] = True
+    return ref.typed(np.where(top, 3e38, ref.LOWEST[dtype]), dtype)
+
+
+def spread(N, V, K, seed):
+    """K ids a row, none twice."""
+    rng = np.random.default_rng(seed)
+    return np.stack([rng.permutation(V)[:K] for _ in range(N)]).astype(np.int32)
+
+
+def loss_tolerance(x, ids, values, tau, weight, logprobs=False):
+    q, lnq = ref.teacher(ids, values, x.shape[1], tau, logprobs)
+    lp = np.stack([ref.probs(r, tau)[1][i] for r, i in zip(x, np.maximum(ids, 0))])
+    with np.errstate(invalid="ignore"):
+        size = np.where(q > 0, q * (np.abs(lnq) + np.abs(lp)), 0.0).sum(1)
+        return np.abs(weight) * tau * tau * (2e-5 + 1e-5 * np.nan_to_num(size, posinf=0.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [1e-4, 0.5, 1.0, 2.0, 1e4])
+@pytest.mark.parametrize("V", [37, 33001])
+@pytest.mark.parametrize("kind", ["few_allowed_lowest", "all_lowest", "both_ends"])
+def test_a_loss_at_the_ends_of_the_range(kind, V, tau, dtype):
+    """Finite logits give the finite loss, or the end of the range that it passes, whatever the
+    order in which its factors are taken; +inf is left to entries that the student masks."""
+    tau = float(np.float32(tau))
+    N, K = 7, 12
+    x = end_rows(kind, N, V, dtype, 5)
+    ids = spread(N, V, K, 3)
+    values = (2 * tau * np.random.default_rng(4).standard_normal((N, K))).astype(np.float32)
+    x[3, ids[3, 2]] = -np.inf
+    w = np.array([1.0, 3.5, 1 / 64, 2.0, 1e-8, 0.75, 1e-30], np.float32)
+    want, _, _, _, _ = ref.distill(x, ids, values, tau, w)
+    assert np.isposinf(want[3]) and np.isfinite(np.delete(want, 3)).all()
+    tol = loss_tolerance(x, ids, values, tau, w)
+    held = np.where(np.isfinite(want), np.clip(want, -FLT_MAX, FLT_MAX), want)
+    args = dev(x, dtype), to_dev(ids), dev(values)
+    kw = {"weight": to_dev(w), "temperature": tau}
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    near(kb.spec_distill(*args, dev_status=st, **kw)[0], held, tol, "loss")
+    near(kb.spec_distill_step(*args, dev_status=st, **kw)[0], held, tol, "loss of the step")
+    assert int(st) == 0
+
+
+def test_a_loss_past_the_range_keeps_its_sign():
+    """Weights may be negative; one that is infinite or no number, and an empty row, stay so."""
+    x = ref.typed(np.full((6, 50), ref.LOWEST["f32"]), "f32")
+    x[:, 7] = 1.0
+    x[4] = -np.inf
+    ids, values = np.tile(np.int32([[3, 9]]), (6, 1)), np.zeros((6, 2), np.float32)
+    w = np.array([2.0, -2.0, np.inf, np.nan, 2.0, 1e-38], np.float32)
+    loss = kb.spec_distill(dev(x), to_dev(ids), dev(values), weight=to_dev(w), temperature=2.0)[0].cpu().numpy()
+    assert loss[0] == FLT_MAX and loss[1] == -FLT_MAX and np.isposinf(loss[2]) and np.isnan(loss[3])
+    assert np.isposinf(loss[4])
+    assert abs(loss[5] - 2 * 1e-38 * -ref.LOWEST["f32"]) <= 1e-5 * loss[5]
