@@ -92,18 +92,18 @@ struct Reader {
         const int lane = threadIdx.x & 31;
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            if (!a.value_logprobs)
-                v[i] *= a.z.inv;
+        for (int i = 0; i < EACH; ++i)
             top = max_nan(top, v[i]);
-        }
         top = warp_max_nan(top);
         const bool none = top == -INFINITY;
-        const float ref = none || a.value_logprobs ? 0.0f : top;
         float e[EACH], Q = 0.0f;
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
-            e[i] = 32 * i < a.K ? expf(v[i] - ref) : 0.0f;
+            // the difference before the quotient: at a low temperature v / tau alone is large, and
+            // its rounding would be q's, or past the range
+            if (!a.value_logprobs && !none)
+                v[i] = (v[i] - top) * a.z.inv;
+            e[i] = 32 * i < a.K ? expf(v[i]) : 0.0f;
             Q += e[i];
         }
         Q = warp_sum(Q);
@@ -117,7 +117,7 @@ struct Reader {
             t.id[lane + 32 * i] = id[i];
             t.off[lane + 32 * i] = q;
             t.q[lane + 32 * i] = q;
-            t.lnq[lane + 32 * i] = v[i] - ref - lnsum;
+            t.lnq[lane + 32 * i] = v[i] - lnsum;
         }
         if (lane == 0)
             t.Q = whole && Q == Q ? 1.0f : Q;

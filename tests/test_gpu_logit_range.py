@@ -101,3 +101,53 @@ def test_a_loss_past_the_range_keeps_its_sign():
     assert loss[0] == FLT_MAX and loss[1] == -FLT_MAX and np.isposinf(loss[2]) and np.isnan(loss[3])
     assert np.isposinf(loss[4])
     assert abs(loss[5] - 2 * 1e-38 * -ref.LOWEST["f32"]) <= 1e-5 * loss[5]
+
+
+@pytest.mark.parametrize("vdtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tau", [1e-4, 1e-3, 1e-2, 0.5, 1e4])
+@pytest.mark.parametrize("offset", [0.0, 25.0, -1000.0])
+def test_teacher_logits_of_a_common_offset(offset, tau, vdtype):
+    """q depends on the differences of a row's values alone, at every temperature."""
+    tau = float(np.float32(tau))
+    N, V, K = 6, 3001, 20
+    rng = np.random.default_rng(7)
+    x = ref.rows("normal", N, V, "f32", 4)
+    ids = spread(N, V, K, 3)
+    values = ref.typed(offset + 3 * tau * rng.standard_normal((N, K)), vdtype)
+    want, _, grad, P, D = ref.distill(x, ids, values, tau)
+    tol = loss_tolerance(x, ids, values, tau, np.ones(N))
+    gtol = tau * (1e-5 * D + 5e-5 * P + 1e-30)
+    args = dev(x), to_dev(ids), dev(values, vdtype)
+    loss, stats = kb.spec_distill(*args, temperature=tau)
+    near(loss, want, tol, "loss")
+    near(kb.spec_distill_backward(*args, stats, temperature=tau), grad, gtol, "gradient")
+    loss, _, got = kb.spec_distill_step(*args, temperature=tau)
+    near(loss, want, tol, "loss of the step")
+    near(got, grad, gtol, "gradient of the step")
+
+
+@pytest.mark.parametrize("vdtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tau", [1e-4, 0.5, 1.0, 1e4])
+def test_finite_teacher_logits_are_numbers(tau, vdtype):
+    """Values at the ends of their type's range: a mask of the lowest value leaves q = 0, a row of
+    nothing else a flat q; no row is left out and none becomes NaN."""
+    tau = float(np.float32(tau))
+    N, V, K = 4, 500, 6
+    low = ref.LOWEST[vdtype]
+    x = ref.rows("normal", N, V, "f32", 4)
+    ids = spread(N, V, K, 3)
+    values = ref.typed(np.random.default_rng(2).standard_normal((N, K)), vdtype)
+    values[0, 3:] = low
+    values[1] = low
+    values[2, :3], values[2, 3:] = -low, low
+    values[3] = -low
+    want, _, grad, P, D = ref.distill(x, ids, values, tau)
+    assert np.isfinite(want).all() and np.allclose(D.sum(1), 1.0)
+    tol = loss_tolerance(x, ids, values, tau, np.ones(N))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = dev(x), to_dev(ids), dev(values, vdtype)
+    near(kb.spec_distill(*args, temperature=tau, dev_status=st)[0], want, tol, "loss")
+    loss, _, got = kb.spec_distill_step(*args, temperature=tau, dev_status=st)
+    near(loss, want, tol, "loss of the step")
+    near(got, grad, tau * (1e-5 * D + 5e-5 * P + 1e-30), "gradient of the step")
+    assert int(st) == 0
