@@ -70,7 +70,9 @@ extern "C" {
 
 /* bits OR-ed into *dev_status by kernels */
 #define KDA_ST_NAN 0x1      /* accept: a consulted row holds a NaN (greedy: row j,
-                               the bonus row; sampled: any row the walk reads) */
+                               the bonus row; sampled: any row the walk reads);
+                               scores and losses: a row holds a NaN or +inf, or
+                               a teacher's entries of the row do               */
 #define KDA_ST_BADKEEP 0x2  /* a device keep outside 1..T, or a device row count
                                outside 1..T (the *_var calls); that session is
                                left untouched                                    */
@@ -626,7 +628,9 @@ int spec_logprobs_backward(const void *logits, int logit_dtype, int N, int V, lo
 
 /* The teacher's K (1..KDA_TOPK_MAX) entries of every row, all device memory: ids int32
  * [N][K] (negative: no entry; V or more: none, and KDA_ST_BADTOKEN), values [N][K]
- * (value_dtype KDA_F32 or KDA_BF16; -inf gives q = 0), weight f32 [N] or NULL for 1.
+ * (value_dtype KDA_F32 or KDA_BF16; -inf gives q = 0; a NaN or +inf among a row's entries
+ * gives NaN for its loss and gradient, and KDA_ST_NAN from spec_distill and
+ * spec_distill_step), weight f32 [N] or NULL for 1.
  * An id that a row lists twice counts with both entries. */
 typedef struct kda_teacher {
     const int *ids;

@@ -212,7 +212,8 @@ __device__ __forceinline__ void write_loss(const Distill &a, long long n, float 
         }
     }
     kl = warp_sum(kl);
-    float loss = t.Q == 0.0f ? 0.0f : kl * (a.tau * a.tau) * w;
+    // (Q is NaN where a value is no number or +inf, whatever the sum has made of it)
+    float loss = t.Q == 0.0f ? 0.0f : t.Q != t.Q ? t.Q : kl * (a.tau * a.tau) * w;
     // (the sum, and with it this, is the same in every lane)
     if (!(fabsf(loss) <= FLT_MAX) && fabsf(st.m) <= FLT_MAX && fabsf(t.Q) <= FLT_MAX && fabsf(w) <= FLT_MAX)
         loss = loss_in_64_bits(t, a.K, st.m, st.lnS, a.tau, w);

@@ -151,3 +151,29 @@ def test_finite_teacher_logits_are_numbers(tau, vdtype):
     near(loss, want, tol, "loss of the step")
     near(got, grad, tau * (1e-5 * D + 5e-5 * P + 1e-30), "gradient of the step")
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("kind", [kb.TEACHER_LOGITS, kb.TEACHER_LOGPROBS])
+@pytest.mark.parametrize("what", [np.nan, np.inf])
+def test_teacher_rows_that_are_no_numbers(what, kind):
+    """A NaN or +inf among a row's values: NaN for the row's loss and gradient, and the status
+    says so, in every call; the other rows are as without it."""
+    x = ref.rows("normal", 4, 500, "f32", 4)
+    ids = spread(4, 500, 7, 5)
+    values = -np.random.default_rng(6).random((4, 7)).astype(np.float32) - 1.0
+    args = dev(x), to_dev(ids)
+    good = kb.spec_distill(*args, dev(values), kind=kind)[0], kb.spec_distill_step(*args, dev(values), kind=kind)[0]
+    values[1, 3] = what
+    values[2, 2], ids[2, 2] = what, -1  # no entry: its value is not looked at
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = dev(x), to_dev(ids), dev(values)
+    loss, stats = kb.spec_distill(*args, kind=kind, dev_status=st)
+    assert int(st) == kb.ST_NAN
+    grad = kb.spec_distill_backward(*args, stats, kind=kind)
+    st.zero_()
+    loss2, _, grad2 = kb.spec_distill_step(*args, kind=kind, dev_status=st)
+    assert int(st) == kb.ST_NAN
+    for a, d, before in ((loss, grad, good[0]), (loss2, grad2, good[1])):
+        assert torch.isnan(a[1]) and torch.isnan(d[1]).all()
+        assert torch.isfinite(a[[0, 2, 3]]).all() and torch.isfinite(d[[0, 2, 3]]).all()
+        assert torch.equal(a[[0, 3]], before[[0, 3]])
