@@ -584,8 +584,8 @@ int spec_accept_noalloc(const void *logits, int logit_dtype, int B, int T, int V
  * they lose nothing where m is large (log sum exp z = m / temperature + s).  A logit of
  * -inf is a masked token: p = 0.  A row without any other logit is empty: stats -inf,
  * H = 0, every log-probability -inf, gradients 0.  A row holding a NaN or +inf has NaN
- * for its stats and results, and KDA_ST_NAN is set.  Results do not depend on the order
- * in which blocks run.
+ * for its stats and results, and KDA_ST_NAN is set.  A log-probability of a finite logit that
+ * passes the range of f32 is -inf.  Results do not depend on the order in which blocks run.
  */
 #define KDA_TOPK_MAX 128
 #define KDA_ROW_MAX (1 << 30) /* logits of a row */

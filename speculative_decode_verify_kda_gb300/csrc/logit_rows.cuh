@@ -559,6 +559,14 @@ __device__ __forceinline__ Stats join(const Part *parts, int n, float c)
     return Stats{m, lnS, fmaxf(lnS - LN2 * __fdividef(E, 1.0f + R), 0.0f)};
 }
 
+// ln p of a logit, inv = 1 / temperature.  The difference is formed of the halves, which are
+// exact (but for subnormals): between logits at both ends of the range it would pass it, and
+// the quotient by a temperature above 1 need not.
+__device__ __forceinline__ float log_prob(float x, const Stats &st, float inv)
+{
+    return (0.5f * x - 0.5f * st.m) * (2.0f * inv) - st.lnS;
+}
+
 // The CTA's place: its row, its run of the row's vectors, and its cluster.
 struct Place {
     long long row;

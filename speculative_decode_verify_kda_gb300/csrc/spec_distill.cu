@@ -207,7 +207,7 @@ __device__ __forceinline__ void write_loss(const Distill &a, long long n, float 
     for (int i = 0; i < EACH; ++i) {
         const int k = lane + 32 * i;
         if (t.q[k] != 0.0f) {
-            const float lp = st.empty() ? -INFINITY : (t.x[k] - st.m) * a.z.inv - st.lnS;
+            const float lp = st.empty() ? -INFINITY : log_prob(t.x[k], st, a.z.inv);
             kl += t.q[k] * (t.lnq[k] - lp);
         }
     }

@@ -198,7 +198,7 @@ __device__ __forceinline__ void write_scores(const Score &a, long long n, const 
         if (token >= a.V && a.status)
             atomicOr(a.status, KDA_ST_BADTOKEN);
         if (token >= 0 && token < a.V)
-            lp = st.bad() ? NAN : st.empty() ? -INFINITY : (row.at(token) - st.m) * a.z.inv - st.lnS;
+            lp = st.bad() ? NAN : st.empty() ? -INFINITY : log_prob(row.at(token), st, a.z.inv);
     }
     if (a.logprob)
         a.logprob[n] = lp;
@@ -213,7 +213,7 @@ __device__ __forceinline__ void write_scores(const Score &a, long long n, const 
 }
 
 // The alternatives from the row's list, by all threads of a CTA.
-__device__ __forceinline__ void write_top(const Score &a, long long n, float m, float lnS, const Key *list, int found)
+__device__ __forceinline__ void write_top(const Score &a, long long n, const Stats &st, const Key *list, int found)
 {
     const long long o = n * a.K;
 #pragma unroll 1
@@ -225,13 +225,13 @@ __device__ __forceinline__ void write_top(const Score &a, long long n, float m, 
             place += list[j] > key;
         if (place < a.K) {
             a.top_ids[o + place] = key_id(key);
-            a.top_logprobs[o + place] = (from_ordered(static_cast<uint32_t>(key >> 32)) - m) * a.z.inv - lnS;
+            a.top_logprobs[o + place] = log_prob(from_ordered(static_cast<uint32_t>(key >> 32)), st, a.z.inv);
         }
     }
 #pragma unroll 1
     for (int k = found + threadIdx.x; k < a.K; k += blockDim.x) {
         a.top_ids[o + k] = -1;
-        a.top_logprobs[o + k] = m != m ? NAN : -INFINITY;
+        a.top_logprobs[o + k] = st.bad() ? NAN : -INFINITY;
     }
 }
 
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(CLUSTER_T) logprobs_cluster_kernel(const Score
             list_by_rounds(a.K, row, sh);
             found = sh.count;
         }
-        write_top(a, at.row, st.m, st.lnS, sh.list, found);
+        write_top(a, at.row, st, sh.list, found);
     }
     at.wait();
 }
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(T, T >= 128 ? 1024 / T : 12) logprobs_row_kern
         if (found > 2 * a.K + 64)  // (a short row, whose vectors are hardly more than K)
             found = thin_list<T, LIST>(a.K, sh.top.list, &sh.top.count, &sh.bound);
     }
-    write_top(a, n, m < INFINITY ? m : NAN, sh.lnS, sh.top.list, found);
+    write_top(a, n, Stats{m < INFINITY ? m : NAN, sh.lnS, 0.0f}, sh.top.list, found);
 }
 
 struct ScoreGrad {

@@ -177,3 +177,27 @@ def test_teacher_rows_that_are_no_numbers(what, kind):
         assert torch.isnan(a[1]) and torch.isnan(d[1]).all()
         assert torch.isfinite(a[[0, 2, 3]]).all() and torch.isfinite(d[[0, 2, 3]]).all()
         assert torch.equal(a[[0, 3]], before[[0, 3]])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 4.0, 1e4])
+@pytest.mark.parametrize("N,V,K", [(5, 37, 37), (5, 3001, 128), (2, 33001, 20), (330, 33001, 9)])
+@pytest.mark.parametrize("kind", ["both_ends", "few_allowed_lowest", "all_lowest"])
+def test_log_probabilities_at_both_ends_of_the_range(kind, N, V, K, tau, dtype):
+    """A log-probability that f32 holds is given, however far its logit lies from the row's
+    maximum; one past the range is -inf, as in rounding."""
+    tau = float(np.float32(tau))
+    x = end_rows(kind, N, V, dtype, 5)
+    tokens = np.random.default_rng(1).integers(0, V, N).astype(np.int32)
+    rows = [0, 1, N // 2, N - 1]
+    want = ref.score(x[rows], tokens[rows], K, tau)
+    with np.errstate(over="ignore"):
+        held = [np.asarray(a, np.float64).astype(np.float32).astype(np.float64) for a in want]
+    lp, H, stats, ids, top = kb.spec_logprobs(dev(x, dtype), to_dev(tokens), K, tau)
+    u = 2.0**-24
+    assert np.array_equal(ids[rows].cpu().numpy(), want[3])
+    with np.errstate(invalid="ignore"):
+        near(lp[rows], held[0], 1e-5 + 4 * u * np.abs(want[0]), "logprob")
+        near(top[rows], held[4], 1e-5 + 4 * u * np.abs(want[4]), "top_logprobs")
+    near(H[rows], want[1], 2e-5 + 1e-6 * np.abs(want[1]), "entropy")
+    near(stats[rows][:, 1], want[2][:, 1], 1e-5 + 4 * u * np.abs(want[2][:, 1]), "ln S")
