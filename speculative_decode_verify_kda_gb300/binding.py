@@ -823,15 +823,24 @@ def _stream_pool(stream):
 class _LogitPlan:
     """Arguments of one call over logits, checked and marshalled once; a call of the plan is
     one foreign call.  The tensors are referenced, and the outputs are the same tensors at
-    every call.  The stream is the one given (or current) when the plan is made."""
+    every call.  The stream is the one given (or current) when the plan is made; the tensors'
+    device has to be current then and at every call."""
 
     def __init__(self, name: str, logits: torch.Tensor, temperature: float, stream):
         self.name, self.logits = name, logits
         self.lead, self.N, self.V, self.ld = _logit_rows(logits, "logits")
+        # of one device there is nothing to compare at a call
+        self._device = logits.device.index if torch.cuda.device_count() > 1 else None
+        self._check_device()
         self.temperature, self.stream = float(temperature), stream
         self._fn = getattr(lib(), name)
         self._keep = [logits]
         self._head = [_ptr(logits), _row_dtype(logits), self.N, self.V, self.ld]
+
+    def _check_device(self):
+        if self._device is not None and torch.cuda.current_device() != self._device:
+            raise RuntimeError(f"{self.name}: the tensors are on {self.logits.device}, "
+                               f"the current device is cuda:{torch.cuda.current_device()}")
 
     def _in(self, t, name, dtype, shape=None):
         """Pointer of an input (or None)."""
@@ -879,6 +888,8 @@ class _LogitPlan:
         self._args = tuple(t(a) if isinstance(a, (int, float)) else a for t, a in zip(self._fn.argtypes, args))
 
     def __call__(self):
+        if self._device is not None:
+            self._check_device()
         rc = self._fn(*self._args)
         if rc:
             _check(self.name, rc)

@@ -64,3 +64,23 @@ def test_the_largest_sizes_reach_the_library():
     for make in plans((2,), 2**30 + 1, 4):
         with pytest.raises(kb.KdaError, match="V must lie in"):
             make()()
+
+
+def test_a_plan_is_launched_on_the_device_of_its_tensors(monkeypatch):
+    """Pointers of one device are not handed to a kernel of another: neither when the plan is made,
+    which takes the current stream, nor at a later call.  (No rows: nothing is launched.)"""
+    current = [0]
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    made = [make() for make in plans((0,), 8, 4)]
+    for plan in made:
+        plan()
+    current[0] = 1
+    for plan, make in zip(made, plans((0,), 8, 4)):
+        with pytest.raises(RuntimeError, match="current device"):
+            plan()
+        with pytest.raises(RuntimeError, match="current device"):
+            make()
+    current[0] = 0
+    for plan in made:
+        plan()
