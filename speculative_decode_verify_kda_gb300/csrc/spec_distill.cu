@@ -462,7 +462,7 @@ int launch(Distill a, int dtype, cudaStream_t stream)
     const long long nvec = vectors_of(a.x, a.V, a.ld, bf16);
     // With a gradient a run is held if an SM then has three CTAs (or two, where eight CTAs a row
     // cannot do better); beyond that a row is read twice by one CTA.  Held against read twice, us:
-    // 4096 bf16 rows of 131072 (four CTAs a row) 332 against 456, 480 of 32768 14.3 against 17.2.
+    // 4096 bf16 rows of 131072 (four CTAs a row) 340 against 456, 480 of 32768 14.4 against 17.2.
     a.cl = 1;
     bool held = GRAD;
     if (GRAD) {
