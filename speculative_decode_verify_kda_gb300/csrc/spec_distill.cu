@@ -175,50 +175,30 @@ struct Reader {
     }
 };
 
-// The loss of finite terms, one of which or a product of which passes the range of f32 on the way:
-// in 64 bits, held at the ends of the range.  +inf for an entry that the student masks.  By
-// one warp; rows of logits of the type's lowest value come here, no others.
-__device__ __noinline__ float loss_in_64_bits(const Entries &t, int K, float m, float lnS, float tau, float w)
-{
-    double sum = 0.0;
-    bool masked = false;
-#pragma unroll 1
-    for (int k = threadIdx.x & 31; k < K; k += 32) {
-        if (t.q[k] == 0.0f)
-            continue;
-        masked |= t.x[k] == -INFINITY;
-        sum += static_cast<double>(t.q[k]) *
-               ((static_cast<double>(t.lnq[k]) + lnS) * tau - (static_cast<double>(t.x[k]) - m));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (__any_sync(0xffffffffu, masked))
-        return w * INFINITY;
-    return static_cast<float>(fmin(fmax(sum * tau * w, -static_cast<double>(FLT_MAX)), static_cast<double>(FLT_MAX)));
-}
-
-// Loss and statistics of a row, by one warp.
+// Loss and statistics of a row, by one warp.  The loss is formed as
+//   w tau sum_k q_k (tau (ln q_k + s) - (x_k - m)),
+// the sum 2^-40 times as large: no difference of finite logits, no quotient by tau and no sum of
+// such terms then passes the range of f32, although the loss may (it is held at its end).
 __device__ __forceinline__ void write_loss(const Distill &a, long long n, float w, const Stats &st, const Entries &t)
 {
+    constexpr float UP = 1099511627776.0f, DOWN = 1.0f / UP;  // 2^40
     const int lane = threadIdx.x & 31;
-    float kl = 0.0f;
+    const float tau = a.tau * DOWN, m = st.m * DOWN;
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int k = lane + 32 * i;
-        if (t.q[k] != 0.0f) {
-            const float lp = st.empty() ? -INFINITY : log_prob(t.x[k], st, a.z.inv);
-            kl += t.q[k] * (t.lnq[k] - lp);
-        }
+        if (t.q[k] != 0.0f)  // (a masked logit's term is +inf)
+            sum += st.empty() ? INFINITY : t.q[k] * fmaf(t.lnq[k] + st.lnS, tau, m - t.x[k] * DOWN);
     }
-    kl = warp_sum(kl);
-    // (Q is NaN where a value is no number or +inf, whatever the sum has made of it)
-    float loss = t.Q == 0.0f ? 0.0f : t.Q != t.Q ? t.Q : kl * (a.tau * a.tau) * w;
-    // (the sum, and with it this, is the same in every lane)
-    if (!(fabsf(loss) <= FLT_MAX) && fabsf(st.m) <= FLT_MAX && fabsf(t.Q) <= FLT_MAX && fabsf(w) <= FLT_MAX)
-        loss = loss_in_64_bits(t, a.K, st.m, st.lnS, a.tau, w);
+    sum = warp_sum(sum) * a.tau;
+    // times w 2^40, the factor first that brings it towards 1
+    float loss = fabsf(sum) >= UP ? sum * w * UP : sum * UP * w;
+    if (fabsf(sum) <= FLT_MAX && fabsf(w) <= FLT_MAX)
+        loss = fminf(fmaxf(loss, -FLT_MAX), FLT_MAX);
     if (lane == 0) {
-        a.loss[n] = loss;
+        // (Q is NaN where a value is no number or +inf, whatever the sum has made of it)
+        a.loss[n] = t.Q == 0.0f ? 0.0f : t.Q != t.Q ? t.Q : loss;
         if (a.stats_out) {
             a.stats_out[2 * n] = st.m;
             a.stats_out[2 * n + 1] = st.lnS;
