@@ -85,10 +85,15 @@ extern "C" {
    number of ties) */
 #define KDA_ST_BADTOKEN 0x10 /* a token or teacher id of V or more (spec_logprobs,
                                spec_distill*); it is passed over                */
+#define KDA_ST_BADPAGE 0x20 /* a page id outside 0..pages-1 where a call reads or
+                               writes a paged cache: read as zeros, not written */
+#define KDA_ST_BADLEN 0x40  /* a length of a paged cache outside 0..what its pages
+                               hold; that session is left untouched             */
 
-/* element types of raw rows and logits */
+/* element types of raw rows and logits (F32, BF16) and of paged caches (BF16, F16) */
 #define KDA_F32 0
 #define KDA_BF16 1
+#define KDA_F16 2
 
 /* where kda_rollback finds keep[] */
 #define KDA_MEM_HOST 0
@@ -671,6 +676,106 @@ int spec_distill_backward(const void *logits, int logit_dtype, int N, int V, lon
 int spec_distill_step(const void *logits, int logit_dtype, int N, int V, long long ld, const kda_teacher *teacher,
                       float temperature, const float *grad_loss, float *loss, float *stats, void *dlogits,
                       long long ldg, int *dev_status, cudaStream_t stream);
+
+/*
+ * A paged cache: keys and values of one softmax-attention layer, for the layers that a
+ * hybrid model puts between its KDA layers (dflash.rs, the dense-KV rollback kv.len -=
+ * vt - keep).  A verify round passes its T rows through them as it does through the KDA
+ * layers: spec_cache_append writes the rows' keys and values behind the committed tokens,
+ * spec_attend reads them, and the rollback is lens[b] += keep[b] (spec_accept's keep_out):
+ * what was written behind is not counted and the next round writes over it.
+ *
+ *   k, v    [pages][Hkv][page][D] in any order of the first three (page_stride,
+ *           head_stride, slot_stride, in elements, the same for both; D is dense), dtype
+ *           KDA_BF16 or KDA_F16.  Base addresses and strides are multiples of 16 bytes.
+ *           D is 64 or 128, page a power of two in 8..1024.
+ *   table   int32 [B][table_cols]: token j of session b lies in page table[b][j / page],
+ *           slot j % page.  Only entries of tokens that a call reads or writes are looked
+ *           at; of those, ids outside 0..pages-1 set KDA_ST_BADPAGE, read as zeros and are
+ *           not written.  A page that a call writes belongs to one place of one session.
+ *   lens    int32 [B]: tokens that each session holds before the call's rows.  A length
+ *           that is negative, or whose rows would pass table_cols * page tokens, sets
+ *           KDA_ST_BADLEN and leaves the session untouched.
+ *
+ * Rows of a call are [B][T][heads][D] of the cache's type, heads and D dense, ld elements
+ * (a multiple of 8) from one row of T to the next ([b][t] lies at (b T + t) ld), 16-byte
+ * aligned, so q, k and v may be parts of one projection's output.  t_rows int32 [B] on
+ * the device (NULL: T each) gives the rows that session b has, 0..T; the rest are neither
+ * read nor written.  Another count sets KDA_ST_BADKEEP and leaves the session untouched.
+ * Row t of session b stands at position lens[b] + t.
+ */
+#define KDA_CACHE_MAX (1 << 30) /* tokens that a session's pages may hold        */
+#define KDA_GROUP_MAX 128       /* query heads that read one kv head             */
+typedef struct kda_cache {
+    void *k, *v;
+    const int *table, *lens;
+    long long page_stride, head_stride, slot_stride;
+    int B, Hkv, D;
+    int page, pages, table_cols;
+    int dtype;
+} kda_cache;
+
+/*
+ * spec_cache_append -- the rows' keys and values [B][T][Hkv][D] enter the cache at
+ * positions lens[b] .. lens[b] + t_rows[b] - 1.  lens is not changed.
+ */
+int spec_cache_append(const kda_cache *cache, const void *k_rows, const void *v_rows, int T, long long ld_k,
+                      long long ld_v, const int *t_rows, int *dev_status, cudaStream_t stream);
+
+/*
+ * spec_attend -- attention of the rows q [B][T][Hq][D] over the cache, the rows' own keys
+ * among it (spec_cache_append them first).  Query head h reads kv head h / (Hq / Hkv);
+ * Hq is a multiple of Hkv, at most KDA_GROUP_MAX times as large.  The row at position p sees key j when
+ *   j <= p  and  (window == 0  or  p - j < window  or  j < sinks),
+ * that is everything before it, or the last `window` keys (itself among them) and the
+ * first `sinks` ones.  With s_j = scale q.k_j (scale > 0) over the visible keys
+ *   lse = ln sum_j exp s_j,   o = sum_j exp(s_j - lse) v_j:
+ *   out [B][T][Hq][D] of the cache's type, dense; lse f32 [B][T][Hq] (may be NULL).
+ * Sums and statistics are f32; the weights enter the product with v in the cache's type.
+ * Keys and values that no row of the call sees may hold anything (pages behind the window
+ * may have been given back), and one that only later rows see does not reach earlier ones.
+ * Of a key that some rows of a session see and others do not, a value that is not finite
+ * makes the whole of a row that sees it NaN.  A row whose scores are all -inf gives zeros
+ * and lse -inf.
+ *   workspace: device memory of spec_attend_workspace_bytes(B, T, Hq, Hkv, D) bytes, 16-byte
+ *   aligned, no initialisation needed; calls that overlap need one each.
+ */
+size_t spec_attend_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+int spec_attend(const kda_cache *cache, const void *q, int T, int Hq, long long ld_q, const int *t_rows, int window,
+                int sinks, float scale, void *out, float *lse, int *dev_status, void *workspace,
+                size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * spec_attend_mass -- what every key was worth to the rows, for an eviction by it:
+ *   share_j = sum over the rows and the query heads of kv head h of exp(s_j - lse),
+ * with lse f32 [B][T][Hq] as spec_attend gave it (-inf gives 0) and the same visible keys.
+ * mass f32 [B][Hkv][ld_mass] (ld_mass >= table_cols * page): mass[b][h][j] += share_j for
+ * the tokens j < lens[b], mass[b][h][j] = share_j for the rows' own (their places may hold
+ * what a rejected draft left); the others are left as they are.  After an accept, t_rows =
+ * keep counts the accepted rows alone.
+ */
+int spec_attend_mass(const kda_cache *cache, const void *q, int T, int Hq, long long ld_q, const float *lse,
+                     const int *t_rows, int window, int sinks, float scale, float *mass, long long ld_mass,
+                     int *dev_status, cudaStream_t stream);
+
+/*
+ * spec_cache_evict -- every session's cache cut to `budget` tokens, each kv head by itself.
+ * Of the n = lens[b] tokens the first `sinks`, the last `recent` and, of those between, the
+ * budget - sinks - recent of the largest mass are kept (the lowest position first among
+ * equal ones, a NaN after every number); all when n <= budget.  They keep their order and
+ * move to places 0, 1, ... of the session:
+ *   kept int32 [B][Hkv][budget]: the positions kept, rising; -1 behind them;
+ *   mass_out f32 [B][Hkv][ld_mass_out] (ld_mass_out >= budget; NULL for none): their masses;
+ *     it may be mass itself (ld_mass_out == ld_mass), else it lies apart from it;
+ *   lens_out int32 [B]: min(n, budget); it may be the cache's lens;
+ *   dst_table int32 [B][dst_cols] (dst_cols * page >= budget): pages that receive the
+ *     tokens, none of them in any session's table; NULL: the session's own pages, in place.
+ * budget >= 1, sinks + recent <= budget, budget <= table_cols * page.  A session left
+ * untouched has kept -1.
+ */
+int spec_cache_evict(const kda_cache *cache, const float *mass, long long ld_mass, int budget, int recent, int sinks,
+                     const int *dst_table, int dst_cols, int *kept, float *mass_out, long long ld_mass_out,
+                     int *lens_out, int *dev_status, cudaStream_t stream);
 
 /* Static description of a return code, and the calling thread's last error text. */
 const char *kda_error_string(int code);

@@ -22,11 +22,11 @@ D = 128
 TMAX = 15
 HOST_KEEP_MAX = 2048
 OK, EINVAL, ENAN, ECUDA, ETIMEOUT = 0, 1, 2, 3, 4
-ST_NAN, ST_BADKEEP, ST_TIMEOUT, ST_BADTOKEN = 0x1, 0x2, 0x4, 0x10
+ST_NAN, ST_BADKEEP, ST_TIMEOUT, ST_BADTOKEN, ST_BADPAGE, ST_BADLEN = 0x1, 0x2, 0x4, 0x10, 0x20, 0x40
 TOPK_MAX = 128
 TEACHER_LOGITS, TEACHER_LOGPROBS = 0, 1
 TAG_ACCEPT, TAG_DRAW = 0xFFFFFFFE, 0xFFFFFFFF  # counter word 3 of a session's accept tests / draws
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 MEM_HOST, MEM_DEVICE = 0, 1
 
 # every symbol the header declares (checked by the CPU test of the library load)
@@ -38,8 +38,9 @@ EXPORTS = ("kda_verify_scan", "kda_rollback", "kda_verify_scan_var", "kda_rollba
            "spec_window", "spec_accept_sampled", "spec_accept_sampled_session", "kda_philox4x32_10",
            "spec_accept_sampled_scratch_bytes", "spec_accept_scratch_bytes", "spec_accept", "spec_accept_noalloc",
            "spec_logprobs", "spec_logprobs_backward", "spec_distill", "spec_distill_backward", "spec_distill_step",
+           "spec_cache_append", "spec_attend_workspace_bytes", "spec_attend", "spec_attend_mass", "spec_cache_evict",
            "kda_error_string", "kda_last_error", "kda_abi_version")
-ABI_VERSION = 10
+ABI_VERSION = 11
 WIN_CONF_KEEP, WIN_CONFIDENCE, WIN_SLOT_CONFIDENCE = 0, 1, 2
 
 
@@ -70,6 +71,14 @@ class KdaSampling(ctypes.Structure):
 class KdaTeacher(ctypes.Structure):
     _fields_ = [("ids", ctypes.c_void_p), ("values", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("value_dtype", ctypes.c_int), ("kind", ctypes.c_int), ("K", ctypes.c_int)]
+
+
+class KdaCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("page_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("slot_stride", ctypes.c_longlong), ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("page", ctypes.c_int), ("pages", ctypes.c_int), ("table_cols", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
 
 
 class KdaError(RuntimeError):
@@ -161,6 +170,17 @@ def lib(path: str | None = None):
     for fn in (L.spec_logprobs, L.spec_logprobs_backward, L.spec_distill, L.spec_distill_backward,
                L.spec_distill_step):
         fn.restype = ci
+    cf, cl, cache = ctypes.c_float, ctypes.c_longlong, ctypes.POINTER(KdaCache)
+    L.spec_cache_append.argtypes = [cache, vp, vp, ci, cl, cl, vp, vp, vp]
+    L.spec_cache_append.restype = ci
+    L.spec_attend_workspace_bytes.argtypes = [ci, ci, ci, ci, ci]
+    L.spec_attend_workspace_bytes.restype = sz
+    L.spec_attend.argtypes = [cache, vp, ci, ci, cl, vp, ci, ci, cf, vp, vp, vp, vp, sz, vp]
+    L.spec_attend.restype = ci
+    L.spec_attend_mass.argtypes = [cache, vp, ci, ci, cl, vp, vp, ci, ci, cf, vp, cl, vp, vp]
+    L.spec_attend_mass.restype = ci
+    L.spec_cache_evict.argtypes = [cache, vp, cl, ci, ci, ci, vp, ci, vp, vp, cl, vp, vp, vp]
+    L.spec_cache_evict.restype = ci
     L.kda_error_string.argtypes = [ci]
     L.kda_error_string.restype = ctypes.c_char_p
     L.kda_last_error.argtypes = []
@@ -1020,6 +1040,247 @@ def spec_distill_step(logits, ids, values, grad_loss=None, weight=None, kind: in
                       temperature: float = 1.0, **kw):
     """Distillation loss, stats and d logits in one launch: one call of a DistillStepPlan."""
     return DistillStepPlan(logits, ids, values, grad_loss, weight, kind, temperature, **kw)()
+
+
+_CACHE_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+class PagedCache:
+    """Keys and values of one softmax-attention layer in pages: k and v [pages][Hkv][page][D]
+    (bfloat16 or float16, D of 64 or 128 dense, page a power of two in 8..1024; any strides of
+    the first three dimensions that are the same for both), table int32 [B][columns] of page
+    ids, lens int32 [B] of tokens held.  The tensors are referenced: a round commits its
+    accepted rows with ``cache.lens += keep``."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError(f"{name} must be a CUDA tensor")
+        if k.dtype not in _CACHE_DTYPES or v.dtype != k.dtype:
+            raise TypeError("k and v must both be bfloat16 or both float16")
+        if k.dim() != 4 or tuple(v.shape) != tuple(k.shape):
+            raise ValueError("k and v must both have the shape [pages][Hkv][page][D]")
+        pages, hkv, page, d = (_c_int(int(x), "the sizes of k") for x in k.shape)
+        strides = [tuple(1 if n == 1 else s for n, s in zip(t.shape, t.stride())) for t in (k, v)]
+        if strides[0] != strides[1]:
+            raise ValueError("k and v must have the same strides")
+        if k.stride(3) != 1 and d > 1:
+            raise ValueError("k and v must be dense along D")
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must have the shape [B][columns]")
+        b, cols = (_c_int(int(x), "the sizes of table") for x in table.shape)
+        _dev(table, "table", torch.int32)
+        _dev(lens, "lens", torch.int32, (b,))
+        for t, name in ((v, "v"), (table, "table"), (lens, "lens")):
+            if t.device != k.device:
+                raise ValueError(f"{name} must be on {k.device}")
+        # the stride of a dimension of one element says nothing
+        step = [d if n == 1 else s for n, s in zip(k.shape, k.stride())]
+        self.k, self.v, self.table, self.lens = k, v, table, lens
+        self.B, self.Hkv, self.D, self.page, self.pages, self.columns = b, hkv, d, page, pages, cols
+        self.capacity = cols * page
+        self.device, self.dtype = k.device, k.dtype
+        self.c = KdaCache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), step[0], step[1], step[2],
+                          b, hkv, d, page, pages, cols, _CACHE_DTYPES[k.dtype])
+
+
+class _CachePlan:
+    """Arguments of one call over a paged cache, checked and marshalled once; a call of the plan
+    is one foreign call.  Tensors, stream and device as for the plans over logits."""
+
+    def __init__(self, name: str, cache: PagedCache, stream):
+        self.name, self.cache, self.stream = name, cache, stream
+        self._device = cache.device.index if torch.cuda.device_count() > 1 else None
+        self._check_device()
+        self._fn = getattr(lib(), name)
+        self._keep = [cache]
+
+    def _check_device(self):
+        if self._device is not None and torch.cuda.current_device() != self._device:
+            raise RuntimeError(f"{self.name}: the tensors are on {self.cache.device}, "
+                               f"the current device is cuda:{torch.cuda.current_device()}")
+
+    def _in(self, t, name, dtype, shape):
+        """Pointer of an input (or None)."""
+        if t is None:
+            return None
+        _dev(t, name, dtype, shape)
+        return self._hold(t, name)
+
+    def _hold(self, t, name):
+        if t.device != self.cache.device:
+            raise ValueError(f"{name} must be on {self.cache.device}")
+        self._keep.append(t)
+        return _ptr(t)
+
+    def _out(self, t, name, dtype, shape):
+        """An output: the caller's tensor, checked, or a new one."""
+        if t is None:
+            with _stream_pool(self.stream):
+                t = torch.empty(shape, dtype=dtype, device=self.cache.device)
+        self._in(t, name, dtype, shape)
+        return t
+
+    def _rows(self, t, name, heads=None):
+        """Rows [B][T][heads][D]: (pointer, T, heads, ld)."""
+        c = self.cache
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != c.dtype:
+            raise TypeError(f"{name} must be {c.dtype}, got {t.dtype}")
+        if t.dim() != 4 or t.shape[0] != c.B or t.shape[3] != c.D or (heads is not None and t.shape[2] != heads):
+            raise ValueError(f"{name} must have the shape [{c.B}][T][{heads or 'heads'}][{c.D}], got {tuple(t.shape)}")
+        B, T, H, D = (_c_int(int(x), f"the sizes of {name}") for x in t.shape)
+        ld = H * D
+        if t.numel() > 0:
+            if t.stride(3) != 1 or (H > 1 and t.stride(2) != D):
+                raise ValueError(f"{name} must be dense along its heads and D")
+            if T > 1:
+                ld = t.stride(1)
+            elif B > 1:
+                ld = t.stride(0)
+            if B > 1 and t.stride(0) != T * ld:
+                raise ValueError(f"{name} must step evenly from row to row")
+        return self._hold(t, name), T, H, int(ld)
+
+    def _t_rows(self, t):
+        return self._in(t, "t_rows", torch.int32, (self.cache.B,))
+
+    def _mass(self, t, name, width):
+        """Pointer and row step of masses f32 [B][Hkv][at least width], dense."""
+        c = self.cache
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] < width:
+            raise ValueError(f"{name} must have the shape [{c.B}][{c.Hkv}][at least {width}]")
+        return self._in(t, name, torch.float32, (c.B, c.Hkv, int(t.shape[2]))), int(t.shape[2])
+
+    def _status(self, t):
+        return None if t is None else self._in(t, "dev_status", torch.int32, tuple(t.shape))
+
+    def _bind(self, *rest):
+        args = (ctypes.byref(self.cache.c), *rest, ctypes.c_void_p(_stream(self.stream)))
+        self._args = tuple(t(a) if isinstance(a, (int, float)) else a for t, a in zip(self._fn.argtypes, args))
+
+    def __call__(self):
+        if self._device is not None:
+            self._check_device()
+        rc = self._fn(*self._args)
+        if rc:
+            _check(self.name, rc)
+        return self.out
+
+
+class CacheAppendPlan(_CachePlan):
+    """spec_cache_append for fixed tensors: k_rows and v_rows [B][T][Hkv][D] of the cache's type
+    (their rows may be parts of longer ones), t_rows int32 [B] or None for T rows a session.
+    A call returns the cache."""
+
+    def __init__(self, cache: PagedCache, k_rows, v_rows, t_rows=None, dev_status=None, stream=None):
+        super().__init__("spec_cache_append", cache, stream)
+        k, T, _, ld_k = self._rows(k_rows, "k_rows", cache.Hkv)
+        v, Tv, _, ld_v = self._rows(v_rows, "v_rows", cache.Hkv)
+        if T != Tv:
+            raise ValueError("k_rows and v_rows must have the same number of rows")
+        self.out = cache
+        self._bind(k, v, T, ld_k, ld_v, self._t_rows(t_rows), self._status(dev_status))
+
+
+class _QueryPlan(_CachePlan):
+    def _query(self, q, t_rows, window, sinks, scale):
+        ptr, T, H, ld = self._rows(q, "q")
+        self.T, self.Hq = T, H
+        scale = self.cache.D**-0.5 if scale is None else float(scale)
+        return ((ptr, T, H, ld), self._t_rows(t_rows),
+                (_c_int(int(window), "window"), _c_int(int(sinks), "sinks"), scale))
+
+
+class AttendPlan(_QueryPlan):
+    """spec_attend for fixed tensors: q [B][T][Hq][D] of the cache's type (its rows may be parts
+    of longer ones), t_rows int32 [B] or None for T rows a session, window 0 for none, scale
+    1 / sqrt(D) unless given.  A call returns (out [B][T][Hq][D], lse f32 [B][T][Hq]); rows
+    behind a session's last one are not written.  ``workspace`` (uint8, workspace_bytes(...)
+    bytes) may be shared by plans whose calls follow one another."""
+
+    def __init__(self, cache: PagedCache, q, t_rows=None, window: int = 0, sinks: int = 0, scale=None, out=None,
+                 lse_out=None, dev_status=None, workspace=None, stream=None):
+        super().__init__("spec_attend", cache, stream)
+        query, rows, seen = self._query(q, t_rows, window, sinks, scale)
+        B, T, H, D = cache.B, self.T, self.Hq, cache.D
+        out = self._out(out, "out", cache.dtype, (B, T, H, D))
+        lse = self._out(lse_out, "lse_out", torch.float32, (B, T, H))
+        if workspace is None:
+            workspace = self._out(None, "workspace", torch.uint8, (self.workspace_bytes(cache, T, H),))
+        self._in(workspace, "workspace", torch.uint8, tuple(workspace.shape))
+        self.out = (out, lse)
+        self._bind(*query, rows, *seen, _ptr(out), _ptr(lse), self._status(dev_status), _ptr(workspace),
+                   workspace.numel())
+
+    @staticmethod
+    def workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
+        return int(lib().spec_attend_workspace_bytes(cache.B, T, Hq, cache.Hkv, cache.D))
+
+
+class AttendMassPlan(_QueryPlan):
+    """spec_attend_mass for fixed tensors: q as AttendPlan's, lse f32 [B][T][Hq] as it gave it,
+    mass f32 [B][Hkv][cache.capacity or more], which a call updates and returns."""
+
+    def __init__(self, cache: PagedCache, q, lse, mass, t_rows=None, window: int = 0, sinks: int = 0, scale=None,
+                 dev_status=None, stream=None):
+        super().__init__("spec_attend_mass", cache, stream)
+        query, rows, seen = self._query(q, t_rows, window, sinks, scale)
+        lse = self._in(lse, "lse", torch.float32, (cache.B, self.T, self.Hq))
+        ptr, ld = self._mass(mass, "mass", cache.capacity)
+        self.out = mass
+        self._bind(*query, lse, rows, *seen, ptr, ld, self._status(dev_status))
+
+
+class CacheEvictPlan(_CachePlan):
+    """spec_cache_evict for fixed tensors: mass f32 [B][Hkv][cache.capacity or more], budget
+    tokens a session, of which the last ``recent`` and the first ``sinks`` always; dst_table
+    int32 [B][columns] of other pages, or None to move in place.  A call returns (kept int32
+    [B][Hkv][budget], mass_out f32 [B][Hkv][budget or more], lens_out int32 [B]); mass_out may be
+    ``mass`` and lens_out ``cache.lens``."""
+
+    def __init__(self, cache: PagedCache, mass, budget: int, recent: int = 0, sinks: int = 0, dst_table=None,
+                 kept_out=None, mass_out=None, lens_out=None, dev_status=None, stream=None):
+        super().__init__("spec_cache_evict", cache, stream)
+        budget = _c_int(int(budget), "budget")
+        recent, sinks = _c_int(int(recent), "recent"), _c_int(int(sinks), "sinks")
+        ptr, ld = self._mass(mass, "mass", cache.capacity)
+        dst, cols = None, 0
+        if dst_table is not None:
+            if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
+                raise ValueError("dst_table must have the shape [B][columns]")
+            cols = _c_int(int(dst_table.shape[1]), "the columns of dst_table")
+            dst = self._in(dst_table, "dst_table", torch.int32, (cache.B, cols))
+        shape = (cache.B, cache.Hkv, max(budget, 0))
+        kept = self._out(kept_out, "kept_out", torch.int32, shape)
+        if mass_out is None:
+            mass_out = self._out(None, "mass_out", torch.float32, shape)
+        ptr_out, ld_out = self._mass(mass_out, "mass_out", budget)
+        lens = self._out(lens_out, "lens_out", torch.int32, (cache.B,))
+        self.out = (kept, mass_out, lens)
+        self._bind(ptr, ld, budget, recent, sinks, dst, cols, _ptr(kept), ptr_out, ld_out, _ptr(lens),
+                   self._status(dev_status))
+
+
+def spec_cache_append(cache: PagedCache, k_rows, v_rows, t_rows=None, **kw):
+    """The rows' keys and values enter the cache: one call of a CacheAppendPlan."""
+    return CacheAppendPlan(cache, k_rows, v_rows, t_rows, **kw)()
+
+
+def spec_attend(cache: PagedCache, q, t_rows=None, window: int = 0, sinks: int = 0, scale=None, **kw):
+    """Attention of the rows over the cache and its log-sum: one call of an AttendPlan."""
+    return AttendPlan(cache, q, t_rows, window, sinks, scale, **kw)()
+
+
+def spec_attend_mass(cache: PagedCache, q, lse, mass, t_rows=None, window: int = 0, sinks: int = 0, scale=None, **kw):
+    """Every key's share of the rows' attention, added to its mass: one call of an AttendMassPlan."""
+    return AttendMassPlan(cache, q, lse, mass, t_rows, window, sinks, scale, **kw)()
+
+
+def spec_cache_evict(cache: PagedCache, mass, budget: int, recent: int = 0, sinks: int = 0, **kw):
+    """Every session's cache cut to a budget by mass: one call of a CacheEvictPlan."""
+    return CacheEvictPlan(cache, mass, budget, recent, sinks, **kw)()
 
 
 class RoundPlan:

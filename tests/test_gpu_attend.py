@@ -1,0 +1,353 @@
+"""spec_attend and spec_attend_mass against the formulas in 64 bits: lengths, row counts, head
+groups, pages, layouts, windows and sinks; whatever no row sees holds NaN."""
+import math
+
+import pytest
+import torch
+
+from cache_ref import Case, near
+from libs import ensure_built
+
+from speculative_decode_verify_kda_gb300 import binding as kb
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+def run(c, **kw):
+    """out and lse of a call, checked; rows behind a session's last one keep what they held."""
+    out = torch.full((c.B, c.T, c.Hq, c.D), 7.0, dtype=c.dtype, device="cuda")
+    lse = torch.full((c.B, c.T, c.Hq), 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = kb.spec_attend(c.cache(), c.q, out=out, lse_out=lse, dev_status=status, **c.see(), **kw)
+    assert got[0] is out and got[1] is lse
+    want, want_lse, tol, tol_lse = c.attend()
+    there = near(out, want, tol, "out")
+    near(lse, want_lse, tol_lse, "lse")
+    assert torch.all(out.cpu()[~there] == 7.0), "rows that are not the call's were written"
+    assert torch.all(lse.cpu()[torch.isnan(want_lse)] == 7.0)
+    assert int(status) == 0
+    return out, lse
+
+
+def weigh(c, lse):
+    """mass after a call, checked against its shares."""
+    cap = c.cache().capacity
+    g = torch.Generator().manual_seed(5)
+    before = torch.rand((c.B, c.Hkv, cap + 3), generator=g)
+    for b in range(c.B):
+        before[b, :, c.n[b]:] = math.nan  # what a rejected draft may have left
+    mass = before.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert kb.spec_attend_mass(c.cache(), c.q, lse, mass, dev_status=status, **c.see()) is mass
+    got = mass.cpu()
+    for b in range(c.B):
+        n, t = c.n[b], c.t[b]
+        assert torch.isnan(got[b, :, n + t:]).all()
+        if t == 0:
+            assert torch.equal(got[b, :, :n], before[b, :, :n])
+            continue
+        share, tol = c.share(lse.cpu(), b)
+        old = torch.cat((before[b, :, :n], torch.zeros(c.Hkv, t)), 1).double()
+        near(got[b, :, :n + t], old + share, tol + 2.0**-23 * (old + share), f"mass of session {b}")
+        unseen = [j for j in range(n) if not c.seen_by_any(b, j)]
+        assert torch.equal(got[b][:, unseen], before[b][:, unseen])
+    assert int(status) == 0
+
+
+def both(c):
+    _, lse = run(c)
+    weigh(c, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [8, 16, 64, 128, 256])
+def test_pages_and_types(page, D, dtype):
+    both(Case([0, 1, 15, 16, 129, 300], T=3, D=D, page=page, dtype=dtype, seed=page))
+
+
+@pytest.mark.parametrize("n", [0, 1, 7, 63, 64, 126, 127, 128, 129, 255, 256, 257, 511, 1000])
+def test_lengths(n):
+    both(Case([n], T=2, Hq=8, Hkv=1, seed=n))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (3, 1), (5, 1), (6, 2), (7, 1), (16, 1), (64, 8), (100, 1),
+                                    (128, 1)])
+@pytest.mark.parametrize("T", [1, 4])
+def test_groups(Hq, Hkv, T):
+    both(Case([200, 77], T=T, Hq=Hq, Hkv=Hkv, seed=Hq))
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(15, 64, 8), (16, 8, 1), (17, 8, 1), (31, 9, 1), (33, 8, 1), (64, 4, 1),
+                                      (130, 1, 1), (129, 2, 2), (257, 3, 1), (300, 4, 2), (5, 100, 1), (40, 65, 1)])
+def test_rows(T, Hq, Hkv):
+    both(Case([150, 0], T=T, Hq=Hq, Hkv=Hkv, seed=T))
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 3), (16, 0), (17, 4), (100, 16), (128, 128), (130, 200),
+                                          (1000, 4), (3, 1000)])
+@pytest.mark.parametrize("T", [1, 6, 70])
+def test_windows(window, sinks, T):
+    both(Case([0, 5, 140, 517], T=T, Hq=4, Hkv=2, window=window, sinks=sinks, seed=window))
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("T", [4, 90])
+def test_sessions_with_fewer_rows(T, window):
+    both(Case([0, 33, 250, 90, 128], T=T, Hq=6, Hkv=2, t_rows=[T, 0, 1, T - 1, T // 2], window=window, sinks=2,
+              seed=T))
+
+
+@pytest.mark.parametrize("layout", ["nhd", "paired"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_layouts(layout, D):
+    both(Case([260, 31], T=5, Hq=12, Hkv=3, D=D, layout=layout, fused=True, seed=D))
+
+
+def test_many_sessions():
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 200, (90,), generator=g).tolist()
+    rows = torch.randint(0, 4, (90,), generator=g).tolist()
+    both(Case(lens, T=3, Hq=4, Hkv=2, t_rows=rows, seed=11))
+
+
+def test_one_head_shared_by_many_sessions_pages():
+    """Sessions that share their first pages, as those of one prompt do."""
+    c = Case([160, 160, 160], T=2, Hq=8, Hkv=2, page=32, seed=21)
+    c.table[1:, :4] = c.table[0, :4]
+    for b in (1, 2):
+        c.dense[b][:, :, :128] = c.dense[0][:, :, :128]
+    both(c)
+
+
+@pytest.mark.parametrize("n,T", [(5000, 1), (5000, 15), (3000, 40)])
+def test_long_texts_are_split_and_joined(n, T):
+    both(Case([n, 3], T=T, Hq=8, Hkv=2, page=64, seed=n + T))
+
+
+def test_scores_of_a_wide_range():
+    """Scores of hundreds: the running maximum moves far at every tile."""
+    run(Case([700], T=3, Hq=8, Hkv=2, q_scale=60.0, seed=2))
+    run(Case([700], T=40, Hq=8, Hkv=2, q_scale=60.0, dtype=F16, seed=3))
+
+
+def test_rising_scores():
+    """Every key scores above the ones before it: the maximum moves in every tile, by little and by much."""
+    for step in (0.01, 0.3):
+        c = Case([900], T=4, Hq=4, Hkv=1, seed=4)
+        unit = torch.zeros(c.D)
+        unit[0] = 1.0
+        for j in range(904):
+            k = (c.dense[0][0, :, j].float() * 0.01 + unit * step * j).to(c.dtype)
+            c.dense[0][0, :, j] = k
+            c.k[c.table[0, j // c.page], :, j % c.page] = k.cuda()
+        c.q_host = (c.q_host.float() * 0.01 + 4.0 * unit).to(c.dtype)
+        c.fuse(False)
+        run(c)
+
+
+def test_scale():
+    c = Case([100], T=2)
+    c.scale = 0.02
+    out = kb.spec_attend(c.cache(), c.q, scale=0.02)[0]
+    want, _, tol, _ = c.attend()
+    near(out, want, tol)
+
+
+def test_values_that_only_later_rows_see_do_not_reach_earlier_ones():
+    """The second of three rows brings NaN and infinite values: the first row is as without it,
+    the rows that see it are NaN."""
+    for bad in (math.nan, math.inf, -math.inf):
+        for T, G in ((3, 4), (80, 2)):
+            c = Case([130], T=T, Hq=G, Hkv=1, seed=9)
+            j = 131
+            c.v[c.table[0, j // c.page], :, j % c.page, 5] = bad
+            out, lse = kb.spec_attend(c.cache(), c.q)
+            want, want_lse, tol, tol_lse = c.attend()
+            near(out[:, :1], want[:, :1], tol[:, :1])
+            near(lse, want_lse, tol_lse)
+            assert torch.isnan(out[0, 1:, :, 5]).all() or math.isinf(bad)
+            assert not torch.isfinite(out[0, 1:, :, 5]).any()
+
+
+def test_keys_that_only_later_rows_see_do_not_reach_earlier_ones():
+    c = Case([130], T=3, Hq=4, Hkv=1, seed=9)
+    j = 131
+    c.k[c.table[0, j // c.page], :, j % c.page, 5] = math.nan
+    out, lse = kb.spec_attend(c.cache(), c.q)
+    want, want_lse, tol, tol_lse = c.attend()
+    near(out[:, :1], want[:, :1], tol[:, :1])
+    near(lse[:, :1], want_lse[:, :1], tol_lse[:, :1])
+    assert torch.isnan(out[:, 1:]).all() and torch.isnan(lse[:, 1:]).all()
+
+
+def test_all_scores_minus_infinity():
+    c = Case([40], T=2, Hq=4, Hkv=1, seed=1)
+    unit = torch.zeros(c.D, dtype=c.dtype)
+    unit[0] = -math.inf
+    for j in range(42):
+        c.k[c.table[0, j // c.page], :, j % c.page] = unit.cuda()
+    c.q = c.q.abs() + 1.0
+    c.q[..., 1:] = 1.0
+    out, lse = kb.spec_attend(c.cache(), c.q)
+    assert torch.all(out == 0) and torch.all(lse == -math.inf)
+    mass = torch.ones((1, 1, c.cache().capacity), device="cuda")
+    kb.spec_attend_mass(c.cache(), c.q, lse, mass)
+    assert torch.all(mass[..., :40] == 1.0) and torch.all(mass[..., 40:42] == 0.0)
+
+
+def test_mass_adds_up():
+    """Twice the same rows: twice their shares on the tokens before, once on the rows' own."""
+    c = Case([300, 90], T=4, Hq=8, Hkv=2, seed=6)
+    _, lse = kb.spec_attend(c.cache(), c.q)
+    mass = torch.zeros((2, 2, c.cache().capacity), device="cuda")
+    plan = kb.AttendMassPlan(c.cache(), c.q, lse, mass)
+    plan()
+    once = mass.clone()
+    plan()
+    for b, n in enumerate(c.n):
+        assert torch.equal(mass[b, :, :n], 2 * once[b, :, :n])
+        assert torch.equal(mass[b, :, n:n + 4], once[b, :, n:n + 4])
+        # every row and head hands out one
+        assert torch.allclose(once[b].sum(1), torch.full((2,), 16.0, device="cuda"), rtol=1e-4)
+
+
+def test_sessions_out_of_range_are_left_untouched():
+    c = Case([100, 100, 100, 100, 100], T=3, Hq=4, Hkv=2, t_rows=[3, 3, 3, 3, 3], seed=8)
+    cap = c.cache().capacity
+    c.lens[1], c.lens[2] = -1, cap - 2
+    c.t_rows[3], c.t_rows[4] = 4, -1
+    out = torch.full((5, 3, 4, 128), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((5, 3, 4), 7.0, device="cuda")
+    mass = torch.full((5, 2, cap), 7.0, device="cuda")
+    want, want_lse, tol, tol_lse = c.attend()
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    kb.spec_attend(c.cache(), c.q, t_rows=c.t_rows, out=out, lse_out=lse, dev_status=status[:1])
+    kb.spec_attend_mass(c.cache(), c.q, lse, mass, t_rows=c.t_rows, dev_status=status[1:])
+    near(out[:1], want[:1], tol[:1])
+    assert torch.all(out[1:] == 7.0) and torch.all(lse[1:] == 7.0) and torch.all(mass[1:] == 7.0)
+    assert status.tolist() == [kb.ST_BADKEEP | kb.ST_BADLEN] * 2
+
+
+def test_bad_pages_read_as_zeros():
+    for bad in (-1, -(2**31), 2**31 - 1, None):
+        c = Case([200, 200], T=3, Hq=4, Hkv=2, seed=12)
+        c.table[0, 5] = c.k.shape[0] if bad is None else bad
+        c.dense[0][:, :, 80:96] = 0.0
+        out = torch.full((2, 3, 4, 128), 7.0, dtype=BF16, device="cuda")
+        status = torch.zeros(2, dtype=torch.int32, device="cuda")
+        mass = torch.zeros((2, 2, c.cache().capacity), device="cuda")
+        _, lse = kb.spec_attend(c.cache(), c.q, out=out, dev_status=status[:1])
+        want, want_lse, tol, tol_lse = c.attend()
+        near(out, want, tol)
+        near(lse, want_lse, tol_lse)
+        kb.spec_attend_mass(c.cache(), c.q, lse, mass, dev_status=status[1:])
+        share, tol = c.share(lse.cpu(), 0)
+        near(mass[0, :, :203], share, tol + 1e-7)
+        assert status.tolist() == [kb.ST_BADPAGE] * 2
+
+
+def test_pages_behind_the_window_are_not_looked_at():
+    c = Case([500], T=3, window=64, sinks=4, page=16, seed=13)
+    gone = [i for i in range(c.table.shape[1]) if not any(c.seen_by_any(0, j) for j in range(16 * i, 16 * i + 16)
+                                                          if j < 503)]
+    assert len(gone) > 20
+    c.table[0, gone] = 2**30
+    both(c)
+
+
+def test_a_call_on_another_stream_and_twice_the_same_bits():
+    c = Case([900, 40], T=15, Hq=16, Hkv=2, seed=14)
+    first, lse = kb.spec_attend(c.cache(), c.q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    again, lse2 = kb.spec_attend(c.cache(), c.q, stream=side)
+    side.synchronize()
+    assert torch.equal(first, again) and torch.equal(lse, lse2)
+
+
+def test_captured_and_replayed_with_other_lengths():
+    """One graph serves lengths, rows and pages that change between its replays."""
+    a = Case([300, 20, 77], T=4, Hq=8, Hkv=2, t_rows=[4, 0, 2], seed=15)
+    b = Case([17, 290, 0], T=4, Hq=8, Hkv=2, t_rows=[1, 4, 3], seed=16, cols=a.table.shape[1])
+    out = torch.full((3, 4, 8, 128), 7.0, dtype=BF16, device="cuda")
+    side = torch.cuda.Stream()
+    live = Case([300, 20, 77], T=4, Hq=8, Hkv=2, t_rows=[4, 0, 2], seed=15)
+    plan = kb.AttendPlan(live.cache(), live.q, t_rows=live.t_rows, out=out, stream=side)
+    mass = torch.zeros((3, 2, live.cache().capacity), device="cuda")
+    weigh_plan = kb.AttendMassPlan(live.cache(), live.q, plan.out[1], mass, t_rows=live.t_rows, stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        plan()
+        weigh_plan()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        plan()
+        weigh_plan()
+    for c in (b, a):
+        for name in ("k", "v", "table", "lens", "t_rows", "q"):
+            getattr(live, name).copy_(getattr(c, name))
+        out.fill_(7.0)
+        mass.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want, _, tol, _ = c.attend()
+        there = near(out, want, tol)
+        assert torch.all(out.cpu()[~there] == 7.0)
+        for s in range(3):
+            if c.t[s]:
+                share, tol = c.share(plan.out[1].cpu(), s)
+                near(mass[s, :, :c.n[s] + c.t[s]], share, tol + 1e-7)
+
+
+def test_calls_in_a_row_share_a_workspace():
+    cases = [Case([n, 40], T=6, Hq=16, Hkv=2, seed=n) for n in (1200, 64, 700)]
+    work = torch.empty(max(kb.AttendPlan.workspace_bytes(c.cache(), c.T, c.Hq) for c in cases), dtype=torch.uint8,
+                       device="cuda")
+    plans = [kb.AttendPlan(c.cache(), c.q, workspace=work) for c in cases]
+    for _ in range(3):
+        for p in plans:
+            p()
+    for c, p in zip(cases, plans):
+        want, want_lse, tol, tol_lse = c.attend()
+        near(p.out[0], want, tol)
+        near(p.out[1], want_lse, tol_lse)
+
+
+def test_two_calls_at_once():
+    cases = [Case([800 + s, 100], T=8, Hq=16, Hkv=2, seed=s) for s in range(2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    plans = [kb.AttendPlan(c.cache(), c.q, stream=s) for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p in plans:
+            p()
+    torch.cuda.synchronize()
+    for c, p in zip(cases, plans):
+        want, _, tol, _ = c.attend()
+        near(p.out[0], want, tol)
+
+
+def test_no_rows_and_no_sessions():
+    c = Case([10, 20], T=2)
+    out, lse = kb.spec_attend(c.cache(), c.q[:, :0])
+    assert out.shape == (2, 0, 4, 128) and lse.shape == (2, 0, 4)
+    empty = kb.PagedCache(c.k, c.v, c.table[:0], c.lens[:0])
+    assert kb.spec_attend(empty, c.q[:0])[0].shape == (0, 2, 4, 128)
+    kb.spec_attend_mass(empty, c.q[:0], torch.empty((0, 2, 4), device="cuda"),
+                        torch.empty((0, 2, empty.capacity), device="cuda"))
+
+
+def test_a_workspace_that_is_too_small_is_refused():
+    c = Case([10], T=2)
+    need = kb.AttendPlan.workspace_bytes(c.cache(), 2, 4)
+    with pytest.raises(kb.KdaError, match="workspace"):
+        kb.spec_attend(c.cache(), c.q, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
