@@ -25,7 +25,7 @@ NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUD
 
 LIBS = {
     "libkda_spec.so": ["kda_scan.cu", "spec_accept.cu", "spec_sampled.cu", "spec_logprobs.cu", "spec_distill.cu",
-                       "spec_cache.cu", "spec_attend.cu", "kda_round.cpp", "kda_abi.cpp"],
+                       "spec_cache.cu", "spec_attend.cu", "spec_attend_mass.cu", "kda_round.cpp", "kda_abi.cpp"],
     "libkda_synth.so": ["synth_fill.cu"],
 }
 
