@@ -25,7 +25,10 @@ using namespace tiles;
 
 constexpr int KT = 128;              // keys of a tile, and rows of a tile
 constexpr int COPY_WARP = 8, MMA_WARP = 9;
-constexpr int THREADS = 320;
+constexpr int THREADS = 384;         // two groups of 128 and four warps more, two of them idle
+// Registers are handed from the last four warps to the groups (a row of 128 scores is held in
+// them): 256 x 216 + 128 x 72 = 384 x 168, what the launch has.
+constexpr int GROUP_REGS = 216, OTHER_REGS = 72;
 constexpr int SPARE = 2048;          // barriers and what the groups tell each other
 // The running maximum that weights are taken against follows the true one only when it falls
 // behind by more than this many powers of two: weights stay below 2^8, and the sums in tensor
@@ -53,11 +56,11 @@ struct Unit {
     int near, far, count; // key tiles: [0, far) for the sinks, then from `near`
 };
 
-__device__ __forceinline__ Unit unit_of(const Walk &w, long long i)
+__device__ __forceinline__ Unit unit_of(const Walk &w, int i)
 {
     Unit u;
-    u.b = static_cast<int>(i / w.nq);
-    u.t0 = static_cast<int>(i - static_cast<long long>(u.b) * w.nq) * w.TQ;
+    u.b = i / w.nq;
+    u.t0 = (i - u.b * w.nq) * w.TQ;
     int t, bad;
     session(w.a.c, w.a.t_rows, w.a.T, u.b, u.n, t, bad);
     u.nt = min(w.TQ, t - u.t0);
@@ -92,45 +95,41 @@ struct Share {
     long long pair, before; // the (session, unit) of `first`, and the tiles before that
 };
 
-// A run of one unit's tiles within a share.
-struct Run {
-    Unit u;
-    int h, off, todo;
-    bool whole;
-    int slot;  // of the workspace, when not whole
-};
-
+// The runs of one unit's tiles after another within a share.
 struct Runs {
     const Walk &w;
-    long long at, last, first, pair, before;
-    int h;
+    long long left;      // tiles from this run on
+    int pair, slot;
     Unit u;
-    __device__ Runs(const Walk &w_, const Share &s) : w(w_), at(s.first), last(s.last), first(s.first), pair(s.pair), before(s.before)
+    int h, off, todo;    // tiles off .. off + todo - 1 of the unit
+    bool whole;          // all of them; else the parts go to `slot` of the workspace
+    __device__ Runs(const Walk &w_, const Share &s)
+        : w(w_), left(s.last - s.first), pair(static_cast<int>(s.pair)), slot(2 * blockIdx.x), todo(0)
     {
-        if (at < last) {
+        if (left > 0) {
             u = unit_of(w, pair);
-            h = static_cast<int>((at - before) / u.count);
+            h = static_cast<int>((s.first - s.before) / u.count);
+            off = static_cast<int>(s.first - s.before - static_cast<long long>(u.count) * h);
         }
     }
-    __device__ __forceinline__ bool next(Run &r)
+    __device__ __forceinline__ bool next()
     {
-        if (at >= last)
+        if (todo > 0) {
+            left -= todo;
+            off = 0;
+            slot |= 1;
+            ++h;
+        }
+        if (left <= 0)
             return false;
         if (h == w.a.c.Hkv) {
-            before += static_cast<long long>(u.count) * h;
             h = 0;
             do
                 u = unit_of(w, ++pair);
             while (u.count == 0);
         }
-        r.u = u;
-        r.h = h;
-        r.off = static_cast<int>(at - before - static_cast<long long>(u.count) * h);
-        r.todo = static_cast<int>(min(static_cast<long long>(u.count - r.off), last - at));
-        r.whole = r.todo == u.count;
-        r.slot = 2 * blockIdx.x + (at == first ? 0 : 1);
-        at += r.todo;
-        ++h;
+        todo = static_cast<int>(min(static_cast<long long>(u.count - off), left));
+        whole = todo == u.count;
         return true;
     }
 };
@@ -141,7 +140,7 @@ __device__ Share share_of(const Walk &w, long long *part, Share *found)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long P = static_cast<long long>(w.a.c.B) * w.nq;
-    auto tiles_of = [&](long long i) { return i < P ? static_cast<long long>(unit_of(w, i).count) * w.a.c.Hkv : 0ll; };
+    auto tiles_of = [&](long long i) { return i < P ? static_cast<long long>(unit_of(w, static_cast<int>(i)).count) * w.a.c.Hkv : 0ll; };
     // over all: one chunk of THREADS units, or more
     long long mine = 0;
     for (long long i = tid; i < P; i += THREADS)
@@ -266,165 +265,168 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
     const Share share = share_of(w, part, found);
     const Watch watch{gave_up, w.a.status};
-    Runs runs(w, share);
-    Run r;
+    Runs r(w, share);
     uint32_t seq = 0;  // tiles that passed through the ring before this run
     int nth = 0;       // runs before this one
 
-    if (warp == COPY_WARP) {
-        auto tile_of = [&](const Run &run, int i) {
-            const int x = run.off + i;
-            return x < run.u.far ? x : run.u.near + x - run.u.far;
-        };
-        const int boxes = KT / w.box, page = 1 << w.a.c.shift;
-        auto load = [&](const Run &run, const CUtensorMap *m, int i, uint32_t s) {
-            const uint32_t st = s % ST;
-            warp_wait(watch, empty(st), ((s / ST) & 1) ^ 1);
-            if (__any_sync(0xffffffffu, *gave_up))
-                return;
-            const int j0 = tile_of(run, i) * KT;
-            const int j = j0 + lane * w.box;  // up to 16 boxes: one a lane
-            int id = 0;
-            const bool want = lane < boxes && j < run.u.hi && (j + w.box > run.u.lo || j < w.a.seen.sinks);
-            if (want) {
-                id = w.a.c.table[static_cast<long long>(run.u.b) * w.a.c.cols + (j >> w.a.c.shift)];
-                if (id < 0 || id >= w.a.c.pages) {
-                    raise(w.a.status, KDA_ST_BADPAGE);
-                    id = w.a.c.pages;  // behind the last: zeros
-                }
-            }
-            const int count = __popc(__ballot_sync(0xffffffffu, want));
-            if (lane == 0)
-                bar_expect(full(st), static_cast<uint32_t>(count) * w.box * D * 2);
-            __syncwarp();
-            if (want) {
-                const uint32_t dst = ring + st * TILE + lane * w.box * 128;
-#pragma unroll
-                for (int half = 0; half < HALVES; ++half)
-                    copy_4d(dst + half * HALF, m, half * 64, j & (page - 1), run.h, id, full(st));
-            }
-        };
-        auto load_q = [&](const Run &run) {
-            const int buf = PAIR ? 0 : nth & 1;
-            warp_wait(watch, q_empty(buf), ((PAIR ? nth : nth >> 1) & 1) ^ 1);
-            if (lane != 0 || *gave_up)
-                return;
-            const int two = PAIR && run.u.nt > w.TT;
-            bar_expect(q_full(buf), static_cast<uint32_t>(1 + two) * w.TT * w.a.G * D * 2);
-            for (int i = 0; i <= two; ++i)
-                for (int half = 0; half < HALVES; ++half)
-                    copy_3d(q_at + (PAIR ? i : buf) * TILE + half * HALF, &map_q, half * 64, run.h * w.a.G,
-                            run.u.b * w.a.T + run.u.t0 + i * w.TT, q_full(buf));
-        };
-        while (runs.next(r)) {
-            const int lead = min(LEAD, r.todo);
-            for (int i = 0; i < lead; ++i)
-                load(r, &map_k, i, seq + i);
-            load_q(r);
-            for (int i = 0; i < r.todo; ++i) {
-                const uint32_t s = seq + value_at(lead, r.todo, i);
-                load(r, &map_v, i, s);
-                if (i + LEAD < r.todo)
-                    load(r, &map_k, i + LEAD, s + 1);
-            }
-            seq += 2 * r.todo;
-            ++nth;
-        }
-        if (*gave_up && lane == 0) {  // copies in flight land before the CTA ends
-            for (uint32_t s = seq > ST ? seq - ST : 0; s < seq; ++s)
-                bar_wait_long(watch, full(s % ST), (s / ST) & 1, true);
-        }
-    } else if (warp == MMA_WARP) {
-        if (lane == 0) {
-            constexpr uint32_t SCORES = product_desc(BF16, KT, KT, false), VALUES = product_desc(BF16, KT, D, true);
-            uint32_t done[2] = {0, 0};
-            auto stage_full = [&](uint32_t s) { bar_wait(watch, full(s % ST), (s / ST) & 1); };
-            auto scores = [&](int g, uint32_t q, uint32_t s) {
-                const uint64_t a = tile_desc(q, 16, 1024), b = tile_desc(ring + (s % ST) * TILE, 16, 1024);
-                if (*gave_up)
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+        if (warp == COPY_WARP) {
+            auto tile_of = [&](const Runs &run, int i) {
+                const int x = run.off + i;
+                return x < run.u.far ? x : run.u.near + x - run.u.far;
+            };
+            const int boxes = KT / w.box, page = 1 << w.a.c.shift;
+            auto load = [&](const Runs &run, const CUtensorMap *m, int i, uint32_t s) {
+                const uint32_t st = s % ST;
+                warp_wait(watch, empty(st), ((s / ST) & 1) ^ 1);
+                if (__any_sync(0xffffffffu, *gave_up))
                     return;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
-                    mma_ss(tmem + g * KT, a + step, b + step, SCORES, k > 0);
+                const int j0 = tile_of(run, i) * KT;
+                const int j = j0 + lane * w.box;  // up to 16 boxes: one a lane
+                int id = 0;
+                const bool want = lane < boxes && j < run.u.hi && (j + w.box > run.u.lo || j < w.a.seen.sinks);
+                if (want) {
+                    id = w.a.c.table[static_cast<long long>(run.u.b) * w.a.c.cols + (j >> w.a.c.shift)];
+                    if (id < 0 || id >= w.a.c.pages) {
+                        raise(w.a.status, KDA_ST_BADPAGE);
+                        id = w.a.c.pages;  // behind the last: zeros
+                    }
                 }
-                mma_commit(s_full(g));
+                const int count = __popc(__ballot_sync(0xffffffffu, want));
+                if (lane == 0)
+                    bar_expect(full(st), static_cast<uint32_t>(count) * w.box * D * 2);
+                __syncwarp();
+                if (want) {
+                    const uint32_t dst = ring + st * TILE + lane * w.box * 128;
+    #pragma unroll
+                    for (int half = 0; half < HALVES; ++half)
+                        copy_4d(dst + half * HALF, m, half * 64, j & (page - 1), run.h, id, full(st));
+                }
             };
-            auto values = [&](int g, uint32_t s, bool add) {
-                const uint64_t b = tile_desc(ring + (s % ST) * TILE, HALF, 1024);
-                bar_wait(watch, p_full(g), done[g] & 1);
-                ++done[g];
-                fence_after();
-                if (*gave_up)
+            auto load_q = [&](const Runs &run) {
+                const int buf = PAIR ? 0 : nth & 1;
+                warp_wait(watch, q_empty(buf), ((PAIR ? nth : nth >> 1) & 1) ^ 1);
+                if (lane != 0 || *gave_up)
                     return;
-#pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    mma_ts(tmem + 2 * KT + g * KT, tmem + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES, add || k > 0);
-                mma_commit(o_full(g));
+                const int two = PAIR && run.u.nt > w.TT;
+                bar_expect(q_full(buf), static_cast<uint32_t>(1 + two) * w.TT * w.a.G * D * 2);
+                for (int i = 0; i <= two; ++i)
+                    for (int half = 0; half < HALVES; ++half)
+                        copy_3d(q_at + (PAIR ? i : buf) * TILE + half * HALF, &map_q, half * 64, run.h * w.a.G,
+                                run.u.b * w.a.T + run.u.t0 + i * w.TT, q_full(buf));
             };
-            auto commit = [&](uint32_t bar) {
-                if (!*gave_up)
-                    mma_commit(bar);
-            };
-            while (runs.next(r)) {
-                const int lead = min(LEAD, r.todo), buf = PAIR ? 0 : nth & 1;
-                const int groups = PAIR ? (r.u.nt > w.TT ? 2 : 1) : 0;
-                const uint32_t q = q_at + (PAIR ? 0 : buf * TILE);
-                bar_wait(watch, q_full(buf), (PAIR ? nth : nth >> 1) & 1);
-                for (int i = 0; i < lead; ++i) {
-                    stage_full(seq + i);
-                    fence_after();
-                    if (PAIR)
-                        for (int g = 0; g < groups; ++g)
-                            scores(g, q + g * TILE, seq + i);
-                    else
-                        scores(i, q, seq + i);
-                    commit(empty((seq + i) % ST));
-                }
-                if (r.todo <= LEAD)
-                    commit(q_empty(buf));
+            while (r.next()) {
+                const int lead = min(LEAD, r.todo);
+                for (int i = 0; i < lead; ++i)
+                    load(r, &map_k, i, seq + i);
+                load_q(r);
                 for (int i = 0; i < r.todo; ++i) {
-                    const uint32_t sv = seq + value_at(lead, r.todo, i), sk = sv + 1;
-                    const bool more = i + LEAD < r.todo;
-                    stage_full(sv);
-                    if (PAIR) {
-                        for (int g = 0; g < groups; ++g) {
-                            values(g, sv, i > 0);
-                            if (more) {
-                                if (g == 0)
-                                    stage_full(sk);
-                                scores(g, q + g * TILE, sk);
-                            }
-                        }
-                    } else {
-                        values(i & 1, sv, i > 1);
-                    }
-                    commit(empty(sv % ST));
-                    if (more) {
-                        if (!PAIR) {
-                            stage_full(sk);
-                            scores(i & 1, q, sk);
-                        }
-                        commit(empty(sk % ST));
-                        if (i + LEAD == r.todo - 1)
-                            commit(q_empty(buf));
-                    }
+                    const uint32_t s = seq + value_at(lead, r.todo, i);
+                    load(r, &map_v, i, s);
+                    if (i + LEAD < r.todo)
+                        load(r, &map_k, i + LEAD, s + 1);
                 }
                 seq += 2 * r.todo;
                 ++nth;
             }
-            if (*gave_up) {  // products in flight end before the tensor memory is freed
-                mma_commit(drained);
-                bar_wait_long(watch, drained, 0, true);
+            if (*gave_up && lane == 0) {  // copies in flight land before the CTA ends
+                for (uint32_t s = seq > ST ? seq - ST : 0; s < seq; ++s)
+                    bar_wait_long(watch, full(s % ST), (s / ST) & 1, true);
+            }
+        } else if (warp == MMA_WARP) {
+        if (lane == 0) {
+                constexpr uint32_t SCORES = product_desc(BF16, KT, KT, false), VALUES = product_desc(BF16, KT, D, true);
+                uint32_t done[2] = {0, 0};
+                auto stage_full = [&](uint32_t s) { bar_wait(watch, full(s % ST), (s / ST) & 1); };
+                auto scores = [&](int g, uint32_t q, uint32_t s) {
+                    const uint64_t a = tile_desc(q, 16, 1024), b = tile_desc(ring + (s % ST) * TILE, 16, 1024);
+                    if (*gave_up)
+                        return;
+    #pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
+                        mma_ss(tmem + g * KT, a + step, b + step, SCORES, k > 0);
+                    }
+                    mma_commit(s_full(g));
+                };
+                auto values = [&](int g, uint32_t s, bool add) {
+                    const uint64_t b = tile_desc(ring + (s % ST) * TILE, HALF, 1024);
+                    bar_wait(watch, p_full(g), done[g] & 1);
+                    ++done[g];
+                    fence_after();
+                    if (*gave_up)
+                        return;
+    #pragma unroll
+                    for (int k = 0; k < KT / 16; ++k)
+                        mma_ts(tmem + 2 * KT + g * KT, tmem + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES, add || k > 0);
+                    mma_commit(o_full(g));
+                };
+                auto commit = [&](uint32_t bar) {
+                    if (!*gave_up)
+                        mma_commit(bar);
+                };
+                while (r.next()) {
+                    const int lead = min(LEAD, r.todo), buf = PAIR ? 0 : nth & 1;
+                    const int groups = PAIR ? (r.u.nt > w.TT ? 2 : 1) : 0;
+                    const uint32_t q = q_at + (PAIR ? 0 : buf * TILE);
+                    bar_wait(watch, q_full(buf), (PAIR ? nth : nth >> 1) & 1);
+                    for (int i = 0; i < lead; ++i) {
+                        stage_full(seq + i);
+                        fence_after();
+                        if (PAIR)
+                            for (int g = 0; g < groups; ++g)
+                                scores(g, q + g * TILE, seq + i);
+                        else
+                            scores(i, q, seq + i);
+                        commit(empty((seq + i) % ST));
+                    }
+                    if (r.todo <= LEAD)
+                        commit(q_empty(buf));
+                    for (int i = 0; i < r.todo; ++i) {
+                        const uint32_t sv = seq + value_at(lead, r.todo, i), sk = sv + 1;
+                        const bool more = i + LEAD < r.todo;
+                        stage_full(sv);
+                        if (PAIR) {
+                            for (int g = 0; g < groups; ++g) {
+                                values(g, sv, i > 0);
+                                if (more) {
+                                    if (g == 0)
+                                        stage_full(sk);
+                                    scores(g, q + g * TILE, sk);
+                                }
+                            }
+                        } else {
+                            values(i & 1, sv, i > 1);
+                        }
+                        commit(empty(sv % ST));
+                        if (more) {
+                            if (!PAIR) {
+                                stage_full(sk);
+                                scores(i & 1, q, sk);
+                            }
+                            commit(empty(sk % ST));
+                            if (i + LEAD == r.todo - 1)
+                                commit(q_empty(buf));
+                        }
+                    }
+                    seq += 2 * r.todo;
+                    ++nth;
+                }
+                if (*gave_up) {  // products in flight end before the tensor memory is freed
+                    mma_commit(drained);
+                    bar_wait_long(watch, drained, 0, true);
+                }
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GROUP_REGS));
         const int g = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // lane 32 (warp % 4)
         const uint32_t s_at = lanes + g * KT, o_at = lanes + 2 * KT + g * KT;
         const int rt = row / w.a.G, rg = row - rt * w.a.G;
         uint32_t done[2] = {0, 0}, cleaned = 0, joins = 0;
-        while (runs.next(r)) {
+        while (r.next()) {
             const Unit &u = r.u;
             const int lead = min(LEAD, r.todo);
             const int t = (PAIR ? g * w.TT : 0) + rt;  // of the unit's rows
@@ -468,11 +470,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                             if (k > most || (k < low && k >= sinks))
                                 s[k] = 0xff800000u;
                     }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < KT; ++k)
-                        top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[k]));
-                    m = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    for (int k = 0; k < KT; k += 2)
+                        top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    m = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     if (x == 0) {
                         used = m;
                     } else if (__any_sync(0xffffffffu, (m - used) * w.c > LAG || (used == -INFINITY && m > used))) {
@@ -493,21 +495,22 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         }
                     }
                     const float off = used == -INFINITY ? 0.0f : used * w.c;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const Two cc = two(w.c, w.c), minus = two(-off, -off);
+                    Two sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
 #pragma unroll
                     for (int k = 0; k < KT; k += 64) {
                         uint32_t weights[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const float p0 = ex2(fmaf(__uint_as_float(s[k + 2 * e]), w.c, -off));
-                            const float p1 = ex2(fmaf(__uint_as_float(s[k + 2 * e + 1]), w.c, -off));
-                            sum[2 * e & 3] += p0;
-                            sum[(2 * e & 3) + 1] += p1;
+                            const float2 z = apart(fma2(two(s[k + 2 * e], s[k + 2 * e + 1]), cc, minus));
+                            const float p0 = ex2(z.x), p1 = ex2(z.y);
+                            sum[e & 1] = add2(sum[e & 1], two(p0, p1));
                             weights[e] = pack<BF16>(p0, p1);
                         }
                         tmem_st32(s_at + k / 2, weights);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 all = apart(add2(sum[0], sum[1]));
+                    l += all.x + all.y;
                     tmem_wait_st();
                 }
                 if (edge) {
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(JOIN_T) attend_join_kernel(const __grid_consta
         const long long bt = i / w.a.Hq;
         const int hq = static_cast<int>(i - bt * w.a.Hq), b = static_cast<int>(bt / w.a.T);
         const int t = static_cast<int>(bt - static_cast<long long>(b) * w.a.T), h = hq / w.a.G;
-        const long long pair = static_cast<long long>(b) * w.nq + t / w.TQ;
+        const int pair = b * w.nq + t / w.TQ;
         const Unit u = unit_of(w, pair);
         if (t - u.t0 >= u.nt)
             continue;

@@ -56,7 +56,7 @@ struct Watch {
     int *status;
 };
 
-static __device__ __noinline__ void bar_wait_long(const Watch w, uint32_t bar, uint32_t parity, bool keep_on)
+__device__ __forceinline__ void bar_wait_long(const Watch w, uint32_t bar, uint32_t parity, bool keep_on)
 {
     const uint64_t t0 = now_ns();
     for (uint32_t n = 1;; ++n) {
@@ -203,6 +203,55 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi)
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     else
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));  // a NaN is passed over
+    return r;
+}
+
+// Two f32 in one instruction.
+struct Two {
+    uint64_t x;
+};
+
+__device__ __forceinline__ Two two(uint32_t lo, uint32_t hi)
+{
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.x) : "r"(lo), "r"(hi));
+    return r;
+}
+
+__device__ __forceinline__ Two two(float lo, float hi) { return two(__float_as_uint(lo), __float_as_uint(hi)); }
+
+__device__ __forceinline__ float2 apart(Two a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.x));
+    return r;
+}
+
+__device__ __forceinline__ Two add2(Two a, Two b)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.x) : "l"(a.x), "l"(b.x));
+    return r;
+}
+
+__device__ __forceinline__ Two mul2(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.x) : "l"(a.x), "l"(b.x));
+    return r;
+}
+
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.x) : "l"(a.x), "l"(b.x), "l"(c.x));
     return r;
 }
 
