@@ -44,9 +44,15 @@ struct Walk {
     int TT, TQ, nq;  // tokens of a tile, of a unit; units a session and kv head
     int box;         // rows of a copied box: a page, or 128 rows of a larger one
     float c;         // scale log2 e
-    long long *plan;         // [P + 1]: tiles before each (session, unit), and a CTA's share
+    struct Cut *cuts;        // [grid] the unit that is cut at a CTA's end
     float2 *stats;           // [2 grid][rows] maximum and sum of a part
     float *parts;            // [2 grid][rows][D] its sums
+};
+
+// A unit that begins as the last of CTA c's and goes on in the CTAs behind: its n parts lie in
+// `slot`, 2 (c + 1), 2 (c + 2), ...  n = 0: none.
+struct Cut {
+    int n, slot, b, t0, nt, h, pad[2];
 };
 
 // One session's unit: which rows, and which key tiles they see.
@@ -89,28 +95,30 @@ __device__ __forceinline__ bool all_see(const Walk &w, const Unit &u, int j)
            (!w.a.seen.window || u.hi - 1 - j < w.a.seen.window || j < w.a.seen.sinks);
 }
 
-// A CTA's share of the tiles and where it begins.
+// The bits 0 .. n - 1 of 32.
+__device__ __forceinline__ uint32_t bits_below(int n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Where a CTA's share of the tiles begins.
 struct Share {
-    long long first, last;  // tiles
-    long long pair, before; // the (session, unit) of `first`, and the tiles before that
+    Unit u;
+    int left, per;  // tiles of this share (0: none), of a full one
+    int pair, h, off;
 };
 
 // The runs of one unit's tiles after another within a share.
 struct Runs {
     const Walk &w;
-    long long left;      // tiles from this run on
-    int pair, slot;
     Unit u;
+    int left;            // tiles from this run on
+    int pair, slot;
     int h, off, todo;    // tiles off .. off + todo - 1 of the unit
     bool whole;          // all of them; else the parts go to `slot` of the workspace
     __device__ Runs(const Walk &w_, const Share &s)
-        : w(w_), left(s.last - s.first), pair(static_cast<int>(s.pair)), slot(2 * blockIdx.x), todo(0)
+        : w(w_), u(s.u), left(s.left), pair(s.pair), slot(2 * blockIdx.x), h(s.h), off(s.off), todo(0)
     {
-        if (left > 0) {
-            u = unit_of(w, pair);
-            h = static_cast<int>((s.first - s.before) / u.count);
-            off = static_cast<int>(s.first - s.before - static_cast<long long>(u.count) * h);
-        }
     }
     __device__ __forceinline__ bool next()
     {
@@ -128,66 +136,59 @@ struct Runs {
                 u = unit_of(w, ++pair);
             while (u.count == 0);
         }
-        todo = static_cast<int>(min(static_cast<long long>(u.count - off), left));
+        todo = min(u.count - off, left);
         whole = todo == u.count;
         return true;
     }
 };
 
-// Every CTA finds its share: the tiles of all units in the order (session, unit, kv head).
-// CTA 0 leaves the tiles before each (session, unit) in the workspace.  `part`: 16 long longs.
-__device__ Share share_of(const Walk &w, long long *part, Share *found)
+// Every CTA finds its share of the tiles of all units in the order (session, unit, kv head).
+// `part`: a word a warp.
+__device__ __forceinline__ void share_of(const Walk &w, int *part, Share *found)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long P = static_cast<long long>(w.a.c.B) * w.nq;
-    auto tiles_of = [&](long long i) { return i < P ? static_cast<long long>(unit_of(w, static_cast<int>(i)).count) * w.a.c.Hkv : 0ll; };
-    // over all: one chunk of THREADS units, or more
-    long long mine = 0;
-    for (long long i = tid; i < P; i += THREADS)
-        mine += tiles_of(i);
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-        mine += __shfl_xor_sync(0xffffffffu, mine, d);
-    if (lane == 0)
-        part[warp] = mine;
-    if (tid == 0)
-        *found = Share{0, 0, 0, 0};
-    __syncthreads();
-    long long total = 0;
-    for (int i = 0; i < THREADS / 32; ++i)
-        total += part[i];
-    __syncthreads();
-    const long long per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
-    const long long first = per * blockIdx.x, last = min(total, first + per);
-    long long carry = 0;
-    for (long long i0 = 0; i0 < P && (carry <= first || blockIdx.x == 0); i0 += THREADS) {
-        const long long x = tiles_of(i0 + tid);
-        long long s = x;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d)
-                s += y;
-        }
-        if (lane == 31)
-            part[warp] = s;
-        __syncthreads();
-        long long before = carry + s - x;
-        for (int i = 0; i < THREADS / 32; ++i) {
-            if (i < warp)
-                before += part[i];
-            carry += part[i];
-        }
-        if (first < last && before <= first && first < before + x)
-            *found = Share{first, last, i0 + tid, before};
-        if (blockIdx.x == 0 && i0 + tid < P)
-            w.plan[i0 + tid] = before;
-        __syncthreads();
+    const int P = w.a.c.B * w.nq, each = (P - 1) / THREADS + 1;
+    const int i0 = tid * each, i1 = min(P, i0 + each);
+    Unit u;
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) {
+        u = unit_of(w, i);
+        mine += u.count * w.a.c.Hkv;
     }
-    if (blockIdx.x == 0 && tid == 0)
-        w.plan[P] = per;
+    int s = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d)
+            s += y;
+    }
+    if (lane == 31)
+        part[warp] = s;
+    if (tid == 0)
+        found->left = 0;
     __syncthreads();
-    return *found;
+    int before = s - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i == warp)
+            before += total;
+        total += part[i];
+    }
+    const int per = (total + gridDim.x - 1) / gridDim.x;
+    const int first = per * blockIdx.x, last = min(total, first + per);
+    if (first < last && before <= first && first < before + mine) {
+        int i = i1 - 1;
+        if (each > 1)
+            for (i = i0;; ++i) {
+                u = unit_of(w, i);
+                if (first < before + u.count * w.a.c.Hkv)
+                    break;
+                before += u.count * w.a.c.Hkv;
+            }
+        const int h = (first - before) / u.count;
+        *found = Share{u, last - first, per, i, h, first - before - h * u.count};
+    }
+    __syncthreads();
 }
 
 // The place in the ring's order of a run's i-th value tile: key tiles run `lead` ahead.
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
     uint32_t *poison = reinterpret_cast<uint32_t *>(spare + 16);             // [2 groups][2][4]
-    long long *part = reinterpret_cast<long long *>(spare + 128);            // [10]
+    int *part = reinterpret_cast<int *>(spare + 128);                        // [12]
     Share *found = reinterpret_cast<Share *>(spare + 256);
     float2 *other = reinterpret_cast<float2 *>(spare + 512);                 // [128]: the second group's statistics
     static_assert(8 * (2 * stages(64) + 17) <= 512 && 512 + 512 + 128 * 8 <= SPARE, "room behind the ring");
@@ -263,69 +264,83 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             if (bad)
                 raise(w.a.status, bad);
         }
-    const Share share = share_of(w, part, found);
+    share_of(w, part, found);
     const Watch watch{gave_up, w.a.status};
-    Runs r(w, share);
+    Runs r(w, *found);
     uint32_t seq = 0;  // tiles that passed through the ring before this run
     int nth = 0;       // runs before this one
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         if (warp == COPY_WARP) {
-            auto tile_of = [&](const Runs &run, int i) {
-                const int x = run.off + i;
-                return x < run.u.far ? x : run.u.near + x - run.u.far;
-            };
+            // A lane has a box of each tile (a page, or part of a large one); up to 16 boxes.
             const int boxes = KT / w.box, page = 1 << w.a.c.shift;
-            auto load = [&](const Runs &run, const CUtensorMap *m, int i, uint32_t s) {
+            constexpr int UNSEEN = -1 << 31;
+            auto key_of = [&](int i) {
+                const int x = r.off + i;
+                return (x < r.u.far ? x : r.u.near + x - r.u.far) * KT + lane * w.box;
+            };
+            // the page of this lane's box of tile i, or UNSEEN
+            auto look = [&](int i) {
+                const int j = key_of(i);
+                if (i >= r.todo || lane >= boxes || j >= r.u.hi || (j + w.box <= r.u.lo && j >= w.a.seen.sinks))
+                    return UNSEEN;
+                const int id = w.a.c.table[static_cast<long long>(r.u.b) * w.a.c.cols + (j >> w.a.c.shift)];
+                return id == UNSEEN ? -1 : id;
+            };
+            auto load = [&](const CUtensorMap *m, int i, int id, uint32_t s) {
                 const uint32_t st = s % ST;
                 warp_wait(watch, empty(st), ((s / ST) & 1) ^ 1);
                 if (__any_sync(0xffffffffu, *gave_up))
                     return;
-                const int j0 = tile_of(run, i) * KT;
-                const int j = j0 + lane * w.box;  // up to 16 boxes: one a lane
-                int id = 0;
-                const bool want = lane < boxes && j < run.u.hi && (j + w.box > run.u.lo || j < w.a.seen.sinks);
-                if (want) {
-                    id = w.a.c.table[static_cast<long long>(run.u.b) * w.a.c.cols + (j >> w.a.c.shift)];
+                const uint32_t want = __ballot_sync(0xffffffffu, id != UNSEEN);
+                if (lane == 0)
+                    bar_expect(full(st), static_cast<uint32_t>(__popc(want)) * w.box * D * 2);
+                __syncwarp();
+                if (id != UNSEEN) {
                     if (id < 0 || id >= w.a.c.pages) {
                         raise(w.a.status, KDA_ST_BADPAGE);
                         id = w.a.c.pages;  // behind the last: zeros
                     }
-                }
-                const int count = __popc(__ballot_sync(0xffffffffu, want));
-                if (lane == 0)
-                    bar_expect(full(st), static_cast<uint32_t>(count) * w.box * D * 2);
-                __syncwarp();
-                if (want) {
                     const uint32_t dst = ring + st * TILE + lane * w.box * 128;
-    #pragma unroll
+#pragma unroll
                     for (int half = 0; half < HALVES; ++half)
-                        copy_4d(dst + half * HALF, m, half * 64, j & (page - 1), run.h, id, full(st));
+                        copy_4d(dst + half * HALF, m, half * 64, key_of(i) & (page - 1), r.h, id, full(st));
                 }
             };
-            auto load_q = [&](const Runs &run) {
+            auto load_q = [&] {
                 const int buf = PAIR ? 0 : nth & 1;
                 warp_wait(watch, q_empty(buf), ((PAIR ? nth : nth >> 1) & 1) ^ 1);
                 if (lane != 0 || *gave_up)
                     return;
-                const int two = PAIR && run.u.nt > w.TT;
+                const int two = PAIR && r.u.nt > w.TT;
                 bar_expect(q_full(buf), static_cast<uint32_t>(1 + two) * w.TT * w.a.G * D * 2);
                 for (int i = 0; i <= two; ++i)
                     for (int half = 0; half < HALVES; ++half)
-                        copy_3d(q_at + (PAIR ? i : buf) * TILE + half * HALF, &map_q, half * 64, run.h * w.a.G,
-                                run.u.b * w.a.T + run.u.t0 + i * w.TT, q_full(buf));
+                        copy_3d(q_at + (PAIR ? i : buf) * TILE + half * HALF, &map_q, half * 64, r.h * w.a.G,
+                                r.u.b * w.a.T + r.u.t0 + i * w.TT, q_full(buf));
             };
             while (r.next()) {
                 const int lead = min(LEAD, r.todo);
-                for (int i = 0; i < lead; ++i)
-                    load(r, &map_k, i, seq + i);
-                load_q(r);
+                int id[LEAD + 2];  // of value tile i, ..., key tile i + LEAD, and the next one
+#pragma unroll
+                for (int i = 0; i < LEAD + 2; ++i)
+                    id[i] = look(i);
+#pragma unroll
+                for (int i = 0; i < LEAD; ++i)
+                    if (i < lead)
+                        load(&map_k, i, id[i], seq + i);
+                load_q();
                 for (int i = 0; i < r.todo; ++i) {
                     const uint32_t s = seq + value_at(lead, r.todo, i);
-                    load(r, &map_v, i, s);
+                    const int next = look(i + LEAD + 2);
+                    load(&map_v, i, id[0], s);
                     if (i + LEAD < r.todo)
-                        load(r, &map_k, i + LEAD, s + 1);
+                        load(&map_k, i + LEAD, id[LEAD], s + 1);
+#pragma unroll
+                    for (int k = 0; k < LEAD + 1; ++k)
+                        id[k] = id[k + 1];
+                    id[LEAD + 1] = next;
                 }
                 seq += 2 * r.todo;
                 ++nth;
@@ -418,6 +433,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     bar_wait_long(watch, drained, 0, true);
                 }
             }
+        } else if (warp == MMA_WARP + 1) {
+            // what the second launch has to join
+            Cut cut{};
+            while (r.next())
+                if (r.todo == r.left && r.off == 0 && !r.whole)
+                    cut = Cut{1 + (r.u.count - r.todo - 1) / found->per + 1, r.slot, r.u.b, r.u.t0, r.u.nt, r.h, {}};
+            if (lane == 0)
+                w.cuts[blockIdx.x] = cut;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GROUP_REGS));
@@ -464,11 +487,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         tmem_ld32(s_at + k, s + k);
                     tmem_wait_ld();
                     if (edge) {
-                        const int most = p - j0, low = p_low - j0, sinks = w.a.seen.sinks - j0;
+                        const int end = p + 1 - j0, low = p_low - j0, sinks = w.a.seen.sinks - j0;
 #pragma unroll
-                        for (int k = 0; k < KT; ++k)
-                            if (k > most || (k < low && k >= sinks))
-                                s[k] = 0xff800000u;
+                        for (int k = 0; k < KT; k += 32) {
+                            const uint32_t seen = bits_below(end - k) & (~bits_below(low - k) | bits_below(sinks - k));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[k + e] = seen >> e & 1 ? s[k + e] : 0xff800000u;
+                        }
                     }
                     float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -663,7 +689,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
 }
 
-// The second launch: a warp a row and head joins the parts of a unit that was cut.
+// The second launch joins the parts of the units that were cut: CTAs for each, a warp a row.
 constexpr int JOIN_T = 256;
 
 template <int D, bool BF16>
@@ -671,66 +697,63 @@ __global__ void __launch_bounds__(JOIN_T) attend_join_kernel(const __grid_consta
 {
     after_previous();
     constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long items = static_cast<long long>(w.a.c.B) * w.a.T * w.a.Hq;
-    const long long P = static_cast<long long>(w.a.c.B) * w.nq, per = w.plan[P];
-    for (long long i = static_cast<long long>(blockIdx.x) * (JOIN_T / 32) + (threadIdx.x >> 5); i < items;
-         i += static_cast<long long>(gridDim.x) * (JOIN_T / 32)) {
-        const long long bt = i / w.a.Hq;
-        const int hq = static_cast<int>(i - bt * w.a.Hq), b = static_cast<int>(bt / w.a.T);
-        const int t = static_cast<int>(bt - static_cast<long long>(b) * w.a.T), h = hq / w.a.G;
-        const int pair = b * w.nq + t / w.TQ;
-        const Unit u = unit_of(w, pair);
-        if (t - u.t0 >= u.nt)
-            continue;
-        const long long from = w.plan[pair] + static_cast<long long>(h) * u.count;
-        const long long c0 = from / per, c1 = (from + u.count - 1) / per;
-        if (c0 == c1)
-            continue;
-        const int tl = t - u.t0, row = tl / w.TT * KT + tl % w.TT * w.a.G + hq - h * w.a.G;
-        auto slot = [&](long long c) { return (2 * c + (from > c * per ? 1 : 0)) * rows_a_part + row; };
-        float top = -INFINITY;
-        for (long long c = c0 + lane; c <= c1; c += 32)
-            top = fmaxf(top, w.stats[slot(c)].x);
+    const Cut cut = w.cuts[blockIdx.x];
+    const int lane = threadIdx.x & 31, rows = cut.n > 0 ? cut.nt * w.a.G : 0;
+    for (int i = blockIdx.y * (JOIN_T / 32) + (threadIdx.x >> 5); i < rows; i += gridDim.y * (JOIN_T / 32)) {
+        const int t = i / w.a.G, g = i - t * w.a.G, row = t / w.TT * KT + t % w.TT * w.a.G + g;
+        auto place = [&](int k) {
+            const int slot = k == 0 ? cut.slot : 2 * (static_cast<int>(blockIdx.x) + k);
+            return static_cast<size_t>(slot) * rows_a_part + row;
+        };
+        float top = -INFINITY, l = 0.0f, o[E] = {};
+        for (int k0 = 0; k0 < cut.n; k0 += 32) {
+            // a lane a part: its maximum and sum; then a part after another
+            const float2 s = k0 + lane < cut.n ? w.stats[place(k0 + lane)] : make_float2(-INFINITY, 0.0f);
+            float most = fmaxf(top, s.x);
 #pragma unroll
-        for (int d = 16; d; d >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float o[E] = {}, l = 0.0f;
-        for (long long c = c0; c <= c1; ++c) {
-            const float2 s = w.stats[slot(c)];
-            const float f = s.x == top ? 1.0f : ex2((s.x - top) * w.c);
-            const float *x = w.parts + slot(c) * D + lane * E;
-            l += s.y * f;
-            if (E == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(x);
-                o[0] += v.x * f;
-                o[1] += v.y * f;
-                o[2 % E] += v.z * f;
-                o[3 % E] += v.w * f;
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(x);
-                o[0] += v.x * f;
-                o[1] += v.y * f;
+            for (int d = 16; d; d >>= 1)
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+            const float again = top == most ? 1.0f : ex2((top - most) * w.c);
+            const float f = s.x == most ? 1.0f : ex2((s.x - most) * w.c);
+            float sum = s.y * f;
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            l = l * again + sum;
+            top = most;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                o[e] *= again;
+#pragma unroll 8
+            for (int k = 0; k < min(32, cut.n - k0); ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, k);
+                const float *x = w.parts + place(k0 + k) * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(x);
+                    o[0] += v.x * fk;
+                    o[1] += v.y * fk;
+                    o[2] += v.z * fk;
+                    o[3] += v.w * fk;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(x);
+                    o[0] += v.x * fk;
+                    o[1] += v.y * fk;
+                }
             }
         }
+        const long long to = (static_cast<long long>(cut.b) * w.a.T + cut.t0 + t) * w.a.Hq + cut.h * w.a.G + g;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(w.a.out + i * D + lane * E);
-        dst[0] = pack<BF16>(o[0] * inv, o[1] * inv);
-        if (E == 4)
-            dst[1] = pack<BF16>(o[2 % E] * inv, o[3 % E] * inv);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(w.a.out + to * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            dst[e / 2] = pack<BF16>(o[e] * inv, o[e + 1] * inv);
         if (lane == 0 && w.a.lse)
-            w.a.lse[i] = l == 0.0f ? -INFINITY : (top * w.c + log2f(l)) * LN2;
+            w.a.lse[to] = l == 0.0f ? -INFINITY : (top * w.c + log2f(l)) * LN2;
     }
 }
 
 // More than 128 rows of a session and kv head fill two tiles.
 bool is_pair(int T, int G) { return static_cast<long long>(T) > KT / G; }
-
-size_t plan_bytes(int B, int T, int G)
-{
-    const long long TQ = KT / G * (is_pair(T, G) ? 2 : 1);
-    return (static_cast<size_t>(B) * ((T + TQ - 1) / TQ) * 8 + 8 + 15) / 16 * 16;
-}
 
 template <int D, bool PAIR, bool BF16>
 int run(const Walk &w, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, unsigned grid,
@@ -743,9 +766,7 @@ int run(const Walk &w, const CUtensorMap &q, const CUtensorMap &k, const CUtenso
     if (int rc = launch(attend_kernel<D, PAIR, BF16>, dim3(grid), THREADS, shared_bytes(D), stream, "attend_kernel", w,
                         q, k, v))
         return rc;
-    const long long items = static_cast<long long>(w.a.c.B) * w.a.T * w.a.Hq;
-    const unsigned blocks = static_cast<unsigned>(std::min<long long>((items + JOIN_T / 32 - 1) / (JOIN_T / 32), 8 * SMS));
-    return launch(attend_join_kernel<D, BF16>, dim3(blocks), JOIN_T, 0, stream, "attend_join_kernel", w,
+    return launch(attend_join_kernel<D, BF16>, dim3(grid, PAIR ? 8 : 4), JOIN_T, 0, stream, "attend_join_kernel", w,
                   PAIR ? 2 * KT : KT);
 }
 
@@ -759,7 +780,7 @@ extern "C" size_t spec_attend_workspace_bytes(int B, int T, int Hq, int Hkv, int
     if (B < 1 || T < 1 || Hkv < 1 || Hq < Hkv || Hq / Hkv > KDA_GROUP_MAX)
         return 16;
     const size_t rows = 2 * pages::SMS * (is_pair(T, Hq / Hkv) ? 2 * KT : KT);
-    return plan_bytes(B, T, Hq / Hkv) + rows * (8 + 4 * static_cast<size_t>(D));
+    return pages::SMS * sizeof(Cut) + rows * (8 + 4 * static_cast<size_t>(D));
 }
 
 extern "C" int spec_attend(const kda_cache *cache, const void *q, int T, int Hq, long long ld_q, const int *t_rows,
@@ -789,8 +810,8 @@ extern "C" int spec_attend(const kda_cache *cache, const void *q, int T, int Hq,
     w.box = std::min(page, KT);
     w.c = scale * pages::LOG2E;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    w.plan = reinterpret_cast<long long *>(ws);
-    ws += plan_bytes(a.c.B, T, a.G);
+    w.cuts = reinterpret_cast<Cut *>(ws);
+    ws += pages::SMS * sizeof(Cut);
     w.stats = reinterpret_cast<float2 *>(ws);
     w.parts = reinterpret_cast<float *>(ws + sizeof(float2) * 2 * pages::SMS * (pair ? 2 * KT : KT));
 
@@ -812,8 +833,10 @@ extern "C" int spec_attend(const kda_cache *cache, const void *q, int T, int Hq,
     if (int rc = tiles::encode_map(&map_q, bf16, 3, q, q_dims, q_strides, q_box))
         return rc;
     // as many CTAs as there can be tiles, one an SM at most
-    const long long most = static_cast<long long>(a.c.B) * w.nq * a.c.Hkv * ((a.c.capacity() + KT - 1) / KT);
-    const unsigned grid = static_cast<unsigned>(std::min<long long>(most, pages::SMS));
+    const double most = static_cast<double>(a.c.B) * w.nq * a.c.Hkv * ((a.c.capacity() + KT - 1) / KT);
+    if (most > 2147483647.0)
+        return fail(KDA_EINVAL, "too many tiles of keys for one call");
+    const unsigned grid = static_cast<unsigned>(std::min(most, static_cast<double>(pages::SMS)));
     auto go = [&](auto d, auto two) {
         return bf16 ? run<decltype(d)::value, decltype(two)::value, true>(w, map_q, map_k, map_v, grid, stream)
                     : run<decltype(d)::value, decltype(two)::value, false>(w, map_q, map_k, map_v, grid, stream);
