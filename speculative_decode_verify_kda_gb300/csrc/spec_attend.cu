@@ -24,8 +24,8 @@ using namespace pages;
 using namespace tiles;
 
 constexpr int KT = 128;              // keys of a tile, and rows of a tile
-constexpr int COPY_WARP = 8, MMA_WARP = 9;
-constexpr int THREADS = 384;         // two groups of 128 and four warps more, two of them idle
+constexpr int KEY_WARP = 8, MMA_WARP = 9, VALUE_WARP = 10, CUT_WARP = 11;
+constexpr int THREADS = 384;         // two groups of 128 and four warps more
 // Registers are handed from the last four warps to the groups (a row of 128 scores is held in
 // them): 256 x 216 + 128 x 72 = 384 x 168, what the launch has.
 constexpr int GROUP_REGS = 216, OTHER_REGS = 72;
@@ -36,7 +36,9 @@ constexpr int SPARE = 2048;          // barriers and what the groups tell each o
 constexpr float LAG = 8.0f;
 
 __host__ __device__ constexpr int tile_bytes(int D) { return KT * D * 2; }
-__host__ __device__ constexpr int stages(int D) { return D == 128 ? 5 : 8; }
+__host__ __device__ constexpr int key_stages(int D) { return D == 128 ? 3 : 5; }
+__host__ __device__ constexpr int value_stages(int D) { return D == 128 ? 2 : 4; }
+__host__ __device__ constexpr int stages(int D) { return key_stages(D) + value_stages(D); }
 __host__ __device__ constexpr int shared_bytes(int D) { return 2 * tile_bytes(D) + stages(D) * tile_bytes(D) + SPARE + 1024; }
 
 struct Walk {
@@ -94,6 +96,20 @@ __device__ __forceinline__ bool all_see(const Walk &w, const Unit &u, int j)
     return j <= u.n + u.t0 &&
            (!w.a.seen.window || u.hi - 1 - j < w.a.seen.window || j < w.a.seen.sinks);
 }
+
+// A place in the ring of tiles and the parity of its turn.
+template <int ST>
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step()
+    {
+        if (++stage == ST) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // The bits 0 .. n - 1 of 32.
 __device__ __forceinline__ uint32_t bits_below(int n)
@@ -191,22 +207,19 @@ __device__ __forceinline__ void share_of(const Walk &w, int *part, Share *found)
     __syncthreads();
 }
 
-// The place in the ring's order of a run's i-th value tile: key tiles run `lead` ahead.
-__device__ __forceinline__ uint32_t value_at(int lead, int todo, int i) { return lead + i + min(i, todo - lead); }
-
 template <int D, bool PAIR, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Walk w,
                                                             const __grid_constant__ CUtensorMap map_q,
                                                             const __grid_constant__ CUtensorMap map_k,
                                                             const __grid_constant__ CUtensorMap map_v)
 {
-    constexpr int TILE = tile_bytes(D), HALF = KT * 128, HALVES = D / 64, ST = stages(D);
+    constexpr int TILE = tile_bytes(D), HALF = KT * 128, HALVES = D / 64, ST = stages(D), KS = key_stages(D), VS = value_stages(D);
     constexpr int LEAD = PAIR ? 1 : 2;  // key tiles ahead of value tiles
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    const uint32_t q_at = base, ring = base + 2 * TILE, bars = ring + ST * TILE;
+    const uint32_t q_at = base, ring = base + 2 * TILE, ring_v = ring + KS * TILE, bars = ring + ST * TILE;
     // barriers
-    auto full = [&](int s) { return bars + 8u * s; };
+    auto full = [&](int s) { return bars + 8u * s; };  // key stages, then value stages
     auto empty = [&](int s) { return bars + 8u * (ST + s); };
     auto q_full = [&](int i) { return bars + 8u * (2 * ST + i); };
     auto q_empty = [&](int i) { return bars + 8u * (2 * ST + 2 + i); };
@@ -267,173 +280,174 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     share_of(w, part, found);
     const Watch watch{gave_up, w.a.status};
     Runs r(w, *found);
-    uint32_t seq = 0;  // tiles that passed through the ring before this run
-    int nth = 0;       // runs before this one
+    uint32_t seq = 0;   // tiles before this run
+    int nth = 0;        // runs before this one
+    bool dead = false;  // a wait gave up: nothing more is issued
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-        if (warp == COPY_WARP) {
+        if (warp == KEY_WARP || warp == VALUE_WARP) {
+            const bool keys = warp == KEY_WARP;
+            const CUtensorMap *m = keys ? &map_k : &map_v;
+            const int first = keys ? 0 : KS, count = keys ? KS : VS;
+            int stage = 0;
+            uint32_t phase = 0;
             // A lane has a box of each tile (a page, or part of a large one); up to 16 boxes.
             const int boxes = KT / w.box, page = 1 << w.a.c.shift;
-            constexpr int UNSEEN = -1 << 31;
             auto key_of = [&](int i) {
                 const int x = r.off + i;
                 return (x < r.u.far ? x : r.u.near + x - r.u.far) * KT + lane * w.box;
             };
-            // the page of this lane's box of tile i, or UNSEEN
-            auto look = [&](int i) {
+            // whether some row sees this lane's box of tile i, and its page
+            auto seen = [&](int i) {
                 const int j = key_of(i);
-                if (i >= r.todo || lane >= boxes || j >= r.u.hi || (j + w.box <= r.u.lo && j >= w.a.seen.sinks))
-                    return UNSEEN;
-                const int id = w.a.c.table[static_cast<long long>(r.u.b) * w.a.c.cols + (j >> w.a.c.shift)];
-                return id == UNSEEN ? -1 : id;
+                return i < r.todo && lane < boxes && j < r.u.hi && (j + w.box > r.u.lo || j < w.a.seen.sinks);
             };
-            auto load = [&](const CUtensorMap *m, int i, int id, uint32_t s) {
-                const uint32_t st = s % ST;
-                warp_wait(watch, empty(st), ((s / ST) & 1) ^ 1);
-                if (__any_sync(0xffffffffu, *gave_up))
-                    return;
-                const uint32_t want = __ballot_sync(0xffffffffu, id != UNSEEN);
-                if (lane == 0)
-                    bar_expect(full(st), static_cast<uint32_t>(__popc(want)) * w.box * D * 2);
-                __syncwarp();
-                if (id != UNSEEN) {
-                    if (id < 0 || id >= w.a.c.pages) {
-                        raise(w.a.status, KDA_ST_BADPAGE);
-                        id = w.a.c.pages;  // behind the last: zeros
-                    }
-                    const uint32_t dst = ring + st * TILE + lane * w.box * 128;
-#pragma unroll
-                    for (int half = 0; half < HALVES; ++half)
-                        copy_4d(dst + half * HALF, m, half * 64, key_of(i) & (page - 1), r.h, id, full(st));
-                }
-            };
-            auto load_q = [&] {
-                const int buf = PAIR ? 0 : nth & 1;
-                warp_wait(watch, q_empty(buf), ((PAIR ? nth : nth >> 1) & 1) ^ 1);
-                if (lane != 0 || *gave_up)
-                    return;
-                const int two = PAIR && r.u.nt > w.TT;
-                bar_expect(q_full(buf), static_cast<uint32_t>(1 + two) * w.TT * w.a.G * D * 2);
-                for (int i = 0; i <= two; ++i)
-                    for (int half = 0; half < HALVES; ++half)
-                        copy_3d(q_at + (PAIR ? i : buf) * TILE + half * HALF, &map_q, half * 64, r.h * w.a.G,
-                                r.u.b * w.a.T + r.u.t0 + i * w.TT, q_full(buf));
+            auto look = [&](int i) {
+                return seen(i) ? w.a.c.table[static_cast<long long>(r.u.b) * w.a.c.cols + (key_of(i) >> w.a.c.shift)] : 0;
             };
             while (r.next()) {
-                const int lead = min(LEAD, r.todo);
-                int id[LEAD + 2];  // of value tile i, ..., key tile i + LEAD, and the next one
-#pragma unroll
-                for (int i = 0; i < LEAD + 2; ++i)
-                    id[i] = look(i);
-#pragma unroll
-                for (int i = 0; i < LEAD; ++i)
-                    if (i < lead)
-                        load(&map_k, i, id[i], seq + i);
-                load_q();
+                int id = look(0);
                 for (int i = 0; i < r.todo; ++i) {
-                    const uint32_t s = seq + value_at(lead, r.todo, i);
-                    const int next = look(i + LEAD + 2);
-                    load(&map_v, i, id[0], s);
-                    if (i + LEAD < r.todo)
-                        load(&map_k, i + LEAD, id[LEAD], s + 1);
+                    const int next = look(i + 1);  // on its way while this tile is copied
+                    if (!warp_wait(watch, empty(first + stage), phase ^ 1))
+                        dead = true;
+                    const bool want = seen(i);
+                    const uint32_t bar = full(first + stage), all = __ballot_sync(0xffffffffu, want);
+                    if (!dead) {
+                        if (lane == 0)
+                            bar_expect(bar, static_cast<uint32_t>(__popc(all)) * w.box * D * 2);
+                        __syncwarp();
+                        if (want) {
+                            if (id < 0 || id >= w.a.c.pages) {
+                                raise(w.a.status, KDA_ST_BADPAGE);
+                                id = w.a.c.pages;  // behind the last: zeros
+                            }
+                            const uint32_t dst = ring + (first + stage) * TILE + lane * w.box * 128;
 #pragma unroll
-                    for (int k = 0; k < LEAD + 1; ++k)
-                        id[k] = id[k + 1];
-                    id[LEAD + 1] = next;
+                            for (int half = 0; half < HALVES; ++half)
+                                copy_4d(dst + half * HALF, m, half * 64, key_of(i) & (page - 1), r.h, id, bar);
+                        }
+                        __syncwarp();
+                    }
+                    if (++stage == count) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    id = next;
+                    if (keys && i == min(LEAD, r.todo) - 1) {  // the rows, behind the first keys
+                        const int buf = PAIR ? 0 : nth & 1;
+                        if (!warp_wait(watch, q_empty(buf), ((PAIR ? nth : nth >> 1) & 1) ^ 1))
+                            dead = true;
+                        const bool two = PAIR && r.u.nt > w.TT;
+                        if (!dead && lane == 0) {
+                            bar_expect(q_full(buf), (two ? 2u : 1u) * w.TT * w.a.G * D * 2);
+                            for (int x = 0; x <= two; ++x)
+                                for (int half = 0; half < HALVES; ++half)
+                                    copy_3d(q_at + (PAIR ? x : buf) * TILE + half * HALF, &map_q, half * 64,
+                                            r.h * w.a.G, r.u.b * w.a.T + r.u.t0 + x * w.TT, q_full(buf));
+                        }
+                        __syncwarp();
+                    }
                 }
-                seq += 2 * r.todo;
                 ++nth;
             }
-            if (*gave_up && lane == 0) {  // copies in flight land before the CTA ends
-                for (uint32_t s = seq > ST ? seq - ST : 0; s < seq; ++s)
-                    bar_wait_long(watch, full(s % ST), (s / ST) & 1, true);
-            }
+            if (dead)  // copies in flight land before the CTA ends
+                for (int i = 0; i < count; ++i) {
+                    bar_wait_long(watch, full(first + stage), phase ^ 1, true);
+                    if (++stage == count) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
         } else if (warp == MMA_WARP) {
-        if (lane == 0) {
-                constexpr uint32_t SCORES = product_desc(BF16, KT, KT, false), VALUES = product_desc(BF16, KT, D, true);
-                uint32_t done[2] = {0, 0};
-                auto stage_full = [&](uint32_t s) { bar_wait(watch, full(s % ST), (s / ST) & 1); };
-                auto scores = [&](int g, uint32_t q, uint32_t s) {
-                    const uint64_t a = tile_desc(q, 16, 1024), b = tile_desc(ring + (s % ST) * TILE, 16, 1024);
-                    if (*gave_up)
-                        return;
-    #pragma unroll
+            // The whole warp walks; one lane issues.
+            constexpr uint32_t SCORES = product_desc(BF16, KT, KT, false), VALUES = product_desc(BF16, KT, D, true);
+            const uint32_t acc = uniform(tmem);
+            uint32_t done = 0;  // bit g: the phase of group g's weights
+            Ring<KS> key;
+            Ring<VS> val;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (!warp_wait(watch, bar, parity))
+                    dead = true;
+            };
+            auto scores = [&](int g, uint32_t q) {
+                const uint64_t a = tile_desc(q, 16, 1024), b = tile_desc(ring + key.stage * TILE, 16, 1024);
+                if (!dead && elect()) {
+#pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
-                        mma_ss(tmem + g * KT, a + step, b + step, SCORES, k > 0);
+                        mma_ss(acc + g * KT, a + step, b + step, SCORES, k > 0);
                     }
                     mma_commit(s_full(g));
-                };
-                auto values = [&](int g, uint32_t s, bool add) {
-                    const uint64_t b = tile_desc(ring + (s % ST) * TILE, HALF, 1024);
-                    bar_wait(watch, p_full(g), done[g] & 1);
-                    ++done[g];
-                    fence_after();
-                    if (*gave_up)
-                        return;
-    #pragma unroll
+                }
+                __syncwarp();
+            };
+            auto values = [&](int g, bool add) {
+                const uint64_t b = tile_desc(ring_v + val.stage * TILE, HALF, 1024);
+                wait(p_full(g), done >> g & 1);
+                done ^= 1u << g;
+                fence_after();
+                if (!dead && elect()) {
+#pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
-                        mma_ts(tmem + 2 * KT + g * KT, tmem + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES, add || k > 0);
+                        mma_ts(acc + 2 * KT + g * KT, acc + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES, add || k > 0);
                     mma_commit(o_full(g));
-                };
-                auto commit = [&](uint32_t bar) {
-                    if (!*gave_up)
-                        mma_commit(bar);
-                };
-                while (r.next()) {
-                    const int lead = min(LEAD, r.todo), buf = PAIR ? 0 : nth & 1;
-                    const int groups = PAIR ? (r.u.nt > w.TT ? 2 : 1) : 0;
-                    const uint32_t q = q_at + (PAIR ? 0 : buf * TILE);
-                    bar_wait(watch, q_full(buf), (PAIR ? nth : nth >> 1) & 1);
-                    for (int i = 0; i < lead; ++i) {
-                        stage_full(seq + i);
-                        fence_after();
-                        if (PAIR)
-                            for (int g = 0; g < groups; ++g)
-                                scores(g, q + g * TILE, seq + i);
-                        else
-                            scores(i, q, seq + i);
-                        commit(empty((seq + i) % ST));
-                    }
-                    if (r.todo <= LEAD)
-                        commit(q_empty(buf));
-                    for (int i = 0; i < r.todo; ++i) {
-                        const uint32_t sv = seq + value_at(lead, r.todo, i), sk = sv + 1;
-                        const bool more = i + LEAD < r.todo;
-                        stage_full(sv);
-                        if (PAIR) {
-                            for (int g = 0; g < groups; ++g) {
-                                values(g, sv, i > 0);
-                                if (more) {
-                                    if (g == 0)
-                                        stage_full(sk);
-                                    scores(g, q + g * TILE, sk);
-                                }
-                            }
-                        } else {
-                            values(i & 1, sv, i > 1);
-                        }
-                        commit(empty(sv % ST));
-                        if (more) {
-                            if (!PAIR) {
-                                stage_full(sk);
-                                scores(i & 1, q, sk);
-                            }
-                            commit(empty(sk % ST));
-                            if (i + LEAD == r.todo - 1)
-                                commit(q_empty(buf));
-                        }
-                    }
-                    seq += 2 * r.todo;
-                    ++nth;
                 }
-                if (*gave_up) {  // products in flight end before the tensor memory is freed
-                    mma_commit(drained);
-                    bar_wait_long(watch, drained, 0, true);
+                __syncwarp();
+            };
+            auto commit = [&](uint32_t bar) {
+                if (!dead && elect())
+                    mma_commit(bar);
+                __syncwarp();
+            };
+            while (r.next()) {
+                const int todo = uniform(r.todo), buf = PAIR ? 0 : nth & 1;
+                const bool two = uniform(r.u.nt > w.TT);
+                const uint32_t q = q_at + (PAIR ? 0 : buf * TILE);
+                wait(q_full(buf), (PAIR ? nth : nth >> 1) & 1);
+                for (int i = 0; i < min(LEAD, todo); ++i) {
+                    wait(full(key.stage), key.phase);
+                    scores(i, q);
+                    if (PAIR && two)
+                        scores(1, q + TILE);
+                    commit(empty(key.stage));
+                    key.step();
                 }
+                if (todo <= LEAD)
+                    commit(q_empty(buf));
+                for (int i = 0; i < todo; ++i) {
+                    const bool more = i + LEAD < todo;
+                    const int g = PAIR ? 0 : i & 1;
+                    wait(full(KS + val.stage), val.phase);
+                    values(g, i > LEAD - 1);
+                    if (more) {
+                        wait(full(key.stage), key.phase);
+                        scores(g, q);
+                    }
+                    if (PAIR && two) {
+                        values(1, i > 0);
+                        if (more)
+                            scores(1, q + TILE);
+                    }
+                    commit(empty(KS + val.stage));
+                    val.step();
+                    if (more) {
+                        commit(empty(key.stage));
+                        key.step();
+                        if (i + LEAD == todo - 1)
+                            commit(q_empty(buf));
+                    }
+                }
+                ++nth;
             }
-        } else if (warp == MMA_WARP + 1) {
+            if (dead) {  // products in flight end before the tensor memory is freed
+                if (elect())
+                    mma_commit(drained);
+                __syncwarp();
+                bar_wait_long(watch, drained, 0, true);
+            }
+        } else if (warp == CUT_WARP) {
             // what the second launch has to join
             Cut cut{};
             while (r.next())
@@ -451,7 +465,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         uint32_t done[2] = {0, 0}, cleaned = 0, joins = 0;
         while (r.next()) {
             const Unit &u = r.u;
-            const int lead = min(LEAD, r.todo);
             const int t = (PAIR ? g * w.TT : 0) + rt;  // of the unit's rows
             const bool live = rt < w.TT && t < u.nt;
             const bool busy = __any_sync(0xffffffffu, live);
@@ -543,13 +556,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     // Values of keys that no row sees become zeros (a weight of 0 times anything is
                     // then 0); of a key that only some rows see, values that are not finite do too,
                     // and the rows that see it are marked.
-                    const uint32_t place = seq + value_at(lead, r.todo, i), st = place % ST;
+                    const uint32_t place = seq + i, st = place % VS;
                     const int who = PAIR ? 0 : g;
                     uint32_t *said = poison + (who * 2 + (cleaned & 1)) * 4;
                     if (g == who) {
-                        warp_wait(watch, full(st), (place / ST) & 1);
+                        warp_wait(watch, full(KS + st), (place / VS) & 1);
                         const int j = j0 + row;
-                        unsigned char *v = raw + (ring + st * TILE - smem_addr(raw)) + row * 128;
+                        unsigned char *v = raw + (ring_v + st * TILE - smem_addr(raw)) + row * 128;
                         bool zero = !some_see(w, u, j), bad = false;
                         if (!zero && !all_see(w, u, j)) {
                             constexpr uint32_t E = BF16 ? 0x7f807f80u : 0x7c007c00u;
@@ -677,7 +690,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     fence_after();
                 }
             }
-            seq += 2 * r.todo;
+            seq += r.todo;
             ++nth;
         }
     }

@@ -56,15 +56,15 @@ struct Watch {
     int *status;
 };
 
-__device__ __forceinline__ void bar_wait_long(const Watch w, uint32_t bar, uint32_t parity, bool keep_on)
+__device__ __forceinline__ bool bar_wait_long(const Watch w, uint32_t bar, uint32_t parity, bool keep_on)
 {
     const uint64_t t0 = now_ns();
     for (uint32_t n = 1;; ++n) {
         if (bar_try(bar, parity))
-            return;
+            return true;
         if ((n & 15) == 0) {
             if (*w.gave_up && !keep_on)
-                return;
+                return false;
             if (now_ns() - t0 > WAIT_NS)
                 break;
         }
@@ -72,21 +72,30 @@ __device__ __forceinline__ void bar_wait_long(const Watch w, uint32_t bar, uint3
     *w.gave_up = 1;
     if (w.status)
         atomicOr(w.status, KDA_ST_TIMEOUT);
+    return false;
 }
 
-// Wait for the phase of `bar` with `parity`, for a second at most.
-__device__ __forceinline__ void bar_wait(const Watch &w, uint32_t bar, uint32_t parity)
+// A warp's wait for the phase of `bar` with `parity`, for a second at most; the warp goes on
+// together.  False (in every lane) when a lane gave up.
+__device__ __forceinline__ bool warp_wait(const Watch &w, uint32_t bar, uint32_t parity)
 {
-    if (!bar_try(bar, parity))
-        bar_wait_long(w, bar, parity, false);
+    if (__all_sync(0xffffffffu, bar_try(bar, parity)))
+        return true;
+    const bool ok = bar_wait_long(w, bar, parity, false);
+    return __all_sync(0xffffffffu, ok);
 }
 
-// The same for a whole warp, which goes on together.
-__device__ __forceinline__ void warp_wait(const Watch &w, uint32_t bar, uint32_t parity)
+// One lane of a warp that is together.  Products, copies and their barriers are issued by
+// `if (elect())` from values that are the same in every lane: so they stay in uniform registers
+// (eight products issue in 206 cycles so, in 418 from inside `if (lane == 0)`).
+__device__ __forceinline__ bool elect()
 {
-    bar_wait(w, bar, parity);
-    __syncwarp();
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Ordinary writes to shared memory before this are seen by copies and products after it.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
