@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     auto q_empty = [&](int i) { return bars + 8u * (2 * ST + 2 + i); };
     auto s_full = [&](int g) { return bars + 8u * (2 * ST + 4 + g); };
     auto p_full = [&](int g) { return bars + 8u * (2 * ST + 6 + g); };
+    auto p_half = [&](int g) { return bars + 8u * (2 * ST + 17 + g); };  // the first 64 keys' weights
     auto o_full = [&](int g) { return bars + 8u * (2 * ST + 8 + g); };
     auto v_clean = [&](int i) { return bars + 8u * (2 * ST + 10 + i); };
     const uint32_t told = bars + 8u * (2 * ST + 14), joined = told + 8, drained = told + 16;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     int *part = reinterpret_cast<int *>(spare + 128);                        // [12]
     Share *found = reinterpret_cast<Share *>(spare + 256);
     float2 *other = reinterpret_cast<float2 *>(spare + 512);                 // [128]: the second group's statistics
-    static_assert(8 * (2 * stages(64) + 17) <= 512 && 512 + 512 + 128 * 8 <= SPARE, "room behind the ring");
+    static_assert(8 * (2 * stages(64) + 19) <= 512 && 512 + 512 + 128 * 8 <= SPARE, "room behind the ring");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == MMA_WARP)
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             bar_init(q_full(g), 1);
             bar_init(q_empty(g), 1);
             bar_init(s_full(g), 1);
+            bar_init(p_half(g), 4);
             bar_init(p_full(g), 4);
             bar_init(o_full(g), 1);
             bar_init(v_clean(2 * g), 4);
@@ -385,16 +387,21 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             };
             auto values = [&](int g, bool add) {
                 const uint64_t b = tile_desc(ring_v + val.stage * TILE, HALF, 1024);
-                wait(p_full(g), done >> g & 1);
-                done ^= 1u << g;
-                fence_after();
-                if (!dead && elect()) {
 #pragma unroll
-                    for (int k = 0; k < KT / 16; ++k)
-                        mma_ts(acc + 2 * KT + g * KT, acc + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES, add || k > 0);
-                    mma_commit(o_full(g));
+                for (int half = 0; half < 2; ++half) {
+                    wait(half == 0 ? p_half(g) : p_full(g), done >> g & 1);
+                    fence_after();
+                    if (!dead && elect()) {
+#pragma unroll
+                        for (int k = half * KT / 32; k < (half + 1) * KT / 32; ++k)
+                            mma_ts(acc + 2 * KT + g * KT, acc + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES,
+                                   add || k > 0);
+                        if (half == 1)
+                            mma_commit(o_full(g));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                done ^= 1u << g;
             };
             auto commit = [&](uint32_t bar) {
                 if (!dead && elect())
@@ -491,6 +498,48 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 const int i = PAIR ? x : 2 * x + g;
                 const int j0 = key_of(i);
                 const bool edge = is_edge(j0);
+                if (edge) {
+                    // Values of keys that no row sees become zeros (a weight of 0 times anything is
+                    // then 0); of a key that only some rows see, values that are not finite do too,
+                    // and the rows that see it are marked.
+                    const uint32_t place = seq + i, st = place % VS;
+                    const int who = PAIR ? 0 : g;
+                    uint32_t *said = poison + (who * 2 + (cleaned & 1)) * 4;
+                    if (g == who) {
+                        warp_wait(watch, full(KS + st), (place / VS) & 1);
+                        const int j = j0 + row;
+                        unsigned char *v = raw + (ring_v + st * TILE - smem_addr(raw)) + row * 128;
+                        bool zero = !some_see(w, u, j), bad = false;
+                        if (!zero && !all_see(w, u, j)) {
+                            constexpr uint32_t E = BF16 ? 0x7f807f80u : 0x7c007c00u;
+                            for (int k = 0; k < D / 8; ++k) {
+                                const uint4 q = *reinterpret_cast<const uint4 *>(v + (k / 8) * HALF + ((k ^ row) & 7) * 16);
+                                for (uint32_t e : {q.x, q.y, q.z, q.w})
+                                    bad |= (e & E & 0xffffu) == (E & 0xffffu) || (e & E) >> 16 == E >> 16;
+                            }
+                            zero = bad;
+                        }
+                        if (zero)
+                            for (int k = 0; k < D / 8; ++k)
+                                *reinterpret_cast<uint4 *>(v + (k / 8) * HALF + ((k ^ row) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        const uint32_t mask = __ballot_sync(0xffffffffu, bad);
+                        if (lane == 0)
+                            said[warp & 3] = mask;
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_arrive(v_clean(2 * who + (cleaned & 1)));
+                    }
+                    // two barriers in turn: the first group may be a tile ahead of the second
+                    warp_wait(watch, v_clean(2 * who + (cleaned & 1)), (cleaned >> 1) & 1);
+                    ++cleaned;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        for (uint32_t left = said[k]; left; left &= left - 1) {
+                            const int j = j0 + 32 * k + __ffs(left) - 1;
+                            spoiled |= j <= p && (j >= p_low || j < w.a.seen.sinks);
+                        }
+                }
                 warp_wait(watch, s_full(g), (done[g] + x) & 1);
                 if (busy) {
                     fence_after();
@@ -547,52 +596,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                             weights[e] = pack<BF16>(p0, p1);
                         }
                         tmem_st32(s_at + k / 2, weights);
+                        if (k == 0) {  // the product with the first values may begin
+                            tmem_wait_st();
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                bar_arrive(p_half(g));
+                        }
                     }
                     const float2 all = apart(add2(sum[0], sum[1]));
                     l += all.x + all.y;
                     tmem_wait_st();
-                }
-                if (edge) {
-                    // Values of keys that no row sees become zeros (a weight of 0 times anything is
-                    // then 0); of a key that only some rows see, values that are not finite do too,
-                    // and the rows that see it are marked.
-                    const uint32_t place = seq + i, st = place % VS;
-                    const int who = PAIR ? 0 : g;
-                    uint32_t *said = poison + (who * 2 + (cleaned & 1)) * 4;
-                    if (g == who) {
-                        warp_wait(watch, full(KS + st), (place / VS) & 1);
-                        const int j = j0 + row;
-                        unsigned char *v = raw + (ring_v + st * TILE - smem_addr(raw)) + row * 128;
-                        bool zero = !some_see(w, u, j), bad = false;
-                        if (!zero && !all_see(w, u, j)) {
-                            constexpr uint32_t E = BF16 ? 0x7f807f80u : 0x7c007c00u;
-                            for (int k = 0; k < D / 8; ++k) {
-                                const uint4 q = *reinterpret_cast<const uint4 *>(v + (k / 8) * HALF + ((k ^ row) & 7) * 16);
-                                for (uint32_t e : {q.x, q.y, q.z, q.w})
-                                    bad |= (e & E & 0xffffu) == (E & 0xffffu) || (e & E) >> 16 == E >> 16;
-                            }
-                            zero = bad;
-                        }
-                        if (zero)
-                            for (int k = 0; k < D / 8; ++k)
-                                *reinterpret_cast<uint4 *>(v + (k / 8) * HALF + ((k ^ row) & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        const uint32_t mask = __ballot_sync(0xffffffffu, bad);
-                        if (lane == 0)
-                            said[warp & 3] = mask;
-                        fence_async();
-                        __syncwarp();
-                        if (lane == 0)
-                            bar_arrive(v_clean(2 * who + (cleaned & 1)));
-                    }
-                    // two barriers in turn: the first group may be a tile ahead of the second
-                    warp_wait(watch, v_clean(2 * who + (cleaned & 1)), (cleaned >> 1) & 1);
-                    ++cleaned;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        for (uint32_t left = said[k]; left; left &= left - 1) {
-                            const int j = j0 + 32 * k + __ffs(left) - 1;
-                            spoiled |= j <= p && (j >= p_low || j < w.a.seen.sinks);
-                        }
+                } else if (lane == 0) {
+                    bar_arrive(p_half(g));
                 }
                 fence_before();
                 __syncwarp();
