@@ -29,7 +29,7 @@ constexpr int THREADS = 384;         // two groups of 128 and four warps more
 // Registers are handed from the last four warps to the groups (a row of 128 scores is held in
 // them): 256 x 216 + 128 x 72 = 384 x 168, what the launch has.
 constexpr int GROUP_REGS = 216, OTHER_REGS = 72;
-constexpr int SPARE = 2048;          // barriers and what the groups tell each other
+constexpr int SPARE = 2560;          // barriers and what the warps tell each other
 // The running maximum that weights are taken against follows the true one only when it falls
 // behind by more than this many powers of two: weights stay below 2^8, and the sums in tensor
 // memory are seldom rescaled.
@@ -39,7 +39,7 @@ __host__ __device__ constexpr int tile_bytes(int D) { return KT * D * 2; }
 __host__ __device__ constexpr int key_stages(int D) { return D == 128 ? 3 : 5; }
 __host__ __device__ constexpr int value_stages(int D) { return D == 128 ? 2 : 4; }
 __host__ __device__ constexpr int stages(int D) { return key_stages(D) + value_stages(D); }
-__host__ __device__ constexpr int shared_bytes(int D) { return 2 * tile_bytes(D) + stages(D) * tile_bytes(D) + SPARE + 1024; }
+__host__ __device__ constexpr int shared_bytes(int D) { return (2 + stages(D)) * tile_bytes(D) + SPARE; }
 
 struct Walk {
     Attend a;
@@ -111,6 +111,14 @@ struct Ring {
     }
 };
 
+// The largest of 64 scores, in four strands.
+__device__ __forceinline__ void highest(float (&top)[4], const uint32_t *s)
+{
+#pragma unroll
+    for (int k = 0; k < 64; k += 2)
+        top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+}
+
 // The bits 0 .. n - 1 of 32.
 __device__ __forceinline__ uint32_t bits_below(int n)
 {
@@ -126,17 +134,16 @@ struct Share {
 
 // The runs of one unit's tiles after another within a share.
 struct Runs {
-    const Walk &w;
     Unit u;
     int left;            // tiles from this run on
     int pair, slot;
     int h, off, todo;    // tiles off .. off + todo - 1 of the unit
     bool whole;          // all of them; else the parts go to `slot` of the workspace
-    __device__ Runs(const Walk &w_, const Share &s)
-        : w(w_), u(s.u), left(s.left), pair(s.pair), slot(2 * blockIdx.x), h(s.h), off(s.off), todo(0)
+    __device__ explicit Runs(const Share &s)
+        : u(s.u), left(s.left), pair(s.pair), slot(2 * blockIdx.x), h(s.h), off(s.off), todo(0), whole(false)
     {
     }
-    __device__ __forceinline__ bool next()
+    __device__ __forceinline__ bool next(const Walk &w)
     {
         if (todo > 0) {
             left -= todo;
@@ -215,8 +222,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 {
     constexpr int TILE = tile_bytes(D), HALF = KT * 128, HALVES = D / 64, ST = stages(D), KS = key_stages(D), VS = value_stages(D);
     constexpr int LEAD = PAIR ? 1 : 2;  // key tiles ahead of value tiles
-    extern __shared__ unsigned char raw[];
-    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    const uint32_t base = smem_addr(raw);
     const uint32_t q_at = base, ring = base + 2 * TILE, ring_v = ring + KS * TILE, bars = ring + ST * TILE;
     // barriers
     auto full = [&](int s) { return bars + 8u * s; };  // key stages, then value stages
@@ -230,14 +237,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     auto v_clean = [&](int i) { return bars + 8u * (2 * ST + 10 + i); };
     const uint32_t told = bars + 8u * (2 * ST + 14), joined = told + 8, drained = told + 16;
     // behind the barriers
-    unsigned char *spare = raw + (bars - smem_addr(raw)) + 512;
+    unsigned char *spare = raw + (bars - base) + 384;
     volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
     uint32_t *poison = reinterpret_cast<uint32_t *>(spare + 16);             // [2 groups][2][4]
-    int *part = reinterpret_cast<int *>(spare + 128);                        // [12]
-    Share *found = reinterpret_cast<Share *>(spare + 256);
-    float2 *other = reinterpret_cast<float2 *>(spare + 512);                 // [128]: the second group's statistics
-    static_assert(8 * (2 * stages(64) + 19) <= 512 && 512 + 512 + 128 * 8 <= SPARE, "room behind the ring");
+    int *part = reinterpret_cast<int *>(spare + 96);                         // [12]
+    Share *found = reinterpret_cast<Share *>(spare + 160);
+    float2 *other = reinterpret_cast<float2 *>(spare + 256);                 // [128]: the second group's statistics
+    Runs *runs = reinterpret_cast<Runs *>(spare + 256 + 1024);               // [8]: a softmax warp's
+    static_assert(8 * (2 * stages(64) + 19) <= 384 && sizeof(Share) <= 96 &&
+                      384 + 256 + 1024 + 8 * sizeof(Runs) <= SPARE, "room behind the ring");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == MMA_WARP)
@@ -281,13 +290,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
     share_of(w, part, found);
     const Watch watch{gave_up, w.a.status};
-    Runs r(w, *found);
     uint32_t seq = 0;   // tiles before this run
     int nth = 0;        // runs before this one
     bool dead = false;  // a wait gave up: nothing more is issued
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+        Runs r(*found);
         if (warp == KEY_WARP || warp == VALUE_WARP) {
             const bool keys = warp == KEY_WARP;
             const CUtensorMap *m = keys ? &map_k : &map_v;
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             auto look = [&](int i) {
                 return seen(i) ? w.a.c.table[static_cast<long long>(r.u.b) * w.a.c.cols + (key_of(i) >> w.a.c.shift)] : 0;
             };
-            while (r.next()) {
+            while (r.next(w)) {
                 int id = look(0);
                 for (int i = 0; i < r.todo; ++i) {
                     const int next = look(i + 1);  // on its way while this tile is copied
@@ -408,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     mma_commit(bar);
                 __syncwarp();
             };
-            while (r.next()) {
+            while (r.next(w)) {
                 const int todo = uniform(r.todo), buf = PAIR ? 0 : nth & 1;
                 const bool two = uniform(r.u.nt > w.TT);
                 const uint32_t q = q_at + (PAIR ? 0 : buf * TILE);
@@ -457,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         } else if (warp == CUT_WARP) {
             // what the second launch has to join
             Cut cut{};
-            while (r.next())
+            while (r.next(w))
                 if (r.todo == r.left && r.off == 0 && !r.whole)
                     cut = Cut{1 + (r.u.count - r.todo - 1) / found->per + 1, r.slot, r.u.b, r.u.t0, r.u.nt, r.h, {}};
             if (lane == 0)
@@ -470,7 +479,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const uint32_t s_at = lanes + g * KT, o_at = lanes + 2 * KT + g * KT;
         const int rt = row / w.a.G, rg = row - rt * w.a.G;
         uint32_t done[2] = {0, 0}, cleaned = 0, joins = 0;
-        while (r.next()) {
+        Runs &r = runs[warp];  // in shared memory: registers are short here
+        if (lane == 0)
+            r = Runs(*found);
+        for (;;) {
+            bool on = false;
+            __syncwarp();
+            if (lane == 0)
+                on = r.next(w);
+            if (!__any_sync(0xffffffffu, on))
+                break;
+            __syncwarp();
             const Unit &u = r.u;
             const int t = (PAIR ? g * w.TT : 0) + rt;  // of the unit's rows
             const bool live = rt < w.TT && t < u.nt;
@@ -508,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     if (g == who) {
                         warp_wait(watch, full(KS + st), (place / VS) & 1);
                         const int j = j0 + row;
-                        unsigned char *v = raw + (ring_v + st * TILE - smem_addr(raw)) + row * 128;
+                        unsigned char *v = raw + (ring_v + st * TILE - base) + row * 128;
                         bool zero = !some_see(w, u, j), bad = false;
                         if (!zero && !all_see(w, u, j)) {
                             constexpr uint32_t E = BF16 ? 0x7f807f80u : 0x7c007c00u;
@@ -544,9 +563,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 if (busy) {
                     fence_after();
                     uint32_t s[KT];
-#pragma unroll
-                    for (int k = 0; k < KT; k += 32)
-                        tmem_ld32(s_at + k, s + k);
+                    float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+                    tmem_ld32(s_at, s);
+                    tmem_ld32(s_at + 32, s + 32);
+                    tmem_wait_ld();
+                    tmem_ld32(s_at + 64, s + 64);
+                    tmem_ld32(s_at + 96, s + 96);
+                    if (!edge)
+                        highest(top, s);
                     tmem_wait_ld();
                     if (edge) {
                         const int end = p + 1 - j0, low = p_low - j0, sinks = w.a.seen.sinks - j0;
@@ -558,10 +582,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                                 s[k + e] = seen >> e & 1 ? s[k + e] : 0xff800000u;
                         }
                     }
-                    float top[4] = {m, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < KT; k += 2)
-                        top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    if (edge)
+                        highest(top, s);
+                    highest(top, s + 64);
                     m = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     if (x == 0) {
                         used = m;
@@ -586,23 +609,23 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     const Two cc = two(w.c, w.c), minus = two(-off, -off);
                     Two sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
 #pragma unroll
-                    for (int k = 0; k < KT; k += 64) {
-                        uint32_t weights[32];
+                    for (int k = 0; k < KT; k += 32) {
+                        uint32_t weights[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const float2 z = apart(fma2(two(s[k + 2 * e], s[k + 2 * e + 1]), cc, minus));
                             const float p0 = ex2(z.x), p1 = ex2(z.y);
                             sum[e & 1] = add2(sum[e & 1], two(p0, p1));
                             weights[e] = pack<BF16>(p0, p1);
                         }
-                        tmem_st32(s_at + k / 2, weights);
-                        if (k == 0) {  // the product with the first values may begin
+                        if (k == 64) {  // the product with the first values may begin
                             tmem_wait_st();
                             fence_before();
                             __syncwarp();
                             if (lane == 0)
                                 bar_arrive(p_half(g));
                         }
+                        tmem_st16(s_at + k / 2, weights);
                     }
                     const float2 all = apart(add2(sum[0], sum[1]));
                     l += all.x + all.y;

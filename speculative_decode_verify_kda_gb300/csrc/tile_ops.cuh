@@ -159,6 +159,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
                  ::"r"(addr), KDA_IN8(r, 0), KDA_IN8(r, 8), KDA_IN8(r, 16), KDA_IN8(r, 24) : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+                 "%13, %14, %15, %16};"
+                 ::"r"(addr), KDA_IN8(r, 0), KDA_IN8(r, 8) : "memory");
+}
+
 // ---- products -----------------------------------------------------------------------
 // A tile in shared memory is rows of 128 bytes in groups of eight with the 128-byte swizzle, as
 // a tensor copy writes it.  `group` bytes lie between groups of eight rows; `block` bytes between
