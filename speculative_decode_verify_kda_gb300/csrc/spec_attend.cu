@@ -15,7 +15,6 @@
 // same rows and take every other key tile, and their results are joined at the end.  While one
 // group computes weights, the tensor cores work for the other.
 #include "attend_common.cuh"
-#include "tile_ops.cuh"
 
 namespace kda {
 namespace {
@@ -23,7 +22,6 @@ namespace {
 using namespace pages;
 using namespace tiles;
 
-constexpr int KT = 128;              // keys of a tile, and rows of a tile
 constexpr int KEY_WARP = 8, MMA_WARP = 9, VALUE_WARP = 10, CUT_WARP = 11;
 constexpr int THREADS = 384;         // two groups of 128 and four warps more
 // Registers are handed from the last four warps to the groups (a row of 128 scores is held in
@@ -35,17 +33,12 @@ constexpr int SPARE = 2560;          // barriers and what the warps tell each ot
 // memory are seldom rescaled.
 constexpr float LAG = 8.0f;
 
-__host__ __device__ constexpr int tile_bytes(int D) { return KT * D * 2; }
 __host__ __device__ constexpr int key_stages(int D) { return D == 128 ? 3 : 5; }
 __host__ __device__ constexpr int value_stages(int D) { return D == 128 ? 2 : 4; }
 __host__ __device__ constexpr int stages(int D) { return key_stages(D) + value_stages(D); }
 __host__ __device__ constexpr int shared_bytes(int D) { return (2 + stages(D)) * tile_bytes(D) + SPARE; }
 
-struct Walk {
-    Attend a;
-    int TT, TQ, nq;  // tokens of a tile, of a unit; units a session and kv head
-    int box;         // rows of a copied box: a page, or 128 rows of a larger one
-    float c;         // scale log2 e
+struct Walk : Span {
     struct Cut *cuts;        // [grid] the unit that is cut at a CTA's end
     float2 *stats;           // [2 grid][rows] maximum and sum of a part
     float *parts;            // [2 grid][rows][D] its sums
@@ -57,72 +50,12 @@ struct Cut {
     int n, slot, b, t0, nt, h, pad[2];
 };
 
-// One session's unit: which rows, and which key tiles they see.
-struct Unit {
-    int b, n, t0, nt;     // tokens before the call, first row, rows
-    int hi, lo;           // keys [lo, hi) and below `sinks` are seen by some row
-    int near, far, count; // key tiles: [0, far) for the sinks, then from `near`
-};
-
-__device__ __forceinline__ Unit unit_of(const Walk &w, int i)
-{
-    Unit u;
-    u.b = i / w.nq;
-    u.t0 = (i - u.b * w.nq) * w.TQ;
-    int t, bad;
-    session(w.a.c, w.a.t_rows, w.a.T, u.b, u.n, t, bad);
-    u.nt = min(w.TQ, t - u.t0);
-    u.count = u.hi = u.lo = u.near = u.far = 0;
-    if (u.nt <= 0)
-        return u;
-    u.hi = u.n + u.t0 + u.nt;
-    if (w.a.seen.window) {
-        u.lo = max(0, u.n + u.t0 - w.a.seen.window + 1);
-        u.near = u.lo / KT;
-        u.far = min((min(w.a.seen.sinks, u.hi) + KT - 1) / KT, u.near);
-    }
-    u.count = u.far + (u.hi + KT - 1) / KT - u.near;
-    return u;
-}
-
-// Keys that some row of the unit sees, and keys that every row sees.
-__device__ __forceinline__ bool some_see(const Walk &w, const Unit &u, int j)
-{
-    return j < u.hi && (j >= u.lo || j < w.a.seen.sinks);
-}
-
-__device__ __forceinline__ bool all_see(const Walk &w, const Unit &u, int j)
-{
-    return j <= u.n + u.t0 &&
-           (!w.a.seen.window || u.hi - 1 - j < w.a.seen.window || j < w.a.seen.sinks);
-}
-
-// A place in the ring of tiles and the parity of its turn.
-template <int ST>
-struct Ring {
-    int stage = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void step()
-    {
-        if (++stage == ST) {
-            stage = 0;
-            phase ^= 1;
-        }
-    }
-};
-
 // The largest of 64 scores, in four strands.
 __device__ __forceinline__ void highest(float (&top)[4], const uint32_t *s)
 {
 #pragma unroll
     for (int k = 0; k < 64; k += 2)
         top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-}
-
-// The bits 0 .. n - 1 of 32.
-__device__ __forceinline__ uint32_t bits_below(int n)
-{
-    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
 // Where a CTA's share of the tiles begins.
@@ -303,44 +236,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             const int first = keys ? 0 : KS, count = keys ? KS : VS;
             int stage = 0;
             uint32_t phase = 0;
-            // A lane has a box of each tile (a page, or part of a large one); up to 16 boxes.
-            const int boxes = KT / w.box, page = 1 << w.a.c.shift;
-            auto key_of = [&](int i) {
-                const int x = r.off + i;
-                return (x < r.u.far ? x : r.u.near + x - r.u.far) * KT + lane * w.box;
-            };
-            // whether some row sees this lane's box of tile i, and its page
-            auto seen = [&](int i) {
-                const int j = key_of(i);
-                return i < r.todo && lane < boxes && j < r.u.hi && (j + w.box > r.u.lo || j < w.a.seen.sinks);
-            };
-            auto look = [&](int i) {
-                return seen(i) ? w.a.c.table[static_cast<long long>(r.u.b) * w.a.c.cols + (key_of(i) >> w.a.c.shift)] : 0;
-            };
+            auto key_of = [&](int i) { return tile_key(r.u, r.off + i); };
+            auto look = [&](int i) { return i < r.todo ? page_of(w, r.u, key_of(i)) : 0; };
             while (r.next(w)) {
                 int id = look(0);
                 for (int i = 0; i < r.todo; ++i) {
                     const int next = look(i + 1);  // on its way while this tile is copied
                     if (!warp_wait(watch, empty(first + stage), phase ^ 1))
                         dead = true;
-                    const bool want = seen(i);
-                    const uint32_t bar = full(first + stage), all = __ballot_sync(0xffffffffu, want);
-                    if (!dead) {
-                        if (lane == 0)
-                            bar_expect(bar, static_cast<uint32_t>(__popc(all)) * w.box * D * 2);
-                        __syncwarp();
-                        if (want) {
-                            if (id < 0 || id >= w.a.c.pages) {
-                                raise(w.a.status, KDA_ST_BADPAGE);
-                                id = w.a.c.pages;  // behind the last: zeros
-                            }
-                            const uint32_t dst = ring + (first + stage) * TILE + lane * w.box * 128;
-#pragma unroll
-                            for (int half = 0; half < HALVES; ++half)
-                                copy_4d(dst + half * HALF, m, half * 64, key_of(i) & (page - 1), r.h, id, bar);
-                        }
-                        __syncwarp();
-                    }
+                    if (!dead)
+                        copy_tile<D>(w, r.u, r.h, key_of(i), id, m, ring + (first + stage) * TILE, full(first + stage));
                     if (++stage == count) {
                         stage = 0;
                         phase ^= 1;
@@ -501,10 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             const int tiles = g == 0 ? tiles0 : tiles1;
             float m = -INFINITY, used = -INFINITY, l = 0.0f;
             bool spoiled = false;
-            auto key_of = [&](int i) {
-                const int y = r.off + i;
-                return (y < u.far ? y : u.near + y - u.far) * KT;
-            };
+            auto key_of = [&](int i) { return tile_key(u, r.off + i); };
             // some key of the tile is hidden from some row
             auto is_edge = [&](int j0) {
                 return !all_see(w, u, j0) || !all_see(w, u, j0 + KT - 1) ||
@@ -855,12 +757,8 @@ extern "C" int spec_attend(const kda_cache *cache, const void *q, int T, int Hq,
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
     const bool bf16 = cache->dtype == KDA_BF16, pair = is_pair(T, a.G);
-    const int D = a.c.D, page = cache->page;
-    w.TT = KT / a.G;
-    w.TQ = w.TT * (pair ? 2 : 1);
-    w.nq = (T + w.TQ - 1) / w.TQ;
-    w.box = std::min(page, KT);
-    w.c = scale * pages::LOG2E;
+    const int D = a.c.D;
+    pages::lay_out(&w, pages::KT / a.G * (pair ? 2 : 1));
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     w.cuts = reinterpret_cast<Cut *>(ws);
     ws += pages::SMS * sizeof(Cut);
@@ -868,21 +766,11 @@ extern "C" int spec_attend(const kda_cache *cache, const void *q, int T, int Hq,
     w.parts = reinterpret_cast<float *>(ws + sizeof(float2) * 2 * pages::SMS * (pair ? 2 * KT : KT));
 
     CUtensorMap map_q, map_k, map_v;
-    const cuuint64_t kv_dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page),
-                                   static_cast<cuuint64_t>(a.c.Hkv), static_cast<cuuint64_t>(a.c.pages)};
-    const cuuint64_t kv_strides[3] = {static_cast<cuuint64_t>(a.c.slot_stride) * 2,
-                                      static_cast<cuuint64_t>(a.c.head_stride) * 2,
-                                      static_cast<cuuint64_t>(a.c.page_stride) * 2};
-    const cuuint32_t kv_box[4] = {64, static_cast<cuuint32_t>(w.box), 1, 1};
-    const cuuint64_t q_dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
-                                  static_cast<cuuint64_t>(a.c.B) * T};
-    const cuuint64_t q_strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(ld_q) * 2};
-    const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(w.TT)};
-    if (int rc = tiles::encode_map(&map_k, bf16, 4, a.c.k, kv_dims, kv_strides, kv_box))
+    if (int rc = pages::cache_map(&map_k, w, a.c.k, bf16))
         return rc;
-    if (int rc = tiles::encode_map(&map_v, bf16, 4, a.c.v, kv_dims, kv_strides, kv_box))
+    if (int rc = pages::cache_map(&map_v, w, a.c.v, bf16))
         return rc;
-    if (int rc = tiles::encode_map(&map_q, bf16, 3, q, q_dims, q_strides, q_box))
+    if (int rc = pages::query_map(&map_q, w, bf16))
         return rc;
     // as many CTAs as there can be tiles, one an SM at most
     const double most = static_cast<double>(a.c.B) * w.nq * a.c.Hkv * ((a.c.capacity() + KT - 1) / KT);

@@ -1,75 +1,458 @@
 // spec_attend_mass.cu -- what every key of a paged cache was worth to a call's rows.
+//
+// The products are turned round: a tile of 128 keys times a tile of up to 128 rows gives each
+// key's scores against the rows in one lane of tensor memory, so a thread sums its key's weights
+// exp(s - lse) by itself, in the order of the rows: no sum depends on the order of blocks, and
+// nothing is joined.  All sessions' key tiles, each counted as often as there are tiles of rows,
+// are cut into equal shares, one a CTA.  Two groups of 128 threads have a key tile each and share
+// the row tiles that pass by; a warp copies keys, a warp rows (and their lse), a warp issues the
+// products.  Bound by the keys' bytes for a verify round's rows, by exp2 and the products for a
+// prompt's.
 #include "attend_common.cuh"
 
 namespace kda {
 namespace {
 
 using namespace pages;
+using namespace tiles;
 
-template <bool BF16>
-__device__ __forceinline__ float widen(uint16_t x)
+constexpr int KEY_WARP = 8, ROW_WARP = 9, MMA_WARP = 10;
+constexpr int THREADS = 352;
+constexpr int KS = 4;  // key tiles in shared memory: two pairs
+
+__host__ __device__ constexpr int row_stages(int D) { return D == 128 ? 3 : 6; }
+// behind the tiles: barriers, what the warps tell each other, the rows' lse
+__host__ __device__ constexpr int shared_bytes(int D)
 {
-    if (BF16)
-        return __uint_as_float(static_cast<uint32_t>(x) << 16);
-    return __half2float(__ushort_as_half(x));
+    return (KS + row_stages(D)) * tile_bytes(D) + 256 + 128 + row_stages(D) * KT * 4;
 }
 
-__device__ __forceinline__ float warp_sum(float x)
+struct Mass : Span {
+    const float *lse;
+    float *mass;
+    long long ld;
+};
+
+// Where a CTA's share of the tiles begins: the tiles whose place in the order (session, kv head,
+// key tile), counted in tiles of rows, lies in [first, last).
+struct Share {
+    Unit u;
+    int h, tile, at, last;
+};
+
+// The runs of one session's and kv head's key tiles within a share.
+struct Runs {
+    Unit u;
+    int nr;         // tiles of rows
+    int h, from, to;  // key tiles
+    int at, last;
+    __device__ explicit Runs(const Span &w, const Share &s)
+        : u(s.u), nr((s.u.nt + w.TT - 1) / w.TT), h(s.h), from(s.tile), to(s.tile), at(s.at), last(s.last)
+    {
+    }
+    __device__ __forceinline__ bool next(const Span &w)
+    {
+        at += (to - from) * nr;
+        if (at >= last)
+            return false;
+        from = to;
+        if (from == u.count) {
+            from = 0;
+            if (++h == w.a.c.Hkv) {
+                h = 0;
+                do
+                    u = unit_of(w, u.b + 1);
+                while (u.count == 0);
+                nr = (u.nt + w.TT - 1) / w.TT;
+            }
+        }
+        to = min(u.count, from + (last - at - 1) / nr + 1);
+        return true;
+    }
+};
+
+// The tiles of rows that see the key tile from j0 on: first .. second.
+__device__ __forceinline__ int2 rows_of(const Span &w, const Unit &u, int nr, int j0)
 {
-#pragma unroll
-    for (int d = 16; d; d >>= 1)
-        x += __shfl_xor_sync(0xffffffffu, x, d);
+    const int low = max(0, j0 - u.n) / w.TT;
+    int high = nr - 1;
+    if (w.a.seen.window && j0 >= w.a.seen.sinks)
+        high = min(high, max(0, j0 + KT - 1 - u.n + w.a.seen.window - 1) / w.TT);
+    return make_int2(low, high);
+}
+
+// The same of one or two tiles: what passes by a pair.
+__device__ __forceinline__ int2 rows_of_pair(const Span &w, const Runs &r, int i)
+{
+    int2 x = rows_of(w, r.u, r.nr, tile_key(r.u, i));
+    if (i + 1 < r.to) {
+        const int2 y = rows_of(w, r.u, r.nr, tile_key(r.u, i + 1));
+        x = make_int2(min(x.x, y.x), max(x.y, y.y));
+    }
     return x;
 }
 
-struct Mass {
-    Attend a;
-    const float *lse;
-    float *mass;
-    long long ld_mass;
-};
-
-// A warp for a key: the rows that see it one after another.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(128) attend_mass_kernel(const Mass x)
+__device__ __forceinline__ void share_of(const Span &w, int *part, Share *found)
 {
-    after_previous();
-    constexpr int E = D / 32;
-    const Attend &a = x.a;
-    const int lane = threadIdx.x & 31, b = blockIdx.y / a.c.Hkv, h = blockIdx.y - b * a.c.Hkv;
-    const int j = blockIdx.x * 4 + (threadIdx.x >> 5);
-    int n, tb, bad;
-    session(a.c, a.t_rows, a.T, b, n, tb, bad);
-    if (bad && j == 0 && lane == 0)
-        raise(a.status, bad);
-    if (j >= n + tb || tb == 0)
-        return;
-    long long at = -2;
-    float k[E], sum = 0.0f;
-    for (int t = max(0, j - n); t < tb; ++t) {
-        if (a.seen.window && n + t - j >= a.seen.window && j >= a.seen.sinks)
-            break;
-        if (at == -2) {
-            at = token_at(a.c, a.c.table + static_cast<long long>(b) * a.c.cols, h, j);
-            if (at < 0 && lane == 0)
-                raise(a.status, KDA_ST_BADPAGE);
-            for (int e = 0; e < E; ++e)
-                k[e] = at < 0 ? 0.0f : widen<BF16>(a.c.k[at + lane + 32 * e]) * (a.scale * LOG2E);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int B = w.a.c.B, each = (B - 1) / THREADS + 1;
+    const int i0 = tid * each, i1 = min(B, i0 + each);
+    Unit u{};
+    auto weight = [&] { return u.count * ((u.nt + w.TT - 1) / w.TT) * w.a.c.Hkv; };
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) {
+        u = unit_of(w, i);
+        if (u.count > 0)
+            mine += weight();
+    }
+    int s = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d)
+            s += y;
+    }
+    if (lane == 31)
+        part[warp] = s;
+    if (tid == 0)
+        found->at = found->last = found->tile = found->u.nt = 0;
+    __syncthreads();
+    int before = s - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i == warp)
+            before += total;
+        total += part[i];
+    }
+    const int per = (total - 1) / static_cast<int>(gridDim.x) + 1;
+    const long long begin = static_cast<long long>(per) * blockIdx.x;
+    if (begin < total && before <= begin && begin < before + mine) {
+        const int first = static_cast<int>(begin);
+        for (int i = i0;; ++i) {
+            u = unit_of(w, i);
+            if (u.count == 0)
+                continue;
+            if (first < before + weight())
+                break;
+            before += weight();
         }
-        const long long row = static_cast<long long>(b) * a.T + t;
-        for (int g = 0; g < a.G; ++g) {
-            const int hq = h * a.G + g;
-            float s = 0.0f;
-            for (int e = 0; e < E; ++e)
-                s += k[e] * widen<BF16>(a.q[row * a.ld + hq * D + lane + 32 * e]);
-            s = warp_sum(s);
-            const float lse = x.lse[row * a.Hq + hq];
-            sum += lse == -INFINITY ? 0.0f : exp2f(s - lse * LOG2E);
+        const int nr = (u.nt + w.TT - 1) / w.TT, head = u.count * nr;
+        const int h = (first - before) / head, tile = (first - before - h * head + nr - 1) / nr;
+        *found = Share{u, h, tile, before + h * head + tile * nr, min(total, first + per)};
+    }
+    __syncthreads();
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_constant__ Mass w,
+                                                                 const __grid_constant__ CUtensorMap map_q,
+                                                                 const __grid_constant__ CUtensorMap map_k)
+{
+    constexpr int TILE = tile_bytes(D), HALF = KT * 128, RS = row_stages(D);
+    extern __shared__ __align__(1024) unsigned char raw[];
+    const uint32_t base = smem_addr(raw), keys = base, rows = base + KS * TILE, bars = rows + RS * TILE;
+    auto k_full = [&](int s) { return bars + 8u * s; };
+    auto k_empty = [&](int s) { return bars + 8u * (KS + s); };
+    auto q_full = [&](int s) { return bars + 8u * (2 * KS + s); };
+    auto q_empty = [&](int s) { return bars + 8u * (2 * KS + RS + s); };
+    auto s_full = [&](int g, int i) { return bars + 8u * (2 * KS + 2 * RS + 2 * g + i); };
+    auto s_empty = [&](int g, int i) { return bars + 8u * (2 * KS + 2 * RS + 4 + 2 * g + i); };
+    const uint32_t drained = bars + 8u * (2 * KS + 2 * RS + 8);
+    unsigned char *spare = raw + (bars - base) + 256;
+    volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
+    int *part = reinterpret_cast<int *>(spare + 16);  // [11]
+    Share *found = reinterpret_cast<Share *>(spare + 64);
+    float *lse2 = reinterpret_cast<float *>(spare + 128);  // [RS][128]: lse log2 e of the rows
+    static_assert(8 * (2 * KS + 2 * RS + 9) <= 256 && sizeof(Share) <= 64, "room behind the rings");
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == MMA_WARP)
+        tmem_alloc<512>(smem_addr(tmem_at));
+    if (tid == 0) {
+        for (int s = 0; s < KS; ++s) {
+            bar_init(k_full(s), 1);
+            bar_init(k_empty(s), 1);
+        }
+        for (int s = 0; s < RS; ++s) {
+            bar_init(q_full(s), 2);
+            bar_init(q_empty(s), 9);
+        }
+        for (int g = 0; g < 2; ++g)
+            for (int i = 0; i < 2; ++i) {
+                bar_init(s_full(g, i), 1);
+                bar_init(s_empty(g, i), 4);
+            }
+        bar_init(drained, 1);
+        *gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+        prefetch_map(&map_q);
+        prefetch_map(&map_k);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_at;
+    after_previous();
+    if (blockIdx.x == 0 && w.a.status)  // sessions that are left untouched
+        for (int b = tid; b < w.a.c.B; b += THREADS) {
+            int n, t, bad;
+            session(w.a.c, w.a.t_rows, w.a.T, b, n, t, bad);
+            if (bad)
+                raise(w.a.status, bad);
+        }
+    share_of(w, part, found);
+    const Watch watch{gave_up, w.a.status};
+    Runs r(w, *found);
+    bool dead = false;  // a wait gave up: nothing more is issued
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!warp_wait(watch, bar, parity))
+            dead = true;
+    };
+
+    if (warp == KEY_WARP) {
+        Ring<KS> to;
+        while (r.next(w)) {
+            int id = page_of(w, r.u, tile_key(r.u, r.from));
+            for (int i = r.from; i < r.to; ++i) {
+                const int next = i + 1 < r.to ? page_of(w, r.u, tile_key(r.u, i + 1)) : 0;
+                wait(k_empty(to.stage), to.phase ^ 1);
+                if (!dead)
+                    copy_tile<D>(w, r.u, r.h, tile_key(r.u, i), id, &map_k, keys + to.stage * TILE, k_full(to.stage));
+                to.step();
+                id = next;
+            }
+        }
+        if (dead)  // copies in flight land before the CTA ends
+            for (int i = 0; i < KS; ++i, to.step())
+                bar_wait_long(watch, k_full(to.stage), to.phase ^ 1, true);
+    } else if (warp == ROW_WARP) {
+        Ring<RS> to;
+        const int c0 = lane * 4;  // this lane's columns of a tile of rows
+        int t_of[4], g_of[4];
+        for (int e = 0; e < 4; ++e) {
+            t_of[e] = (c0 + e) / w.a.G;
+            g_of[e] = c0 + e - t_of[e] * w.a.G;
+        }
+        auto load = [&](int x) {
+            float l[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = x * w.TT + t_of[e];
+                l[e] = INFINITY;  // of a row that is not there: weight 0
+                if (t_of[e] < w.TT && t < r.u.nt)
+                    l[e] = w.lse[(static_cast<long long>(r.u.b) * w.a.T + t) * w.a.Hq + r.h * w.a.G + g_of[e]];
+            }
+            wait(q_empty(to.stage), to.phase ^ 1);
+            if (!dead) {
+                if (lane == 0) {
+                    bar_expect(q_full(to.stage), static_cast<uint32_t>(w.TT) * w.a.G * D * 2);
+                    for (int half = 0; half < D / 64; ++half)
+                        copy_3d(rows + to.stage * TILE + half * HALF, &map_q, half * 64, r.h * w.a.G,
+                                r.u.b * w.a.T + x * w.TT, q_full(to.stage));
+                }
+                // a row without any score has lse -inf and no weight
+                *reinterpret_cast<float4 *>(lse2 + to.stage * KT + c0) =
+                    make_float4(l[0] == -INFINITY ? INFINITY : l[0] * LOG2E, l[1] == -INFINITY ? INFINITY : l[1] * LOG2E,
+                                l[2] == -INFINITY ? INFINITY : l[2] * LOG2E, l[3] == -INFINITY ? INFINITY : l[3] * LOG2E);
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(q_full(to.stage));
+            }
+            __syncwarp();
+            to.step();
+        };
+        while (r.next(w)) {
+            if (r.nr == 1) {  // one tile of rows stays for the whole run
+                load(0);
+                continue;
+            }
+            for (int i = r.from; i < r.to; i += 2) {
+                const int2 x = rows_of_pair(w, r, i);
+                for (int y = x.x; y <= x.y; ++y)
+                    load(y);
+            }
+        }
+        if (dead)
+            for (int i = 0; i < RS; ++i, to.step())
+                bar_wait_long(watch, q_full(to.stage), to.phase ^ 1, true);
+    } else if (warp == MMA_WARP) {
+        // The whole warp walks; one lane issues.
+        const uint32_t acc = uniform(tmem);
+        Ring<KS> key;
+        Ring<RS> row;
+        uint32_t count[2] = {0, 0};  // products of a group
+        auto commit = [&](uint32_t bar) {
+            if (!dead && elect())
+                mma_commit(bar);
+            __syncwarp();
+        };
+        while (r.next(w)) {
+            const bool hold = uniform(r.nr) == 1;
+            const int from = uniform(r.from), to = uniform(r.to);
+            const int cols = uniform((min(r.u.nt, w.TT) * w.a.G + 15) & ~15);
+            const uint32_t desc = product_desc(BF16, KT, 0, false) | static_cast<uint32_t>(cols >> 3) << 17;
+            for (int i = from; i < to; i += 2) {
+                const int2 x = rows_of_pair(w, r, i);
+                const bool two = i + 1 < to;
+                Ring<KS> second = key;
+                second.step();
+                wait(k_full(key.stage), key.phase);
+                if (two)
+                    wait(k_full(second.stage), second.phase);
+                const int last = uniform(x.y);
+                for (int y = uniform(x.x); y <= last; ++y) {
+                    if (!hold || i == from)
+                        wait(q_full(row.stage), row.phase);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (g == 1 && !two)
+                            continue;
+                        const int buf = count[g] & 1;
+                        wait(s_empty(g, buf), (count[g] >> 1 & 1) ^ 1);
+                        ++count[g];
+                        fence_after();
+                        const uint64_t a = tile_desc(keys + (g == 0 ? key.stage : second.stage) * TILE, 16, 1024);
+                        const uint64_t b = tile_desc(rows + row.stage * TILE, 16, 1024);
+                        if (!dead && elect()) {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
+                                mma_ss(acc + g * 2 * KT + buf * KT, a + step, b + step, desc, k > 0);
+                            }
+                            mma_commit(s_full(g, buf));
+                        }
+                        __syncwarp();
+                    }
+                    if (!hold) {
+                        commit(q_empty(row.stage));
+                        row.step();
+                    }
+                }
+                commit(k_empty(key.stage));
+                key.step();
+                if (two) {
+                    commit(k_empty(key.stage));
+                    key.step();
+                }
+            }
+            if (hold) {
+                commit(q_empty(row.stage));
+                row.step();
+            }
+        }
+        if (dead) {  // products in flight end before the tensor memory is freed
+            if (elect())
+                mma_commit(drained);
+            __syncwarp();
+            bar_wait_long(watch, drained, 0, true);
+        }
+    } else {
+        const int g = warp >> 2, line = tid & 127;
+        const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + g * 2 * KT;
+        const Two cc = two(w.c, w.c), zero = two(0.0f, 0.0f);
+        Ring<RS> row;
+        uint32_t count = 0;
+        while (r.next(w)) {
+            const bool hold = r.nr == 1;
+            const int cols = min(r.u.nt, w.TT) * w.a.G;
+            for (int i = r.from; i < r.to; i += 2) {
+                const int2 x = rows_of_pair(w, r, i);
+                const bool mine = i + g < r.to;
+                const int j = tile_key(r.u, mine ? i + g : i) + line;
+                // the rows t0 .. t1 - 1 see this key
+                const int t0 = max(0, j - r.u.n);
+                const int t1 = w.a.seen.window && j >= w.a.seen.sinks ? min(r.u.nt, j - r.u.n + w.a.seen.window) : r.u.nt;
+                Two sum[2] = {zero, zero};
+                for (int y = x.x; y <= x.y; ++y) {
+                    if (!hold || i == r.from)
+                        wait(q_full(row.stage), row.phase);
+                    if (mine) {
+                        const int buf = count & 1;
+                        wait(s_full(g, buf), count >> 1 & 1);
+                        ++count;
+                        fence_after();
+                        // its columns of this tile of rows
+                        const int a = max(0, min(w.TT, t0 - y * w.TT)) * w.a.G, b = max(0, min(w.TT, t1 - y * w.TT)) * w.a.G;
+                        const float *l = lse2 + row.stage * KT;
+#pragma unroll
+                        for (int k0 = 0; k0 < KT; k0 += 64) {
+                            if (k0 >= cols)
+                                break;
+                            uint32_t s[64];
+                            tmem_ld32(at + buf * KT + k0, s);
+                            tmem_ld32(at + buf * KT + k0 + 32, s + 32);
+                            tmem_wait_ld();
+                            if (k0 + 64 >= cols) {  // the last of it: the next product may come
+                                fence_before();
+                                __syncwarp();
+                                if (lane == 0)
+                                    bar_arrive(s_empty(g, buf));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 64; k += 32) {
+                                const uint32_t seen = bits_below(b - k0 - k) & ~bits_below(a - k0 - k);
+                                if (__all_sync(0xffffffffu, seen == 0xffffffffu)) {
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 4) {
+                                        const float4 f = *reinterpret_cast<const float4 *>(l + k0 + k + e);
+                                        const float2 u = apart(fma2(two(s[k + e], s[k + e + 1]), cc, two(-f.x, -f.y)));
+                                        const float2 v = apart(fma2(two(s[k + e + 2], s[k + e + 3]), cc, two(-f.z, -f.w)));
+                                        sum[0] = add2(sum[0], two(ex2(u.x), ex2(u.y)));
+                                        sum[1] = add2(sum[1], two(ex2(v.x), ex2(v.y)));
+                                    }
+                                } else if (__any_sync(0xffffffffu, seen != 0)) {
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) {
+                                        const float2 f = *reinterpret_cast<const float2 *>(l + k0 + k + e);
+                                        const float2 u = apart(fma2(two(s[k + e], s[k + e + 1]), cc, two(-f.x, -f.y)));
+                                        sum[e >> 1 & 1] = add2(sum[e >> 1 & 1],
+                                                               two(seen >> e & 1 ? ex2(u.x) : 0.0f,
+                                                                   seen >> (e + 1) & 1 ? ex2(u.y) : 0.0f));
+                                    }
+                                }
+                            }
+                        }
+                    }
+                    if (!hold) {
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_arrive(q_empty(row.stage));
+                        row.step();
+                    }
+                }
+                if (mine && some_see(w, r.u, j) && !*gave_up) {
+                    float *to = w.mass + (static_cast<long long>(r.u.b) * w.a.c.Hkv + r.h) * w.ld + j;
+                    const float2 all = apart(add2(sum[0], sum[1]));
+                    *to = (j < r.u.n ? *to : 0.0f) + (all.x + all.y);
+                }
+                __syncwarp();
+            }
+            if (hold) {
+                if (lane == 0)
+                    bar_arrive(q_empty(row.stage));
+                row.step();
+            }
         }
     }
-    float *to = x.mass + static_cast<long long>(blockIdx.y) * x.ld_mass + j;
-    if (lane == 0 && (at != -2 || j >= n))
-        *to = (j < n ? *to : 0.0f) + sum;
+    fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        __syncwarp();
+        tmem_free<512>(tmem);
+    }
+}
+
+template <int D, bool BF16>
+int run(const Mass &w, const CUtensorMap &q, const CUtensorMap &k, unsigned grid, cudaStream_t stream)
+{
+    const cudaError_t e = cudaFuncSetAttribute(attend_mass_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               shared_bytes(D));
+    if (e != cudaSuccess)
+        return fail(KDA_ECUDA, std::string("attend_mass_kernel shared memory: ") + cudaGetErrorString(e));
+    return launch(attend_mass_kernel<D, BF16>, dim3(grid), THREADS, shared_bytes(D), stream, "attend_mass_kernel", w, q,
+                  k);
 }
 
 }  // namespace
@@ -81,21 +464,30 @@ extern "C" int spec_attend_mass(const kda_cache *cache, const void *q, int T, in
                                 const int *t_rows, int window, int sinks, float scale, float *mass, long long ld_mass,
                                 int *dev_status, cudaStream_t stream)
 {
-    Mass x{};
-    if (int rc = pages::check_attend(cache, q, T, Hq, ld_q, t_rows, window, sinks, scale, dev_status, &x.a))
+    Mass w{};
+    if (int rc = pages::check_attend(cache, q, T, Hq, ld_q, t_rows, window, sinks, scale, dev_status, &w.a))
         return rc;
-    if (ld_mass < x.a.c.capacity() || ld_mass >= (1ll << 40))
+    if (ld_mass < w.a.c.capacity() || ld_mass >= (1ll << 40))
         return fail(KDA_EINVAL, "ld_mass must be at least table_cols * page");
-    if (x.a.c.B == 0 || T == 0)
+    if (w.a.c.B == 0 || T == 0)
         return ok();
     if (!lse || !mass || !pages::aligned4(lse) || !pages::aligned4(mass))
         return fail(KDA_EINVAL, "lse and mass must not be NULL and must be 4-byte aligned");
-    x.lse = lse;
-    x.mass = mass;
-    x.ld_mass = ld_mass;
+    w.lse = lse;
+    w.mass = mass;
+    w.ld = ld_mass;
+    pages::lay_out(&w, T);
     const bool bf16 = cache->dtype == KDA_BF16;
-    auto *kernel = x.a.c.D == 128 ? (bf16 ? attend_mass_kernel<true, 128> : attend_mass_kernel<false, 128>)
-                                  : (bf16 ? attend_mass_kernel<true, 64> : attend_mass_kernel<false, 64>);
-    return pages::launch(kernel, dim3(static_cast<unsigned>((x.a.c.capacity() + 3) / 4), x.a.c.B * x.a.c.Hkv), 128, 0,
-                         stream, "attend_mass_kernel", x);
+    CUtensorMap map_q, map_k;
+    if (int rc = pages::cache_map(&map_k, w, w.a.c.k, bf16))
+        return rc;
+    if (int rc = pages::query_map(&map_q, w, bf16))
+        return rc;
+    const double tiles = static_cast<double>(w.a.c.B) * w.a.c.Hkv * ((w.a.c.capacity() + pages::KT - 1) / pages::KT);
+    if (tiles * ((T - 1) / w.TT + 1) > 2147483647.0)
+        return fail(KDA_EINVAL, "too many tiles of keys and rows for one call");
+    const unsigned grid = static_cast<unsigned>(std::min(tiles, static_cast<double>(pages::SMS)));
+    if (w.a.c.D == 128)
+        return bf16 ? run<128, true>(w, map_q, map_k, grid, stream) : run<128, false>(w, map_q, map_k, grid, stream);
+    return bf16 ? run<64, true>(w, map_q, map_k, grid, stream) : run<64, false>(w, map_q, map_k, grid, stream);
 }
