@@ -1,5 +1,7 @@
 // spec_cache.cu -- what enters and leaves a paged cache: spec_cache_append writes a round's keys
 // and values behind the committed tokens, spec_cache_evict cuts sessions to a budget by mass.
+#include <cooperative_groups.h>
+
 #include "paged_cache.cuh"
 
 namespace kda {
@@ -51,11 +53,13 @@ __global__ void __launch_bounds__(APPEND_T) cache_append_kernel(const Append a)
 }
 
 // ---- evict --------------------------------------------------------------------------
-// First launch, a CTA for a (session, kv head): the masses between the first `sinks` and the
-// last `recent` tokens as whole numbers in the order of the floats; three passes of 11, 11 and
-// 10 bits count digits (a histogram in shared memory) to find the smallest kept number and how
-// many of its equals are kept; a last pass gives the kept positions their places in order.
-// Second launch: the kept keys and values move.
+// First launch, a cluster of one or eight CTAs for a (session, kv head): the masses between the
+// first `sinks` and the last `recent` tokens as whole numbers in the order of the floats; three
+// passes of 11, 11 and 10 bits count digits (a histogram in each CTA's shared memory, summed
+// over the cluster) and find the smallest kept number and how many of its equals are kept.  Then
+// every warp has a run of positions: one pass counts what it keeps, one gives the kept positions
+// their places.  The passes after the first find the masses in the L1 cache.
+// Second launch: the kept keys, values and masses move.
 constexpr int SELECT_T = 1024, BINS = 2048;
 
 struct Evict {
@@ -104,14 +108,34 @@ __device__ int scan_before(int x, int *part, int &total)
     return s - x + __shfl_sync(0xffffffffu, p - mine, w);
 }
 
+template <int CL>
+__device__ __forceinline__ void meet()
+{
+    if constexpr (CL > 1)
+        cooperative_groups::this_cluster().sync();
+    else
+        __syncthreads();
+}
+
+// CTA r's copy of a word of shared memory.
+template <int CL>
+__device__ __forceinline__ int of_cta(int *x, int r)
+{
+    if constexpr (CL > 1)
+        return *cooperative_groups::this_cluster().map_shared_rank(x, r);
+    else
+        return *x;
+}
+
+template <int CL>
 __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
 {
-    __shared__ int hist[BINS], part[32], found[2];
+    __shared__ int hist[BINS], part[32], found[2], sums[2];
     after_previous();
-    const int tid = threadIdx.x, b = blockIdx.x / a.c.Hkv;
-    const float *mass = a.mass + blockIdx.x * a.ld;
-    float *mass_out = a.mass_out ? a.mass_out + blockIdx.x * a.ld_out : nullptr;
-    int *kept = a.kept + static_cast<long long>(blockIdx.x) * a.budget;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cta = blockIdx.x % CL, head = blockIdx.x / CL, b = head / a.c.Hkv;
+    const float *mass = a.mass + head * a.ld;
+    int *kept = a.kept + static_cast<long long>(head) * a.budget;
     int n = a.c.lens[b];
     if (n < 0 || n > a.c.capacity()) {
         if (tid == 0)
@@ -119,7 +143,11 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
         n = 0;
     }
     const int low = a.sinks, high = n - a.recent;  // chosen by mass: low <= j < high
-    uint32_t edge = 0;                             // kept: rank > edge, and `ties` of rank == edge
+    // this CTA's positions, and this warp's
+    const int cta_run = (n + CL - 1) / CL, begin = min(n, cta * cta_run), end = min(n, begin + cta_run);
+    const int warp_run = ((end - begin + 31) / 32 + 31) / 32 * 32;
+    const int from = min(end, begin + warp * warp_run), to = min(end, from + warp_run);
+    uint32_t edge = 0;  // kept: rank > edge, and `ties` of rank == edge
     int ties = 0;
     if (n > a.budget) {
         int need = a.budget - a.sinks - a.recent;
@@ -132,15 +160,30 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
             for (int i = tid; i < BINS; i += SELECT_T)
                 hist[i] = 0;
             __syncthreads();
-            for (int j = low + tid; j < high; j += SELECT_T) {
-                const uint32_t r = rank_of(mass[j]);
-                if ((r & mask) == edge)
-                    atomicAdd(&hist[(r >> shift) & ((1 << bits) - 1)], 1);
+            for (int j0 = from; j0 < to; j0 += 32) {
+                const int j = j0 + lane;
+                const uint32_t r = j < to ? rank_of(mass[j]) : 0;
+                const bool in = j < to && j >= low && j < high && (r & mask) == edge;
+                const int bin = in ? static_cast<int>(r >> shift) & ((1 << bits) - 1) : -1;
+                const int first = __shfl_sync(0xffffffffu, bin, 0);
+                if (__all_sync(0xffffffffu, bin == first)) {  // equal masses: one addition for all
+                    if (lane == 0 && in)
+                        atomicAdd(&hist[bin], 32);
+                } else if (in) {
+                    atomicAdd(&hist[bin], 1);
+                }
             }
-            __syncthreads();
+            meet<CL>();
             // thread i holds the bins 2i and 2i + 1 from the top
             const int top = (1 << bits) - 1 - 2 * tid;
-            const int x = top >= 0 ? hist[top] : 0, y = top >= 1 ? hist[top - 1] : 0;
+            int x = 0, y = 0;
+            if (top > 0) {
+#pragma unroll
+                for (int c = 0; c < CL; ++c) {
+                    x += of_cta<CL>(&hist[top], c);
+                    y += of_cta<CL>(&hist[top - 1], c);
+                }
+            }
             int total;
             const int before = scan_before(x + y, part, total);
             if (before < need && before + x + y >= need) {
@@ -148,75 +191,215 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
                 found[0] = top - second;
                 found[1] = need - before - (second ? x : 0);
             }
-            __syncthreads();
+            meet<CL>();  // and the histograms have been read
             edge |= static_cast<uint32_t>(found[0]) << shift;
             mask |= ((1u << bits) - 1) << shift;
             need = found[1];
-            __syncthreads();
         }
         ties = need;
     }
-    int done = 0, tied = 0;  // kept, and equal to the edge, among the positions before
-    for (int j0 = 0; j0 < n; j0 += SELECT_T) {
-        const int j = j0 + tid;
-        const float m = j < n ? mass[j] : 0.0f;
-        bool sure = j < n && (n <= a.budget || j < low || j >= high), tie = false;
-        if (j < n && !sure) {
-            const uint32_t r = rank_of(m);
+    auto look = [&](int j, bool &sure, bool &tie) {
+        sure = j < to && (n <= a.budget || j < low || j >= high);
+        tie = false;
+        if (j < to && !sure) {
+            const uint32_t r = rank_of(mass[j]);
             sure = r > edge;
             tie = r == edge && ties > 0;
         }
-        int total;
-        const int before = scan_before((sure ? 1 : 0) | (tie ? 1 << 16 : 0), part, total);
-        const int ties_before = tied + (before >> 16);
-        if (sure || (tie && ties_before < ties)) {
-            const int place = done + (before & 0xffff) + min(ties_before, ties) - min(tied, ties);
-            kept[place] = j;
-            if (mass_out)
-                mass_out[place] = m;  // at or before j: everything there has been read
-        }
-        const int all = tied + (total >> 16);
-        done += (total & 0xffff) + min(all, ties) - min(tied, ties);
-        tied = all;
+    };
+    int sures = 0, equals = 0;
+    for (int j0 = from; j0 < to; j0 += 32) {
+        bool sure, tie;
+        look(j0 + lane, sure, tie);
+        sures += __popc(__ballot_sync(0xffffffffu, sure));
+        equals += __popc(__ballot_sync(0xffffffffu, tie));
     }
-    for (int i = done + tid; i < a.budget; i += SELECT_T)
+    // before this warp: in the warps and CTAs before it
+    int cta_sures, cta_equals;
+    int sure_before = scan_before(lane == 0 ? sures : 0, part, cta_sures);
+    int tie_before = scan_before(lane == 0 ? equals : 0, part, cta_equals);
+    sure_before = __shfl_sync(0xffffffffu, sure_before, 0);
+    tie_before = __shfl_sync(0xffffffffu, tie_before, 0);
+    if (tid == 0) {
+        sums[0] = cta_sures;
+        sums[1] = cta_equals;
+    }
+    meet<CL>();
+    int all_sures = 0, all_equals = 0;
+#pragma unroll
+    for (int c = 0; c < CL; ++c) {
+        const int s = of_cta<CL>(&sums[0], c), t = of_cta<CL>(&sums[1], c);
+        if (c < cta) {
+            sure_before += s;
+            tie_before += t;
+        }
+        all_sures += s;
+        all_equals += t;
+    }
+    for (int j0 = from; j0 < to; j0 += 32) {
+        bool sure, tie;
+        look(j0 + lane, sure, tie);
+        const uint32_t s = __ballot_sync(0xffffffffu, sure), t = __ballot_sync(0xffffffffu, tie);
+        const uint32_t below = (1u << lane) - 1;
+        const int t_before = tie_before + __popc(t & below);
+        if (sure || (tie && t_before < ties))
+            kept[sure_before + __popc(s & below) + min(t_before, ties)] = j0 + lane;
+        sure_before += __popc(s);
+        tie_before += __popc(t);
+    }
+    for (int i = all_sures + min(all_equals, ties) + cta * SELECT_T + tid; i < a.budget; i += CL * SELECT_T)
         kept[i] = -1;
+    if constexpr (CL > 1)
+        meet<CL>();  // no CTA ends while another may read its sums
 }
 
-// A CTA takes 64 bytes of every kept row of k or v of one (session, kv head) in rising order:
-// a row moves to a place at or before its own, so what a step writes was read by it or before.
-constexpr int MOVE_T = 256, MOVE_ROWS = MOVE_T / 4;
+// The move.  Into other pages, rows are independent: a CTA takes 64 kept rows of a (session, kv
+// head), D / 8 threads a row, each 16 bytes of k and of v at a time.  In place, a CTA takes 64
+// bytes of every kept row of k or v in rising order, STEP rows at a time: a row moves to a place at
+// or before its own, so what a step writes has been read by it or by a step before.  The masses go the
+// same way as one more part.
+constexpr int MOVE_T = 256, DEEP = 8, MOVE_ROWS = 64;
 
-__global__ void __launch_bounds__(MOVE_T) evict_move_kernel(const Evict a)
+__device__ __forceinline__ void move_masses(const Evict &a, int head, const int *kept)
 {
-    after_previous();
-    const int slices = a.c.D / 32, part = blockIdx.y;
-    const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x - b * a.c.Hkv;
-    const int *kept = a.kept + static_cast<long long>(blockIdx.x) * a.budget;
-    const int *from = a.c.table + static_cast<long long>(b) * a.c.cols;
-    const int *to = a.dst + static_cast<long long>(b) * a.dst_cols;
-    uint16_t *x = (part < slices ? a.c.k : a.c.v) + (part % slices) * 32 + (threadIdx.x & 3) * 8;
-    if (h == 0 && part == 0 && threadIdx.x == 0) {
-        const int n = a.c.lens[b];  // lens_out may be lens: read and written here alone
-        if (n >= 0 && n <= a.c.capacity())
-            a.lens_out[b] = min(n, a.budget);
-    }
-    for (int i0 = 0; i0 < a.budget; i0 += MOVE_ROWS) {
-        const int i = i0 + (threadIdx.x >> 2);
-        const int j = i < a.budget ? kept[i] : -1;
-        long long dst = -1;
-        uint4 w;
-        if (j >= 0) {
-            const long long src = token_at(a.c, from, h, j);
-            dst = token_at(a.c, to, h, i);
-            if (src < 0 || dst < 0)
-                raise(a.status, KDA_ST_BADPAGE);
-            w = src < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(x + src);
+    const float *from = a.mass + head * a.ld;
+    float *to = a.mass_out + head * a.ld_out;
+    for (int i0 = 0; i0 < a.budget; i0 += MOVE_T * DEEP) {
+        float m[DEEP];
+        int place[DEEP];
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e) {
+            const int i = i0 + e * MOVE_T + threadIdx.x, j = i < a.budget ? kept[i] : -1;
+            place[e] = j >= 0 ? i : -1;
+            m[e] = j >= 0 ? from[j] : 0.0f;
         }
         __syncthreads();
-        if (dst >= 0)
-            *reinterpret_cast<uint4 *>(x + dst) = w;
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e)
+            if (place[e] >= 0)
+                to[place[e]] = m[e];
     }
+}
+
+__device__ __forceinline__ void new_length(const Evict &a, int b)
+{
+    const int n = a.c.lens[b];  // lens_out may be lens: read and written by one thread
+    if (n >= 0 && n <= a.c.capacity())
+        a.lens_out[b] = min(n, a.budget);
+}
+
+template <int D>
+__global__ void __launch_bounds__(MOVE_T) evict_move_kernel(const Evict a, int chunks)
+{
+    after_previous();
+    const int head = blockIdx.x / chunks, chunk = blockIdx.x - head * chunks;
+    const int b = head / a.c.Hkv, h = head - b * a.c.Hkv;
+    const int *kept = a.kept + static_cast<long long>(head) * a.budget;
+    if (chunk == chunks - 1) {
+        if (h == 0 && threadIdx.x == 0)
+            new_length(a, b);
+        if (a.mass_out)
+            move_masses(a, head, kept);
+        return;
+    }
+    constexpr int V = D / 8, R = MOVE_T / V, E = MOVE_ROWS / R;  // threads a row, rows at a time, times
+    const int *from = a.c.table + static_cast<long long>(b) * a.c.cols;
+    const int *to = a.dst + static_cast<long long>(b) * a.dst_cols;
+    const int x = (threadIdx.x % V) * 8;
+    long long src[E], dst[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = chunk * MOVE_ROWS + e * R + threadIdx.x / V, j = i < a.budget ? kept[i] : -1;
+        src[e] = j >= 0 ? token_at(a.c, from, h, j) : 0;
+        dst[e] = j >= 0 ? token_at(a.c, to, h, i) : -1;
+        if (j >= 0 && (src[e] < 0 || dst[e] < 0))
+            raise(a.status, KDA_ST_BADPAGE);
+    }
+    uint4 k[E], v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        k[e] = v[e] = make_uint4(0, 0, 0, 0);
+        if (src[e] >= 0 && dst[e] >= 0) {
+            k[e] = *reinterpret_cast<const uint4 *>(a.c.k + src[e] + x);
+            v[e] = *reinterpret_cast<const uint4 *>(a.c.v + src[e] + x);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (dst[e] >= 0) {
+            *reinterpret_cast<uint4 *>(a.c.k + dst[e] + x) = k[e];
+            *reinterpret_cast<uint4 *>(a.c.v + dst[e] + x) = v[e];
+        }
+}
+
+__global__ void __launch_bounds__(MOVE_T) evict_in_place_kernel(const Evict a)
+{
+    after_previous();
+    const int slices = a.c.D / 32, part = blockIdx.y, head = blockIdx.x;
+    const int b = head / a.c.Hkv, h = head - b * a.c.Hkv;
+    const int *kept = a.kept + static_cast<long long>(head) * a.budget;
+    if (part == 2 * slices) {
+        if (h == 0 && threadIdx.x == 0)
+            new_length(a, b);
+        if (a.mass_out)
+            move_masses(a, head, kept);
+        return;
+    }
+    const int *table = a.c.table + static_cast<long long>(b) * a.c.cols;
+    uint16_t *x = (part < slices ? a.c.k : a.c.v) + (part % slices) * 32 + (threadIdx.x & 3) * 8;
+    constexpr int R = MOVE_T / 4, STEP = R * DEEP;
+    int j[DEEP];
+    auto look = [&](int i0) {
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e) {
+            const int i = i0 + e * R + (threadIdx.x >> 2);
+            j[e] = i < a.budget ? kept[i] : -1;
+        }
+    };
+    look(0);
+    for (int i0 = 0; i0 < a.budget; i0 += STEP) {
+        uint4 w[DEEP];
+        long long dst[DEEP];
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e) {
+            const int i = i0 + e * R + (threadIdx.x >> 2);
+            dst[e] = -1;
+            if (j[e] >= 0 && j[e] != i) {
+                const long long src = token_at(a.c, table, h, j[e]);
+                dst[e] = token_at(a.c, table, h, i);
+                if (src < 0 || dst[e] < 0)
+                    raise(a.status, KDA_ST_BADPAGE);
+                w[e] = src < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(x + src);
+            }
+        }
+        look(i0 + STEP);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e)
+            if (dst[e] >= 0)
+                *reinterpret_cast<uint4 *>(x + dst[e]) = w[e];
+    }
+}
+
+template <int CL>
+int select(const Evict &a, unsigned heads, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(heads * CL);
+    cfg.blockDim = dim3(SELECT_T);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CL;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<CL>, a);
+    if (e != cudaSuccess)
+        return fail(KDA_ECUDA, std::string("evict_select_kernel launch: ") + cudaGetErrorString(e));
+    return check_launch("evict_select_kernel");
 }
 
 }  // namespace
@@ -302,7 +485,16 @@ extern "C" int spec_cache_evict(const kda_cache *cache, const float *mass, long 
     a.lens_out = lens_out;
     a.status = dev_status;
     const unsigned heads = static_cast<unsigned>(a.c.B) * a.c.Hkv;
-    if (int rc = pages::launch(evict_select_kernel, dim3(heads), SELECT_T, 0, stream, "evict_select_kernel", a))
+    // eight CTAs a head while the device has room for them and a head has work for them
+    const bool wide = heads * 8ll <= 2 * pages::SMS && capacity > 4096;
+    if (int rc = wide ? select<8>(a, heads, stream) : select<1>(a, heads, stream))
         return rc;
-    return pages::launch(evict_move_kernel, dim3(heads, 2 * a.c.D / 32), MOVE_T, 0, stream, "evict_move_kernel", a);
+    if (!dst_table)
+        return pages::launch(evict_in_place_kernel, dim3(heads, 2 * a.c.D / 32 + 1), MOVE_T, 0, stream,
+                             "evict_in_place_kernel", a);
+    const int chunks = (budget + MOVE_ROWS - 1) / MOVE_ROWS + 1;
+    if (static_cast<long long>(heads) * chunks > 0x7fffffffll)
+        return fail(KDA_EINVAL, "too many rows for one launch");
+    return pages::launch(a.c.D == 128 ? evict_move_kernel<128> : evict_move_kernel<64>, dim3(heads * chunks), MOVE_T, 0,
+                         stream, "evict_move_kernel", a, chunks);
 }
