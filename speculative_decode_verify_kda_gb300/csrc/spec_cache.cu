@@ -55,12 +55,13 @@ __global__ void __launch_bounds__(APPEND_T) cache_append_kernel(const Append a)
 // ---- evict --------------------------------------------------------------------------
 // First launch, a cluster of one or eight CTAs for a (session, kv head): the masses between the
 // first `sinks` and the last `recent` tokens as whole numbers in the order of the floats; three
-// passes of 11, 11 and 10 bits count digits (a histogram in each CTA's shared memory, summed
-// over the cluster) and find the smallest kept number and how many of its equals are kept.  Then
-// every warp has a run of positions: one pass counts what it keeps, one gives the kept positions
-// their places.  The passes after the first find the masses in the L1 cache.
+// passes of 11, 11 and 10 bits count digits (a histogram in each CTA's shared memory) and find the
+// smallest kept number and how many of its equals are kept: a warp reads the cluster's sums of 64
+// bins, then the 64 bins that hold the digit.  Every warp has a run of positions: one pass counts
+// what it keeps, one gives the kept positions their places.  Up to HELD numbers a lane are read
+// once and stay in registers; longer runs are read again, from the caches, by every pass.
 // Second launch: the kept keys, values and masses move.
-constexpr int SELECT_T = 1024, BINS = 2048;
+constexpr int SELECT_T = 512, SELECT_W = SELECT_T / 32, BINS = 2048, HELD = 16;
 
 struct Evict {
     Cache c;
@@ -79,33 +80,6 @@ __device__ __forceinline__ uint32_t rank_of(float x)
         return 0;
     const uint32_t u = __float_as_uint(x + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// Sum over the CTA of the values of threads before this one; `total` over all.
-__device__ int scan_before(int x, int *part, int &total)
-{
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int s = x;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d)
-            s += y;
-    }
-    __syncthreads();
-    if (lane == 31)
-        part[w] = s;
-    __syncthreads();
-    const int mine = part[lane];  // SELECT_T / 32 = 32 warps
-    int p = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, p, d);
-        if (lane >= d)
-            p += y;
-    }
-    total = __shfl_sync(0xffffffffu, p, 31);
-    return s - x + __shfl_sync(0xffffffffu, p - mine, w);
 }
 
 template <int CL>
@@ -127,10 +101,24 @@ __device__ __forceinline__ int of_cta(int *x, int r)
         return *x;
 }
 
+// Sum over the lanes before this one; `total` over all.
+__device__ __forceinline__ int lanes_before(int x, int &total)
+{
+    int s = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, d);
+        if ((threadIdx.x & 31) >= d)
+            s += y;
+    }
+    total = __shfl_sync(0xffffffffu, s, 31);
+    return s - x;
+}
+
 template <int CL>
 __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
 {
-    __shared__ int hist[BINS], part[32], found[2], sums[2];
+    __shared__ int hist[BINS], group[BINS / 64], found[2], sums[2], part[2][SELECT_W];
     after_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cta = blockIdx.x % CL, head = blockIdx.x / CL, b = head / a.c.Hkv;
@@ -143,13 +131,33 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
         n = 0;
     }
     const int low = a.sinks, high = n - a.recent;  // chosen by mass: low <= j < high
+    const bool choose = n > a.budget;
     // this CTA's positions, and this warp's
     const int cta_run = (n + CL - 1) / CL, begin = min(n, cta * cta_run), end = min(n, begin + cta_run);
-    const int warp_run = ((end - begin + 31) / 32 + 31) / 32 * 32;
+    const int warp_run = ((end - begin + SELECT_W - 1) / SELECT_W + 31) / 32 * 32;
     const int from = min(end, begin + warp * warp_run), to = min(end, from + warp_run);
-    uint32_t edge = 0;  // kept: rank > edge, and `ties` of rank == edge
+    auto number = [&](int j) { return choose && j < to && j >= low && j < high ? rank_of(mass[j]) : 0; };
+    const bool held = warp_run <= 32 * HELD;
+    uint32_t own[HELD];
+#pragma unroll
+    for (int e = 0; e < HELD; ++e)
+        own[e] = held && from + 32 * e < to ? number(from + 32 * e + lane) : 0;
+    // f(position, number) for 32 positions at a time
+    auto each = [&](auto f) {
+        if (held) {
+#pragma unroll
+            for (int e = 0; e < HELD; ++e)
+                if (from + 32 * e < to)
+                    f(from + 32 * e + lane, own[e]);
+        } else {
+#pragma unroll 4
+            for (int j0 = from; j0 < to; j0 += 32)
+                f(j0 + lane, number(j0 + lane));
+        }
+    };
+    uint32_t edge = 0;  // kept: a number above it, and `ties` equal to it
     int ties = 0;
-    if (n > a.budget) {
+    if (choose) {
         int need = a.budget - a.sinks - a.recent;
         uint32_t mask = 0;
         if (need == 0)
@@ -160,9 +168,7 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
             for (int i = tid; i < BINS; i += SELECT_T)
                 hist[i] = 0;
             __syncthreads();
-            for (int j0 = from; j0 < to; j0 += 32) {
-                const int j = j0 + lane;
-                const uint32_t r = j < to ? rank_of(mass[j]) : 0;
+            each([&](int j, uint32_t r) {
                 const bool in = j < to && j >= low && j < high && (r & mask) == edge;
                 const int bin = in ? static_cast<int>(r >> shift) & ((1 << bits) - 1) : -1;
                 const int first = __shfl_sync(0xffffffffu, bin, 0);
@@ -172,24 +178,38 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
                 } else if (in) {
                     atomicAdd(&hist[bin], 1);
                 }
+            });
+            __syncthreads();
+            for (int i = warp; i < BINS / 64; i += SELECT_W) {
+                int total;
+                lanes_before(hist[64 * i + lane] + hist[64 * i + 32 + lane], total);
+                if (lane == 0)
+                    group[i] = total;
             }
             meet<CL>();
-            // thread i holds the bins 2i and 2i + 1 from the top
-            const int top = (1 << bits) - 1 - 2 * tid;
-            int x = 0, y = 0;
-            if (top > 0) {
+            if (warp == 0) {
+                // lane i: the groups, then the pairs of bins, from the top
+                int x = 0, total;
+#pragma unroll
+                for (int c = 0; c < CL; ++c)
+                    x += of_cta<CL>(&group[BINS / 64 - 1 - lane], c);
+                int before = lanes_before(x, total);
+                const uint32_t at = __ballot_sync(0xffffffffu, before < need && before + x >= need);
+                const int g = __ffs(at) - 1, rest = need - __shfl_sync(0xffffffffu, before, g);
+                const int top = 64 * (BINS / 64 - g) - 1 - 2 * lane;
+                int y = 0;
+                x = 0;
 #pragma unroll
                 for (int c = 0; c < CL; ++c) {
                     x += of_cta<CL>(&hist[top], c);
                     y += of_cta<CL>(&hist[top - 1], c);
                 }
-            }
-            int total;
-            const int before = scan_before(x + y, part, total);
-            if (before < need && before + x + y >= need) {
-                const bool second = before + x < need;
-                found[0] = top - second;
-                found[1] = need - before - (second ? x : 0);
+                before = lanes_before(x + y, total);
+                if (before < rest && before + x + y >= rest) {
+                    const bool second = before + x < rest;
+                    found[0] = top - second;
+                    found[1] = rest - before - (second ? x : 0);
+                }
             }
             meet<CL>();  // and the histograms have been read
             edge |= static_cast<uint32_t>(found[0]) << shift;
@@ -198,55 +218,58 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
         }
         ties = need;
     }
-    auto look = [&](int j, bool &sure, bool &tie) {
-        sure = j < to && (n <= a.budget || j < low || j >= high);
-        tie = false;
-        if (j < to && !sure) {
-            const uint32_t r = rank_of(mass[j]);
-            sure = r > edge;
-            tie = r == edge && ties > 0;
-        }
+    auto look = [&](int j, uint32_t r, bool &sure, bool &tie) {
+        sure = j < to && (!choose || j < low || j >= high || r > edge);
+        tie = j < to && !sure && r == edge && ties > 0;
     };
     int sures = 0, equals = 0;
-    for (int j0 = from; j0 < to; j0 += 32) {
+    each([&](int j, uint32_t r) {
         bool sure, tie;
-        look(j0 + lane, sure, tie);
+        look(j, r, sure, tie);
         sures += __popc(__ballot_sync(0xffffffffu, sure));
         equals += __popc(__ballot_sync(0xffffffffu, tie));
+    });
+    if (lane == 0) {
+        part[0][warp] = sures;
+        part[1][warp] = equals;
     }
+    __syncthreads();
     // before this warp: in the warps and CTAs before it
     int cta_sures, cta_equals;
-    int sure_before = scan_before(lane == 0 ? sures : 0, part, cta_sures);
-    int tie_before = scan_before(lane == 0 ? equals : 0, part, cta_equals);
-    sure_before = __shfl_sync(0xffffffffu, sure_before, 0);
-    tie_before = __shfl_sync(0xffffffffu, tie_before, 0);
-    if (tid == 0) {
-        sums[0] = cta_sures;
-        sums[1] = cta_equals;
-    }
-    meet<CL>();
-    int all_sures = 0, all_equals = 0;
-#pragma unroll
-    for (int c = 0; c < CL; ++c) {
-        const int s = of_cta<CL>(&sums[0], c), t = of_cta<CL>(&sums[1], c);
-        if (c < cta) {
-            sure_before += s;
-            tie_before += t;
+    int sure_before = lanes_before(lane < SELECT_W ? part[0][lane] : 0, cta_sures);
+    int tie_before = lanes_before(lane < SELECT_W ? part[1][lane] : 0, cta_equals);
+    sure_before = __shfl_sync(0xffffffffu, sure_before, warp);
+    tie_before = __shfl_sync(0xffffffffu, tie_before, warp);
+    int all_sures = cta_sures, all_equals = cta_equals;
+    if constexpr (CL > 1) {
+        if (tid == 0) {
+            sums[0] = cta_sures;
+            sums[1] = cta_equals;
         }
-        all_sures += s;
-        all_equals += t;
+        meet<CL>();
+        all_sures = all_equals = 0;
+#pragma unroll
+        for (int c = 0; c < CL; ++c) {
+            const int s = of_cta<CL>(&sums[0], c), t = of_cta<CL>(&sums[1], c);
+            if (c < cta) {
+                sure_before += s;
+                tie_before += t;
+            }
+            all_sures += s;
+            all_equals += t;
+        }
     }
-    for (int j0 = from; j0 < to; j0 += 32) {
+    each([&](int j, uint32_t r) {
         bool sure, tie;
-        look(j0 + lane, sure, tie);
+        look(j, r, sure, tie);
         const uint32_t s = __ballot_sync(0xffffffffu, sure), t = __ballot_sync(0xffffffffu, tie);
         const uint32_t below = (1u << lane) - 1;
         const int t_before = tie_before + __popc(t & below);
         if (sure || (tie && t_before < ties))
-            kept[sure_before + __popc(s & below) + min(t_before, ties)] = j0 + lane;
+            kept[sure_before + __popc(s & below) + min(t_before, ties)] = j;
         sure_before += __popc(s);
         tie_before += __popc(t);
-    }
+    });
     for (int i = all_sures + min(all_equals, ties) + cta * SELECT_T + tid; i < a.budget; i += CL * SELECT_T)
         kept[i] = -1;
     if constexpr (CL > 1)
