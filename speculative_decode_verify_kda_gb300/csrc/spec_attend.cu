@@ -22,7 +22,7 @@ namespace {
 using namespace pages;
 using namespace tiles;
 
-constexpr int KEY_WARP = 8, MMA_WARP = 9, VALUE_WARP = 10, CUT_WARP = 11;
+constexpr int KEY_WARP = 8, VALUE_WARP = 9, MMA_WARP = 10;
 constexpr int THREADS = 384;         // two groups of 128 and four warps more
 // Registers are handed from the last four warps to the groups (a row of 128 scores is held in
 // them): 256 x 216 + 128 x 72 = 384 x 168, what the launch has.
@@ -33,12 +33,19 @@ constexpr int SPARE = 2560;          // barriers and what the warps tell each ot
 // memory are seldom rescaled.
 constexpr float LAG = 8.0f;
 
-__host__ __device__ constexpr int key_stages(int D) { return D == 128 ? 3 : 5; }
+// Tiles in shared memory.  Two of rows for two groups' rows, else one.  Where the groups take every
+// other key tile the number of value stages is even: a stage then serves one group alone (a wait
+// tells a phase from the one before it, not from the one before that).
+__host__ __device__ constexpr int row_tiles(bool pair) { return pair ? 2 : 1; }
+__host__ __device__ constexpr int key_stages(int D, bool pair) { return D == 128 ? (pair ? 3 : 4) : 6; }
 __host__ __device__ constexpr int value_stages(int D) { return D == 128 ? 2 : 4; }
-__host__ __device__ constexpr int stages(int D) { return key_stages(D) + value_stages(D); }
-__host__ __device__ constexpr int shared_bytes(int D) { return (2 + stages(D)) * tile_bytes(D) + SPARE; }
+__host__ __device__ constexpr int shared_bytes(int D, bool pair)
+{
+    return (row_tiles(pair) + key_stages(D, pair) + value_stages(D)) * tile_bytes(D) + SPARE;
+}
 
 struct Walk : Span {
+    bool wide;               // out is 32-byte aligned
     struct Cut *cuts;        // [grid] the unit that is cut at a CTA's end
     float2 *stats;           // [2 grid][rows] maximum and sum of a part
     float *parts;            // [2 grid][rows][D] its sums
@@ -153,32 +160,32 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                                                             const __grid_constant__ CUtensorMap map_k,
                                                             const __grid_constant__ CUtensorMap map_v)
 {
-    constexpr int TILE = tile_bytes(D), HALF = KT * 128, HALVES = D / 64, ST = stages(D), KS = key_stages(D), VS = value_stages(D);
+    constexpr int TILE = tile_bytes(D), HALF = KT * 128, HALVES = D / 64, KS = key_stages(D, PAIR), VS = value_stages(D), ST = KS + VS;
     constexpr int LEAD = PAIR ? 1 : 2;  // key tiles ahead of value tiles
     extern __shared__ __align__(1024) unsigned char raw[];
     const uint32_t base = smem_addr(raw);
-    const uint32_t q_at = base, ring = base + 2 * TILE, ring_v = ring + KS * TILE, bars = ring + ST * TILE;
+    const uint32_t q_at = base, ring = base + row_tiles(PAIR) * TILE, ring_v = ring + KS * TILE, bars = ring + ST * TILE;
     // barriers
     auto full = [&](int s) { return bars + 8u * s; };  // key stages, then value stages
     auto empty = [&](int s) { return bars + 8u * (ST + s); };
-    auto q_full = [&](int i) { return bars + 8u * (2 * ST + i); };
-    auto q_empty = [&](int i) { return bars + 8u * (2 * ST + 2 + i); };
-    auto s_full = [&](int g) { return bars + 8u * (2 * ST + 4 + g); };
-    auto p_full = [&](int g) { return bars + 8u * (2 * ST + 6 + g); };
-    auto p_half = [&](int g) { return bars + 8u * (2 * ST + 17 + g); };  // the first 64 keys' weights
-    auto o_full = [&](int g) { return bars + 8u * (2 * ST + 8 + g); };
-    auto v_clean = [&](int i) { return bars + 8u * (2 * ST + 10 + i); };
-    const uint32_t told = bars + 8u * (2 * ST + 14), joined = told + 8, drained = told + 16;
+    auto more = [&](int i) { return bars + 8u * (2 * ST + i); };
+    const uint32_t q_full = more(0), q_empty = more(1);
+    auto s_full = [&](int g) { return more(4 + g); };
+    auto p_half = [&](int g) { return more(6 + g); };  // the first 64 keys' weights
+    auto p_full = [&](int g) { return more(8 + g); };
+    auto o_full = [&](int g) { return more(10 + g); };
+    const uint32_t drained = more(12), told = more(13), joined = more(14);
+    auto v_clean = [&](int g, uint32_t i) { return more(16 + g * VS + i % VS); };
     // behind the barriers
     unsigned char *spare = raw + (bars - base) + 384;
     volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
-    uint32_t *poison = reinterpret_cast<uint32_t *>(spare + 16);             // [2 groups][2][4]
-    int *part = reinterpret_cast<int *>(spare + 96);                         // [12]
-    Share *found = reinterpret_cast<Share *>(spare + 160);
-    float2 *other = reinterpret_cast<float2 *>(spare + 256);                 // [128]: the second group's statistics
+    uint32_t *poison = reinterpret_cast<uint32_t *>(spare + 16);             // [2 groups][VS][4]
+    int *part = reinterpret_cast<int *>(spare + 144);                        // [12]
+    Share *found = reinterpret_cast<Share *>(spare + 192);
+    float2 *other = reinterpret_cast<float2 *>(spare + 256);                 // [128]: the other group's statistics
     Runs *runs = reinterpret_cast<Runs *>(spare + 256 + 1024);               // [8]: a softmax warp's
-    static_assert(8 * (2 * stages(64) + 19) <= 384 && sizeof(Share) <= 96 &&
+    static_assert(8 * (2 * ST + 16 + 2 * VS) <= 384 && 8 * VS <= 32 && sizeof(Share) <= 64 &&
                       384 + 256 + 1024 + 8 * sizeof(Runs) <= SPARE, "room behind the ring");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -190,18 +197,18 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             bar_init(empty(s), 1);
         }
         for (int g = 0; g < 2; ++g) {
-            bar_init(q_full(g), 1);
-            bar_init(q_empty(g), 1);
             bar_init(s_full(g), 1);
             bar_init(p_half(g), 4);
             bar_init(p_full(g), 4);
             bar_init(o_full(g), 1);
-            bar_init(v_clean(2 * g), 4);
-            bar_init(v_clean(2 * g + 1), 4);
+            for (int i = 0; i < VS; ++i)
+                bar_init(v_clean(g, i), 4);
         }
+        bar_init(q_full, 1);
+        bar_init(q_empty, 1);
+        bar_init(drained, 1);
         bar_init(told, 4);
         bar_init(joined, 4);
-        bar_init(drained, 1);
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
@@ -238,46 +245,59 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             uint32_t phase = 0;
             auto key_of = [&](int i) { return tile_key(r.u, r.off + i); };
             auto look = [&](int i) { return i < r.todo ? page_of(w, r.u, key_of(i)) : 0; };
+            uint32_t copied = 0, asked = 0;  // tiles, and rows
+            auto load_rows = [&] {
+                if (!warp_wait(watch, q_empty, (nth & 1) ^ 1))
+                    dead = true;
+                const bool two = PAIR && r.u.nt > w.TT;
+                asked += !dead;
+                if (!dead && lane == 0) {
+                    bar_expect(q_full, (two ? 2u : 1u) * w.TT * w.a.G * D * 2);
+                    for (int x = 0; x <= two; ++x)
+                        for (int half = 0; half < HALVES; ++half)
+                            copy_3d(q_at + x * TILE + half * HALF, &map_q, half * 64, r.h * w.a.G,
+                                    r.u.b * w.a.T + r.u.t0 + x * w.TT, q_full);
+                }
+                __syncwarp();
+            };
+            Cut cut{};  // what the second launch has to join
             while (r.next(w)) {
+                if (r.todo == r.left && r.off == 0 && !r.whole)
+                    cut = Cut{1 + (r.u.count - r.todo - 1) / found->per + 1, r.slot, r.u.b, r.u.t0, r.u.nt, r.h, {}};
                 int id = look(0);
+                // the rows before the first keys, which keep the memory busy; behind them where the
+                // rows of the run before may still be read
+                const bool early = nth == 0;
+                if (keys && early)
+                    load_rows();
                 for (int i = 0; i < r.todo; ++i) {
                     const int next = look(i + 1);  // on its way while this tile is copied
                     if (!warp_wait(watch, empty(first + stage), phase ^ 1))
                         dead = true;
-                    if (!dead)
+                    if (!dead) {
                         copy_tile<D>(w, r.u, r.h, key_of(i), id, m, ring + (first + stage) * TILE, full(first + stage));
+                        ++copied;
+                    }
                     if (++stage == count) {
                         stage = 0;
                         phase ^= 1;
                     }
                     id = next;
-                    if (keys && i == min(LEAD, r.todo) - 1) {  // the rows, behind the first keys
-                        const int buf = PAIR ? 0 : nth & 1;
-                        if (!warp_wait(watch, q_empty(buf), ((PAIR ? nth : nth >> 1) & 1) ^ 1))
-                            dead = true;
-                        const bool two = PAIR && r.u.nt > w.TT;
-                        if (!dead && lane == 0) {
-                            bar_expect(q_full(buf), (two ? 2u : 1u) * w.TT * w.a.G * D * 2);
-                            for (int x = 0; x <= two; ++x)
-                                for (int half = 0; half < HALVES; ++half)
-                                    copy_3d(q_at + (PAIR ? x : buf) * TILE + half * HALF, &map_q, half * 64,
-                                            r.h * w.a.G, r.u.b * w.a.T + r.u.t0 + x * w.TT, q_full(buf));
-                        }
-                        __syncwarp();
-                    }
+                    if (keys && !early && i == min(LEAD, r.todo) - 1)
+                        load_rows();
                 }
                 ++nth;
             }
-            if (dead)  // copies in flight land before the CTA ends
-                for (int i = 0; i < count; ++i) {
-                    bar_wait_long(watch, full(first + stage), phase ^ 1, true);
-                    if (++stage == count) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
+            if (!keys && lane == 0)
+                w.cuts[blockIdx.x] = cut;
+            // copies in flight land before the CTA ends, whatever was given up
+            for (uint32_t i = copied > static_cast<uint32_t>(count) ? copied - count : 0; i < copied; ++i)
+                bar_wait_long(watch, full(first + i % count), i / count & 1, true);
+            if (asked > 0)
+                bar_wait_long(watch, q_full, (asked - 1) & 1, true);
         } else if (warp == MMA_WARP) {
-            // The whole warp walks; one lane issues.
+            // The whole warp walks; one lane issues.  One warp for both groups: with a warp each, their
+            // products ran into each other (a prompt's chunk took 1078 us for 828).
             constexpr uint32_t SCORES = product_desc(BF16, KT, KT, false), VALUES = product_desc(BF16, KT, D, true);
             const uint32_t acc = uniform(tmem);
             uint32_t done = 0;  // bit g: the phase of group g's weights
@@ -287,29 +307,34 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 if (!warp_wait(watch, bar, parity))
                     dead = true;
             };
-            auto scores = [&](int g, uint32_t q) {
+            // `math` false: a group without rows, which keeps step with the other
+            auto scores = [&](int g, uint32_t q, bool math) {
                 const uint64_t a = tile_desc(q, 16, 1024), b = tile_desc(ring + key.stage * TILE, 16, 1024);
                 if (!dead && elect()) {
+                    if (math) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
-                        mma_ss(acc + g * KT, a + step, b + step, SCORES, k > 0);
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
+                            mma_ss(acc + g * KT, a + step, b + step, SCORES, k > 0);
+                        }
                     }
                     mma_commit(s_full(g));
                 }
                 __syncwarp();
             };
-            auto values = [&](int g, bool add) {
+            auto values = [&](int g, bool add, bool math) {
                 const uint64_t b = tile_desc(ring_v + val.stage * TILE, HALF, 1024);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     wait(half == 0 ? p_half(g) : p_full(g), done >> g & 1);
                     fence_after();
                     if (!dead && elect()) {
+                        if (math) {
 #pragma unroll
-                        for (int k = half * KT / 32; k < (half + 1) * KT / 32; ++k)
-                            mma_ts(acc + 2 * KT + g * KT, acc + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES,
-                                   add || k > 0);
+                            for (int k = half * KT / 32; k < (half + 1) * KT / 32; ++k)
+                                mma_ts(acc + 2 * KT + g * KT, acc + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES,
+                                       add || k > 0);
+                        }
                         if (half == 1)
                             mma_commit(o_full(g));
                     }
@@ -323,33 +348,32 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 __syncwarp();
             };
             while (r.next(w)) {
-                const int todo = uniform(r.todo), buf = PAIR ? 0 : nth & 1;
+                const int todo = uniform(r.todo), lead = PAIR ? 0 : seq & 1;
                 const bool two = uniform(r.u.nt > w.TT);
-                const uint32_t q = q_at + (PAIR ? 0 : buf * TILE);
-                wait(q_full(buf), (PAIR ? nth : nth >> 1) & 1);
+                wait(q_full, nth & 1);
                 for (int i = 0; i < min(LEAD, todo); ++i) {
                     wait(full(key.stage), key.phase);
-                    scores(i, q);
-                    if (PAIR && two)
-                        scores(1, q + TILE);
+                    scores(PAIR ? 0 : i ^ lead, q_at, true);
+                    if (PAIR)
+                        scores(1, q_at + TILE, two);
                     commit(empty(key.stage));
                     key.step();
                 }
                 if (todo <= LEAD)
-                    commit(q_empty(buf));
+                    commit(q_empty);
                 for (int i = 0; i < todo; ++i) {
                     const bool more = i + LEAD < todo;
-                    const int g = PAIR ? 0 : i & 1;
+                    const int g = PAIR ? 0 : (i & 1) ^ lead;
                     wait(full(KS + val.stage), val.phase);
-                    values(g, i > LEAD - 1);
+                    values(g, i > LEAD - 1, true);
                     if (more) {
                         wait(full(key.stage), key.phase);
-                        scores(g, q);
+                        scores(g, q_at, true);
                     }
-                    if (PAIR && two) {
-                        values(1, i > 0);
+                    if (PAIR) {
+                        values(1, i > 0, two);
                         if (more)
-                            scores(1, q + TILE);
+                            scores(1, q_at + TILE, two);
                     }
                     commit(empty(KS + val.stage));
                     val.step();
@@ -357,25 +381,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         commit(empty(key.stage));
                         key.step();
                         if (i + LEAD == todo - 1)
-                            commit(q_empty(buf));
+                            commit(q_empty);
                     }
                 }
+                seq += todo;
                 ++nth;
             }
-            if (dead) {  // products in flight end before the tensor memory is freed
-                if (elect())
-                    mma_commit(drained);
-                __syncwarp();
-                bar_wait_long(watch, drained, 0, true);
-            }
-        } else if (warp == CUT_WARP) {
-            // what the second launch has to join
-            Cut cut{};
-            while (r.next(w))
-                if (r.todo == r.left && r.off == 0 && !r.whole)
-                    cut = Cut{1 + (r.u.count - r.todo - 1) / found->per + 1, r.slot, r.u.b, r.u.t0, r.u.nt, r.h, {}};
-            if (lane == 0)
-                w.cuts[blockIdx.x] = cut;
+            // products in flight end before the tensor memory is freed, whatever was given up
+            if (elect())
+                mma_commit(drained);
+            __syncwarp();
+            bar_wait_long(watch, drained, 0, true);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GROUP_REGS));
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // lane 32 (warp % 4)
         const uint32_t s_at = lanes + g * KT, o_at = lanes + 2 * KT + g * KT;
         const int rt = row / w.a.G, rg = row - rt * w.a.G;
-        uint32_t done[2] = {0, 0}, cleaned = 0, joins = 0;
+        uint32_t done = 0, cleaned = 0, joins = 0;
         Runs &r = runs[warp];  // in shared memory: registers are short here
         if (lane == 0)
             r = Runs(*found);
@@ -401,9 +417,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             const bool busy = __any_sync(0xffffffffu, live);
             const int p = u.n + u.t0 + t;
             const int p_low = w.a.seen.window ? max(0, p - w.a.seen.window + 1) : 0;
-            const int tiles0 = PAIR ? r.todo : (r.todo + 1) / 2;
-            const int tiles1 = PAIR ? (u.nt > w.TT ? r.todo : 0) : r.todo / 2;
-            const int tiles = g == 0 ? tiles0 : tiles1;
+            // tiles alternate over all runs; the group with a run's first tile leads it
+            const int lead = PAIR ? 0 : seq & 1, first = PAIR ? 0 : g ^ lead;
+            const int tiles = PAIR ? r.todo : (r.todo + 1 - first) / 2;
             float m = -INFINITY, used = -INFINITY, l = 0.0f;
             bool spoiled = false;
             auto key_of = [&](int i) { return tile_key(u, r.off + i); };
@@ -412,20 +428,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 return !all_see(w, u, j0) || !all_see(w, u, j0 + KT - 1) ||
                        (w.a.seen.window && j0 < w.a.seen.sinks && j0 + KT > w.a.seen.sinks);
             };
-            if (PAIR && tiles == 0)  // the first group cleans tiles without the second
-                for (int i = 0; i < r.todo; ++i)
-                    cleaned += is_edge(key_of(i));
             for (int x = 0; x < tiles; ++x) {
-                const int i = PAIR ? x : 2 * x + g;
+                const int i = PAIR ? x : 2 * x + first;
                 const int j0 = key_of(i);
                 const bool edge = is_edge(j0);
-                if (edge) {
+                auto clean = [&] {
+                    if (!edge)
+                        return;
                     // Values of keys that no row sees become zeros (a weight of 0 times anything is
                     // then 0); of a key that only some rows see, values that are not finite do too,
                     // and the rows that see it are marked.
                     const uint32_t place = seq + i, st = place % VS;
                     const int who = PAIR ? 0 : g;
-                    uint32_t *said = poison + (who * 2 + (cleaned & 1)) * 4;
+                    uint32_t *said = poison + (who * VS + cleaned % VS) * 4;
                     if (g == who) {
                         warp_wait(watch, full(KS + st), (place / VS) & 1);
                         const int j = j0 + row;
@@ -449,10 +464,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         fence_async();
                         __syncwarp();
                         if (lane == 0)
-                            bar_arrive(v_clean(2 * who + (cleaned & 1)));
+                            bar_arrive(v_clean(who, cleaned));
                     }
-                    // two barriers in turn: the first group may be a tile ahead of the second
-                    warp_wait(watch, v_clean(2 * who + (cleaned & 1)), (cleaned >> 1) & 1);
+                    // a barrier for each value stage in turn: so far may the first group be ahead
+                    warp_wait(watch, v_clean(who, cleaned), cleaned / VS & 1);
                     ++cleaned;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -460,8 +475,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                             const int j = j0 + 32 * k + __ffs(left) - 1;
                             spoiled |= j <= p && (j >= p_low || j < w.a.seen.sinks);
                         }
-                }
-                warp_wait(watch, s_full(g), (done[g] + x) & 1);
+                };
+                // a value stage's barrier is looked at when its tile before this one has landed: known
+                // from the scores before these, or with every other tile from these
+                if (PAIR)
+                    clean();
+                warp_wait(watch, s_full(g), (done + x) & 1);
+                if (!PAIR)
+                    clean();
                 if (busy) {
                     fence_after();
                     uint32_t s[KT];
@@ -491,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     if (x == 0) {
                         used = m;
                     } else if (__any_sync(0xffffffffu, (m - used) * w.c > LAG || (used == -INFINITY && m > used))) {
-                        warp_wait(watch, o_full(g), (done[g] + x - 1) & 1);
+                        warp_wait(watch, o_full(g), (done + x - 1) & 1);
                         fence_after();
                         const float f = m == used ? 1.0f : ex2((used - m) * w.c);
                         l *= f;
@@ -542,22 +563,20 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             }
             // the result of the run
             if (tiles > 0)
-                warp_wait(watch, o_full(g), (done[g] + tiles - 1) & 1);
-            done[0] += tiles0;
-            done[1] += tiles1;
+                warp_wait(watch, o_full(g), (done + tiles - 1) & 1);
+            done += tiles;
             fence_after();
-            const bool join = !PAIR && tiles1 > 0;
+            const bool join = !PAIR && r.todo > 1;
             float f0 = 1.0f, f1 = 0.0f;
-            if (join && g == 1) {
+            if (join && g != lead) {
                 other[row] = make_float2(used, spoiled ? -1.0f : l);
                 fence_before();
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(told);
             }
-            if (join && g == 0) {
+            if (join && g == lead) {
                 warp_wait(watch, told, joins & 1);
-                ++joins;
                 fence_after();
                 const float2 o = other[row];
                 spoiled |= o.y < 0.0f;
@@ -569,7 +588,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 used = both;
                 l = l * f0 + l1 * f1;
             }
-            if (busy && (PAIR ? tiles > 0 : g == 0) && !__any_sync(0xffffffffu, *gave_up)) {
+            if (busy && (PAIR || g == lead) && !__any_sync(0xffffffffu, *gave_up)) {
                 const int hq = r.h * w.a.G + rg;
                 const long long to = (static_cast<long long>(u.b) * w.a.T + u.t0 + t) * w.a.Hq + hq;
                 const long long slot = static_cast<long long>(r.slot) * (PAIR ? 2 * KT : KT) + (PAIR ? g * KT : 0) + row;
@@ -586,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
                     if (join) {
                         uint32_t o1[32];
-                        tmem_ld32(o_at + KT + k, o1);
+                        tmem_ld32(o_at + (g == 0 ? KT : -KT) + k, o1);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
@@ -597,20 +616,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         for (int e = 0; e < 32; ++e)
                             o[e] = 0x7fc00000u;
                     if (live && r.whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(w.a.out + to * D + k);
+                        uint32_t x[16];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t x[4];
-#pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                x[z] = pack<BF16>(__uint_as_float(o[8 * e + 2 * z]), __uint_as_float(o[8 * e + 2 * z + 1]));
-                            dst[e] = make_uint4(x[0], x[1], x[2], x[3]);
-                        }
+                        for (int e = 0; e < 16; ++e)
+                            x[e] = pack<BF16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                        store8(w.a.out + to * D + k, x, w.wide);
+                        store8(w.a.out + to * D + k + 16, x + 8, w.wide);
                     } else if (live) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(w.parts + slot * D + k);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 32; e += 8)
+                            store8(w.parts + slot * D + k + e, o + e, true);
                     }
                     __syncwarp();
                 }
@@ -619,17 +634,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 if (live && !r.whole)
                     w.stats[slot] = make_float2(used, l);
             }
-            if (join) {  // the second group's sums and statistics have been read
+            if (join) {  // the other group's sums and statistics have been read
                 fence_before();
                 __syncwarp();
-                if (g == 0) {
+                if (g == lead) {
                     if (lane == 0)
                         bar_arrive(joined);
                 } else {
                     warp_wait(watch, joined, joins & 1);
-                    ++joins;
                     fence_after();
                 }
+                ++joins;
             }
             seq += r.todo;
             ++nth;
@@ -714,10 +729,10 @@ int run(const Walk &w, const CUtensorMap &q, const CUtensorMap &k, const CUtenso
         cudaStream_t stream)
 {
     const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, PAIR, BF16>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes(D));
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes(D, PAIR));
     if (e != cudaSuccess)
         return fail(KDA_ECUDA, std::string("attend_kernel shared memory: ") + cudaGetErrorString(e));
-    if (int rc = launch(attend_kernel<D, PAIR, BF16>, dim3(grid), THREADS, shared_bytes(D), stream, "attend_kernel", w,
+    if (int rc = launch(attend_kernel<D, PAIR, BF16>, dim3(grid), THREADS, shared_bytes(D, PAIR), stream, "attend_kernel", w,
                         q, k, v))
         return rc;
     return launch(attend_join_kernel<D, BF16>, dim3(grid, PAIR ? 8 : 4), JOIN_T, 0, stream, "attend_join_kernel", w,
@@ -734,7 +749,7 @@ extern "C" size_t spec_attend_workspace_bytes(int B, int T, int Hq, int Hkv, int
     if (B < 1 || T < 1 || Hkv < 1 || Hq < Hkv || Hq / Hkv > KDA_GROUP_MAX)
         return 16;
     const size_t rows = 2 * pages::SMS * (is_pair(T, Hq / Hkv) ? 2 * KT : KT);
-    return pages::SMS * sizeof(Cut) + rows * (8 + 4 * static_cast<size_t>(D));
+    return 32 + pages::SMS * sizeof(Cut) + rows * (8 + 4 * static_cast<size_t>(D));
 }
 
 extern "C" int spec_attend(const kda_cache *cache, const void *q, int T, int Hq, long long ld_q, const int *t_rows,
@@ -760,6 +775,8 @@ extern "C" int spec_attend(const kda_cache *cache, const void *q, int T, int Hq,
     const int D = a.c.D;
     pages::lay_out(&w, pages::KT / a.G * (pair ? 2 : 1));
     unsigned char *ws = static_cast<unsigned char *>(workspace);
+    ws += 31 - (reinterpret_cast<uintptr_t>(ws) + 31) % 32;  // 32-byte stores
+    w.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     w.cuts = reinterpret_cast<Cut *>(ws);
     ws += pages::SMS * sizeof(Cut);
     w.stats = reinterpret_cast<float2 *>(ws);

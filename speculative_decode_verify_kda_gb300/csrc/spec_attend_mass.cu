@@ -213,22 +213,26 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
 
     if (warp == KEY_WARP) {
         Ring<KS> to;
+        uint32_t copied = 0;
         while (r.next(w)) {
             int id = page_of(w, r.u, tile_key(r.u, r.from));
             for (int i = r.from; i < r.to; ++i) {
                 const int next = i + 1 < r.to ? page_of(w, r.u, tile_key(r.u, i + 1)) : 0;
                 wait(k_empty(to.stage), to.phase ^ 1);
-                if (!dead)
+                if (!dead) {
                     copy_tile<D>(w, r.u, r.h, tile_key(r.u, i), id, &map_k, keys + to.stage * TILE, k_full(to.stage));
+                    ++copied;
+                }
                 to.step();
                 id = next;
             }
         }
-        if (dead)  // copies in flight land before the CTA ends
-            for (int i = 0; i < KS; ++i, to.step())
-                bar_wait_long(watch, k_full(to.stage), to.phase ^ 1, true);
+        // copies in flight land before the CTA ends, whatever was given up
+        for (uint32_t i = copied > KS ? copied - KS : 0; i < copied; ++i)
+            bar_wait_long(watch, k_full(i % KS), i / KS & 1, true);
     } else if (warp == ROW_WARP) {
         Ring<RS> to;
+        uint32_t copied = 0;
         const int c0 = lane * 4;  // this lane's columns of a tile of rows
         int t_of[4], g_of[4];
         for (int e = 0; e < 4; ++e) {
@@ -259,6 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(q_full(to.stage));
+                ++copied;
             }
             __syncwarp();
             to.step();
@@ -274,9 +279,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                     load(y);
             }
         }
-        if (dead)
-            for (int i = 0; i < RS; ++i, to.step())
-                bar_wait_long(watch, q_full(to.stage), to.phase ^ 1, true);
+        for (uint32_t i = copied > RS ? copied - RS : 0; i < copied; ++i)
+            bar_wait_long(watch, q_full(i % RS), i / RS & 1, true);
     } else if (warp == MMA_WARP) {
         // The whole warp walks; one lane issues.
         const uint32_t acc = uniform(tmem);
@@ -342,12 +346,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 row.step();
             }
         }
-        if (dead) {  // products in flight end before the tensor memory is freed
-            if (elect())
-                mma_commit(drained);
-            __syncwarp();
-            bar_wait_long(watch, drained, 0, true);
-        }
+        // products in flight end before the tensor memory is freed, whatever was given up
+        if (elect())
+            mma_commit(drained);
+        __syncwarp();
+        bar_wait_long(watch, drained, 0, true);
     } else {
         const int g = warp >> 2, line = tid & 127;
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + g * 2 * KT;

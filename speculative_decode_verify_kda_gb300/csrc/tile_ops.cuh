@@ -211,6 +211,18 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
+// 32 bytes of a row: one store where they are aligned to their size.  (A thread a row touches a
+// cache line a store; with 16 bytes a store the results took twice as many turns.)
+__device__ __forceinline__ void store8(void *to, const uint32_t *x, bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), KDA_IN8(x, 0) : "memory");
+    } else {
+        static_cast<uint4 *>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        static_cast<uint4 *>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack(float lo, float hi)
 {

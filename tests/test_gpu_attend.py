@@ -127,7 +127,7 @@ def test_one_head_shared_by_many_sessions_pages():
     both(c)
 
 
-@pytest.mark.parametrize("n,T", [(5000, 1), (5000, 15), (3000, 40)])
+@pytest.mark.parametrize("n,T", [(5000, 1), (5000, 15), (3000, 40), (3000, 70), (2000, 193)])
 def test_long_texts_are_split_and_joined(n, T):
     both(Case([n, 3], T=T, Hq=8, Hkv=2, page=64, seed=n + T))
 
