@@ -303,49 +303,33 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             uint32_t done = 0;  // bit g: the phase of group g's weights
             Ring<KS> key;
             Ring<VS> val;
+            // (the next elect() brings the lanes together again)
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                if (!warp_wait(watch, bar, parity))
+                if (!bar_try(bar, parity) && !bar_wait_long(watch, bar, parity, false))
                     dead = true;
             };
             // `math` false: a group without rows, which keeps step with the other
             auto scores = [&](int g, uint32_t q, bool math) {
                 const uint64_t a = tile_desc(q, 16, 1024), b = tile_desc(ring + key.stage * TILE, 16, 1024);
-                if (!dead && elect()) {
-                    if (math) {
+                if (math) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
-                            mma_ss(acc + g * KT, a + step, b + step, SCORES, k > 0);
-                        }
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
+                        mma_ss(acc + g * KT, a + step, b + step, SCORES, k > 0);
                     }
-                    mma_commit(s_full(g));
                 }
-                __syncwarp();
+                mma_commit(s_full(g));
             };
-            auto values = [&](int g, bool add, bool math) {
+            auto values = [&](int g, int half, bool add, bool math) {
                 const uint64_t b = tile_desc(ring_v + val.stage * TILE, HALF, 1024);
+                if (math) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    wait(half == 0 ? p_half(g) : p_full(g), done >> g & 1);
-                    fence_after();
-                    if (!dead && elect()) {
-                        if (math) {
-#pragma unroll
-                            for (int k = half * KT / 32; k < (half + 1) * KT / 32; ++k)
-                                mma_ts(acc + 2 * KT + g * KT, acc + g * KT + k * 8, b + (k * 16 * 128 >> 4), VALUES,
-                                       add || k > 0);
-                        }
-                        if (half == 1)
-                            mma_commit(o_full(g));
-                    }
-                    __syncwarp();
+                    for (int k = 0; k < KT / 32; ++k)
+                        mma_ts(acc + 2 * KT + g * KT, acc + g * KT + (half * KT / 32 + k) * 8,
+                               b + ((half * KT / 32 + k) * 16 * 128 >> 4), VALUES, add || half > 0 || k > 0);
                 }
-                done ^= 1u << g;
-            };
-            auto commit = [&](uint32_t bar) {
-                if (!dead && elect())
-                    mma_commit(bar);
-                __syncwarp();
+                if (half == 1)
+                    mma_commit(o_full(g));
             };
             while (r.next(w)) {
                 const int todo = uniform(r.todo), lead = PAIR ? 0 : seq & 1;
@@ -353,36 +337,59 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 wait(q_full, nth & 1);
                 for (int i = 0; i < min(LEAD, todo); ++i) {
                     wait(full(key.stage), key.phase);
-                    scores(PAIR ? 0 : i ^ lead, q_at, true);
-                    if (PAIR)
-                        scores(1, q_at + TILE, two);
-                    commit(empty(key.stage));
+                    if (elect() && !dead) {
+                        scores(PAIR ? 0 : i ^ lead, q_at, true);
+                        if (PAIR)
+                            scores(1, q_at + TILE, two);
+                        mma_commit(empty(key.stage));
+                        if (i == todo - 1)
+                            mma_commit(q_empty);
+                    }
                     key.step();
                 }
-                if (todo <= LEAD)
-                    commit(q_empty);
                 for (int i = 0; i < todo; ++i) {
                     const bool more = i + LEAD < todo;
-                    const int g = PAIR ? 0 : (i & 1) ^ lead;
                     wait(full(KS + val.stage), val.phase);
-                    values(g, i > LEAD - 1, true);
-                    if (more) {
-                        wait(full(key.stage), key.phase);
-                        scores(g, q_at, true);
+#pragma unroll
+                    for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
+                        const int g = PAIR ? x : (i & 1) ^ lead;
+                        const bool math = x == 0 || two, last = x == (PAIR ? 1 : 0);
+                        wait(p_half(g), done >> g & 1);
+                        fence_after();
+                        if (elect() && !dead)
+                            values(g, 0, i >= LEAD, math);
+                        // few steps between the products: as one where the keys are at hand
+                        wait(p_full(g), done >> g & 1);
+                        done ^= 1u << g;
+                        if (PAIR && more && x == 0)
+                            wait(full(key.stage), key.phase);
+                        fence_after();
+                        if (elect() && !dead) {
+                            values(g, 1, i >= LEAD, math);
+                            if (last)
+                                mma_commit(empty(KS + val.stage));
+                            if (PAIR && more) {
+                                scores(g, q_at + g * TILE, math);
+                                if (last) {
+                                    mma_commit(empty(key.stage));
+                                    if (i + LEAD == todo - 1)
+                                        mma_commit(q_empty);
+                                }
+                            }
+                        }
+                        if (!PAIR && more) {
+                            wait(full(key.stage), key.phase);
+                            if (elect() && !dead) {
+                                scores(g, q_at, true);
+                                mma_commit(empty(key.stage));
+                                if (i + LEAD == todo - 1)
+                                    mma_commit(q_empty);
+                            }
+                        }
                     }
-                    if (PAIR) {
-                        values(1, i > 0, two);
-                        if (more)
-                            scores(1, q_at + TILE, two);
-                    }
-                    commit(empty(KS + val.stage));
                     val.step();
-                    if (more) {
-                        commit(empty(key.stage));
+                    if (more)
                         key.step();
-                        if (i + LEAD == todo - 1)
-                            commit(q_empty);
-                    }
                 }
                 seq += todo;
                 ++nth;
