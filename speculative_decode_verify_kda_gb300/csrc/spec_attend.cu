@@ -184,9 +184,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     int *part = reinterpret_cast<int *>(spare + 144);                        // [12]
     Share *found = reinterpret_cast<Share *>(spare + 192);
     float2 *other = reinterpret_cast<float2 *>(spare + 256);                 // [128]: the other group's statistics
-    Runs *runs = reinterpret_cast<Runs *>(spare + 256 + 1024);               // [8]: a softmax warp's
+    Runs *runs = reinterpret_cast<Runs *>(spare + 256 + 1024);               // [12]: a warp's
     static_assert(8 * (2 * ST + 16 + 2 * VS) <= 384 && 8 * VS <= 32 && sizeof(Share) <= 64 &&
-                      384 + 256 + 1024 + 8 * sizeof(Runs) <= SPARE, "room behind the ring");
+                      384 + 256 + 1024 + THREADS / 32 * sizeof(Runs) <= SPARE, "room behind the ring");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == MMA_WARP)
@@ -234,9 +234,22 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     int nth = 0;        // runs before this one
     bool dead = false;  // a wait gave up: nothing more is issued
 
+    // a warp's walk lies in shared memory: registers are short everywhere
+    Runs &r = runs[warp];
+    if (lane == 0)
+        r = Runs(*found);
+    auto next_run = [&] {
+        bool on = false;
+        __syncwarp();
+        if (lane == 0)
+            on = r.next(w);
+        on = __any_sync(0xffffffffu, on);
+        __syncwarp();
+        return on;
+    };
+
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-        Runs r(*found);
         if (warp == KEY_WARP || warp == VALUE_WARP) {
             const bool keys = warp == KEY_WARP;
             const CUtensorMap *m = keys ? &map_k : &map_v;
@@ -261,7 +274,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 __syncwarp();
             };
             Cut cut{};  // what the second launch has to join
-            while (r.next(w)) {
+            while (next_run()) {
                 if (r.todo == r.left && r.off == 0 && !r.whole)
                     cut = Cut{1 + (r.u.count - r.todo - 1) / found->per + 1, r.slot, r.u.b, r.u.t0, r.u.nt, r.h, {}};
                 int id = look(0);
@@ -331,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 if (half == 1)
                     mma_commit(o_full(g));
             };
-            while (r.next(w)) {
+            while (next_run()) {
                 const int todo = uniform(r.todo), lead = PAIR ? 0 : seq & 1;
                 const bool two = uniform(r.u.nt > w.TT);
                 wait(q_full, nth & 1);
@@ -407,17 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const uint32_t s_at = lanes + g * KT, o_at = lanes + 2 * KT + g * KT;
         const int rt = row / w.a.G, rg = row - rt * w.a.G;
         uint32_t done = 0, cleaned = 0, joins = 0;
-        Runs &r = runs[warp];  // in shared memory: registers are short here
-        if (lane == 0)
-            r = Runs(*found);
-        for (;;) {
-            bool on = false;
-            __syncwarp();
-            if (lane == 0)
-                on = r.next(w);
-            if (!__any_sync(0xffffffffu, on))
-                break;
-            __syncwarp();
+        while (next_run()) {
             const Unit &u = r.u;
             const int t = (PAIR ? g * w.TT : 0) + rt;  // of the unit's rows
             const bool live = rt < w.TT && t < u.nt;
