@@ -76,6 +76,13 @@ __device__ __forceinline__ bool all_see(const Span &w, const Unit &u, int j)
            (!w.a.seen.window || u.hi - 1 - j < w.a.seen.window || j < w.a.seen.sinks);
 }
 
+// Some key of the tile from j0 on is hidden from some row.
+__device__ __forceinline__ bool is_edge(const Span &w, const Unit &u, int j0)
+{
+    return !all_see(w, u, j0) || !all_see(w, u, j0 + KT - 1) ||
+           (w.a.seen.window && j0 < w.a.seen.sinks && j0 + KT > w.a.seen.sinks);
+}
+
 // The first key of a unit's i-th tile.
 __device__ __forceinline__ int tile_key(const Unit &u, int i) { return (i < u.far ? i : u.near + i - u.far) * KT; }
 

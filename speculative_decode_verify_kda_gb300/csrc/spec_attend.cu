@@ -22,20 +22,18 @@ namespace {
 using namespace pages;
 using namespace tiles;
 
-constexpr int KEY_WARP = 8, VALUE_WARP = 9, MMA_WARP = 10;
+constexpr int KEY_WARP = 8, VALUE_WARP = 9, MMA_WARP = 10, CLEAN_WARP = 11;
 constexpr int THREADS = 384;         // two groups of 128 and four warps more
 // Registers are handed from the last four warps to the groups (a row of 128 scores is held in
 // them): 256 x 216 + 128 x 72 = 384 x 168, what the launch has.
 constexpr int GROUP_REGS = 216, OTHER_REGS = 72;
-constexpr int SPARE = 2560;          // barriers and what the warps tell each other
+constexpr int SPARE = 2816;          // barriers and what the warps tell each other
 // The running maximum that weights are taken against follows the true one only when it falls
 // behind by more than this many powers of two: weights stay below 2^8, and the sums in tensor
 // memory are seldom rescaled.
 constexpr float LAG = 8.0f;
 
-// Tiles in shared memory.  Two of rows for two groups' rows, else one.  Where the groups take every
-// other key tile the number of value stages is even: a stage then serves one group alone (a wait
-// tells a phase from the one before it, not from the one before that).
+// Tiles in shared memory: two of rows for two groups' rows, else one.
 __host__ __device__ constexpr int row_tiles(bool pair) { return pair ? 2 : 1; }
 __host__ __device__ constexpr int key_stages(int D, bool pair) { return D == 128 ? (pair ? 3 : 4) : 6; }
 __host__ __device__ constexpr int value_stages(int D) { return D == 128 ? 2 : 4; }
@@ -43,6 +41,14 @@ __host__ __device__ constexpr int shared_bytes(int D, bool pair)
 {
     return (row_tiles(pair) + key_stages(D, pair) + value_stages(D)) * tile_bytes(D) + SPARE;
 }
+
+// Keys of a run that only some rows see and whose values are not finite: bit j - (n + t0) of the
+// first half for the call's own, bit j - lo of the second for those at the window's end.
+struct Poison {
+    uint32_t any, bits[16];
+};
+// Runs whose poison is held: the cleaning is at most the value stages and a run ahead of the results.
+__host__ __device__ constexpr int held_runs(int D) { return value_stages(D) + 2; }
 
 struct Walk : Span {
     bool wide;               // out is 32-byte aligned
@@ -175,18 +181,20 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     auto p_full = [&](int g) { return more(8 + g); };
     auto o_full = [&](int g) { return more(10 + g); };
     const uint32_t drained = more(12), told = more(13), joined = more(14);
-    auto v_clean = [&](int g, uint32_t i) { return more(16 + g * VS + i % VS); };
+    auto v_clean = [&](int s) { return more(15 + s); };
     // behind the barriers
-    unsigned char *spare = raw + (bars - base) + 384;
+    unsigned char *spare = raw + (bars - base) + 320;
     volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
-    uint32_t *poison = reinterpret_cast<uint32_t *>(spare + 16);             // [2 groups][VS][4]
-    int *part = reinterpret_cast<int *>(spare + 144);                        // [12]
-    Share *found = reinterpret_cast<Share *>(spare + 192);
-    float2 *other = reinterpret_cast<float2 *>(spare + 256);                 // [128]: the other group's statistics
-    Runs *runs = reinterpret_cast<Runs *>(spare + 256 + 1024);               // [12]: a warp's
-    static_assert(8 * (2 * ST + 16 + 2 * VS) <= 384 && 8 * VS <= 32 && sizeof(Share) <= 64 &&
-                      384 + 256 + 1024 + THREADS / 32 * sizeof(Runs) <= SPARE, "room behind the ring");
+    int *part = reinterpret_cast<int *>(spare + 16);                         // [12]
+    Share *found = reinterpret_cast<Share *>(spare + 64);
+    float2 *other = reinterpret_cast<float2 *>(spare + 128);                 // [128]: the other group's statistics
+    Runs *runs = reinterpret_cast<Runs *>(spare + 128 + 1024);               // [12]: a warp's
+    Poison *poison = reinterpret_cast<Poison *>(runs + THREADS / 32);        // [HELD]
+    constexpr int HELD = held_runs(D);
+    static_assert(8 * (2 * ST + 15 + VS) <= 320 && sizeof(Share) <= 64 &&
+                      320 + 128 + 1024 + THREADS / 32 * sizeof(Runs) + HELD * sizeof(Poison) <= SPARE,
+                  "room behind the ring");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == MMA_WARP)
@@ -201,9 +209,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             bar_init(p_half(g), 4);
             bar_init(p_full(g), 4);
             bar_init(o_full(g), 1);
-            for (int i = 0; i < VS; ++i)
-                bar_init(v_clean(g, i), 4);
         }
+        for (int s = 0; s < VS; ++s)
+            bar_init(v_clean(s), 1);
         bar_init(q_full, 1);
         bar_init(q_empty, 1);
         bar_init(drained, 1);
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 }
                 for (int i = 0; i < todo; ++i) {
                     const bool more = i + LEAD < todo;
-                    wait(full(KS + val.stage), val.phase);
+                    wait(v_clean(val.stage), val.phase);
 #pragma unroll
                     for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
                         const int g = PAIR ? x : (i & 1) ^ lead;
@@ -412,6 +420,90 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 mma_commit(drained);
             __syncwarp();
             bar_wait_long(watch, drained, 0, true);
+        } else if (warp == CLEAN_WARP) {
+            // Value tiles pass from the copies to the products through this warp.  Values of keys that
+            // no row sees become zeros (a weight of 0 times anything is then 0); of a key that only
+            // some rows see, values that are not finite do too, and the key is marked: the rows that
+            // see it become NaN at the end.
+            Ring<VS> at;
+            const int line = lane >> 3, chunk = lane & 7;  // 8 lanes a row, 4 rows at a time
+            while (next_run()) {
+                const Unit u = r.u;
+                Poison &p = poison[nth % HELD];
+                if (lane < 17)
+                    (lane == 0 ? p.any : p.bits[(lane - 1) & 15]) = 0;
+                __syncwarp();
+                for (int i = 0; i < r.todo; ++i) {
+                    const int j0 = tile_key(u, r.off + i);
+                    warp_wait(watch, full(KS + at.stage), at.phase);
+                    if (is_edge(w, u, j0)) {
+                        unsigned char *tile = raw + (ring_v + at.stage * TILE - base);
+                        auto place = [&](int row) {
+                            return reinterpret_cast<uint4 *>(tile + row * 128 + ((chunk ^ row) & 7) * 16);
+                        };
+                        auto hide = [&](int from, int to) {  // keys that no row sees
+                            const int end = min(to - j0, KT);
+#pragma unroll 4
+                            for (int row = max(from - j0, 0) + line; row < end; row += 4)
+#pragma unroll
+                                for (int half = 0; half < HALVES; ++half)
+                                    place(row)[half * HALF / 16] = make_uint4(0, 0, 0, 0);
+                        };
+                        auto look = [&](int from, int to) {  // keys that some rows may not see
+                            const int first = max(from - j0, 0), end = min(to - j0, KT);
+                            uint32_t sum[4] = {0, 0, 0, 0};  // x * 0 is NaN where x is not finite, and stays
+#pragma unroll 2
+                            for (int row = first + line; row < end; row += 4)
+#pragma unroll
+                                for (int half = 0; half < HALVES; ++half) {
+                                    const uint4 x = place(row)[half * HALF / 16];
+                                    sum[0] = times_zero<BF16>(x.x, sum[0]);
+                                    sum[1] = times_zero<BF16>(x.y, sum[1]);
+                                    sum[2] = times_zero<BF16>(x.z, sum[2]);
+                                    sum[3] = times_zero<BF16>(x.w, sum[3]);
+                                }
+                            const bool none = !(is_nan2<BF16>(sum[0]) || is_nan2<BF16>(sum[1]) ||
+                                                is_nan2<BF16>(sum[2]) || is_nan2<BF16>(sum[3]));
+                            if (__all_sync(0xffffffffu, none))
+                                return;
+#pragma unroll 1
+                            for (int row0 = first; row0 < end; row0 += 4) {  // which ones
+                                const int row = row0 + line, j = j0 + row;
+                                bool bad = false;
+                                if (row < end)
+                                    for (int half = 0; half < HALVES; ++half) {
+                                        const uint4 x = place(row)[half * HALF / 16];
+                                        for (uint32_t e : {x.x, x.y, x.z, x.w})
+                                            bad |= is_nan2<BF16>(times_zero<BF16>(e, 0u));
+                                    }
+                                const uint32_t lanes = __ballot_sync(0xffffffffu, bad) >> (8 * line) & 0xffu;
+                                if (lanes && some_see(w, u, j) && !all_see(w, u, j)) {
+                                    for (int half = 0; half < HALVES; ++half)
+                                        place(row)[half * HALF / 16] = make_uint4(0, 0, 0, 0);
+                                    if (chunk == 0) {
+                                        const int bit = j > u.n + u.t0 ? j - (u.n + u.t0) : 256 + j - u.lo;
+                                        atomicOr(&p.bits[bit >> 5], 1u << (bit & 31));
+                                        p.any = 1;
+                                    }
+                                }
+                                __syncwarp();
+                            }
+                        };
+                        hide(u.hi, u.hi + KT);
+                        look(u.n + u.t0 + 1, u.hi);
+                        if (w.a.seen.window) {
+                            hide(w.a.seen.sinks, u.lo);
+                            look(max(u.lo, w.a.seen.sinks), min(u.lo + u.nt, u.n + u.t0 + 1));
+                        }
+                        fence_async();
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(v_clean(at.stage));
+                    at.step();
+                }
+                ++nth;
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GROUP_REGS));
@@ -419,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);  // lane 32 (warp % 4)
         const uint32_t s_at = lanes + g * KT, o_at = lanes + 2 * KT + g * KT;
         const int rt = row / w.a.G, rg = row - rt * w.a.G;
-        uint32_t done = 0, cleaned = 0, joins = 0;
+        uint32_t done = 0, joins = 0;
         while (next_run()) {
             const Unit &u = r.u;
             const int t = (PAIR ? g * w.TT : 0) + rt;  // of the unit's rows
@@ -431,68 +523,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             const int lead = PAIR ? 0 : seq & 1, first = PAIR ? 0 : g ^ lead;
             const int tiles = PAIR ? r.todo : (r.todo + 1 - first) / 2;
             float m = -INFINITY, used = -INFINITY, l = 0.0f;
-            bool spoiled = false;
             auto key_of = [&](int i) { return tile_key(u, r.off + i); };
-            // some key of the tile is hidden from some row
-            auto is_edge = [&](int j0) {
-                return !all_see(w, u, j0) || !all_see(w, u, j0 + KT - 1) ||
-                       (w.a.seen.window && j0 < w.a.seen.sinks && j0 + KT > w.a.seen.sinks);
-            };
             for (int x = 0; x < tiles; ++x) {
                 const int i = PAIR ? x : 2 * x + first;
                 const int j0 = key_of(i);
-                const bool edge = is_edge(j0);
-                auto clean = [&] {
-                    if (!edge)
-                        return;
-                    // Values of keys that no row sees become zeros (a weight of 0 times anything is
-                    // then 0); of a key that only some rows see, values that are not finite do too,
-                    // and the rows that see it are marked.
-                    const uint32_t place = seq + i, st = place % VS;
-                    const int who = PAIR ? 0 : g;
-                    uint32_t *said = poison + (who * VS + cleaned % VS) * 4;
-                    if (g == who) {
-                        warp_wait(watch, full(KS + st), (place / VS) & 1);
-                        const int j = j0 + row;
-                        unsigned char *v = raw + (ring_v + st * TILE - base) + row * 128;
-                        bool zero = !some_see(w, u, j), bad = false;
-                        if (!zero && !all_see(w, u, j)) {
-                            constexpr uint32_t E = BF16 ? 0x7f807f80u : 0x7c007c00u;
-                            for (int k = 0; k < D / 8; ++k) {
-                                const uint4 q = *reinterpret_cast<const uint4 *>(v + (k / 8) * HALF + ((k ^ row) & 7) * 16);
-                                for (uint32_t e : {q.x, q.y, q.z, q.w})
-                                    bad |= (e & E & 0xffffu) == (E & 0xffffu) || (e & E) >> 16 == E >> 16;
-                            }
-                            zero = bad;
-                        }
-                        if (zero)
-                            for (int k = 0; k < D / 8; ++k)
-                                *reinterpret_cast<uint4 *>(v + (k / 8) * HALF + ((k ^ row) & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        const uint32_t mask = __ballot_sync(0xffffffffu, bad);
-                        if (lane == 0)
-                            said[warp & 3] = mask;
-                        fence_async();
-                        __syncwarp();
-                        if (lane == 0)
-                            bar_arrive(v_clean(who, cleaned));
-                    }
-                    // a barrier for each value stage in turn: so far may the first group be ahead
-                    warp_wait(watch, v_clean(who, cleaned), cleaned / VS & 1);
-                    ++cleaned;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        for (uint32_t left = said[k]; left; left &= left - 1) {
-                            const int j = j0 + 32 * k + __ffs(left) - 1;
-                            spoiled |= j <= p && (j >= p_low || j < w.a.seen.sinks);
-                        }
-                };
-                // a value stage's barrier is looked at when its tile before this one has landed: known
-                // from the scores before these, or with every other tile from these
-                if (PAIR)
-                    clean();
+                const bool edge = is_edge(w, u, j0);
                 warp_wait(watch, s_full(g), (done + x) & 1);
-                if (!PAIR)
-                    clean();
                 if (busy) {
                     fence_after();
                     uint32_t s[KT];
@@ -510,9 +546,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll
                         for (int k = 0; k < KT; k += 32) {
                             const uint32_t seen = bits_below(end - k) & (~bits_below(low - k) | bits_below(sinks - k));
+                            if (!__all_sync(0xffffffffu, seen == 0xffffffffu))
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                s[k + e] = seen >> e & 1 ? s[k + e] : 0xff800000u;
+                                for (int e = 0; e < 32; ++e)
+                                    s[k + e] = seen >> e & 1 ? s[k + e] : 0xff800000u;
                         }
                     }
                     if (edge)
@@ -579,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             const bool join = !PAIR && r.todo > 1;
             float f0 = 1.0f, f1 = 0.0f;
             if (join && g != lead) {
-                other[row] = make_float2(used, spoiled ? -1.0f : l);
+                other[row] = make_float2(used, l);
                 fence_before();
                 __syncwarp();
                 if (lane == 0)
@@ -589,15 +626,23 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 warp_wait(watch, told, joins & 1);
                 fence_after();
                 const float2 o = other[row];
-                spoiled |= o.y < 0.0f;
-                const float l1 = o.y < 0.0f ? 0.0f : o.y, both = fmaxf(used, o.x);
+                const float both = fmaxf(used, o.x);
                 if (both != -INFINITY) {
                     f0 = used == both ? 1.0f : ex2((used - both) * w.c);
                     f1 = o.x == both ? 1.0f : ex2((o.x - both) * w.c);
                 }
                 used = both;
-                l = l * f0 + l1 * f1;
+                l = l * f0 + o.y * f1;
             }
+            bool spoiled = false;
+            const Poison &bad = poison[nth % HELD];
+            if (bad.any)
+                for (int k = 0; k < 16; ++k)
+                    for (uint32_t left = bad.bits[k]; left; left &= left - 1) {
+                        const int bit = 32 * (k & 7) + __ffs(left) - 1, j = k < 8 ? u.n + u.t0 + bit : u.lo + bit;
+                        spoiled |= j <= p && (j >= p_low || j < w.a.seen.sinks);
+                    }
+            __syncwarp();
             if (busy && (PAIR || g == lead) && !__any_sync(0xffffffffu, *gave_up)) {
                 const int hq = r.h * w.a.G + rg;
                 const long long to = (static_cast<long long>(u.b) * w.a.T + u.t0 + t) * w.a.Hq + hq;

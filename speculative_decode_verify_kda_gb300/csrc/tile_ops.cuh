@@ -234,6 +234,25 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi)
     return r;
 }
 
+// a pair of 16-bit values times 0 plus another: NaN where a value is not finite or the other is NaN
+template <bool BF16>
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t sum)
+{
+    uint32_t r;
+    if (BF16)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(sum));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(sum));
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ bool is_nan2(uint32_t x)
+{
+    constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
+    return (x & 0x7fffu) > E || (x >> 16 & 0x7fffu) > E;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
