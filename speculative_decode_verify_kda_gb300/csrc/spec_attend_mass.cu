@@ -239,8 +239,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
             t_of[e] = (c0 + e) / w.a.G;
             g_of[e] = c0 + e - t_of[e] * w.a.G;
         }
-        auto load = [&](int x) {
-            float l[4];
+        float l[4];  // lse of this lane's rows of the next tile
+        auto fetch = [&](int x) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = x * w.TT + t_of[e];
@@ -248,6 +248,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 if (t_of[e] < w.TT && t < r.u.nt)
                     l[e] = w.lse[(static_cast<long long>(r.u.b) * w.a.T + t) * w.a.Hq + r.h * w.a.G + g_of[e]];
             }
+        };
+        auto load = [&](int x, int next) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // a row without any score has lse -inf and no weight
+                f[e] = l[e] == -INFINITY ? INFINITY : l[e] * LOG2E;
+            if (next >= 0)
+                fetch(next);  // on its way while this tile is copied
             wait(q_empty(to.stage), to.phase ^ 1);
             if (!dead) {
                 if (lane == 0) {
@@ -256,10 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                         copy_3d(rows + to.stage * TILE + half * HALF, &map_q, half * 64, r.h * w.a.G,
                                 r.u.b * w.a.T + x * w.TT, q_full(to.stage));
                 }
-                // a row without any score has lse -inf and no weight
-                *reinterpret_cast<float4 *>(lse2 + to.stage * KT + c0) =
-                    make_float4(l[0] == -INFINITY ? INFINITY : l[0] * LOG2E, l[1] == -INFINITY ? INFINITY : l[1] * LOG2E,
-                                l[2] == -INFINITY ? INFINITY : l[2] * LOG2E, l[3] == -INFINITY ? INFINITY : l[3] * LOG2E);
+                *reinterpret_cast<float4 *>(lse2 + to.stage * KT + c0) = make_float4(f[0], f[1], f[2], f[3]);
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(q_full(to.stage));
@@ -270,13 +275,15 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         };
         while (r.next(w)) {
             if (r.nr == 1) {  // one tile of rows stays for the whole run
-                load(0);
+                fetch(0);
+                load(0, -1);
                 continue;
             }
             for (int i = r.from; i < r.to; i += 2) {
                 const int2 x = rows_of_pair(w, r, i);
+                fetch(x.x);
                 for (int y = x.x; y <= x.y; ++y)
-                    load(y);
+                    load(y, y < x.y ? y + 1 : -1);
             }
         }
         for (uint32_t i = copied > RS ? copied - RS : 0; i < copied; ++i)
@@ -286,11 +293,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         const uint32_t acc = uniform(tmem);
         Ring<KS> key;
         Ring<RS> row;
-        uint32_t count[2] = {0, 0};  // products of a group
-        auto commit = [&](uint32_t bar) {
-            if (!dead && elect())
-                mma_commit(bar);
-            __syncwarp();
+        uint32_t count = 0, single = 0;  // products of the first group, and how many fewer of the second
+        // (the next elect() brings the lanes together again)
+        auto see = [&](uint32_t bar, uint32_t parity) {
+            if (!bar_try(bar, parity) && !bar_wait_long(watch, bar, parity, false))
+                dead = true;
         };
         while (r.next(w)) {
             const bool hold = uniform(r.nr) == 1;
@@ -302,47 +309,62 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 const bool two = i + 1 < to;
                 Ring<KS> second = key;
                 second.step();
-                wait(k_full(key.stage), key.phase);
+                see(k_full(key.stage), key.phase);
                 if (two)
-                    wait(k_full(second.stage), second.phase);
+                    see(k_full(second.stage), second.phase);
+                const uint64_t a0 = tile_desc(keys + key.stage * TILE, 16, 1024);
+                const uint64_t a1 = tile_desc(keys + second.stage * TILE, 16, 1024);
                 const int last = uniform(x.y);
                 for (int y = uniform(x.x); y <= last; ++y) {
                     if (!hold || i == from)
-                        wait(q_full(row.stage), row.phase);
+                        see(q_full(row.stage), row.phase);
+                    const uint32_t c1 = count - single, b0 = count & 1, b1 = c1 & 1;
+                    const uint64_t b = tile_desc(rows + row.stage * TILE, 16, 1024);
+                    see(s_empty(0, b0), (count >> 1 & 1) ^ 1);
+                    fence_after();
+                    if (elect() && !dead) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (g == 1 && !two)
-                            continue;
-                        const int buf = count[g] & 1;
-                        wait(s_empty(g, buf), (count[g] >> 1 & 1) ^ 1);
-                        ++count[g];
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
+                            mma_ss(acc + b0 * KT, a0 + step, b + step, desc, k > 0);
+                        }
+                        mma_commit(s_full(0, b0));
+                        if (!two && !hold)
+                            mma_commit(q_empty(row.stage));
+                        if (!two && y == last)
+                            mma_commit(k_empty(key.stage));
+                    }
+                    if (two) {
+                        see(s_empty(1, b1), (c1 >> 1 & 1) ^ 1);
                         fence_after();
-                        const uint64_t a = tile_desc(keys + (g == 0 ? key.stage : second.stage) * TILE, 16, 1024);
-                        const uint64_t b = tile_desc(rows + row.stage * TILE, 16, 1024);
-                        if (!dead && elect()) {
+                        if (elect() && !dead) {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
                                 const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
-                                mma_ss(acc + g * 2 * KT + buf * KT, a + step, b + step, desc, k > 0);
+                                mma_ss(acc + (2 + b1) * KT, a1 + step, b + step, desc, k > 0);
                             }
-                            mma_commit(s_full(g, buf));
+                            mma_commit(s_full(1, b1));
+                            if (!hold)
+                                mma_commit(q_empty(row.stage));
+                            if (y == last) {
+                                mma_commit(k_empty(key.stage));
+                                mma_commit(k_empty(second.stage));
+                            }
                         }
-                        __syncwarp();
+                    } else {
+                        ++single;
                     }
-                    if (!hold) {
-                        commit(q_empty(row.stage));
+                    ++count;
+                    if (!hold)
                         row.step();
-                    }
                 }
-                commit(k_empty(key.stage));
                 key.step();
-                if (two) {
-                    commit(k_empty(key.stage));
+                if (two)
                     key.step();
-                }
             }
             if (hold) {
-                commit(q_empty(row.stage));
+                if (elect() && !dead)
+                    mma_commit(q_empty(row.stage));
                 row.step();
             }
         }
