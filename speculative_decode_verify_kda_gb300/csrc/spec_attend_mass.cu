@@ -5,8 +5,8 @@
 // exp(s - lse) by itself, in the order of the rows: no sum depends on the order of blocks, and
 // nothing is joined.  All sessions' key tiles, each counted as often as there are tiles of rows,
 // are cut into equal shares, one a CTA.  Two groups of 128 threads have a key tile each and share
-// the row tiles that pass by; a warp copies keys, a warp rows (and their lse), a warp issues the
-// products.  Bound by the keys' bytes for a verify round's rows, by exp2 and the products for a
+// the row tiles that pass by (of a single key tile they take the row tiles in turn and add their
+// sums); a warp copies keys, a warp rows (and their lse), a warp issues the products.  Bound by the keys' bytes for a verify round's rows, by exp2 and the products for a
 // prompt's.
 #include "attend_common.cuh"
 
@@ -24,7 +24,7 @@ __host__ __device__ constexpr int row_stages(int D) { return D == 128 ? 3 : 6; }
 // behind the tiles: barriers, what the warps tell each other, the rows' lse
 __host__ __device__ constexpr int shared_bytes(int D)
 {
-    return (KS + row_stages(D)) * tile_bytes(D) + 256 + 128 + row_stages(D) * KT * 4;
+    return (KS + row_stages(D)) * tile_bytes(D) + 256 + 128 + 512 + row_stages(D) * KT * 4;
 }
 
 struct Mass : Span {
@@ -157,14 +157,15 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
     auto q_empty = [&](int s) { return bars + 8u * (2 * KS + RS + s); };
     auto s_full = [&](int g, int i) { return bars + 8u * (2 * KS + 2 * RS + 2 * g + i); };
     auto s_empty = [&](int g, int i) { return bars + 8u * (2 * KS + 2 * RS + 4 + 2 * g + i); };
-    const uint32_t drained = bars + 8u * (2 * KS + 2 * RS + 8);
+    const uint32_t drained = bars + 8u * (2 * KS + 2 * RS + 8), told = drained + 8, joined = drained + 16;
     unsigned char *spare = raw + (bars - base) + 256;
     volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
     int *part = reinterpret_cast<int *>(spare + 16);  // [11]
     Share *found = reinterpret_cast<Share *>(spare + 64);
-    float *lse2 = reinterpret_cast<float *>(spare + 128);  // [RS][128]: lse log2 e of the rows
-    static_assert(8 * (2 * KS + 2 * RS + 9) <= 256 && sizeof(Share) <= 64, "room behind the rings");
+    float *other = reinterpret_cast<float *>(spare + 128);       // [128]: the second group's sums
+    float *lse2 = reinterpret_cast<float *>(spare + 128 + 512);  // [RS][128]: -lse log2 e of the rows
+    static_assert(8 * (2 * KS + 2 * RS + 11) <= 256 && sizeof(Share) <= 64, "room behind the rings");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == MMA_WARP)
@@ -184,6 +185,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 bar_init(s_empty(g, i), 4);
             }
         bar_init(drained, 1);
+        bar_init(told, 4);
+        bar_init(joined, 4);
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
             float f[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)  // a row without any score has lse -inf and no weight
-                f[e] = l[e] == -INFINITY ? INFINITY : l[e] * LOG2E;
+                f[e] = l[e] == -INFINITY ? -INFINITY : -l[e] * LOG2E;
             if (next >= 0)
                 fetch(next);  // on its way while this tile is copied
             wait(q_empty(to.stage), to.phase ^ 1);
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         const uint32_t acc = uniform(tmem);
         Ring<KS> key;
         Ring<RS> row;
-        uint32_t count = 0, single = 0;  // products of the first group, and how many fewer of the second
+        uint32_t count[2] = {0, 0};  // products of a group
         // (the next elect() brings the lanes together again)
         auto see = [&](uint32_t bar, uint32_t parity) {
             if (!bar_try(bar, parity) && !bar_wait_long(watch, bar, parity, false))
@@ -312,49 +315,39 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 see(k_full(key.stage), key.phase);
                 if (two)
                     see(k_full(second.stage), second.phase);
-                const uint64_t a0 = tile_desc(keys + key.stage * TILE, 16, 1024);
-                const uint64_t a1 = tile_desc(keys + second.stage * TILE, 16, 1024);
-                const int last = uniform(x.y);
-                for (int y = uniform(x.x); y <= last; ++y) {
+                const int first = uniform(x.x), last = uniform(x.y);
+                for (int y = first; y <= last; ++y) {
                     if (!hold || i == from)
                         see(q_full(row.stage), row.phase);
-                    const uint32_t c1 = count - single, b0 = count & 1, b1 = c1 & 1;
                     const uint64_t b = tile_desc(rows + row.stage * TILE, 16, 1024);
-                    see(s_empty(0, b0), (count >> 1 & 1) ^ 1);
-                    fence_after();
-                    if (elect() && !dead) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
-                            mma_ss(acc + b0 * KT, a0 + step, b + step, desc, k > 0);
-                        }
-                        mma_commit(s_full(0, b0));
-                        if (!two && !hold)
-                            mma_commit(q_empty(row.stage));
-                        if (!two && y == last)
-                            mma_commit(k_empty(key.stage));
-                    }
-                    if (two) {
-                        see(s_empty(1, b1), (c1 >> 1 & 1) ^ 1);
+                    for (int g = 0; g < 2; ++g) {
+                        // a group a key tile, or both groups in turn where there is one
+                        if (!two && (y - first & 1) != g)
+                            continue;
+                        const uint32_t buf = count[g] & 1;
+                        const uint64_t a = tile_desc(keys + (two && g == 1 ? second.stage : key.stage) * TILE, 16, 1024);
+                        see(s_empty(g, buf), (count[g] >> 1 & 1) ^ 1);
+                        ++count[g];
                         fence_after();
                         if (elect() && !dead) {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k) {
                                 const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
-                                mma_ss(acc + (2 + b1) * KT, a1 + step, b + step, desc, k > 0);
+                                mma_ss(acc + (2 * g + buf) * KT, a + step, b + step, desc, k > 0);
                             }
-                            mma_commit(s_full(1, b1));
-                            if (!hold)
-                                mma_commit(q_empty(row.stage));
-                            if (y == last) {
-                                mma_commit(k_empty(key.stage));
-                                mma_commit(k_empty(second.stage));
+                            mma_commit(s_full(g, buf));
+                            if (g == 1 || !two) {  // the last that reads these rows, these keys
+                                if (!hold)
+                                    mma_commit(q_empty(row.stage));
+                                if (y == last) {
+                                    mma_commit(k_empty(key.stage));
+                                    if (two)
+                                        mma_commit(k_empty(second.stage));
+                                }
                             }
                         }
-                    } else {
-                        ++single;
                     }
-                    ++count;
                     if (!hold)
                         row.step();
                 }
@@ -378,14 +371,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + g * 2 * KT;
         const Two cc = two(w.c, w.c), zero = two(0.0f, 0.0f);
         Ring<RS> row;
-        uint32_t count = 0;
+        uint32_t count = 0, joins = 0;
         while (r.next(w)) {
             const bool hold = r.nr == 1;
             const int cols = min(r.u.nt, w.TT) * w.a.G;
             for (int i = r.from; i < r.to; i += 2) {
                 const int2 x = rows_of_pair(w, r, i);
-                const bool mine = i + g < r.to;
-                const int j = tile_key(r.u, mine ? i + g : i) + line;
+                const bool paired = i + 1 < r.to;
+                const int j = tile_key(r.u, paired ? i + g : i) + line;
                 // the rows t0 .. t1 - 1 see this key
                 const int t0 = max(0, j - r.u.n);
                 const int t1 = w.a.seen.window && j >= w.a.seen.sinks ? min(r.u.nt, j - r.u.n + w.a.seen.window) : r.u.nt;
@@ -393,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 for (int y = x.x; y <= x.y; ++y) {
                     if (!hold || i == r.from)
                         wait(q_full(row.stage), row.phase);
-                    if (mine) {
+                    if (paired || (y - x.x & 1) == g) {
                         const int buf = count & 1;
                         wait(s_full(g, buf), count >> 1 & 1);
                         ++count;
@@ -422,8 +415,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
 #pragma unroll
                                     for (int e = 0; e < 32; e += 4) {
                                         const float4 f = *reinterpret_cast<const float4 *>(l + k0 + k + e);
-                                        const float2 u = apart(fma2(two(s[k + e], s[k + e + 1]), cc, two(-f.x, -f.y)));
-                                        const float2 v = apart(fma2(two(s[k + e + 2], s[k + e + 3]), cc, two(-f.z, -f.w)));
+                                        const float2 u = apart(fma2(two(s[k + e], s[k + e + 1]), cc, two(f.x, f.y)));
+                                        const float2 v = apart(fma2(two(s[k + e + 2], s[k + e + 3]), cc, two(f.z, f.w)));
                                         sum[0] = add2(sum[0], two(ex2(u.x), ex2(u.y)));
                                         sum[1] = add2(sum[1], two(ex2(v.x), ex2(v.y)));
                                     }
@@ -431,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
 #pragma unroll
                                     for (int e = 0; e < 32; e += 2) {
                                         const float2 f = *reinterpret_cast<const float2 *>(l + k0 + k + e);
-                                        const float2 u = apart(fma2(two(s[k + e], s[k + e + 1]), cc, two(-f.x, -f.y)));
+                                        const float2 u = apart(fma2(two(s[k + e], s[k + e + 1]), cc, two(f.x, f.y)));
                                         sum[e >> 1 & 1] = add2(sum[e >> 1 & 1],
                                                                two(seen >> e & 1 ? ex2(u.x) : 0.0f,
                                                                    seen >> (e + 1) & 1 ? ex2(u.y) : 0.0f));
@@ -447,10 +440,28 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                         row.step();
                     }
                 }
-                if (mine && some_see(w, r.u, j) && !*gave_up) {
+                const float2 both = apart(add2(sum[0], sum[1]));
+                float all = both.x + both.y;
+                const bool join = !paired && x.y > x.x;
+                if (join) {
+                    if (g == 1) {
+                        other[line] = all;
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_arrive(told);
+                        wait(joined, joins & 1);
+                    } else {
+                        wait(told, joins & 1);
+                        all += other[line];
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_arrive(joined);
+                    }
+                    ++joins;
+                }
+                if ((paired || g == 0) && some_see(w, r.u, j) && !*gave_up) {
                     float *to = w.mass + (static_cast<long long>(r.u.b) * w.a.c.Hkv + r.h) * w.ld + j;
-                    const float2 all = apart(add2(sum[0], sum[1]));
-                    *to = (j < r.u.n ? *to : 0.0f) + (all.x + all.y);
+                    *to = (j < r.u.n ? *to : 0.0f) + all;
                 }
                 __syncwarp();
             }
