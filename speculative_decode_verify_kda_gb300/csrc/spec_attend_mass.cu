@@ -4,9 +4,10 @@
 // key's scores against the rows in one lane of tensor memory, so a thread sums its key's weights
 // exp(s - lse) by itself, in the order of the rows: no sum depends on the order of blocks, and
 // nothing is joined.  All sessions' key tiles, each counted as often as there are tiles of rows,
-// are cut into equal shares, one a CTA.  Two groups of 128 threads have a key tile each and share
-// the row tiles that pass by (of a single key tile they take the row tiles in turn and add their
-// sums); a warp copies keys, a warp rows (and their lse), a warp issues the products.  Bound by the keys' bytes for a verify round's rows, by exp2 and the products for a
+// are cut into equal shares, one a CTA.  Two key tiles share the row tiles that pass by; each has two
+// groups of 128 threads, which take its products in turn and add their sums at the end (two warps a
+// scheduler left it idle for 60 % of the cycles).  A warp copies keys, a warp rows (and their lse), a
+// warp issues the products.  Bound by the keys' bytes for a verify round's rows, by exp2 and the products for a
 // prompt's.
 #include "attend_common.cuh"
 
@@ -16,15 +17,15 @@ namespace {
 using namespace pages;
 using namespace tiles;
 
-constexpr int KEY_WARP = 8, ROW_WARP = 9, MMA_WARP = 10;
-constexpr int THREADS = 352;
+constexpr int KEY_WARP = 16, ROW_WARP = 17, MMA_WARP = 18;
+constexpr int THREADS = 608;
 constexpr int KS = 4;  // key tiles in shared memory: two pairs
 
 __host__ __device__ constexpr int row_stages(int D) { return D == 128 ? 3 : 6; }
 // behind the tiles: barriers, what the warps tell each other, the rows' lse
 __host__ __device__ constexpr int shared_bytes(int D)
 {
-    return (KS + row_stages(D)) * tile_bytes(D) + 256 + 128 + 512 + row_stages(D) * KT * 4;
+    return (KS + row_stages(D)) * tile_bytes(D) + (8 * (2 * KS + 2 * row_stages(D) + 13) + 31) / 32 * 32 + 144 + 1024 + row_stages(D) * KT * 4;
 }
 
 struct Mass : Span {
@@ -157,15 +158,18 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
     auto q_empty = [&](int s) { return bars + 8u * (2 * KS + RS + s); };
     auto s_full = [&](int g, int i) { return bars + 8u * (2 * KS + 2 * RS + 2 * g + i); };
     auto s_empty = [&](int g, int i) { return bars + 8u * (2 * KS + 2 * RS + 4 + 2 * g + i); };
-    const uint32_t drained = bars + 8u * (2 * KS + 2 * RS + 8), told = drained + 8, joined = drained + 16;
-    unsigned char *spare = raw + (bars - base) + 256;
+    const uint32_t drained = bars + 8u * (2 * KS + 2 * RS + 8);
+    auto told = [&](int g) { return drained + 8u * (1 + g); };
+    auto joined = [&](int g) { return drained + 8u * (3 + g); };
+    constexpr int BARS = (8 * (2 * KS + 2 * RS + 13) + 31) / 32 * 32;
+    unsigned char *spare = raw + (bars - base) + BARS;
     volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
-    int *part = reinterpret_cast<int *>(spare + 16);  // [11]
-    Share *found = reinterpret_cast<Share *>(spare + 64);
-    float *other = reinterpret_cast<float *>(spare + 128);       // [128]: the second group's sums
-    float *lse2 = reinterpret_cast<float *>(spare + 128 + 512);  // [RS][128]: -lse log2 e of the rows
-    static_assert(8 * (2 * KS + 2 * RS + 11) <= 256 && sizeof(Share) <= 64, "room behind the rings");
+    int *part = reinterpret_cast<int *>(spare + 8);  // [19]
+    Share *found = reinterpret_cast<Share *>(spare + 88);
+    float *other = reinterpret_cast<float *>(spare + 144);         // [2][128]: the second groups' sums
+    float *lse2 = reinterpret_cast<float *>(spare + 144 + 1024);   // [RS][128]: -lse log2 e of the rows
+    static_assert(sizeof(Share) <= 56 && THREADS / 32 <= 20, "room behind the rings");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == MMA_WARP)
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         }
         for (int s = 0; s < RS; ++s) {
             bar_init(q_full(s), 2);
-            bar_init(q_empty(s), 9);
+            bar_init(q_empty(s), 17);
         }
         for (int g = 0; g < 2; ++g)
             for (int i = 0; i < 2; ++i) {
@@ -185,8 +189,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 bar_init(s_empty(g, i), 4);
             }
         bar_init(drained, 1);
-        bar_init(told, 4);
-        bar_init(joined, 4);
+        for (int g = 0; g < 2; ++g) {
+            bar_init(told(g), 4);
+            bar_init(joined(g), 4);
+        }
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         const uint32_t acc = uniform(tmem);
         Ring<KS> key;
         Ring<RS> row;
-        uint32_t count[2] = {0, 0};  // products of a group
+        uint32_t count[2] = {0, 0};  // products of a pair's first and second tiles
         // (the next elect() brings the lanes together again)
         auto see = [&](uint32_t bar, uint32_t parity) {
             if (!bar_try(bar, parity) && !bar_wait_long(watch, bar, parity, false))
@@ -315,18 +321,17 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 see(k_full(key.stage), key.phase);
                 if (two)
                     see(k_full(second.stage), second.phase);
-                const int first = uniform(x.x), last = uniform(x.y);
-                for (int y = first; y <= last; ++y) {
+                const int last = uniform(x.y);
+                for (int y = uniform(x.x); y <= last; ++y) {
                     if (!hold || i == from)
                         see(q_full(row.stage), row.phase);
                     const uint64_t b = tile_desc(rows + row.stage * TILE, 16, 1024);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        // a group a key tile, or both groups in turn where there is one
-                        if (!two && (y - first & 1) != g)
+                        if (g == 1 && !two)
                             continue;
                         const uint32_t buf = count[g] & 1;
-                        const uint64_t a = tile_desc(keys + (two && g == 1 ? second.stage : key.stage) * TILE, 16, 1024);
+                        const uint64_t a = tile_desc(keys + (g == 1 ? second.stage : key.stage) * TILE, 16, 1024);
                         see(s_empty(g, buf), (count[g] >> 1 & 1) ^ 1);
                         ++count[g];
                         fence_after();
@@ -367,68 +372,61 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         __syncwarp();
         bar_wait_long(watch, drained, 0, true);
     } else {
-        const int g = warp >> 2, line = tid & 127;
-        const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + g * 2 * KT;
+        const int g = warp >> 3, half = warp >> 2 & 1, line = tid & 127;
+        const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + (2 * g + half) * KT;
         const Two cc = two(w.c, w.c), zero = two(0.0f, 0.0f);
         Ring<RS> row;
-        uint32_t count = 0, joins = 0;
+        uint32_t count = 0, joins = 0;  // products of this tile of the pairs, and pairs with sums to add
         while (r.next(w)) {
             const bool hold = r.nr == 1;
             const int cols = min(r.u.nt, w.TT) * w.a.G;
             for (int i = r.from; i < r.to; i += 2) {
                 const int2 x = rows_of_pair(w, r, i);
-                const bool paired = i + 1 < r.to;
-                const int j = tile_key(r.u, paired ? i + g : i) + line;
+                const bool on = i + g < r.to;
+                const int j = tile_key(r.u, on ? i + g : i) + line;
                 // the rows t0 .. t1 - 1 see this key
                 const int t0 = max(0, j - r.u.n);
                 const int t1 = w.a.seen.window && j >= w.a.seen.sinks ? min(r.u.nt, j - r.u.n + w.a.seen.window) : r.u.nt;
                 Two sum[2] = {zero, zero};
+                bool mine = false;
                 for (int y = x.x; y <= x.y; ++y) {
                     if (!hold || i == r.from)
                         wait(q_full(row.stage), row.phase);
-                    if (paired || (y - x.x & 1) == g) {
-                        const int buf = count & 1;
-                        wait(s_full(g, buf), count >> 1 & 1);
-                        ++count;
+                    if (on && (count++ & 1) == static_cast<uint32_t>(half)) {
+                        mine = true;
+                        wait(s_full(g, half), (count - 1) >> 1 & 1);
                         fence_after();
                         // its columns of this tile of rows
                         const int a = max(0, min(w.TT, t0 - y * w.TT)) * w.a.G, b = max(0, min(w.TT, t1 - y * w.TT)) * w.a.G;
                         const float *l = lse2 + row.stage * KT;
-#pragma unroll
-                        for (int k0 = 0; k0 < KT; k0 += 64) {
-                            if (k0 >= cols)
-                                break;
-                            uint32_t s[64];
-                            tmem_ld32(at + buf * KT + k0, s);
-                            tmem_ld32(at + buf * KT + k0 + 32, s + 32);
+#pragma unroll 1
+                        for (int k = 0; k < cols; k += 32) {
+                            uint32_t s[32];
+                            tmem_ld32(at + k, s);
                             tmem_wait_ld();
-                            if (k0 + 64 >= cols) {  // the last of it: the next product may come
+                            if (k + 32 >= cols) {  // the last of it: the next product may come
                                 fence_before();
                                 __syncwarp();
                                 if (lane == 0)
-                                    bar_arrive(s_empty(g, buf));
+                                    bar_arrive(s_empty(g, half));
                             }
+                            const uint32_t seen = bits_below(b - k) & ~bits_below(a - k);
+                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) {
 #pragma unroll
-                            for (int k = 0; k < 64; k += 32) {
-                                const uint32_t seen = bits_below(b - k0 - k) & ~bits_below(a - k0 - k);
-                                if (__all_sync(0xffffffffu, seen == 0xffffffffu)) {
+                                for (int e = 0; e < 32; e += 4) {
+                                    const float4 f = *reinterpret_cast<const float4 *>(l + k + e);
+                                    const float2 u = apart(fma2(two(s[e], s[e + 1]), cc, two(f.x, f.y)));
+                                    const float2 v = apart(fma2(two(s[e + 2], s[e + 3]), cc, two(f.z, f.w)));
+                                    sum[0] = add2(sum[0], two(ex2(u.x), ex2(u.y)));
+                                    sum[1] = add2(sum[1], two(ex2(v.x), ex2(v.y)));
+                                }
+                            } else if (__any_sync(0xffffffffu, seen != 0)) {
 #pragma unroll
-                                    for (int e = 0; e < 32; e += 4) {
-                                        const float4 f = *reinterpret_cast<const float4 *>(l + k0 + k + e);
-                                        const float2 u = apart(fma2(two(s[k + e], s[k + e + 1]), cc, two(f.x, f.y)));
-                                        const float2 v = apart(fma2(two(s[k + e + 2], s[k + e + 3]), cc, two(f.z, f.w)));
-                                        sum[0] = add2(sum[0], two(ex2(u.x), ex2(u.y)));
-                                        sum[1] = add2(sum[1], two(ex2(v.x), ex2(v.y)));
-                                    }
-                                } else if (__any_sync(0xffffffffu, seen != 0)) {
-#pragma unroll
-                                    for (int e = 0; e < 32; e += 2) {
-                                        const float2 f = *reinterpret_cast<const float2 *>(l + k0 + k + e);
-                                        const float2 u = apart(fma2(two(s[k + e], s[k + e + 1]), cc, two(f.x, f.y)));
-                                        sum[e >> 1 & 1] = add2(sum[e >> 1 & 1],
-                                                               two(seen >> e & 1 ? ex2(u.x) : 0.0f,
-                                                                   seen >> (e + 1) & 1 ? ex2(u.y) : 0.0f));
-                                    }
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 f = *reinterpret_cast<const float2 *>(l + k + e);
+                                    const float2 u = apart(fma2(two(s[e], s[e + 1]), cc, two(f.x, f.y)));
+                                    sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], two(seen >> e & 1 ? ex2(u.x) : 0.0f,
+                                                                                seen >> (e + 1) & 1 ? ex2(u.y) : 0.0f));
                                 }
                             }
                         }
@@ -442,24 +440,24 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 }
                 const float2 both = apart(add2(sum[0], sum[1]));
                 float all = both.x + both.y;
-                const bool join = !paired && x.y > x.x;
-                if (join) {
-                    if (g == 1) {
-                        other[line] = all;
+                if (on && x.y > x.x) {  // two products or more: both groups have some
+                    if (half == 1) {
+                        other[g * KT + line] = all;
                         __syncwarp();
                         if (lane == 0)
-                            bar_arrive(told);
-                        wait(joined, joins & 1);
+                            bar_arrive(told(g));
+                        wait(joined(g), joins & 1);
+                        mine = false;
                     } else {
-                        wait(told, joins & 1);
-                        all += other[line];
+                        wait(told(g), joins & 1);
+                        all += other[g * KT + line];
                         __syncwarp();
                         if (lane == 0)
-                            bar_arrive(joined);
+                            bar_arrive(joined(g));
                     }
                     ++joins;
                 }
-                if ((paired || g == 0) && some_see(w, r.u, j) && !*gave_up) {
+                if (mine && some_see(w, r.u, j) && !*gave_up) {
                     float *to = w.mass + (static_cast<long long>(r.u.b) * w.a.c.Hkv + r.h) * w.ld + j;
                     *to = (j < r.u.n ? *to : 0.0f) + all;
                 }
