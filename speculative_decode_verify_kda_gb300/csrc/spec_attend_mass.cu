@@ -6,8 +6,10 @@
 // nothing is joined.  All sessions' key tiles, each counted as often as there are tiles of rows,
 // are cut into equal shares, one a CTA.  Two key tiles share the row tiles that pass by; each has two
 // groups of 128 threads, which take its products in turn and add their sums at the end (two warps a
-// scheduler left it idle for 60 % of the cycles).  A warp copies keys, a warp rows (and their lse), a
-// warp issues the products.  Bound by the keys' bytes for a verify round's rows, by exp2 and the products for a
+// scheduler left it idle for 60 % of the cycles).  A warp copies keys, a warp rows, a warp issues the
+// products.  A row's -lse / scale is part of the product, as four 16-bit terms of its own against a
+// column of constants: read from shared memory by every thread it bound the kernel (128 bytes a cycle,
+// as do the reads of tensor memory).  Bound by the keys' bytes for a verify round's rows, by exp2 and the products for a
 // prompt's.
 #include "attend_common.cuh"
 
@@ -19,19 +21,57 @@ using namespace tiles;
 
 constexpr int KEY_WARP = 16, ROW_WARP = 17, MMA_WARP = 18;
 constexpr int THREADS = 608;
-constexpr int KS = 4;  // key tiles in shared memory: two pairs
 
-__host__ __device__ constexpr int row_stages(int D) { return D == 128 ? 3 : 6; }
-// behind the tiles: barriers, what the warps tell each other, the rows' lse
+// Tiles in shared memory, keys and rows.
+__host__ __device__ constexpr int key_stages(int D) { return D == 128 ? 4 : 8; }
+__host__ __device__ constexpr int row_stages(int D) { return D == 128 ? 2 : 4; }
+constexpr int TERMS = KT * 32;  // a tile of terms: 16 elements a row
+__host__ __device__ constexpr int barrier_bytes(int D) { return (8 * (2 * key_stages(D) + 2 * row_stages(D) + 13) + 31) / 32 * 32; }
 __host__ __device__ constexpr int shared_bytes(int D)
 {
-    return (KS + row_stages(D)) * tile_bytes(D) + (8 * (2 * KS + 2 * row_stages(D) + 13) + 31) / 32 * 32 + 144 + 1024 + row_stages(D) * KT * 4;
+    return (key_stages(D) + row_stages(D)) * tile_bytes(D) + (row_stages(D) + 1) * TERMS + barrier_bytes(D) + 144 + 1024;
+}
+
+// The constants that a row's four terms are multiplied by: bf16 reaches as far as f32; f16 terms
+// of 11 bits each begin at 2^15, so that 2 10^9 is reached and 10^-9 kept.
+template <bool BF16>
+__device__ __forceinline__ float term_unit(int i)
+{
+    return BF16 ? 1.0f : i == 0 ? 32768.0f : i == 1 ? 32.0f : i == 2 ? 0.03125f : 3.0517578125e-5f;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float rounded(float x)
+{
+    return BF16 ? __bfloat162float(__float2bfloat16_rn(x)) : __half2float(__float2half_rn(x));
+}
+
+// x as its four terms, two to a word
+template <bool BF16>
+__device__ __forceinline__ uint4 terms_of(float x)
+{
+    float t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t[i] = rounded<BF16>(x / term_unit<BF16>(i));
+        // what is not finite, or past the first term's reach, is that term's alone
+        x = isinf(t[i]) || t[i] != t[i] ? 0.0f : x - t[i] * term_unit<BF16>(i);
+    }
+    return make_uint4(pack<BF16>(t[0], t[1]), pack<BF16>(t[2], t[3]), 0, 0);
+}
+
+// Descriptor of a tile of terms: blocks of 8 rows of 16 bytes, the two halves of the 16 elements side by side.
+__device__ __forceinline__ uint64_t terms_desc(uint32_t addr)
+{
+    return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | static_cast<uint64_t>(128 >> 4) << 16 |
+           static_cast<uint64_t>(256 >> 4) << 32 | 1ull << 46;
 }
 
 struct Mass : Span {
     const float *lse;
     float *mass;
     long long ld;
+    float over;  // 1 / scale
 };
 
 // Where a CTA's share of the tiles begins: the tiles whose place in the order (session, kv head,
@@ -149,9 +189,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap map_q,
                                                                  const __grid_constant__ CUtensorMap map_k)
 {
-    constexpr int TILE = tile_bytes(D), HALF = KT * 128, RS = row_stages(D);
+    constexpr int TILE = tile_bytes(D), HALF = KT * 128, KS = key_stages(D), RS = row_stages(D);
     extern __shared__ __align__(1024) unsigned char raw[];
-    const uint32_t base = smem_addr(raw), keys = base, rows = base + KS * TILE, bars = rows + RS * TILE;
+    const uint32_t base = smem_addr(raw), keys = base, rows = base + KS * TILE, units = rows + RS * TILE, terms = units + TERMS,
+                   bars = terms + RS * TERMS;
     auto k_full = [&](int s) { return bars + 8u * s; };
     auto k_empty = [&](int s) { return bars + 8u * (KS + s); };
     auto q_full = [&](int s) { return bars + 8u * (2 * KS + s); };
@@ -161,14 +202,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
     const uint32_t drained = bars + 8u * (2 * KS + 2 * RS + 8);
     auto told = [&](int g) { return drained + 8u * (1 + g); };
     auto joined = [&](int g) { return drained + 8u * (3 + g); };
-    constexpr int BARS = (8 * (2 * KS + 2 * RS + 13) + 31) / 32 * 32;
+    constexpr int BARS = barrier_bytes(D);
     unsigned char *spare = raw + (bars - base) + BARS;
     volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
     int *part = reinterpret_cast<int *>(spare + 8);  // [19]
     Share *found = reinterpret_cast<Share *>(spare + 88);
     float *other = reinterpret_cast<float *>(spare + 144);         // [2][128]: the second groups' sums
-    float *lse2 = reinterpret_cast<float *>(spare + 144 + 1024);   // [RS][128]: -lse log2 e of the rows
     static_assert(sizeof(Share) <= 56 && THREADS / 32 <= 20, "room behind the rings");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -181,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         }
         for (int s = 0; s < RS; ++s) {
             bar_init(q_full(s), 2);
-            bar_init(q_empty(s), 17);
+            bar_init(q_empty(s), 1);
         }
         for (int g = 0; g < 2; ++g)
             for (int i = 0; i < 2; ++i) {
@@ -199,6 +239,15 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         prefetch_map(&map_q);
         prefetch_map(&map_k);
     }
+    // the constants, and zeros behind the terms
+    for (int i = tid; i < (RS + 1) * TERMS / 16; i += THREADS) {
+        const bool unit = i < TERMS / 16 && (i & 8) == 0;
+        reinterpret_cast<uint4 *>(raw + (units - base))[i] =
+            unit ? make_uint4(pack<BF16>(term_unit<BF16>(0), term_unit<BF16>(1)),
+                              pack<BF16>(term_unit<BF16>(2), term_unit<BF16>(3)), 0, 0)
+                 : make_uint4(0, 0, 0, 0);
+    }
+    fence_async();
     fence_before();
     __syncthreads();
     fence_after();
@@ -253,16 +302,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = x * w.TT + t_of[e];
-                l[e] = INFINITY;  // of a row that is not there: weight 0
+                l[e] = 0.0f;  // of a row that is not there: its products are left out
                 if (t_of[e] < w.TT && t < r.u.nt)
                     l[e] = w.lse[(static_cast<long long>(r.u.b) * w.a.T + t) * w.a.Hq + r.h * w.a.G + g_of[e]];
             }
         };
         auto load = [&](int x, int next) {
-            float f[4];
+            uint4 f[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)  // a row without any score has lse -inf and no weight
-                f[e] = l[e] == -INFINITY ? -INFINITY : -l[e] * LOG2E;
+                f[e] = terms_of<BF16>(l[e] == -INFINITY ? -INFINITY : -l[e] * w.over);
             if (next >= 0)
                 fetch(next);  // on its way while this tile is copied
             wait(q_empty(to.stage), to.phase ^ 1);
@@ -273,7 +322,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                         copy_3d(rows + to.stage * TILE + half * HALF, &map_q, half * 64, r.h * w.a.G,
                                 r.u.b * w.a.T + x * w.TT, q_full(to.stage));
                 }
-                *reinterpret_cast<float4 *>(lse2 + to.stage * KT + c0) = make_float4(f[0], f[1], f[2], f[3]);
+                uint4 *t = reinterpret_cast<uint4 *>(raw + (terms + to.stage * TERMS - base)) + (c0 >> 3) * 16 + (c0 & 7);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    t[e] = f[e];
+                fence_async();
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(q_full(to.stage));
@@ -341,6 +394,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                                 const uint64_t step = (k / 4 * HALF + k % 4 * 32) >> 4;
                                 mma_ss(acc + (2 * g + buf) * KT, a + step, b + step, desc, k > 0);
                             }
+                            mma_ss(acc + (2 * g + buf) * KT, terms_desc(units), terms_desc(terms + row.stage * TERMS), desc,
+                                   true);
                             mma_commit(s_full(g, buf));
                             if (g == 1 || !two) {  // the last that reads these rows, these keys
                                 if (!hold)
@@ -375,10 +430,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         const int g = warp >> 3, half = warp >> 2 & 1, line = tid & 127;
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + (2 * g + half) * KT;
         const Two cc = two(w.c, w.c), zero = two(0.0f, 0.0f);
-        Ring<RS> row;
         uint32_t count = 0, joins = 0;  // products of this tile of the pairs, and pairs with sums to add
         while (r.next(w)) {
-            const bool hold = r.nr == 1;
             const int cols = min(r.u.nt, w.TT) * w.a.G;
             for (int i = r.from; i < r.to; i += 2) {
                 const int2 x = rows_of_pair(w, r, i);
@@ -390,15 +443,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 Two sum[2] = {zero, zero};
                 bool mine = false;
                 for (int y = x.x; y <= x.y; ++y) {
-                    if (!hold || i == r.from)
-                        wait(q_full(row.stage), row.phase);
                     if (on && (count++ & 1) == static_cast<uint32_t>(half)) {
                         mine = true;
                         wait(s_full(g, half), (count - 1) >> 1 & 1);
                         fence_after();
                         // its columns of this tile of rows
                         const int a = max(0, min(w.TT, t0 - y * w.TT)) * w.a.G, b = max(0, min(w.TT, t1 - y * w.TT)) * w.a.G;
-                        const float *l = lse2 + row.stage * KT;
 #pragma unroll 1
                         for (int k = 0; k < cols; k += 32) {
                             uint32_t s[32];
@@ -414,28 +464,20 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                             if (__all_sync(0xffffffffu, seen == 0xffffffffu)) {
 #pragma unroll
                                 for (int e = 0; e < 32; e += 4) {
-                                    const float4 f = *reinterpret_cast<const float4 *>(l + k + e);
-                                    const float2 u = apart(fma2(two(s[e], s[e + 1]), cc, two(f.x, f.y)));
-                                    const float2 v = apart(fma2(two(s[e + 2], s[e + 3]), cc, two(f.z, f.w)));
+                                    const float2 u = apart(mul2(two(s[e], s[e + 1]), cc));
+                                    const float2 v = apart(mul2(two(s[e + 2], s[e + 3]), cc));
                                     sum[0] = add2(sum[0], two(ex2(u.x), ex2(u.y)));
                                     sum[1] = add2(sum[1], two(ex2(v.x), ex2(v.y)));
                                 }
                             } else if (__any_sync(0xffffffffu, seen != 0)) {
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
-                                    const float2 f = *reinterpret_cast<const float2 *>(l + k + e);
-                                    const float2 u = apart(fma2(two(s[e], s[e + 1]), cc, two(f.x, f.y)));
+                                    const float2 u = apart(mul2(two(s[e], s[e + 1]), cc));
                                     sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], two(seen >> e & 1 ? ex2(u.x) : 0.0f,
                                                                                 seen >> (e + 1) & 1 ? ex2(u.y) : 0.0f));
                                 }
                             }
                         }
-                    }
-                    if (!hold) {
-                        __syncwarp();
-                        if (lane == 0)
-                            bar_arrive(q_empty(row.stage));
-                        row.step();
                     }
                 }
                 const float2 both = apart(add2(sum[0], sum[1]));
@@ -462,11 +504,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                     *to = (j < r.u.n ? *to : 0.0f) + all;
                 }
                 __syncwarp();
-            }
-            if (hold) {
-                if (lane == 0)
-                    bar_arrive(q_empty(row.stage));
-                row.step();
             }
         }
     }
@@ -510,6 +547,7 @@ extern "C" int spec_attend_mass(const kda_cache *cache, const void *q, int T, in
     w.lse = lse;
     w.mass = mass;
     w.ld = ld_mass;
+    w.over = 1.0f / scale;
     pages::lay_out(&w, T);
     const bool bf16 = cache->dtype == KDA_BF16;
     CUtensorMap map_q, map_k;
