@@ -706,6 +706,10 @@ int spec_distill_step(const void *logits, int logit_dtype, int N, int V, long lo
  */
 #define KDA_CACHE_MAX (1 << 30) /* tokens that a session's pages may hold        */
 #define KDA_GROUP_MAX 128       /* query heads that read one kv head             */
+#define KDA_SCALE_MIN 1e-6f
+#define KDA_SCALE_MAX 1e6f
+#define KDA_TILES_MAX 2e9 /* tiles of 128 keys (times tiles of 128 rows) of a call, at
+                             what the tables hold: more is refused                 */
 typedef struct kda_cache {
     void *k, *v;
     const int *table, *lens;
@@ -728,7 +732,7 @@ int spec_cache_append(const kda_cache *cache, const void *k_rows, const void *v_
  * Hq is a multiple of Hkv, at most KDA_GROUP_MAX times as large.  The row at position p sees key j when
  *   j <= p  and  (window == 0  or  p - j < window  or  j < sinks),
  * that is everything before it, or the last `window` keys (itself among them) and the
- * first `sinks` ones.  With s_j = scale q.k_j (scale > 0) over the visible keys
+ * first `sinks` ones.  With s_j = scale q.k_j (scale in KDA_SCALE_MIN..MAX) over the visible keys
  *   lse = ln sum_j exp s_j,   o = sum_j exp(s_j - lse) v_j:
  *   out [B][T][Hq][D] of the cache's type, dense; lse f32 [B][T][Hq] (may be NULL).
  * Sums and statistics are f32; the weights enter the product with v in the cache's type.
@@ -736,7 +740,8 @@ int spec_cache_append(const kda_cache *cache, const void *k_rows, const void *v_
  * may have been given back), and one that only later rows see does not reach earlier ones.
  * Of a key that some rows of a session see and others do not, a value that is not finite
  * makes the whole of a row that sees it NaN.  A row whose scores are all -inf gives zeros
- * and lse -inf.
+ * and lse -inf.  The same call gives the same bits; how its work is cut, and so a result's
+ * last bits, depends on the lengths of all its sessions.
  *   workspace: device memory of spec_attend_workspace_bytes(B, T, Hq, Hkv, D) bytes, 16-byte
  *   aligned, no initialisation needed; calls that overlap need one each.
  */
@@ -748,7 +753,8 @@ int spec_attend(const kda_cache *cache, const void *q, int T, int Hq, long long 
 /*
  * spec_attend_mass -- what every key was worth to the rows, for an eviction by it:
  *   share_j = sum over the rows and the query heads of kv head h of exp(s_j - lse),
- * with lse f32 [B][T][Hq] as spec_attend gave it (-inf gives 0) and the same visible keys.
+ * with lse f32 [B][T][Hq] as spec_attend gave it (-inf gives 0; with a KDA_F16 cache |lse| / scale
+ * stays below 2e9) and the same visible keys.
  * mass f32 [B][Hkv][ld_mass] (ld_mass >= table_cols * page): mass[b][h][j] += share_j for
  * the tokens j < lens[b], mass[b][h][j] = share_j for the rows' own (their places may hold
  * what a rejected draft left); the others are left as they are.  After an accept, t_rows =

@@ -116,8 +116,8 @@ inline int check_query(const Cache &c, int Hq, int window, int sinks, float scal
         return fail(KDA_EINVAL, "Hq must be 1..128 times Hkv");
     if (window < 0 || sinks < 0)
         return fail(KDA_EINVAL, "window and sinks must be >= 0");
-    if (!(scale > 0.0f) || std::isinf(scale))
-        return fail(KDA_EINVAL, "scale must be positive and finite");
+    if (!(scale >= KDA_SCALE_MIN && scale <= KDA_SCALE_MAX))
+        return fail(KDA_EINVAL, "scale must lie in KDA_SCALE_MIN..KDA_SCALE_MAX");
     return KDA_OK;
 }
 

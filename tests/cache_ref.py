@@ -67,6 +67,15 @@ class Case:
             self.q = self.q_host.to(DEV)
             self.k_rows, self.v_rows = (new[:, :, i].contiguous().to(DEV) for i in (0, 1))
 
+    def spread(self, stride):
+        """Pages `stride` elements apart, a page's keys and values side by side."""
+        pages, block = self.k.shape[0], self.k[0].numel()
+        far = torch.empty(stride * (pages - 1) + 2 * block, dtype=self.dtype, device=DEV)
+        for i, name in enumerate("kv"):
+            x = far.as_strided(self.k.shape, (stride, *self.k[0].contiguous().stride()), i * block)
+            setattr(self, name, x.copy_(getattr(self, name)))
+        return self
+
     def sees(self, p, j):
         return j <= p and (self.window == 0 or p - j < self.window or j < self.sinks)
 

@@ -80,8 +80,8 @@ def test_append_refuses(L, bad):
 
 QUERY = [dict(T=-1), dict(T=2**30), dict(q=None), dict(q=FAKE + 4), dict(ld=504), dict(ld=516), dict(Hq=0),
          dict(Hq=1), dict(Hq=3), dict(Hq=258, ld=2**20), dict(window=-1), dict(sinks=-1), dict(scale=0.0),
-         dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(t_rows=FAKE + 2), dict(status=FAKE + 2),
-         dict(lse=FAKE + 2)]
+         dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(scale=9e-7), dict(scale=1.1e6),
+         dict(t_rows=FAKE + 2), dict(status=FAKE + 2), dict(lse=FAKE + 2)]
 
 
 @pytest.mark.parametrize("bad", [*QUERY, dict(out=None), dict(out=FAKE + 8), dict(work=None), dict(work=FAKE + 8),
@@ -104,6 +104,12 @@ def test_mass_refuses(L, bad):
                                  dict(m_out=FAKE, ld_out=65), dict(kept=FAKE + 1), dict(status=FAKE + 3)], ids=str)
 def test_evict_refuses(L, bad):
     assert evict(L, cache(), **bad) == kb.EINVAL
+
+
+def test_more_tiles_than_a_call_counts_are_refused(L):
+    many = cache(B=2**20, Hkv=64, table_cols=2**16)
+    assert attend(L, many, T=1, Hq=64, ld=64 * 128) == kb.EINVAL and b"tiles" in L.kda_last_error()
+    assert mass(L, many, T=1, Hq=64, ld=64 * 128, ld_mass=2**20) == kb.EINVAL and b"tiles" in L.kda_last_error()
 
 
 def test_no_rows_are_nothing_to_do(L):

@@ -1,6 +1,7 @@
 """spec_attend and spec_attend_mass against the formulas in 64 bits: lengths, row counts, head
 groups, pages, layouts, windows and sinks; whatever no row sees holds NaN."""
 import math
+import random
 
 import pytest
 import torch
@@ -118,6 +119,24 @@ def test_many_sessions():
     both(Case(lens, T=3, Hq=4, Hkv=2, t_rows=rows, seed=11))
 
 
+def test_more_sessions_than_a_block_has_threads():
+    g = torch.Generator().manual_seed(4)
+    both(Case(torch.randint(0, 150, (900,), generator=g).tolist(), T=1, Hq=2, Hkv=1, D=64, seed=12))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_anywhere_in_the_range(seed):
+    """Sizes drawn over the whole range, small enough for the plain form."""
+    r = random.Random(seed)
+    Hkv = r.choice((1, 2, 3))
+    G, T = r.choice((1, 2, 3, 4, 6, 8, 16, 50)), r.choice((1, 2, 7, 15, 33, 100))
+    lens = [r.choice((0, 1, r.randint(0, 300), r.randint(0, 1500))) for _ in range(r.randint(1, 5))]
+    both(Case(lens, T=T, Hq=Hkv * G, Hkv=Hkv, D=r.choice((64, 128)), page=r.choice((8, 16, 32, 64, 128, 512, 1024)),
+              dtype=r.choice((BF16, F16)), t_rows=r.choice((None, [r.randint(0, T) for _ in lens])),
+              window=r.choice((0, 0, r.randint(1, 40), r.randint(1, 600))), sinks=r.choice((0, 3, 130)),
+              layout=r.choice(("hnd", "nhd", "paired")), fused=r.random() < 0.5, seed=seed))
+
+
 def test_one_head_shared_by_many_sessions_pages():
     """Sessions that share their first pages, as those of one prompt do."""
     c = Case([160, 160, 160], T=2, Hq=8, Hkv=2, page=32, seed=21)
@@ -130,6 +149,60 @@ def test_one_head_shared_by_many_sessions_pages():
 @pytest.mark.parametrize("n,T", [(5000, 1), (5000, 15), (3000, 40), (3000, 70), (2000, 193)])
 def test_long_texts_are_split_and_joined(n, T):
     both(Case([n, 3], T=T, Hq=8, Hkv=2, page=64, seed=n + T))
+
+
+@pytest.mark.parametrize("Hkv,D", [(1, 128), (2, 64)])
+def test_pages_past_32_bits(Hkv, D):
+    both(Case([40], T=3, Hq=4, Hkv=Hkv, D=D, page=16, spare=0, seed=D).spread(2**31 + 8 * D))
+
+
+def test_rows_past_32_bits():
+    """2.2 thousand million elements of q: the first rows, and the last, which begin past 2^31."""
+    T, Hq, D, W = 2**17 + 3000, 128, 128, 16
+    g = torch.Generator("cuda").manual_seed(1)
+    k, v = (torch.randn((T // 1024 + 1, 1, 1024, D), generator=g, device="cuda", dtype=BF16) for _ in range(2))
+    table = torch.arange(len(k), dtype=torch.int32, device="cuda")[None]
+    cache = kb.PagedCache(k, v, table, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    q = torch.randn((1, T, Hq, D), generator=g, device="cuda", dtype=BF16)
+    out, lse = kb.spec_attend(cache, q, window=W)
+    mass = kb.spec_attend_mass(cache, q, lse, torch.full((1, 1, cache.capacity), math.nan, device="cuda"), window=W)
+    u = torch.finfo(BF16).eps / 2
+    for t0 in (0, T // 2, T - 40):
+        kk, vv = (x.view(-1, D)[t0:t0 + 40].double().cpu() for x in (k, v))
+        qq = q[0, t0:t0 + 40].double().cpu()
+        s = torch.einsum("thd,nd->thn", qq, kk) * D**-0.5
+        p, j = torch.arange(40)[:, None], torch.arange(40)[None]
+        s = s.masked_fill(((j > p) | (p - j >= W))[:, None], -math.inf)
+        whole = slice(0 if t0 == 0 else W, 40)  # rows whose window lies in the slice
+        total = torch.logsumexp(s, 2)
+        w = (s - total[..., None]).exp()
+        o, size = torch.einsum("thn,nd->thd", w, vv), torch.einsum("thn,nd->thd", w, vv.abs())
+        ds = (D + 4) * 2.0**-24 * D**-0.5 * float(qq.norm(dim=-1).max() * kk.norm(dim=-1).max())
+        rows = slice(t0 + whole.start, t0 + 40)
+        # the bounds of Case.attend and Case.share; 2048 weights in a key's sum
+        near(out[0, rows], o[whole], (u * o.abs() + (u + 2 * ds + 2.0**-17) * size * (1 + u) + 1e-30)[whole])
+        near(lse[0, rows], total[whole], ds + 2.0**-17 + 2.0**-22 * total[whole].abs())
+        seen = slice(whole.start, 40 if t0 == T - 40 else 40 - W)  # keys whose rows lie in the slice
+        x = w.sum((0, 1))
+        far = float(torch.where(s == -math.inf, 0.0, s.abs()).max() + total.abs().max())
+        near(mass[0, 0, t0 + seen.start:t0 + seen.stop], x[seen], (x * (2 * ds + far * 2.0**-21 + 2.0**-14))[seen])
+
+
+def test_a_text_of_sixteen_million_tokens():
+    """Every page the same one: the attention is that page's, its lse larger by the log of their number."""
+    N = 2**24
+    c = Case([1024 - 2], T=2, Hq=4, Hkv=1, D=64, page=1024, spare=0, seed=2)
+    want, _, tol, _ = c.attend()
+    cache = kb.PagedCache(c.k, c.v, torch.zeros((1, N // 1024), dtype=torch.int32, device="cuda"),
+                          torch.tensor([N - 2], dtype=torch.int32, device="cuda"))
+    out, lse = kb.spec_attend(cache, c.q)
+    # the last row sees N keys; a CTA adds up to N / 152 / 16 times to a sum, half an ulp lost each time or,
+    # in the tensor cores, a whole one
+    s, v, ds = c.head(0, 0)
+    lost = N / 152 / 16 * 2.0**-23
+    near(out[:, 1], want[:, 1], tol[:, 1] + lost * v.abs().max())
+    total = torch.logsumexp(s[1], 1) + math.log(N // 1024)
+    near(lse[0, 1], total, ds + 2.0**-17 + 2.0**-22 * total + lost)
 
 
 def test_scores_of_a_wide_range():
@@ -175,6 +248,21 @@ def test_values_that_only_later_rows_see_do_not_reach_earlier_ones():
             near(lse, want_lse, tol_lse)
             assert torch.isnan(out[0, 1:, :, 5]).all() or math.isinf(bad)
             assert not torch.isfinite(out[0, 1:, :, 5]).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,window,at", [(6, 40, 92), (6, 40, 94), (90, 4, 150), (90, 40, 100), (90, 100, 60)])
+def test_values_that_only_some_rows_see_reach_those_alone(T, window, at, dtype):
+    """A value behind the window of the later rows, or of a key that is new: NaN where it is seen."""
+    c = Case([130], T=T, Hq=4, Hkv=1, window=window, sinks=2, dtype=dtype, seed=T)
+    c.v[c.table[0, at // c.page], :, at % c.page, 9] = math.inf
+    out, lse = kb.spec_attend(c.cache(), c.q, **c.see())
+    want, want_lse, tol, tol_lse = c.attend()
+    near(lse, want_lse, tol_lse)
+    sees = torch.tensor([c.sees(130 + t, at) for t in range(T)])
+    assert sees.any() and not sees.all()
+    near(out[:, ~sees], want[:, ~sees], tol[:, ~sees])
+    assert not torch.isfinite(out[:, sees][..., 9]).any()
 
 
 def test_keys_that_only_later_rows_see_do_not_reach_earlier_ones():

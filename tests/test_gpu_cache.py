@@ -59,6 +59,17 @@ def test_append_leaves_bad_sessions_and_pages_alone():
     assert int(status) == kb.ST_BADKEEP | kb.ST_BADLEN | kb.ST_BADPAGE
 
 
+def test_append_pages_past_32_bits():
+    c = Case([14], T=4, Hq=2, Hkv=2, page=16, spare=1, seed=4)
+    k, v = c.k.clone(), c.v.clone()
+    c.spread(2**31 + 1024)
+    for j in range(14, 18):
+        for x in (c.k, c.v):
+            x[c.table[0, j // 16], :, j % 16] = 9.0
+    kb.spec_cache_append(c.cache(), c.k_rows, c.v_rows)
+    assert torch.equal(bits(c.k), bits(k)) and torch.equal(bits(c.v), bits(v))
+
+
 class Evict:
     """A cache of B sessions full of numbers, masses, and what an eviction has to leave."""
 
@@ -130,6 +141,23 @@ def test_evict_layouts(Hkv, D, page, dtype, layout, in_place):
 @pytest.mark.parametrize("n,budget", [(1023, 512), (1025, 1024), (5000, 1111), (20011, 3001), (70001, 9000)])
 def test_evict_long(n, budget, in_place):
     Evict([n, n // 2], Hkv=1, seed=n, page=32).check(budget, 100, 4, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_many_long_sessions(in_place):
+    """More heads than clusters of eight have room for, more tokens than a block holds in registers."""
+    Evict([9000 - 37 * b for b in range(40)], Hkv=1, page=64, seed=3).check(700, 20, 4, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_pages_past_32_bits(in_place):
+    e = Evict([40], seed=6)
+    stride, block = 2**31 + 512, e.k[0].numel()
+    far = torch.empty(stride * (e.k.shape[0] - 1) + 2 * block, dtype=BF16, device="cuda")
+    k, v = (far.as_strided(e.k.shape, (stride, *e.k.stride()[1:]), i * block).copy_(x)
+            for i, x in enumerate((e.k, e.v)))
+    e.k, e.v, e.cache = k, v, kb.PagedCache(k, v, e.table, e.lens)
+    e.check(20, 4, 2, in_place)
 
 
 def test_evict_orders_nan_zero_and_infinity():
