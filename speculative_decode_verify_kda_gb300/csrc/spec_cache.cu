@@ -58,10 +58,13 @@ __global__ void __launch_bounds__(APPEND_T) cache_append_kernel(const Append a)
 // passes of 11, 11 and 10 bits count digits (a histogram in each CTA's shared memory) and find the
 // smallest kept number and how many of its equals are kept: a warp reads the cluster's sums of 64
 // bins, then the 64 bins that hold the digit.  Every warp has a run of positions: one pass counts
-// what it keeps, one gives the kept positions their places.  Up to HELD numbers a lane are read
-// once and stay in registers; longer runs are read again, from the caches, by every pass.
+// what it keeps, one gives the kept positions their places.  The numbers are read once: up to
+// HELD a lane stay in registers, longer runs in shared memory (a head of 131072 tokens took 74 us
+// for 50 when every pass read them again); more than 393 thousand tokens of a head fit neither and are
+// read again, from the caches, by every pass.
 // Second launch: the kept keys, values and masses move.
 constexpr int SELECT_T = 512, SELECT_W = SELECT_T / 32, BINS = 2048, HELD = 16;
+constexpr int STORED = 96 * 32;  // numbers of a warp in shared memory
 
 struct Evict {
     Cache c;
@@ -71,6 +74,7 @@ struct Evict {
     int budget, recent, sinks, dst_cols;
     const int *dst;  // the pages that receive the tokens
     int *kept, *lens_out, *status;
+    int room;  // numbers that a warp has room for in shared memory
 };
 
 // Rising with the float, the two zeros equal, a NaN below every number.
@@ -118,6 +122,7 @@ __device__ __forceinline__ int lanes_before(int x, int &total)
 template <int CL>
 __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
 {
+    extern __shared__ uint32_t stored[];
     __shared__ int hist[BINS], group[BINS / 64], found[2], sums[2], part[2][SELECT_W];
     after_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -142,6 +147,12 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
 #pragma unroll
     for (int e = 0; e < HELD; ++e)
         own[e] = held && from + 32 * e < to ? number(from + 32 * e + lane) : 0;
+    const bool kept_near = !held && warp_run <= a.room;
+    uint32_t *near = stored + warp * a.room + lane;
+    if (kept_near)
+#pragma unroll 8
+        for (int j0 = from; j0 < to; j0 += 32)
+            near[j0 - from] = number(j0 + lane);
     // f(position, number) for 32 positions at a time
     auto each = [&](auto f) {
         if (held) {
@@ -149,6 +160,10 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
             for (int e = 0; e < HELD; ++e)
                 if (from + 32 * e < to)
                     f(from + 32 * e + lane, own[e]);
+        } else if (kept_near) {
+#pragma unroll 4
+            for (int j0 = from; j0 < to; j0 += 32)
+                f(j0 + lane, near[j0 - from]);
         } else {
 #pragma unroll 4
             for (int j0 = from; j0 < to; j0 += 32)
@@ -405,9 +420,20 @@ __global__ void __launch_bounds__(MOVE_T) evict_in_place_kernel(const Evict a)
 }
 
 template <int CL>
-int select(const Evict &a, unsigned heads, cudaStream_t stream)
+int select(Evict a, unsigned heads, cudaStream_t stream)
 {
+    // each warp's run at full length, if that is more than registers hold
+    const long long cta_run = (a.c.capacity() + CL - 1) / CL;
+    const long long warp_run = ((cta_run + SELECT_W - 1) / SELECT_W + 31) / 32 * 32;
     cudaLaunchConfig_t cfg{};
+    if (warp_run > 32 * HELD) {
+        a.room = static_cast<int>(std::min(warp_run, static_cast<long long>(STORED)));
+        cfg.dynamicSmemBytes = sizeof(uint32_t) * a.room * SELECT_W;
+        const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(sizeof(uint32_t)) * STORED * SELECT_W);
+        if (e != cudaSuccess)
+            return fail(KDA_ECUDA, std::string("evict_select_kernel shared memory: ") + cudaGetErrorString(e));
+    }
     cfg.gridDim = dim3(heads * CL);
     cfg.blockDim = dim3(SELECT_T);
     cfg.stream = stream;
@@ -508,8 +534,11 @@ extern "C" int spec_cache_evict(const kda_cache *cache, const float *mass, long 
     a.lens_out = lens_out;
     a.status = dev_status;
     const unsigned heads = static_cast<unsigned>(a.c.B) * a.c.Hkv;
-    // eight CTAs a head while the device has room for them and a head has work for them
-    const bool wide = heads * 8ll <= 2 * pages::SMS && capacity > 4096;
+    // Eight CTAs a head while the device has room for them and a head has work for them, and where one
+    // CTA could not hold its numbers.  One against eight, us (budget 1024): 8 heads of 4096 tokens 14.8
+    // and 16.2, of 8192 19.5 and 16.8, of 32768 49 and 20; 64 heads of 8192 37.5 and 44.7, of 32768 78
+    // and 57; 128 heads of 32768 89 and 107, of 65536 241 and 142.
+    const bool wide = capacity > (heads <= pages::SMS / 4 ? 4096 : heads <= pages::SMS / 2 ? 16384 : SELECT_W * STORED);
     if (int rc = wide ? select<8>(a, heads, stream) : select<1>(a, heads, stream))
         return rc;
     if (!dst_table)

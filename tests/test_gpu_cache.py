@@ -143,6 +143,10 @@ def test_evict_long(n, budget, in_place):
     Evict([n, n // 2], Hkv=1, seed=n, page=32).check(budget, 100, 4, in_place)
 
 
+def test_evict_more_tokens_than_a_cluster_holds():
+    Evict([400001], Hkv=1, seed=8, page=1024).check(3000, 100, 4, False)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_many_long_sessions(in_place):
     """More heads than clusters of eight have room for, more tokens than a block holds in registers."""
