@@ -722,7 +722,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
 }
 
-// The second launch joins the parts of the units that were cut: CTAs for each, a warp a row.
+// The second launch joins the parts of the units that were cut: CTAs for each, a warp a row.  It is a
+// chain of latencies, so no warp has a second row (with two to eight a warp a round of 8 rows of 64
+// heads over 32768 keys took 44 us for 39, of 16 rows over 16384 46 for 31), and its code is short: all
+// loads of 16 parts at once, twice the instructions, cost 2 to 11 us where the code was cold.
 constexpr int JOIN_T = 256;
 
 template <int D, bool BF16>
@@ -799,8 +802,9 @@ int run(const Walk &w, const CUtensorMap &q, const CUtensorMap &k, const CUtenso
     if (int rc = launch(attend_kernel<D, PAIR, BF16>, dim3(grid), THREADS, shared_bytes(D, PAIR), stream, "attend_kernel", w,
                         q, k, v))
         return rc;
-    return launch(attend_join_kernel<D, BF16>, dim3(grid, PAIR ? 8 : 4), JOIN_T, 0, stream, "attend_join_kernel", w,
-                  PAIR ? 2 * KT : KT);
+    const int rows = PAIR ? 2 * KT : w.a.T * w.a.G;
+    return launch(attend_join_kernel<D, BF16>, dim3(grid, (rows - 1) / (JOIN_T / 32) + 1), JOIN_T, 0, stream,
+                  "attend_join_kernel", w, PAIR ? 2 * KT : KT);
 }
 
 }  // namespace
