@@ -11,7 +11,8 @@ using namespace pages;
 
 // ---- append -------------------------------------------------------------------------
 // A copy of B T rows of Hkv D elements: nothing but memory.  A CTA takes a few rows, a thread
-// 16 bytes of k and of v at a time.
+// 16 bytes of k and of v at a time.  A verify round's rows take a launch (3.0 us), 8192 rows of 8
+// heads 12.7 us (5.3 TB/s).
 constexpr int APPEND_T = 256;
 
 struct Append {
@@ -62,7 +63,9 @@ __global__ void __launch_bounds__(APPEND_T) cache_append_kernel(const Append a)
 // HELD a lane stay in registers, longer runs in shared memory (a head of 131072 tokens took 74 us
 // for 50 when every pass read them again); more than 393 thousand tokens of a head fit neither and are
 // read again, from the caches, by every pass.
-// Second launch: the kept keys, values and masses move.
+// Second launch: the kept keys, values and masses move.  Bound by the chain of passes and barriers for a
+// few heads (8 heads of 32768 tokens to 4096: 26 us, 5 of them for the bytes), by the move's bytes for many
+// (256 heads of up to 8000 tokens to 2000: 105 us, the bytes 79).
 constexpr int SELECT_T = 512, SELECT_W = SELECT_T / 32, BINS = 2048, HELD = 16;
 constexpr int STORED = 96 * 32;  // numbers of a warp in shared memory
 
