@@ -722,10 +722,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
 }
 
-// The second launch joins the parts of the units that were cut: CTAs for each, a warp a row.  It is a
-// chain of latencies, so no warp has a second row (with two to eight a warp a round of 8 rows of 64
-// heads over 32768 keys took 44 us for 39, of 16 rows over 16384 46 for 31), and its code is short: all
-// loads of 16 parts at once, twice the instructions, cost 2 to 11 us where the code was cold.
+// The second launch joins the parts of the units that were cut: CTAs for each, a warp a row of its
+// tiles.  It is a chain of latencies, so no warp has a second row (with two to eight a warp a round of 8
+// rows of 64 heads over 32768 keys took 44 us for 38, of 16 rows over 16384 46 for 31), and its code is
+// short and loads early: two parts, the usual number where units are many, are joined without the
+// exchange between lanes (a window's prompt chunk 96 us for 93).
 constexpr int JOIN_T = 256;
 
 template <int D, bool BF16>
@@ -734,58 +735,73 @@ __global__ void __launch_bounds__(JOIN_T) attend_join_kernel(const __grid_consta
     after_previous();
     constexpr int E = D / 32;
     const Cut cut = w.cuts[blockIdx.x];
-    const int lane = threadIdx.x & 31, rows = cut.n > 0 ? cut.nt * w.a.G : 0;
-    for (int i = blockIdx.y * (JOIN_T / 32) + (threadIdx.x >> 5); i < rows; i += gridDim.y * (JOIN_T / 32)) {
-        const int t = i / w.a.G, g = i - t * w.a.G, row = t / w.TT * KT + t % w.TT * w.a.G + g;
-        auto place = [&](int k) {
-            const int slot = k == 0 ? cut.slot : 2 * (static_cast<int>(blockIdx.x) + k);
-            return static_cast<size_t>(slot) * rows_a_part + row;
-        };
-        float top = -INFINITY, l = 0.0f, o[E] = {};
-        for (int k0 = 0; k0 < cut.n; k0 += 32) {
-            // a lane a part: its maximum and sum; then a part after another
-            const float2 s = k0 + lane < cut.n ? w.stats[place(k0 + lane)] : make_float2(-INFINITY, 0.0f);
-            float most = fmaxf(top, s.x);
+    const int lane = threadIdx.x & 31, row = blockIdx.y * (JOIN_T / 32) + (threadIdx.x >> 5);
+    // a row's place in the tiles: the token and the head
+    const int tile = row / KT, x = row % KT, rt = x / w.a.G, t = tile * w.TT + rt, g = x - rt * w.a.G;
+    if (cut.n == 0 || rt >= w.TT || t >= cut.nt)
+        return;
+    const float *parts = w.parts + static_cast<size_t>(row) * D + lane * E;
+    const size_t far = static_cast<size_t>(rows_a_part) * D;
+    auto slot_of = [&](int k) { return k == 0 ? cut.slot : 2 * (static_cast<int>(blockIdx.x) + k); };
+    float top = -INFINITY, l = 0.0f, o[E] = {};
+    if (cut.n == 2) {
+        const float2 s0 = w.stats[slot_of(0) * rows_a_part + row], s1 = w.stats[slot_of(1) * rows_a_part + row];
+        float v[2][E];
 #pragma unroll
-            for (int d = 16; d; d >>= 1)
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-            const float again = top == most ? 1.0f : ex2((top - most) * w.c);
-            const float f = s.x == most ? 1.0f : ex2((s.x - most) * w.c);
-            float sum = s.y * f;
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int d = 16; d; d >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            l = l * again + sum;
-            top = most;
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<float2 *>(v[k] + e) = *reinterpret_cast<const float2 *>(parts + slot_of(k) * far + e);
+        top = fmaxf(s0.x, s1.x);
+        const float f0 = s0.x == top ? 1.0f : ex2((s0.x - top) * w.c), f1 = s1.x == top ? 1.0f : ex2((s1.x - top) * w.c);
+        l = s0.y * f0 + s1.y * f1;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                o[e] *= again;
-#pragma unroll 8
-            for (int k = 0; k < min(32, cut.n - k0); ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, k);
-                const float *x = w.parts + place(k0 + k) * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(x);
-                    o[0] += v.x * fk;
-                    o[1] += v.y * fk;
-                    o[2] += v.z * fk;
-                    o[3] += v.w * fk;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2 *>(x);
-                    o[0] += v.x * fk;
-                    o[1] += v.y * fk;
-                }
+        for (int e = 0; e < E; ++e)
+            o[e] = v[0][e] * f0 + v[1][e] * f1;
+    }
+    for (int k0 = 0; k0 < cut.n && cut.n != 2; k0 += 32) {
+        // a lane a part: its maximum and sum; then a part after another
+        const float2 s = k0 + lane < cut.n ? w.stats[slot_of(k0 + lane) * rows_a_part + row] : make_float2(-INFINITY, 0.0f);
+        float most = fmaxf(top, s.x);
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        const float again = top == most ? 1.0f : ex2((top - most) * w.c);
+        const float f = s.x == most ? 1.0f : ex2((s.x - most) * w.c);
+        float sum = s.y * f;
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l = l * again + sum;
+        top = most;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] *= again;
+#pragma unroll 16
+        for (int k = 0; k < min(32, cut.n - k0); ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float *from = parts + slot_of(k0 + k) * far;
+            if constexpr (E == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(from);
+                o[0] += v.x * fk;
+                o[1] += v.y * fk;
+                o[2] += v.z * fk;
+                o[3] += v.w * fk;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(from);
+                o[0] += v.x * fk;
+                o[1] += v.y * fk;
             }
         }
-        const long long to = (static_cast<long long>(cut.b) * w.a.T + cut.t0 + t) * w.a.Hq + cut.h * w.a.G + g;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(w.a.out + to * D + lane * E);
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            dst[e / 2] = pack<BF16>(o[e] * inv, o[e + 1] * inv);
-        if (lane == 0 && w.a.lse)
-            w.a.lse[to] = l == 0.0f ? -INFINITY : (top * w.c + log2f(l)) * LN2;
     }
+    const long long to = (static_cast<long long>(cut.b) * w.a.T + cut.t0 + t) * w.a.Hq + cut.h * w.a.G + g;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(w.a.out + to * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        dst[e / 2] = pack<BF16>(o[e] * inv, o[e + 1] * inv);
+    if (lane == 0 && w.a.lse)
+        w.a.lse[to] = l == 0.0f ? -INFINITY : (top * w.c + log2f(l)) * LN2;
 }
 
 // More than 128 rows of a session and kv head fill two tiles.
