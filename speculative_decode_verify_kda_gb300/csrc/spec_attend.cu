@@ -246,7 +246,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 raise(w.a.status, bad);
         }
     share_of(w, part, found);
-    const Watch watch{gave_up, w.a.status};
     uint32_t seq = 0;   // tiles before this run
     int nth = 0;        // runs before this one
     bool dead = false;  // a wait gave up: nothing more is issued
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             auto look = [&](int i) { return i < r.todo ? page_of(w, r.u, key_of(i)) : 0; };
             uint32_t copied = 0, asked = 0;  // tiles, and rows
             auto load_rows = [&] {
-                if (!warp_wait(watch, q_empty, (nth & 1) ^ 1))
+                if (!warp_wait(gave_up, q_empty, (nth & 1) ^ 1))
                     dead = true;
                 const bool two = PAIR && r.u.nt > w.TT;
                 asked += !dead;
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     load_rows();
                 for (int i = 0; i < r.todo; ++i) {
                     const int next = look(i + 1);  // on its way while this tile is copied
-                    if (!warp_wait(watch, empty(first + stage), phase ^ 1))
+                    if (!warp_wait(gave_up, empty(first + stage), phase ^ 1))
                         dead = true;
                     if (!dead) {
                         copy_tile<D>(w, r.u, r.h, key_of(i), id, m, ring + (first + stage) * TILE, full(first + stage));
@@ -322,9 +321,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 w.cuts[blockIdx.x] = cut;
             // copies in flight land before the CTA ends, whatever was given up
             for (uint32_t i = copied > static_cast<uint32_t>(count) ? copied - count : 0; i < copied; ++i)
-                bar_wait_long(watch, full(first + i % count), i / count & 1, true);
+                bar_wait_long(gave_up, full(first + i % count), i / count & 1, true);
             if (asked > 0)
-                bar_wait_long(watch, q_full, (asked - 1) & 1, true);
+                bar_wait_long(gave_up, q_full, (asked - 1) & 1, true);
         } else if (warp == MMA_WARP) {
             // The whole warp walks; one lane issues.  One warp for both groups: with a warp each, their
             // products ran into each other (a prompt's chunk took 1078 us for 828).
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             Ring<VS> val;
             // (the next elect() brings the lanes together again)
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                if (!bar_try(bar, parity) && !bar_wait_long(watch, bar, parity, false))
+                if (!bar_try(bar, parity) && !bar_wait_long(gave_up, bar, parity, false))
                     dead = true;
             };
             // `math` false: a group without rows, which keeps step with the other
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             if (elect())
                 mma_commit(drained);
             __syncwarp();
-            bar_wait_long(watch, drained, 0, true);
+            bar_wait_long(gave_up, drained, 0, true);
         } else if (warp == CLEAN_WARP) {
             // Value tiles pass from the copies to the products through this warp.  Values of keys that
             // no row sees become zeros (a weight of 0 times anything is then 0); of a key that only
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 __syncwarp();
                 for (int i = 0; i < r.todo; ++i) {
                     const int j0 = tile_key(u, r.off + i);
-                    warp_wait(watch, full(KS + at.stage), at.phase);
+                    warp_wait(gave_up, full(KS + at.stage), at.phase);
                     if (is_edge(w, u, j0)) {
                         unsigned char *tile = raw + (ring_v + at.stage * TILE - base);
                         auto place = [&](int row) {
@@ -537,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 const int i = PAIR ? x : 2 * x + first;
                 const int j0 = key_of(i);
                 const bool edge = is_edge(w, u, j0);
-                warp_wait(watch, s_full(g), (done + x) & 1);
+                warp_wait(gave_up, s_full(g), (done + x) & 1);
                 if (busy) {
                     fence_after();
                     uint32_t s[KT];
@@ -564,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     if (x == 0) {
                         used = m;
                     } else if (__any_sync(0xffffffffu, (m - used) * w.c > LAG || (used == -INFINITY && m > used))) {
-                        warp_wait(watch, o_full(g), (done + x - 1) & 1);
+                        warp_wait(gave_up, o_full(g), (done + x - 1) & 1);
                         fence_after();
                         const float f = m == used ? 1.0f : ex2((used - m) * w.c);
                         l *= f;
@@ -615,7 +614,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             }
             // the result of the run
             if (tiles > 0)
-                warp_wait(watch, o_full(g), (done + tiles - 1) & 1);
+                warp_wait(gave_up, o_full(g), (done + tiles - 1) & 1);
             done += tiles;
             fence_after();
             const bool join = !PAIR && r.todo > 1;
@@ -628,7 +627,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     bar_arrive(told);
             }
             if (join && g == lead) {
-                warp_wait(watch, told, joins & 1);
+                warp_wait(gave_up, told, joins & 1);
                 fence_after();
                 const float2 o = other[row];
                 const float both = fmaxf(used, o.x);
@@ -701,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     if (lane == 0)
                         bar_arrive(joined);
                 } else {
-                    warp_wait(watch, joined, joins & 1);
+                    warp_wait(gave_up, joined, joins & 1);
                     fence_after();
                 }
                 ++joins;
@@ -712,6 +711,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
     fence_before();
     __syncthreads();
+    if (tid == 0 && *gave_up)
+        raise(w.a.status, KDA_ST_TIMEOUT);
     if (warp == MMA_WARP) {
         __syncwarp();
         tmem_free<512>(tmem);

@@ -262,11 +262,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
                 raise(w.a.status, bad);
         }
     share_of(w, part, found);
-    const Watch watch{gave_up, w.a.status};
     Runs r(w, *found);
     bool dead = false;  // a wait gave up: nothing more is issued
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!warp_wait(watch, bar, parity))
+        if (!warp_wait(gave_up, bar, parity))
             dead = true;
     };
 
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         }
         // copies in flight land before the CTA ends, whatever was given up
         for (uint32_t i = copied > KS ? copied - KS : 0; i < copied; ++i)
-            bar_wait_long(watch, k_full(i % KS), i / KS & 1, true);
+            bar_wait_long(gave_up, k_full(i % KS), i / KS & 1, true);
     } else if (warp == ROW_WARP) {
         Ring<RS> to;
         uint32_t copied = 0;
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
             }
         }
         for (uint32_t i = copied > RS ? copied - RS : 0; i < copied; ++i)
-            bar_wait_long(watch, q_full(i % RS), i / RS & 1, true);
+            bar_wait_long(gave_up, q_full(i % RS), i / RS & 1, true);
     } else if (warp == MMA_WARP) {
         // The whole warp walks; one lane issues.
         const uint32_t acc = uniform(tmem);
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         uint32_t count[2] = {0, 0};  // products of a pair's first and second tiles
         // (the next elect() brings the lanes together again)
         auto see = [&](uint32_t bar, uint32_t parity) {
-            if (!bar_try(bar, parity) && !bar_wait_long(watch, bar, parity, false))
+            if (!bar_try(bar, parity) && !bar_wait_long(gave_up, bar, parity, false))
                 dead = true;
         };
         while (r.next(w)) {
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
         if (elect())
             mma_commit(drained);
         __syncwarp();
-        bar_wait_long(watch, drained, 0, true);
+        bar_wait_long(gave_up, drained, 0, true);
     } else {
         const int g = warp >> 3, half = warp >> 2 & 1, line = tid & 127;
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + (2 * g + half) * KT;
@@ -510,6 +509,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
     }
     fence_before();
     __syncthreads();
+    if (tid == 0 && *gave_up)
+        raise(w.a.status, KDA_ST_TIMEOUT);
     if (warp == MMA_WARP) {
         __syncwarp();
         tmem_free<512>(tmem);

@@ -50,38 +50,29 @@ __device__ __forceinline__ uint64_t now_ns()
 }
 
 // What a CTA does when a wait runs out: `gave_up` is set, every later wait returns at once, and
-// the threads walk to the end of the kernel without results (no thread leaves a barrier short).
-struct Watch {
-    volatile int *gave_up;
-    int *status;
-};
-
-__device__ __forceinline__ bool bar_wait_long(const Watch w, uint32_t bar, uint32_t parity, bool keep_on)
+// the threads walk to the end of the kernel without results (no thread leaves a barrier short);
+// there the status is raised.  The loop is short: it stands in the code wherever a warp waits.
+__device__ __forceinline__ bool bar_wait_long(volatile int *gave_up, uint32_t bar, uint32_t parity, bool keep_on)
 {
     const uint64_t t0 = now_ns();
-    for (uint32_t n = 1;; ++n) {
-        if (bar_try(bar, parity))
-            return true;
-        if ((n & 15) == 0) {
-            if (*w.gave_up && !keep_on)
-                return false;
-            if (now_ns() - t0 > WAIT_NS)
-                break;
+    while (!bar_try(bar, parity)) {
+        if (*gave_up && !keep_on)
+            return false;
+        if (now_ns() - t0 > WAIT_NS) {
+            *gave_up = 1;
+            return false;
         }
     }
-    *w.gave_up = 1;
-    if (w.status)
-        atomicOr(w.status, KDA_ST_TIMEOUT);
-    return false;
+    return true;
 }
 
 // A warp's wait for the phase of `bar` with `parity`, for a second at most; the warp goes on
 // together.  False (in every lane) when a lane gave up.
-__device__ __forceinline__ bool warp_wait(const Watch &w, uint32_t bar, uint32_t parity)
+__device__ __forceinline__ bool warp_wait(volatile int *gave_up, uint32_t bar, uint32_t parity)
 {
     if (__all_sync(0xffffffffu, bar_try(bar, parity)))
         return true;
-    const bool ok = bar_wait_long(w, bar, parity, false);
+    const bool ok = bar_wait_long(gave_up, bar, parity, false);
     return __all_sync(0xffffffffu, ok);
 }
 
