@@ -59,12 +59,14 @@ __global__ void __launch_bounds__(APPEND_T) cache_append_kernel(const Append a)
 // passes of 11, 11 and 10 bits count digits (a histogram in each CTA's shared memory) and find the
 // smallest kept number and how many of its equals are kept: a warp reads the cluster's sums of 64
 // bins, then the 64 bins that hold the digit.  Every warp has a run of positions: one pass counts
-// what it keeps, one gives the kept positions their places.  The numbers are read once: up to
-// HELD a lane stay in registers, longer runs in shared memory (a head of 131072 tokens took 74 us
-// for 50 when every pass read them again); more than 393 thousand tokens of a head fit neither and are
-// read again, from the caches, by every pass.
+// what it keeps, one gives the kept positions their places.  The numbers are read once and stay
+// in shared memory (8 heads of 131072 tokens took 74 us for 50 when every pass read them again); more than
+// 393 thousand tokens of a head do not fit and are read again, from the caches, by every pass.  With
+// REGISTERS up to HELD numbers a lane stay in those: better where heads fill the SMs (64 heads of 8192
+// tokens 37.5 us for 45), worse for a few, whose time is that of the code (8 heads of 2048 tokens 12.4 us for
+// 11.0, of 8192 16.5 for 14.8).
 // Second launch: the kept keys, values and masses move.  Bound by the chain of passes and barriers for a
-// few heads (8 heads of 32768 tokens to 4096: 26 us, 5 of them for the bytes), by the move's bytes for many
+// few heads (8 heads of 32768 tokens to 4096: 25 us, 5 of them for the bytes), by the move's bytes for many
 // (256 heads of up to 8000 tokens to 2000: 105 us, the bytes 79).
 constexpr int SELECT_T = 512, SELECT_W = SELECT_T / 32, BINS = 2048, HELD = 16;
 constexpr int STORED = 96 * 32;  // numbers of a warp in shared memory
@@ -122,7 +124,7 @@ __device__ __forceinline__ int lanes_before(int x, int &total)
     return s - x;
 }
 
-template <int CL>
+template <int CL, bool REGISTERS>
 __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
 {
     extern __shared__ uint32_t stored[];
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(SELECT_T) evict_select_kernel(const Evict a)
     const int warp_run = ((end - begin + SELECT_W - 1) / SELECT_W + 31) / 32 * 32;
     const int from = min(end, begin + warp * warp_run), to = min(end, from + warp_run);
     auto number = [&](int j) { return choose && j < to && j >= low && j < high ? rank_of(mass[j]) : 0; };
-    const bool held = warp_run <= 32 * HELD;
+    const bool held = REGISTERS && warp_run <= 32 * HELD;
     uint32_t own[HELD];
 #pragma unroll
     for (int e = 0; e < HELD; ++e)
@@ -422,17 +424,18 @@ __global__ void __launch_bounds__(MOVE_T) evict_in_place_kernel(const Evict a)
     }
 }
 
-template <int CL>
+template <int CL, bool REGISTERS>
 int select(Evict a, unsigned heads, cudaStream_t stream)
 {
-    // each warp's run at full length, if that is more than registers hold
+    // room for each warp's run at full length, unless registers hold that
     const long long cta_run = (a.c.capacity() + CL - 1) / CL;
     const long long warp_run = ((cta_run + SELECT_W - 1) / SELECT_W + 31) / 32 * 32;
     cudaLaunchConfig_t cfg{};
-    if (warp_run > 32 * HELD) {
+    if (!REGISTERS || warp_run > 32 * HELD) {
         a.room = static_cast<int>(std::min(warp_run, static_cast<long long>(STORED)));
         cfg.dynamicSmemBytes = sizeof(uint32_t) * a.room * SELECT_W;
-        const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CL, REGISTERS>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(sizeof(uint32_t)) * STORED * SELECT_W);
         if (e != cudaSuccess)
             return fail(KDA_ECUDA, std::string("evict_select_kernel shared memory: ") + cudaGetErrorString(e));
@@ -448,7 +451,7 @@ int select(Evict a, unsigned heads, cudaStream_t stream)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CL > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<CL>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<CL, REGISTERS>, a);
     if (e != cudaSuccess)
         return fail(KDA_ECUDA, std::string("evict_select_kernel launch: ") + cudaGetErrorString(e));
     return check_launch("evict_select_kernel");
@@ -541,8 +544,10 @@ extern "C" int spec_cache_evict(const kda_cache *cache, const float *mass, long 
     // CTA could not hold its numbers.  One against eight, us (budget 1024): 8 heads of 4096 tokens 14.8
     // and 16.2, of 8192 19.5 and 16.8, of 32768 49 and 20; 64 heads of 8192 37.5 and 44.7, of 32768 78
     // and 57; 128 heads of 32768 89 and 107, of 65536 241 and 142.
-    const bool wide = capacity > (heads <= pages::SMS / 4 ? 4096 : heads <= pages::SMS / 2 ? 16384 : SELECT_W * STORED);
-    if (int rc = wide ? select<8>(a, heads, stream) : select<1>(a, heads, stream))
+    const bool few = heads <= pages::SMS / 4;
+    const bool wide = capacity > (few ? 4096 : heads <= pages::SMS / 2 ? 16384 : SELECT_W * STORED);
+    if (int rc = few ? (wide ? select<8, false>(a, heads, stream) : select<1, false>(a, heads, stream))
+                     : (wide ? select<8, true>(a, heads, stream) : select<1, true>(a, heads, stream)))
         return rc;
     if (!dst_table)
         return pages::launch(evict_in_place_kernel, dim3(heads, 2 * a.c.D / 32 + 1), MOVE_T, 0, stream,
