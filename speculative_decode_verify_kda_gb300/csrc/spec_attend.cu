@@ -18,11 +18,12 @@
 // Rounded to 16 bits: the weights (as an operand of the products must be) and the results.  Weights
 // are taken against a maximum that is at most 2^8 too small, their sum is of the unrounded ones.
 //
-// Measured on GB300 (in a CUDA graph): a prompt's chunk of 2048 rows of 64 heads over 16384 keys 737
-// us, 1.58 PFLOP/s (81 % of the measured product rate); 32 sessions of 15 rows over up to 16384 keys
-// 244 us, 6.2 TB/s; one row of 32 heads over 131072 keys 91 us, 5.9 TB/s.  A round of few keys is
-// bound by a chain of latencies: lengths, table, keys, scores, weights, result, join (15 us for one
-// row of 64 heads over 4096 keys).
+// Measured on GB300 (in a CUDA graph): a prompt's chunk of 2048 rows of 64 heads over 16384 keys 700
+// us, 1.67 PFLOP/s (85 % of the measured product rate); 32 sessions of 15 rows over up to 16384 keys
+// 235 us, 6.4 TB/s; one row of 32 heads over 131072 keys 88 us, 6.1 TB/s.  A round of few keys is
+// bound by a chain of latencies: lengths, table, keys, scores, weights, result, join (14 us for one
+// row of 64 heads over 4096 keys).  Runs are short where windows are, and then the code of their ends
+// and masks is fetched anew each time: loops there are kept short rather than unrolled.
 #include "attend_common.cuh"
 
 namespace kda {
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 bar_wait_long(gave_up, q_full, (asked - 1) & 1, true);
         } else if (warp == MMA_WARP) {
             // The whole warp walks; one lane issues.  One warp for both groups: with a warp each, their
-            // products ran into each other (a prompt's chunk took 1078 us for 828).
+            // products ran into each other (a prompt's chunk took 1078 us for 828 then).
             constexpr uint32_t SCORES = product_desc(BF16, KT, KT, false), VALUES = product_desc(BF16, KT, D, true);
             const uint32_t acc = uniform(tmem);
             uint32_t done = 0;  // bit g: the phase of group g's weights
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         const float f = m == used ? 1.0f : ex2((used - m) * w.c);
                         l *= f;
                         used = m;
-#pragma unroll 1  // with the result's loop: a window prompt's chunk 93 us for 86, 8 rows over 32768 keys 38 for 36
+#pragma unroll 1
                         for (int k = 0; k < D; k += 32) {
                             uint32_t o[32];
                             tmem_ld32(o_at + k, o);
@@ -654,8 +655,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 const float inv = r.whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
                 f0 *= inv;
                 f1 *= inv;
-#pragma unroll 1  // short code: what is fetched once a run is waited for (see the sums' rescaling)
-                for (int k = 0; k < D; k += 32) {
+#pragma unroll 1  // code that runs once a run is waited for: short (with the rescaling's loop 93 us for 86,
+                for (int k = 0; k < D; k += 32) {  // a window prompt's chunk)
                     uint32_t o[32];
                     tmem_ld32(o_at + k, o);
                     tmem_wait_ld();

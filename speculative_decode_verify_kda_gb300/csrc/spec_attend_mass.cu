@@ -11,7 +11,7 @@
 // column of constants: read from shared memory by every thread it bound the kernel (128 bytes a cycle,
 // as do the reads of tensor memory).  Bound by the keys' bytes for a verify round's rows (61 us for 16
 // sessions of 8 rows of 64 heads over up to 16384 keys, 5.6 TB/s), by exp2 and the reads of tensor
-// memory for a prompt's (70 us for 1024 rows of 32 heads over 8192 keys, 1.04 PFLOP/s).
+// memory for a prompt's (67 us for 1024 rows of 32 heads over 8192 keys, 1.1 PFLOP/s).
 #include "attend_common.cuh"
 
 namespace kda {
