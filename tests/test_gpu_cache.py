@@ -301,3 +301,52 @@ def test_rounds_together(window, sinks):
                             assert abs(x - y) < 1e-3
                     text[b][h] = [text[b][h][j] for j in at]
         assert int(status) == 0
+
+
+@pytest.mark.parametrize("T,window", [(3, 0), (40, 100)])
+def test_captured_rounds_are_the_eager_ones(T, window):
+    """Append, attention, masses, the accept's lengths and an eviction in place as one graph: its replays
+    leave the bits that the same calls leave one by one."""
+    def state():
+        c = Case([400, 37, 0], T=T, Hq=8, Hkv=2, t_rows=[T, T - 1, 0], window=window, sinks=4 if window else 0, seed=T,
+                 cols=64)
+        for x in (c.k, c.v):  # an eviction moves what a window has hidden too
+            x.nan_to_num_(0.5)
+        mass = torch.rand((3, 2, c.cache().capacity), generator=torch.Generator().manual_seed(3)).cuda()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        return c, mass, status
+
+    def calls(c, mass, status, stream):
+        kw = {"dev_status": status, "stream": stream}
+        append = kb.CacheAppendPlan(c.cache(), c.k_rows, c.v_rows, t_rows=c.t_rows, **kw)
+        attend = kb.AttendPlan(c.cache(), c.q, **c.see(), **kw)
+        weigh = kb.AttendMassPlan(c.cache(), c.q, attend.out[1], mass, **c.see(), **kw)
+        evict = kb.CacheEvictPlan(c.cache(), mass, 390, 50, 4, mass_out=mass, lens_out=c.lens, **kw)
+
+        def step():
+            append()
+            attend()
+            weigh()
+            c.lens.add_(c.t_rows)
+            evict()
+        return attend, evict, step
+
+    side = torch.cuda.Stream()
+    one, two = state(), state()
+    attend1, evict1, eager = calls(*one, None)
+    attend2, evict2, captured = calls(*two, side)
+    for plan in (attend1, attend2):
+        for x in plan.out:
+            x.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        captured()
+    for _ in range(4):
+        eager()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((one[0].k, one[0].v, one[1], one[0].lens, one[2], *attend1.out, evict1.out[0]),
+                        (two[0].k, two[0].v, two[1], two[0].lens, two[2], *attend2.out, evict2.out[0])):
+            assert torch.equal(x.contiguous().view(torch.int16), y.contiguous().view(torch.int16))
+    assert int(one[2]) == 0 and one[0].lens.tolist() == [390, 37 + 4 * (T - 1), 0]
