@@ -688,7 +688,8 @@ int spec_distill_step(const void *logits, int logit_dtype, int N, int V, long lo
  *   k, v    [pages][Hkv][page][D] in any order of the first three (page_stride,
  *           head_stride, slot_stride, in elements, the same for both; D is dense), dtype
  *           KDA_BF16 or KDA_F16.  Base addresses and strides are multiples of 16 bytes.
- *           D is 64 or 128, page a power of two in 8..1024.
+ *           D is 64 or 128, page a power of two in 8..1024, Hkv at most 65535, table_cols *
+ *           page at most KDA_CACHE_MAX; B * T of a call and B * Hkv fit in 32 bits.
  *   table   int32 [B][table_cols]: token j of session b lies in page table[b][j / page],
  *           slot j % page.  Only entries of tokens that a call reads or writes are looked
  *           at; of those, ids outside 0..pages-1 set KDA_ST_BADPAGE, read as zeros and are
@@ -777,7 +778,8 @@ int spec_attend_mass(const kda_cache *cache, const void *q, int T, int Hq, long 
  *   dst_table int32 [B][dst_cols] (dst_cols * page >= budget): pages that receive the
  *     tokens, none of them in any session's table; NULL: the session's own pages, in place.
  * budget >= 1, sinks + recent <= budget, budget <= table_cols * page.  A session left
- * untouched has kept -1.
+ * untouched has kept -1, its lens_out and mass_out stay as they were.  Two sessions that share
+ * pages (a common beginning) may be read by the other calls but not be cut in place.
  */
 int spec_cache_evict(const kda_cache *cache, const float *mass, long long ld_mass, int budget, int recent, int sinks,
                      const int *dst_table, int dst_cols, int *kept, float *mass_out, long long ld_mass_out,
