@@ -37,11 +37,13 @@ constexpr int THREADS = 384;         // two groups of 128 and four warps more
 // Registers are handed from the last four warps to the groups (a row of 128 scores is held in
 // them): 256 x 216 + 128 x 72 = 384 x 168, what the launch has.
 constexpr int GROUP_REGS = 216, OTHER_REGS = 72;
-constexpr int SPARE = 2816;          // barriers and what the warps tell each other
 // The running maximum that weights are taken against follows the true one only when it falls
 // behind by more than this many powers of two: weights stay below 2^8, and the sums in tensor
 // memory are seldom rescaled.
 constexpr float LAG = 8.0f;
+
+// Barriers and what the warps tell each other.
+__host__ __device__ constexpr int spare_bytes(int D) { return D == 128 ? 3072 : 3200; }
 
 // Tiles in shared memory: two of rows for two groups' rows, else one.
 __host__ __device__ constexpr int row_tiles(bool pair) { return pair ? 2 : 1; }
@@ -49,7 +51,7 @@ __host__ __device__ constexpr int key_stages(int D, bool pair) { return D == 128
 __host__ __device__ constexpr int value_stages(int D) { return D == 128 ? 2 : 4; }
 __host__ __device__ constexpr int shared_bytes(int D, bool pair)
 {
-    return (row_tiles(pair) + key_stages(D, pair) + value_stages(D)) * tile_bytes(D) + SPARE;
+    return (row_tiles(pair) + key_stages(D, pair) + value_stages(D)) * tile_bytes(D) + spare_bytes(D);
 }
 
 // Keys of a run that only some rows see and whose values are not finite: bit j - (n + t0) of the
@@ -81,6 +83,10 @@ __device__ __forceinline__ void highest(float (&top)[4], const uint32_t *s)
         top[k / 2 & 3] = max3(top[k / 2 & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
 }
 
+constexpr int RUNS = 16;  // records of the walk that are held
+constexpr int BARS = 448; // bytes of barriers
+static_assert(RUNS >= 6 + 3, "key stages, the products' run, the groups' run before it, and the next");
+
 // Where a CTA's share of the tiles begins.
 struct Share {
     Unit u;
@@ -89,7 +95,7 @@ struct Share {
 };
 
 // The runs of one unit's tiles after another within a share.
-struct Runs {
+struct alignas(8) Runs {
     Unit u;
     int left;            // tiles from this run on
     int pair, slot;
@@ -192,18 +198,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     auto o_full = [&](int g) { return more(10 + g); };
     const uint32_t drained = more(12), told = more(13), joined = more(14);
     auto v_clean = [&](int s) { return more(15 + s); };
+    auto known = [&](int i) { return more(15 + VS + i); };  // a run of the walk
     // behind the barriers
-    unsigned char *spare = raw + (bars - base) + 320;
+    unsigned char *spare = raw + (bars - base) + BARS;
     volatile int *gave_up = reinterpret_cast<volatile int *>(spare);
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(spare + 4);
     int *part = reinterpret_cast<int *>(spare + 16);                         // [12]
     Share *found = reinterpret_cast<Share *>(spare + 64);
     float2 *other = reinterpret_cast<float2 *>(spare + 128);                 // [128]: the other group's statistics
-    Runs *runs = reinterpret_cast<Runs *>(spare + 128 + 1024);               // [12]: a warp's
-    Poison *poison = reinterpret_cast<Poison *>(runs + THREADS / 32);        // [HELD]
+    Runs *runs = reinterpret_cast<Runs *>(spare + 128 + 1024);               // [RUNS + 1]: the walk, the last the walker's
+    Poison *poison = reinterpret_cast<Poison *>(runs + RUNS + 1);            // [HELD]
     constexpr int HELD = held_runs(D);
-    static_assert(8 * (2 * ST + 15 + VS) <= 320 && sizeof(Share) <= 64 &&
-                      320 + 128 + 1024 + THREADS / 32 * sizeof(Runs) + HELD * sizeof(Poison) <= SPARE,
+    static_assert(8 * (2 * ST + 15 + VS + RUNS) <= BARS && sizeof(Share) <= 64 && sizeof(Runs) == 64 &&
+                      BARS + 128 + 1024 + (RUNS + 1) * sizeof(Runs) + HELD * sizeof(Poison) <= spare_bytes(D),
                   "room behind the ring");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -222,6 +229,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
         for (int s = 0; s < VS; ++s)
             bar_init(v_clean(s), 1);
+        for (int i = 0; i < RUNS; ++i)
+            bar_init(known(i), 1);
         bar_init(q_full, 1);
         bar_init(q_empty, 1);
         bar_init(drained, 1);
@@ -251,18 +260,30 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     int nth = 0;        // runs before this one
     bool dead = false;  // a wait gave up: nothing more is issued
 
-    // a warp's walk lies in shared memory: registers are short everywhere
-    Runs &r = runs[warp];
-    if (lane == 0)
-        r = Runs(*found);
+    // The key warp walks, the others follow its records: short code, and no wait for lengths between
+    // two runs.  The key warp is at most its stages ahead of the products, and those a run ahead of
+    // the slowest group: a record has been read before its place is taken again.
+    const Runs *r = runs;
     auto next_run = [&] {
-        bool on = false;
+        r = runs + nth % RUNS;
+        return warp_wait(gave_up, known(nth % RUNS), nth / RUNS & 1) && r->todo > 0;
+    };
+    auto walk_on = [&] {
+        Runs *walk = runs + RUNS;
+        r = runs + nth % RUNS;
+        if (lane == 0) {
+            if (nth == 0)
+                *walk = Runs(*found);
+            if (!walk->next(w))
+                walk->todo = 0;
+        }
+        __syncwarp();
+        if (lane < 16)
+            reinterpret_cast<int *>(runs + nth % RUNS)[lane] = reinterpret_cast<const int *>(walk)[lane];
         __syncwarp();
         if (lane == 0)
-            on = r.next(w);
-        on = __any_sync(0xffffffffu, on);
-        __syncwarp();
-        return on;
+            bar_arrive(known(nth % RUNS));
+        return r->todo > 0;
     };
 
     if (warp >= 8) {
@@ -273,39 +294,39 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             const int first = keys ? 0 : KS, count = keys ? KS : VS;
             int stage = 0;
             uint32_t phase = 0;
-            auto key_of = [&](int i) { return tile_key(r.u, r.off + i); };
-            auto look = [&](int i) { return i < r.todo ? page_of(w, r.u, key_of(i)) : 0; };
+            auto key_of = [&](int i) { return tile_key(r->u, r->off + i); };
+            auto look = [&](int i) { return i < r->todo ? page_of(w, r->u, key_of(i)) : 0; };
             uint32_t copied = 0, asked = 0;  // tiles, and rows
             auto load_rows = [&] {
                 if (!warp_wait(gave_up, q_empty, (nth & 1) ^ 1))
                     dead = true;
-                const bool two = PAIR && r.u.nt > w.TT;
+                const bool two = PAIR && r->u.nt > w.TT;
                 asked += !dead;
                 if (!dead && lane == 0) {
                     bar_expect(q_full, (two ? 2u : 1u) * w.TT * w.a.G * D * 2);
                     for (int x = 0; x <= two; ++x)
                         for (int half = 0; half < HALVES; ++half)
-                            copy_3d(q_at + x * TILE + half * HALF, &map_q, half * 64, r.h * w.a.G,
-                                    r.u.b * w.a.T + r.u.t0 + x * w.TT, q_full);
+                            copy_3d(q_at + x * TILE + half * HALF, &map_q, half * 64, r->h * w.a.G,
+                                    r->u.b * w.a.T + r->u.t0 + x * w.TT, q_full);
                 }
                 __syncwarp();
             };
             Cut cut{};  // what the second launch has to join
-            while (next_run()) {
-                if (r.todo == r.left && r.off == 0 && !r.whole)
-                    cut = Cut{1 + (r.u.count - r.todo - 1) / found->per + 1, r.slot, r.u.b, r.u.t0, r.u.nt, r.h, {}};
+            while (!dead && (keys ? walk_on() : next_run())) {
+                if (r->todo == r->left && r->off == 0 && !r->whole)
+                    cut = Cut{1 + (r->u.count - r->todo - 1) / found->per + 1, r->slot, r->u.b, r->u.t0, r->u.nt, r->h, {}};
                 int id = look(0);
                 // the rows before the first keys, which keep the memory busy; behind them where the
                 // rows of the run before may still be read
                 const bool early = nth == 0;
                 if (keys && early)
                     load_rows();
-                for (int i = 0; i < r.todo; ++i) {
+                for (int i = 0; i < r->todo; ++i) {
                     const int next = look(i + 1);  // on its way while this tile is copied
                     if (!warp_wait(gave_up, empty(first + stage), phase ^ 1))
                         dead = true;
                     if (!dead) {
-                        copy_tile<D>(w, r.u, r.h, key_of(i), id, m, ring + (first + stage) * TILE, full(first + stage));
+                        copy_tile<D>(w, r->u, r->h, key_of(i), id, m, ring + (first + stage) * TILE, full(first + stage));
                         ++copied;
                     }
                     if (++stage == count) {
@@ -313,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         phase ^= 1;
                     }
                     id = next;
-                    if (keys && !early && i == min(LEAD, r.todo) - 1)
+                    if (keys && !early && i == min(LEAD, r->todo) - 1)
                         load_rows();
                 }
                 ++nth;
@@ -362,8 +383,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     mma_commit(o_full(g));
             };
             while (next_run()) {
-                const int todo = uniform(r.todo), lead = PAIR ? 0 : seq & 1;
-                const bool two = uniform(r.u.nt > w.TT);
+                const int todo = uniform(r->todo), lead = PAIR ? 0 : seq & 1;
+                const bool two = uniform(r->u.nt > w.TT);
                 wait(q_full, nth & 1);
                 for (int i = 0; i < min(LEAD, todo); ++i) {
                     wait(full(key.stage), key.phase);
@@ -437,13 +458,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             Ring<VS> at;
             const int line = lane >> 3, chunk = lane & 7;  // 8 lanes a row, 4 rows at a time
             while (next_run()) {
-                const Unit u = r.u;
+                const Unit u = r->u;
                 Poison &p = poison[nth % HELD];
                 if (lane < 17)
                     (lane == 0 ? p.any : p.bits[(lane - 1) & 15]) = 0;
                 __syncwarp();
-                for (int i = 0; i < r.todo; ++i) {
-                    const int j0 = tile_key(u, r.off + i);
+                for (int i = 0; i < r->todo; ++i) {
+                    const int j0 = tile_key(u, r->off + i);
                     warp_wait(gave_up, full(KS + at.stage), at.phase);
                     if (is_edge(w, u, j0)) {
                         unsigned char *tile = raw + (ring_v + at.stage * TILE - base);
@@ -522,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const int rt = row / w.a.G, rg = row - rt * w.a.G;
         uint32_t done = 0, joins = 0;
         while (next_run()) {
-            const Unit &u = r.u;
+            const Unit &u = r->u;
             const int t = (PAIR ? g * w.TT : 0) + rt;  // of the unit's rows
             const bool live = rt < w.TT && t < u.nt;
             const bool busy = __any_sync(0xffffffffu, live);
@@ -530,9 +551,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             const int p_low = w.a.seen.window ? max(0, p - w.a.seen.window + 1) : 0;
             // tiles alternate over all runs; the group with a run's first tile leads it
             const int lead = PAIR ? 0 : seq & 1, first = PAIR ? 0 : g ^ lead;
-            const int tiles = PAIR ? r.todo : (r.todo + 1 - first) / 2;
+            const int tiles = PAIR ? r->todo : (r->todo + 1 - first) / 2;
             float m = -INFINITY, used = -INFINITY, l = 0.0f;
-            auto key_of = [&](int i) { return tile_key(u, r.off + i); };
+            auto key_of = [&](int i) { return tile_key(u, r->off + i); };
             for (int x = 0; x < tiles; ++x) {
                 const int i = PAIR ? x : 2 * x + first;
                 const int j0 = key_of(i);
@@ -618,7 +639,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 warp_wait(gave_up, o_full(g), (done + tiles - 1) & 1);
             done += tiles;
             fence_after();
-            const bool join = !PAIR && r.todo > 1;
+            const bool join = !PAIR && r->todo > 1;
             float f0 = 1.0f, f1 = 0.0f;
             if (join && g != lead) {
                 other[row] = make_float2(used, l);
@@ -649,10 +670,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     }
             __syncwarp();
             if (busy && (PAIR || g == lead) && !__any_sync(0xffffffffu, *gave_up)) {
-                const int hq = r.h * w.a.G + rg;
+                const int hq = r->h * w.a.G + rg;
                 const long long to = (static_cast<long long>(u.b) * w.a.T + u.t0 + t) * w.a.Hq + hq;
-                const long long slot = static_cast<long long>(r.slot) * (PAIR ? 2 * KT : KT) + (PAIR ? g * KT : 0) + row;
-                const float inv = r.whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+                const long long slot = static_cast<long long>(r->slot) * (PAIR ? 2 * KT : KT) + (PAIR ? g * KT : 0) + row;
+                const float inv = r->whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
                 f0 *= inv;
                 f1 *= inv;
 #pragma unroll 1  // code that runs once a run is waited for: short (with the rescaling's loop 93 us for 86,
@@ -675,7 +696,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             o[e] = 0x7fc00000u;
-                    if (live && r.whole) {
+                    if (live && r->whole) {
                         uint32_t x[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
@@ -689,9 +710,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     }
                     __syncwarp();
                 }
-                if (live && r.whole && w.a.lse)
+                if (live && r->whole && w.a.lse)
                     w.a.lse[to] = l == 0.0f ? -INFINITY : (used * w.c + log2f(l)) * LN2;
-                if (live && !r.whole)
+                if (live && !r->whole)
                     w.stats[slot] = make_float2(used, l);
             }
             if (join) {  // the other group's sums and statistics have been read
@@ -706,7 +727,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                 }
                 ++joins;
             }
-            seq += r.todo;
+            seq += r->todo;
             ++nth;
         }
     }
