@@ -18,8 +18,8 @@
 // Rounded to 16 bits: the weights (as an operand of the products must be) and the results.  Weights
 // are taken against a maximum that is at most 2^8 too small, their sum is of the unrounded ones.
 //
-// Measured on GB300 (in a CUDA graph): a prompt's chunk of 2048 rows of 64 heads over 16384 keys 700
-// us, 1.67 PFLOP/s (85 % of the measured product rate); 32 sessions of 15 rows over up to 16384 keys
+// Measured on GB300 (in a CUDA graph): a prompt's chunk of 2048 rows of 64 heads over 16384 keys 686
+// us, 1.7 PFLOP/s (87 % of the measured product rate); 32 sessions of 15 rows over up to 16384 keys
 // 235 us, 6.4 TB/s; one row of 32 heads over 131072 keys 88 us, 6.1 TB/s.  A round of few keys is
 // bound by a chain of latencies: lengths, table, keys, scores, weights, result, join (14 us for one
 // row of 64 heads over 4096 keys).  Runs are short where windows are, and then the code of their ends
@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     bool dead = false;  // a wait gave up: nothing more is issued
 
     // The key warp walks, the others follow its records: short code, and no wait for lengths between
-    // two runs.  The key warp is at most its stages ahead of the products, and those a run ahead of
-    // the slowest group: a record has been read before its place is taken again.
+    // two runs (each warp's own walk took the prompt's chunk 699 us for 686, a window's 77 for 75).  The
+    // key warp is at most its stages ahead of the products, and those a run ahead of the slowest
+    // group: a record has been read before its place is taken again.
     const Runs *r = runs;
     auto next_run = [&] {
         r = runs + nth % RUNS;
@@ -670,10 +671,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     }
             __syncwarp();
             if (busy && (PAIR || g == lead) && !__any_sync(0xffffffffu, *gave_up)) {
+                const bool whole = r->whole;
                 const int hq = r->h * w.a.G + rg;
                 const long long to = (static_cast<long long>(u.b) * w.a.T + u.t0 + t) * w.a.Hq + hq;
                 const long long slot = static_cast<long long>(r->slot) * (PAIR ? 2 * KT : KT) + (PAIR ? g * KT : 0) + row;
-                const float inv = r->whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+                const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
                 f0 *= inv;
                 f1 *= inv;
 #pragma unroll 1  // code that runs once a run is waited for: short (with the rescaling's loop 93 us for 86,
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             o[e] = 0x7fc00000u;
-                    if (live && r->whole) {
+                    if (live && whole) {
                         uint32_t x[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
@@ -710,9 +712,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     }
                     __syncwarp();
                 }
-                if (live && r->whole && w.a.lse)
+                if (live && whole && w.a.lse)
                     w.a.lse[to] = l == 0.0f ? -INFINITY : (used * w.c + log2f(l)) * LN2;
-                if (live && !r->whole)
+                if (live && !whole)
                     w.stats[slot] = make_float2(used, l);
             }
             if (join) {  // the other group's sums and statistics have been read
