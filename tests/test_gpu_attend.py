@@ -205,6 +205,12 @@ def test_a_text_of_sixteen_million_tokens():
     near(lse[0, 1], total, ds + 2.0**-17 + 2.0**-22 * total + lost)
 
 
+@pytest.mark.parametrize("T,G,n,window", [(33, 16, 90, 0), (31, 16, 300, 0), (250, 16, 0, 0), (600, 4, 200, 0),
+                                          (400, 8, 100, 70), (7, 64, 500, 0), (290, 1, 40, 0), (520, 1, 130, 0)])
+def test_many_tiles_of_rows_for_few_keys(T, G, n, window):
+    both(Case([n], T=T, Hq=G, Hkv=1, window=window, sinks=3 if window else 0, seed=T))
+
+
 def test_scores_of_a_wide_range():
     """Scores of hundreds: the running maximum moves far at every tile."""
     run(Case([700], T=3, Hq=8, Hkv=2, q_scale=60.0, seed=2))
