@@ -271,6 +271,26 @@ def test_values_that_only_some_rows_see_reach_those_alone(T, window, at, dtype):
     assert not torch.isfinite(out[:, sees][..., 9]).any()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_that_are_not_finite_in_many_short_sessions(D):
+    """Units of one key tile follow one another in a block: what one marks does not reach the others."""
+    g = torch.Generator().manual_seed(D)
+    B = 700
+    c = Case(torch.randint(0, 120, (B,), generator=g).tolist(), T=3, Hq=4, Hkv=1, D=D, seed=D)
+    bad = torch.rand(B, generator=g) < 0.5
+    for b in bad.nonzero()[:, 0].tolist():  # the second row's own value
+        j = c.n[b] + 1
+        c.v[c.table[b, j // c.page], :, j % c.page, 9] = math.inf
+    want, want_lse, tol, tol_lse = c.attend()
+    for _ in range(3):
+        out, lse = kb.spec_attend(c.cache(), c.q)
+        near(lse, want_lse, tol_lse)
+        out = out.cpu()
+        near(out[~bad], want[~bad], tol[~bad])
+        near(out[bad][:, :1], want[bad][:, :1], tol[bad][:, :1])
+        assert not torch.isfinite(out[bad][:, 1:, :, 9]).any()
+
+
 def test_keys_that_only_later_rows_see_do_not_reach_earlier_ones():
     c = Case([130], T=3, Hq=4, Hkv=1, seed=9)
     j = 131
