@@ -1220,17 +1220,33 @@ class AttendPlan(_QueryPlan):
 
 
 class AttendMassPlan(_QueryPlan):
-    """spec_attend_mass for fixed tensors: q as AttendPlan's, lse f32 [B][T][Hq] as it gave it,
-    mass f32 [B][Hkv][cache.capacity or more], which a call updates and returns."""
+    """spec_attend_mass for fixed tensors: q as AttendPlan's, lse f32 [B][T][Hq] as it gave it (of
+    any strides: a call copies one that is not dense), mass f32 [B][Hkv][cache.capacity or
+    more], which a call updates and returns."""
 
     def __init__(self, cache: PagedCache, q, lse, mass, t_rows=None, window: int = 0, sinks: int = 0, scale=None,
                  dev_status=None, stream=None):
         super().__init__("spec_attend_mass", cache, stream)
         query, rows, seen = self._query(q, t_rows, window, sinks, scale)
-        lse = self._in(lse, "lse", torch.float32, (cache.B, self.T, self.Hq))
+        shape = (cache.B, self.T, self.Hq)
+        self._strided = None
+        if isinstance(lse, torch.Tensor) and tuple(lse.shape) == shape and lse.dtype == torch.float32 and \
+                not lse.is_contiguous():
+            self._hold(lse, "lse")
+            self._strided, lse = lse, self._out(None, "lse", torch.float32, shape)
+            self._dense, self._on = lse, _stream(stream)
+        lse = self._in(lse, "lse", torch.float32, shape)
         ptr, ld = self._mass(mass, "mass", cache.capacity)
         self.out = mass
         self._bind(*query, lse, rows, *seen, ptr, ld, self._status(dev_status))
+
+    def __call__(self):
+        if self._strided is not None:
+            if self._device is not None:
+                self._check_device()
+            with _stream_pool(self._on):
+                self._dense.copy_(self._strided)
+        return super().__call__()
 
 
 class CacheEvictPlan(_CachePlan):

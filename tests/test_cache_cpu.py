@@ -169,6 +169,14 @@ def test_the_binding_refuses_rows(L):
                           lens_out=fake(2, dtype=torch.int32), stream=0)
 
 
+def test_the_binding_refuses_an_lse_of_another_shape_or_type(L):
+    c, q = paged(), fake(2, 3, 4, 128, dtype=torch.bfloat16)
+    for lse in (fake(2, 4, 3), fake(2, 4, 4).transpose(1, 2), fake(2, 4, 3, dtype=torch.float64).transpose(1, 2),
+                torch.empty(2, 4, 3).transpose(1, 2)):
+        with pytest.raises((TypeError, ValueError)):
+            kb.AttendMassPlan(c, q, lse, fake(2, 2, 64), stream=0)
+
+
 def test_a_plan_is_launched_on_the_device_of_its_tensors(monkeypatch, L):
     """(No sessions: nothing is launched.)"""
     current = [0]

@@ -317,6 +317,30 @@ def test_all_scores_minus_infinity():
     assert torch.all(mass[..., :40] == 1.0) and torch.all(mass[..., 40:42] == 0.0)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(3, 3), (8, 2)])
+def test_mass_with_an_lse_of_any_strides(Hq, Hkv):
+    """Heads before rows in memory, or part of a larger tensor: the bits of a dense lse, also when its
+    values change between a plan's calls."""
+    c = Case([150, 40], T=5, Hq=Hq, Hkv=Hkv, seed=Hq)
+    _, lse = kb.spec_attend(c.cache(), c.q)
+    turned = lse.transpose(1, 2).contiguous().transpose(1, 2)
+    wide = torch.full((2, 5, Hq + 3), math.nan, device="cuda")
+    wide[:, :, 2:2 + Hq] = lse
+    want = kb.spec_attend_mass(c.cache(), c.q, lse, torch.zeros((2, Hkv, c.cache().capacity), device="cuda"))
+    for x in (turned, wide[:, :, 2:2 + Hq]):
+        assert not x.is_contiguous()
+        mass = torch.zeros_like(want)
+        plan = kb.AttendMassPlan(c.cache(), c.q, x, mass)
+        plan()
+        assert torch.equal(mass, want)
+        x.add_(1.0)
+        mass.zero_()
+        plan()
+        # exponents of size 64 at most on either side, off by 2^-21 of that
+        near(mass, want.double() / math.e, 2.0**-14 * want)
+        x.sub_(1.0)
+
+
 def test_mass_adds_up():
     """Twice the same rows: twice their shares on the tokens before, once on the rows' own."""
     c = Case([300, 90], T=4, Hq=8, Hkv=2, seed=6)
