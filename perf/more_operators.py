@@ -316,7 +316,6 @@ def _plan(s):
                                  lens_out=s["lens_out"])
     seen = {"t_rows": s["t_rows"], "window": case["window"], "sinks": case["sinks"], "scale": s["scale"]}
     if s["op"] == "mass":
-        s["lse"] = s["lse"].contiguous()  # one query head a kv head: the plain form leaves its heads strided
         return kb.AttendMassPlan(cache, s["q"], s["lse"], s["mass"], **seen)
     return kb.AttendPlan(cache, s["q"], out=s["out"], lse_out=s["lse"], **seen)
 
