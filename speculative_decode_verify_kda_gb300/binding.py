@@ -1045,12 +1045,28 @@ def spec_distill_step(logits, ids, values, grad_loss=None, weight=None, kind: in
 _CACHE_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
 
 
+def _held(name):
+    """A tensor whose address calls were given: it may change in place (``cache.lens += keep``),
+    another one in its place would go unseen and is refused."""
+    def get(self):
+        return self._tensors[name]
+
+    def put(self, t):
+        if t is not self._tensors[name]:
+            raise AttributeError(f"{name} of a PagedCache is the tensor that it was made with: write into that one, "
+                                 "or make another PagedCache and its plans")
+
+    return property(get, put)
+
+
 class PagedCache:
     """Keys and values of one softmax-attention layer in pages: k and v [pages][Hkv][page][D]
     (bfloat16 or float16, D of 64 or 128 dense, page a power of two in 8..1024; any strides of
     the first three dimensions that are the same for both), table int32 [B][columns] of page
-    ids, lens int32 [B] of tokens held.  The tensors are referenced: a round commits its
-    accepted rows with ``cache.lens += keep``."""
+    ids, lens int32 [B] of tokens held.  The tensors are referenced and kept: a round commits
+    its accepted rows with ``cache.lens += keep``, pages enter by writing into ``cache.table``."""
+
+    k, v, table, lens = (_held(name) for name in ("k", "v", "table", "lens"))
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
         for t, name in ((k, "k"), (v, "v")):
@@ -1076,7 +1092,7 @@ class PagedCache:
                 raise ValueError(f"{name} must be on {k.device}")
         # the stride of a dimension of one element says nothing
         step = [d if n == 1 else s for n, s in zip(k.shape, k.stride())]
-        self.k, self.v, self.table, self.lens = k, v, table, lens
+        self._tensors = {"k": k, "v": v, "table": table, "lens": lens}
         self.B, self.Hkv, self.D, self.page, self.pages, self.columns = b, hkv, d, page, pages, cols
         self.capacity = cols * page
         self.device, self.dtype = k.device, k.dtype

@@ -148,6 +148,21 @@ def test_the_binding_takes_strides():
     assert (one.page_stride, one.head_stride, one.slot_stride) == (16 * 128, 128, 128)
 
 
+@pytest.mark.parametrize("name", ["k", "v", "table", "lens"])
+def test_a_caches_tensors_stay_the_ones_it_was_made_with(name):
+    c = paged(v=fake(8, 2, 16, 128, dtype=torch.bfloat16))
+    first = getattr(c, name)
+    with pytest.raises(AttributeError, match=name):
+        setattr(c, name, first[:])
+    with pytest.raises(AttributeError):
+        delattr(c, name)
+    assert getattr(c, name) is first
+    setattr(c, name, first)
+    c.lens += fake(2, dtype=torch.int32)
+    c.table[0, 1] = 3
+    assert getattr(c, name) is first
+
+
 def test_the_binding_refuses_rows(L):
     c, bf = paged(), torch.bfloat16
     kw = dict(out=fake(2, 3, 4, 128, dtype=bf), lse_out=fake(2, 3, 4), workspace=fake(16, dtype=torch.uint8), stream=0)
