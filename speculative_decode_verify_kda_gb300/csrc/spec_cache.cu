@@ -510,6 +510,9 @@ extern "C" int spec_cache_evict(const kda_cache *cache, const float *mass, long 
         return fail(KDA_EINVAL, "ld_mass_out must be at least the budget");
     if (static_cast<long long>(a.c.B) * a.c.Hkv > 0x7fffffffll)
         return fail(KDA_EINVAL, "B * Hkv must fit in 32 bits");
+    const int chunks = (budget + MOVE_ROWS - 1) / MOVE_ROWS + 1;  // of a head, with other pages
+    if (dst_table && static_cast<long long>(a.c.B) * a.c.Hkv * chunks > 0x7fffffffll)
+        return fail(KDA_EINVAL, "too many rows for one launch");
     if (a.c.B == 0)
         return ok();
     if (!mass || !kept || !lens_out)
@@ -552,9 +555,6 @@ extern "C" int spec_cache_evict(const kda_cache *cache, const float *mass, long 
     if (!dst_table)
         return pages::launch(evict_in_place_kernel, dim3(heads, 2 * a.c.D / 32 + 1), MOVE_T, 0, stream,
                              "evict_in_place_kernel", a);
-    const int chunks = (budget + MOVE_ROWS - 1) / MOVE_ROWS + 1;
-    if (static_cast<long long>(heads) * chunks > 0x7fffffffll)
-        return fail(KDA_EINVAL, "too many rows for one launch");
     return pages::launch(a.c.D == 128 ? evict_move_kernel<128> : evict_move_kernel<64>, dim3(heads * chunks), MOVE_T, 0,
                          stream, "evict_move_kernel", a, chunks);
 }

@@ -112,6 +112,12 @@ def test_more_tiles_than_a_call_counts_are_refused(L):
     assert mass(L, many, T=1, Hq=64, ld=64 * 128, ld_mass=2**20) == kb.EINVAL and b"tiles" in L.kda_last_error()
 
 
+def test_more_rows_than_a_launch_moves_are_refused(L):
+    """(Before the first of the two launches: without a device that one would be KDA_ECUDA.)"""
+    many = cache(B=2**15, Hkv=2**15, table_cols=8)
+    assert evict(L, many, ld=128, budget=128, dst=FAKE, cols=8) == kb.EINVAL and b"rows" in L.kda_last_error()
+
+
 def test_no_rows_are_nothing_to_do(L):
     assert append(L, cache(), T=0, k=None, v=None) == kb.OK
     assert attend(L, cache(), T=0, q=None, out=None, work=None, size=0) == kb.OK
