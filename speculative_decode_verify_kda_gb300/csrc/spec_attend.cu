@@ -41,6 +41,12 @@ constexpr int GROUP_REGS = 216, OTHER_REGS = 72;
 // behind by more than this many powers of two: weights stay below 2^8, and the sums in tensor
 // memory are seldom rescaled.
 constexpr float LAG = 8.0f;
+// f16 ends at 2^-24: its weights, and with them their sum, are held 2^7 times as large, up to 2^15, and one
+// is off by 2^-32 of the largest at most.  (With 2^-25, the small weights of a long text behind a strong key
+// were missing from the result and not from the sum.  A lag of 4 and 2^11 took 1 % longer for a prompt's
+// chunk, 3 % for a window's; this takes no time.)
+template <bool BF16>
+constexpr float LIFT = BF16 ? 0.0f : 7.0f;
 
 // Barriers and what the warps tell each other.
 __host__ __device__ constexpr int spare_bytes(int D) { return D == 128 ? 3072 : 3200; }
@@ -605,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                         }
                     }
                     const float off = used == -INFINITY ? 0.0f : used * w.c;
-                    const Two cc = two(w.c, w.c), minus = two(-off, -off);
+                    const Two cc = two(w.c, w.c), minus = two(LIFT<BF16> - off, LIFT<BF16> - off);
                     Two sum[2] = {two(0.0f, 0.0f), two(0.0f, 0.0f)};
 #pragma unroll
                     for (int k = 0; k < KT; k += 32) {
@@ -715,7 +721,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                     __syncwarp();
                 }
                 if (live && whole && w.a.lse)
-                    w.a.lse[to] = l == 0.0f ? -INFINITY : (used * w.c + log2f(l)) * LN2;
+                    w.a.lse[to] = l == 0.0f ? -INFINITY : (used * w.c + log2f(l) - LIFT<BF16>) * LN2;
                 if (live && !whole)
                     w.stats[slot] = make_float2(used, l);
             }
@@ -824,7 +830,7 @@ __global__ void __launch_bounds__(JOIN_T) attend_join_kernel(const __grid_consta
     for (int e = 0; e < E; e += 2)
         dst[e / 2] = pack<BF16>(o[e] * inv, o[e + 1] * inv);
     if (lane == 0 && w.a.lse)
-        w.a.lse[to] = l == 0.0f ? -INFINITY : (top * w.c + log2f(l)) * LN2;
+        w.a.lse[to] = l == 0.0f ? -INFINITY : (top * w.c + log2f(l) - LIFT<BF16>) * LN2;
 }
 
 // More than 128 rows of a session and kv head fill two tiles.  As two units of one tile, which read the

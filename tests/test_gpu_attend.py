@@ -232,6 +232,33 @@ def test_rising_scores():
         run(c)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_many_small_weights_behind_a_strong_key(dtype):
+    """The first of 2^18 keys scores 14.5 above the rest, which hold an eighth of the weight together;
+    each alone is 8.5 steps of f16's least.  A session a CTA, so that all of it is one running sum."""
+    N, D, B, gap = 2**18, 64, 152, 14.4921875
+    g = torch.Generator().manual_seed(1)
+    k, v = torch.zeros((2, 2, 1, 1024, D))
+    k[0, 0, 0, 0] = gap
+    v.copy_(1.0 + 0.1 * torch.randn(v.shape, generator=g))
+    v[0, 0, 0] = 0.0
+    k, v = k.to(dtype), v.to(dtype)
+    q = torch.zeros((B, 1, 1, D), dtype=dtype)
+    q[..., 0] = D**0.5
+    table = torch.ones((B, N // 1024), dtype=torch.int32)
+    table[:, 0] = 0
+    cache = kb.PagedCache(k.cuda(), v.cuda(), table.cuda(), torch.full((B,), N - 1, dtype=torch.int32, device="cuda"))
+    out, lse = kb.spec_attend(cache, q.cuda())
+    strong = math.exp(float(k[0, 0, 0, 0]))
+    total = strong + N - 1
+    o = (v[0].double().sum(1) + (N // 1024 - 1) * v[1].double().sum(1))[None, None] / total
+    # weights and result rounded to the type; f16's small weights off by 2^-32; sums of N / 16 steps, each
+    # off by an ulp at most
+    u, sums = torch.finfo(dtype).eps / 2, N / 16 * 2.0**-23
+    near(out, o.expand(out.shape), (2 * u + 2.0**-17 + sums) * o.expand(out.shape) * (1 + u) + 2.0**-32 * N)
+    near(lse, torch.full(lse.shape, math.log(total)), torch.full(lse.shape, 2.0**-17 + 2.0**-18 + sums))
+
+
 def test_scale():
     c = Case([100], T=2)
     c.scale = 0.02
