@@ -104,6 +104,10 @@ struct Share {
     int pair, h, off;
 };
 
+// The unit to look at behind unit i: a session's first one without rows is followed by others without,
+// thousands where a session decodes beside another's prompt.
+__device__ __forceinline__ int after(const Walk &w, const Unit &u, int i) { return u.count > 0 ? i + 1 : (u.b + 1) * w.nq; }
+
 // The runs of one unit's tiles after another within a share.
 struct alignas(8) Runs {
     Unit u;
@@ -127,9 +131,10 @@ struct alignas(8) Runs {
             return false;
         if (h == w.a.c.Hkv) {
             h = 0;
-            do
-                u = unit_of(w, ++pair);
-            while (u.count == 0);
+            do {
+                pair = after(w, u, pair);
+                u = unit_of(w, pair);
+            } while (u.count == 0);
         }
         todo = min(u.count - off, left);
         whole = todo == u.count;
@@ -146,7 +151,7 @@ __device__ __forceinline__ void share_of(const Walk &w, int *part, Share *found)
     const int i0 = tid * each, i1 = min(P, i0 + each);
     Unit u;
     int mine = 0;
-    for (int i = i0; i < i1; ++i) {
+    for (int i = i0; i < i1; i = after(w, u, i)) {
         u = unit_of(w, i);
         mine += u.count * w.a.c.Hkv;
     }
@@ -174,7 +179,7 @@ __device__ __forceinline__ void share_of(const Walk &w, int *part, Share *found)
     if (first < last && before <= first && first < before + mine) {
         int i = i1 - 1;
         if (each > 1)
-            for (i = i0;; ++i) {
+            for (i = i0;; i = after(w, u, i)) {
                 u = unit_of(w, i);
                 if (first < before + u.count * w.a.c.Hkv)
                     break;

@@ -137,6 +137,37 @@ def test_anywhere_in_the_range(seed):
               layout=r.choice(("hnd", "nhd", "paired")), fused=r.random() < 0.5, seed=seed))
 
 
+def test_sessions_of_one_row_in_a_call_of_many():
+    """A decode step beside room for a prompt's chunk: 65535 units of two tokens without rows lie between two
+    sessions with one.  They cost a few dozen microseconds, not milliseconds."""
+    B, T, H, D, n = 3, 2**17, 128, 64, 30100
+    g = torch.Generator("cuda").manual_seed(2)
+    cols = n // 1024 + 1
+    k, v = torch.randn((2, B * cols, 1, 1024, D), generator=g, device="cuda", dtype=BF16)
+    table = torch.arange(B * cols, dtype=torch.int32, device="cuda").view(B, cols)
+    cache = kb.PagedCache(k, v, table, torch.full((B,), n - 1, dtype=torch.int32, device="cuda"))
+    q = torch.empty((B, T, H, D), dtype=BF16, device="cuda")
+    q[:, 0] = torch.randn((B, H, D), generator=g, device="cuda", dtype=BF16)
+    plan = kb.AttendPlan(cache, q, t_rows=torch.ones(B, dtype=torch.int32, device="cuda"))
+    best = math.inf
+    for _ in range(4):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        out, lse = plan()
+        end.record()
+        end.synchronize()
+        best = min(best, start.elapsed_time(end))
+    kd, vd = (x.double().view(B, -1, D)[:, :n] for x in (k, v))
+    s = torch.einsum("bhd,bnd->bhn", q[:, 0].double(), kd) * D**-0.5
+    total = torch.logsumexp(s, 2)
+    p = (s - total[..., None]).exp()
+    size, u = p @ vd.abs(), torch.finfo(BF16).eps / 2
+    ds = (D + 4) * 2.0**-24 * D**-0.5 * float(q[:, 0].double().norm(dim=-1).max() * kd.norm(dim=-1).max())
+    near(out[:, 0], p @ vd, u * (p @ vd).abs() + (u + 2 * ds + 2.0**-17) * size * (1 + u) + 1e-30)
+    near(lse[:, 0], total, ds + 2.0**-17 + 2.0**-22 * total)
+    assert best < 1.0, f"{best} ms"
+
+
 def test_one_head_shared_by_many_sessions_pages():
     """Sessions that share their first pages, as those of one prompt do."""
     c = Case([160, 160, 160], T=2, Hq=8, Hkv=2, page=32, seed=21)
