@@ -76,11 +76,14 @@ extern "C" {
 #define KDA_ST_BADKEEP 0x2  /* a device keep outside 1..T, or a device row count
                                outside 1..T (the *_var calls); that session is
                                left untouched                                    */
-#define KDA_ST_TIMEOUT 0x4  /* a wait inside the scan kernel ran out (one second:
-                               a bulk copy or a partner warp never arrived); the
-                               CTA stopped early and its units are unfinished.
+#define KDA_ST_TIMEOUT 0x4  /* a wait inside a kernel ran out (one second: a copy, a
+                               product or a partner warp never arrived); the CTA
+                               stopped early and its units are unfinished.
                                kda_verify_scan has no status word: a caller that
-                               wants this report uses kda_verify_scan_var        */
+                               wants this report uses kda_verify_scan_var.
+                               spec_attend, spec_attend_mass: the rows (masses)
+                               that the CTA had a part in are NaN, with a status
+                               word or without one                               */
 /* 0x8 is reserved (no call raises it: the sampled filter is exact for any
    number of ties) */
 #define KDA_ST_BADTOKEN 0x10 /* a token or teacher id of V or more (spec_logprobs,

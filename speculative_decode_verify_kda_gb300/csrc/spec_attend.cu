@@ -191,6 +191,25 @@ __device__ __forceinline__ void share_of(const Walk &w, int *part, Share *found)
     __syncthreads();
 }
 
+// A CTA that gave up: the rows that it had a part in become NaN, here and, where parts are joined, by its
+// parts' statistics.  (By the groups' threads, which have the registers.)
+template <int D, bool PAIR>
+__device__ __noinline__ void spoil(const Walk &w, const Share &found)
+{
+    constexpr int ROWS = PAIR ? 2 * KT : KT, GROUPS = 256;
+    const float nan = __int_as_float(0x7fffffff);
+    for (int i = threadIdx.x; i < 2 * ROWS; i += GROUPS)
+        w.stats[2 * blockIdx.x * ROWS + i] = make_float2(nan, nan);
+    const int G = w.a.G, words = G * D / 2;
+    for (Runs r(found); r.next(w);) {
+        const long long row = (static_cast<long long>(r.u.b) * w.a.T + r.u.t0) * w.a.Hq + r.h * G;
+        for (int i = threadIdx.x; i < r.u.nt * words; i += GROUPS)
+            reinterpret_cast<uint32_t *>(w.a.out + (row + static_cast<long long>(i / words) * w.a.Hq) * D)[i % words] = 0x7fff7fffu;
+        for (int i = threadIdx.x; w.a.lse && i < r.u.nt * G; i += GROUPS)
+            w.a.lse[row + static_cast<long long>(i / G) * w.a.Hq + i % G] = nan;
+    }
+}
+
 template <int D, bool PAIR, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Walk w,
                                                             const __grid_constant__ CUtensorMap map_q,
@@ -251,7 +270,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         bar_init(drained, 1);
         bar_init(told, 4);
         bar_init(joined, 4);
-        *gave_up = 0;
+        *gave_up = stopped();
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
         prefetch_map(&map_q);
@@ -748,8 +767,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
     fence_before();
     __syncthreads();
-    if (tid == 0 && *gave_up)
-        raise(w.a.status, KDA_ST_TIMEOUT);
+    if (warp < 8 && *gave_up) {
+        if (tid == 0)
+            raise(w.a.status, KDA_ST_TIMEOUT);
+        spoil<D, PAIR>(w, *found);
+    }
     if (warp == MMA_WARP) {
         __syncwarp();
         tmem_free<512>(tmem);

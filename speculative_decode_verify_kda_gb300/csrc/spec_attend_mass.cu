@@ -185,6 +185,17 @@ __device__ __forceinline__ void share_of(const Span &w, int *part, Share *found)
     __syncthreads();
 }
 
+// A CTA that gave up: the masses that it had to add to become NaN.
+__device__ __noinline__ void spoil(const Mass &w, const Share &found)
+{
+    for (Runs r(w, found); r.next(w);)
+        for (int i = threadIdx.x; i < (r.to - r.from) * KT; i += THREADS) {
+            const int j = tile_key(r.u, r.from + i / KT) + i % KT;
+            if (some_see(w, r.u, j))
+                w.mass[(static_cast<long long>(r.u.b) * w.a.c.Hkv + r.h) * w.ld + j] = __int_as_float(0x7fffffff);
+        }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_constant__ Mass w,
                                                                  const __grid_constant__ CUtensorMap map_q,
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
             bar_init(told(g), 4);
             bar_init(joined(g), 4);
         }
-        *gave_up = 0;
+        *gave_up = stopped();
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
         prefetch_map(&map_q);
@@ -509,8 +520,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_mass_kernel(const __grid_co
     }
     fence_before();
     __syncthreads();
-    if (tid == 0 && *gave_up)
-        raise(w.a.status, KDA_ST_TIMEOUT);
+    if (*gave_up) {
+        if (tid == 0)
+            raise(w.a.status, KDA_ST_TIMEOUT);
+        spoil(w, *found);
+    }
     if (warp == MMA_WARP) {
         __syncwarp();
         tmem_free<512>(tmem);

@@ -51,7 +51,8 @@ __device__ __forceinline__ uint64_t now_ns()
 
 // What a CTA does when a wait runs out: `gave_up` is set, every later wait returns at once, and
 // the threads walk to the end of the kernel without results (no thread leaves a barrier short);
-// there the status is raised.  The loop is short: it stands in the code wherever a warp waits.
+// there the status is raised and what the CTA had to compute becomes NaN.  The loop is short: it
+// stands in the code wherever a warp waits.
 __device__ __forceinline__ bool bar_wait_long(volatile int *gave_up, uint32_t bar, uint32_t parity, bool keep_on)
 {
     const uint64_t t0 = now_ns();
@@ -64,6 +65,16 @@ __device__ __forceinline__ bool bar_wait_long(volatile int *gave_up, uint32_t ba
         }
     }
     return true;
+}
+
+// What `gave_up` starts with.  The tests' own build stops every n-th CTA so, as if its first wait had run out.
+__device__ __forceinline__ int stopped()
+{
+#ifdef KDA_STOP_EVERY
+    return blockIdx.x % KDA_STOP_EVERY == 0;
+#else
+    return 0;
+#endif
 }
 
 // A warp's wait for the phase of `bar` with `parity`, for a second at most; the warp goes on

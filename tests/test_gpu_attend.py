@@ -1,7 +1,10 @@
 """spec_attend and spec_attend_mass against the formulas in 64 bits: lengths, row counts, head
 groups, pages, layouts, windows and sinks; whatever no row sees holds NaN."""
+import ctypes
 import math
+import os
 import random
+import subprocess
 
 import pytest
 import torch
@@ -10,6 +13,7 @@ from cache_ref import Case, near
 from libs import ensure_built
 
 from speculative_decode_verify_kda_gb300 import binding as kb
+from speculative_decode_verify_kda_gb300 import build
 
 pytestmark = pytest.mark.gpu
 
@@ -547,3 +551,67 @@ def test_a_workspace_that_is_too_small_is_refused():
     need = kb.AttendPlan.workspace_bytes(c.cache(), 2, 4)
     with pytest.raises(kb.KdaError, match="workspace"):
         kb.spec_attend(c.cache(), c.q, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.fixture(scope="module")
+def stopping(tmp_path_factory):
+    """The two attention kernels built so that every third CTA behaves as if its first wait had run out."""
+    where = tmp_path_factory.mktemp("stopping")
+    parts = [str(where / f"{src}.o") for src in ("spec_attend.cu", "spec_attend_mass.cu", "kda_abi.cpp")]
+    jobs = [subprocess.Popen([build.nvcc(), *build.ARCH, *build.NVFLAGS, "-DKDA_STOP_EVERY=3", "-c",
+                              os.path.join(build.CSRC, os.path.basename(o)[:-2]), "-o", o]) for o in parts]
+    assert [j.wait() for j in jobs] == [0, 0, 0]
+    path = str(where / "stopping.so")
+    subprocess.run([build.nvcc(), *build.ARCH, "-shared", "-o", path, *parts], check=True)
+    return ctypes.CDLL(path)
+
+
+def through(L, plan):
+    """The plan's call, made of another library."""
+    fn = getattr(L, plan.name)
+    fn.argtypes, fn.restype = plan._fn.argtypes, plan._fn.restype
+    plan._fn = fn
+    return plan
+
+
+@pytest.mark.parametrize("D,T,Hq", [(128, 4, 8), (64, 4, 8), (128, 40, 16), (64, 40, 16)])
+def test_what_a_stopped_block_had_to_compute_is_nan(stopping, D, T, Hq):
+    """With a status word, and without one; every other row and mass is as it should be."""
+    c = Case([5000, 3, 700, 128, 0, 100, 50, 20, 2000, 64, 30, 7], T=T, Hq=Hq, Hkv=2, D=D, page=32, seed=D + T,
+             t_rows=[T, T, 1, T, T, T, 0, T, T - 1, T, T, T])
+    want, want_lse, tol, tol_lse = c.attend()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    work = torch.zeros(kb.AttendPlan.workspace_bytes(c.cache(), T, Hq), dtype=torch.uint8, device="cuda")
+    for told in (status, None):
+        out = torch.full((c.B, T, Hq, D), 7.0, dtype=BF16, device="cuda")
+        lse = torch.full((c.B, T, Hq), 7.0, device="cuda")
+        through(stopping, kb.AttendPlan(c.cache(), c.q, t_rows=c.t_rows, out=out, lse_out=lse, dev_status=told,
+                                        workspace=work))()
+        lost = torch.isnan(lse).cpu()
+        there = ~torch.isnan(want_lse)
+        assert (lost & there).any() and (~lost & there).any() and not (lost & ~there).any()
+        assert torch.isnan(out.cpu()[lost]).all()
+        near(lse, want_lse.masked_fill(lost, math.nan), tol_lse, "lse")
+        near(out, want.masked_fill(lost[..., None], math.nan), tol, "out")
+        assert torch.all(out.cpu()[~there] == 7.0) and torch.all(lse.cpu()[~there] == 7.0)
+    assert int(status) == kb.ST_TIMEOUT
+    _, lse = run(c)  # the same call of the library proper
+    status.zero_()
+    for told in (status, None):
+        mass = torch.full((c.B, 2, c.cache().capacity), 7.0, device="cuda")
+        through(stopping, kb.AttendMassPlan(c.cache(), c.q, lse, mass, t_rows=c.t_rows, dev_status=told))()
+        mass = mass.cpu()
+        right = 0
+        for b in range(c.B):
+            n, t = c.n[b], c.t[b]
+            assert torch.all(mass[b, :, n + t:] == 7.0)
+            if t == 0:
+                assert torch.all(mass[b] == 7.0)
+                continue
+            share, tol_share = c.share(lse.cpu(), b)
+            old = torch.cat((torch.full((2, n), 7.0), torch.zeros(2, t)), 1).double()
+            lost = torch.isnan(mass[b, :, :n + t])
+            right += int((~lost).sum())
+            near(mass[b, :, :n + t], (old + share).masked_fill(lost, math.nan), tol_share + 2.0**-23 * (old + share))
+        assert right > 0 and torch.isnan(mass).any()
+    assert int(status) == kb.ST_TIMEOUT
