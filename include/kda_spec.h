@@ -743,8 +743,11 @@ int spec_cache_append(const kda_cache *cache, const void *k_rows, const void *v_
  * off by half a step of it, a KDA_F16 weight under 2^-21 of the row's largest by 2^-32 of that.
  * Keys and values that no row of the call sees may hold anything (pages behind the window
  * may have been given back), and one that only later rows see does not reach earlier ones.
- * Of a key that some rows of a session see and others do not, a value that is not finite
- * makes the whole of a row that sees it NaN.  A row whose scores are all -inf gives zeros
+ * A value that is not finite makes its element of out not finite in every row that sees its
+ * key.  Rows are computed in units of U = 128 / (Hq / Hkv) tokens that follow one another from a
+ * session's first row of the call on (2 U where T > U): where some rows of a unit see the key and
+ * others do not, the whole of a row that sees it is NaN; where all do, the other elements are as
+ * they would be without it.  A row whose scores are all -inf gives zeros
  * and lse -inf.  The same call gives the same bits; how its work is cut, and so a result's
  * last bits, depends on the lengths of all its sessions.
  *   workspace: device memory of spec_attend_workspace_bytes(B, T, Hq, Hkv, D) bytes, 16-byte

@@ -333,6 +333,32 @@ def test_values_that_only_some_rows_see_reach_those_alone(T, window, at, dtype):
     assert not torch.isfinite(out[:, sees][..., 9]).any()
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("T,G,window,at", [(200, 4, 0, 135), (200, 4, 100, 100), (31, 4, 0, 133), (300, 1, 0, 390),
+                                           (40, 100, 0, 132), (200, 4, 0, 60), (150, 16, 70, 199)])
+def test_how_far_a_value_that_is_not_finite_reaches(T, G, window, at, bad):
+    """The whole row where only some of the unit's rows see the key, else its own element alone."""
+    c = Case([130], T=T, Hq=G, Hkv=1, window=window, seed=T + at)
+    c.v[c.table[0, at // c.page], :, at % c.page, 9] = bad
+    out, lse = kb.spec_attend(c.cache(), c.q, **c.see())
+    want, want_lse, tol, tol_lse = c.attend()
+    near(lse, want_lse, tol_lse)
+    unit = 128 // G * (2 if T > 128 // G else 1)
+    sees = [c.sees(130 + t, at) for t in range(T)]
+    out, parts = out.cpu(), 0
+    for t in range(T):
+        mates = sees[t // unit * unit:][:unit]
+        if sees[t] and not all(mates):
+            assert torch.isnan(out[0, t]).all(), t
+            parts += 1
+        else:
+            if sees[t]:
+                assert not torch.isfinite(out[0, t, :, 9]).any(), t
+                out[0, t, :, 9] = want[0, t, :, 9].to(out.dtype)
+            near(out[0, t], want[0, t], tol[0, t], f"row {t}")
+    assert any(sees) and (parts == 0) == (at == 60)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_values_that_are_not_finite_in_many_short_sessions(D):
     """Units of one key tile follow one another in a block: what one marks does not reach the others."""
