@@ -738,7 +738,8 @@ int spec_cache_append(const kda_cache *cache, const void *k_rows, const void *v_
  * that is everything before it, or the last `window` keys (itself among them) and the
  * first `sinks` ones.  With s_j = scale q.k_j (scale in KDA_SCALE_MIN..MAX) over the visible keys
  *   lse = ln sum_j exp s_j,   o = sum_j exp(s_j - lse) v_j:
- *   out [B][T][Hq][D] of the cache's type, dense; lse f32 [B][T][Hq] (may be NULL).
+ *   out [B][T][Hq][D] of the cache's type, dense (q itself, where that is dense, or apart from
+ *   it); lse f32 [B][T][Hq] (may be NULL).
  * Sums and statistics are f32; the weights enter the product with v in the cache's type, each
  * off by half a step of it, a KDA_F16 weight under 2^-21 of the row's largest by 2^-32 of that.
  * Keys and values that no row of the call sees may hold anything (pages behind the window

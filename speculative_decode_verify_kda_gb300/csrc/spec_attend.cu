@@ -908,6 +908,12 @@ extern "C" int spec_attend(const kda_cache *cache, const void *q, int T, int Hq,
         return ok();
     if (!out || !aligned16(out))
         return fail(KDA_EINVAL, "out must not be NULL and must be 16-byte aligned");
+    // q itself is read by the CTAs that write a unit's rows, before they do; rows that lie otherwise are not
+    const double rows = static_cast<double>(a.c.B) * T, q_at = static_cast<double>(reinterpret_cast<uintptr_t>(q)),
+                 out_at = static_cast<double>(reinterpret_cast<uintptr_t>(out)), width = static_cast<double>(Hq) * a.c.D;
+    if (!(q == out && static_cast<double>(ld_q) == width) && q_at < out_at + 2 * rows * width &&
+        out_at < q_at + 2 * ((rows - 1) * static_cast<double>(ld_q) + width))
+        return fail(KDA_EINVAL, "out must be q itself, with dense rows, or lie apart from it");
     if (!workspace || !aligned16(workspace) ||
         workspace_bytes < spec_attend_workspace_bytes(a.c.B, T, Hq, a.c.Hkv, a.c.D))
         return fail(KDA_EINVAL, "workspace must hold spec_attend_workspace_bytes(...) bytes, 16-byte aligned");

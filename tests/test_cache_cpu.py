@@ -106,6 +106,16 @@ def test_evict_refuses(L, bad):
     assert evict(L, cache(), **bad) == kb.EINVAL
 
 
+@pytest.mark.parametrize("ld,out", [(520, 0), (512, 16), (512, -16), (512, 2 * 5 * 512), (4096, 2 * 5 * 4096 + 1008)])
+def test_attend_refuses_an_out_that_overlaps_its_rows(L, ld, out):
+    base = 1 << 24
+    assert attend(L, cache(), q=base, ld=ld, out=base + out) == kb.EINVAL and b"apart" in L.kda_last_error()
+    # q itself, and what lies behind or before it, pass this check (and fail the next)
+    for q_ld, apart in ((512, 0), (ld, 2 * 5 * ld + 1024), (ld, -2 * 6 * 512)):
+        assert attend(L, cache(), q=base, ld=q_ld, out=base + apart, work=None) == kb.EINVAL
+        assert b"workspace" in L.kda_last_error()
+
+
 def test_more_tiles_than_a_call_counts_are_refused(L):
     many = cache(B=2**20, Hkv=64, table_cols=2**16)
     assert attend(L, many, T=1, Hq=64, ld=64 * 128) == kb.EINVAL and b"tiles" in L.kda_last_error()

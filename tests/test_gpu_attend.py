@@ -563,6 +563,19 @@ def test_two_calls_at_once():
         near(p.out[0], want, tol)
 
 
+@pytest.mark.parametrize("T,Hq,D", [(3, 8, 128), (60, 16, 128), (200, 4, 64)])
+def test_results_in_the_place_of_the_rows(T, Hq, D):
+    c = Case([3000, 17, 400, 0], T=T, Hq=Hq, Hkv=2, D=D, t_rows=[T, T, 0, T - 1], seed=T)
+    out, lse = kb.spec_attend(c.cache(), c.q, t_rows=c.t_rows)
+    for _ in range(3):
+        q = c.q.clone()
+        again, lse2 = kb.spec_attend(c.cache(), q, t_rows=c.t_rows, out=q)
+        assert again is q
+        for b, t in enumerate(c.t):
+            assert torch.equal(q[b, :t], out[b, :t]) and torch.equal(lse2[b, :t], lse[b, :t])
+            assert torch.isnan(q[b, t:]).all()
+
+
 def test_no_rows_and_no_sessions():
     c = Case([10, 20], T=2)
     out, lse = kb.spec_attend(c.cache(), c.q[:, :0])
