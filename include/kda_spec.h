@@ -74,8 +74,8 @@ extern "C" {
                                scores and losses: a row holds a NaN or +inf, or
                                a teacher's entries of the row do               */
 #define KDA_ST_BADKEEP 0x2  /* a device keep outside 1..T, or a device row count
-                               outside 1..T (the *_var calls); that session is
-                               left untouched                                    */
+                               outside 1..T (the *_var calls) or 0..T (a paged
+                               cache); that session is left untouched            */
 #define KDA_ST_TIMEOUT 0x4  /* a wait inside a kernel ran out (one second: a copy, a
                                product or a partner warp never arrived); the CTA
                                stopped early and its units are unfinished.

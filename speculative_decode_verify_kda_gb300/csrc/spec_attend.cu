@@ -18,8 +18,8 @@
 // Rounded to 16 bits: the weights (as an operand of the products must be) and the results.  Weights
 // are taken against a maximum that is at most 2^8 too small, their sum is of the unrounded ones.
 //
-// Measured on GB300 (in a CUDA graph): a prompt's chunk of 2048 rows of 64 heads over 16384 keys 686
-// us, 1.7 PFLOP/s (87 % of the measured product rate); 32 sessions of 15 rows over up to 16384 keys
+// Measured on GB300 (alone in a CUDA graph): a prompt's chunk of 2048 rows of 64 heads over 16384 keys 686
+// us, 1.7 PFLOP/s (87 % of the measured product rate; 745 to 768 us, 78 to 80 %, among other calls); 32 sessions of 15 rows over up to 16384 keys
 // 235 us, 6.4 TB/s; one row of 32 heads over 131072 keys 88 us, 6.1 TB/s.  A round of few keys is
 // bound by a chain of latencies: lengths, table, keys, scores, weights, result, join (14 us for one
 // row of 64 heads over 4096 keys).  Runs are short where windows are, and then the code of their ends

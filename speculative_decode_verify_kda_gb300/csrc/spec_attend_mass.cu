@@ -10,8 +10,9 @@
 // products.  A row's -lse / scale is part of the product, as four 16-bit terms of its own against a
 // column of constants: read from shared memory by every thread it bound the kernel (128 bytes a cycle,
 // as do the reads of tensor memory).  Bound by the keys' bytes for a verify round's rows (61 us for 16
-// sessions of 8 rows of 64 heads over up to 16384 keys, 5.6 TB/s), by exp2 and the reads of tensor
-// memory for a prompt's (67 us for 1024 rows of 32 heads over 8192 keys, 1.1 PFLOP/s).
+// sessions of 8 rows of 64 heads over up to 16384 keys, 5.6 TB/s), by exp2 and the reads of scores before
+// it, which add up, for a prompt's (68 us for 1024 rows of 32 heads over 8192 keys, 1.1 PFLOP/s; the
+// tensor pipe and the exponentials' are busy half the time each).
 #include "attend_common.cuh"
 
 namespace kda {

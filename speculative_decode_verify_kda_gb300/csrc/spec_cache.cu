@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(APPEND_T) cache_append_kernel(const Append a)
 // in shared memory (8 heads of 131072 tokens took 74 us for 50 when every pass read them again); more than
 // 393 thousand tokens of a head do not fit and are read again, from the caches, by every pass.  With
 // REGISTERS up to HELD numbers a lane stay in those: better where heads fill the SMs (64 heads of 8192
-// tokens 37.5 us for 45), worse for a few, whose time is that of the code (8 heads of 2048 tokens 12.4 us for
-// 11.0, of 8192 16.5 for 14.8).
+// tokens 31.3 us for 35.5), worse for a few, whose time is that of the code (8 heads of 2048 tokens 12.5 us for
+// 10.9, of 8192 16.4 for 15.0).
 // Second launch: the kept keys, values and masses move.  Bound by the chain of passes and barriers for a
 // few heads (8 heads of 32768 tokens to 4096: 25 us, 5 of them for the bytes), by the move's bytes for many
 // (256 heads of up to 8000 tokens to 2000: 105 us, the bytes 79).
@@ -544,9 +544,9 @@ extern "C" int spec_cache_evict(const kda_cache *cache, const float *mass, long 
     a.status = dev_status;
     const unsigned heads = static_cast<unsigned>(a.c.B) * a.c.Hkv;
     // Eight CTAs a head while the device has room for them and a head has work for them, and where one
-    // CTA could not hold its numbers.  One against eight, us (budget 1024): 8 heads of 4096 tokens 14.8
-    // and 16.2, of 8192 19.5 and 16.8, of 32768 49 and 20; 64 heads of 8192 37.5 and 44.7, of 32768 78
-    // and 57; 128 heads of 32768 89 and 107, of 65536 241 and 142.
+    // CTA could not hold its numbers.  One against eight, us (budget 1024, in a CUDA graph): 8 heads of 4096
+    // tokens 13.6 and 14.1, of 8192 18.5 and 14.8, of 32768 48 and 19; 64 heads of 8192 31 and 39, of
+    // 16384 48 and 43, of 32768 70 and 51; 128 heads of 32768 87 and 105, of 65536 239 and 140.
     const bool few = heads <= pages::SMS / 4;
     const bool wide = capacity > (few ? 4096 : heads <= pages::SMS / 2 ? 16384 : SELECT_W * STORED);
     if (int rc = few ? (wide ? select<8, false>(a, heads, stream) : select<1, false>(a, heads, stream))
