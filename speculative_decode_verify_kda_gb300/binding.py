@@ -1249,7 +1249,7 @@ class AttendMassPlan(_QueryPlan):
         if isinstance(lse, torch.Tensor) and tuple(lse.shape) == shape and lse.dtype == torch.float32 and \
                 not lse.is_contiguous():
             self._hold(lse, "lse")
-            self._strided, lse = lse, self._out(None, "lse", torch.float32, shape)
+            self._strided, lse = lse.detach(), self._out(None, "lse", torch.float32, shape)
             self._dense, self._on = lse, _stream(stream)
         lse = self._in(lse, "lse", torch.float32, shape)
         ptr, ld = self._mass(mass, "mass", cache.capacity)

@@ -428,6 +428,10 @@ def test_mass_with_an_lse_of_any_strides(Hq, Hkv):
         # exponents of size 64 at most on either side, off by 2^-21 of that
         near(mass, want.double() / math.e, 2.0**-14 * want)
         x.sub_(1.0)
+    turned.copy_(lse)
+    plan = kb.AttendMassPlan(c.cache(), c.q, turned.requires_grad_(), torch.zeros_like(want))
+    assert torch.equal(plan(), want)
+    assert not plan.out.requires_grad and not plan._dense.requires_grad
 
 
 def test_mass_adds_up():
